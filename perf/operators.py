@@ -453,15 +453,16 @@ def exact(case, seed):
 
 def _exact_logprobs(case, c, z, y):
     lp = torch.log_softmax(c, 1)
-    keep = (y != IGNORE).double()
+    skip = y == IGNORE
     lse = torch.logsumexp(c, 1)
     entropy = -torch.nan_to_num(lp.exp() * lp, nan=0.0).sum(1)
-    out = [lp.gather(1, y.clamp(min=0).long()[:, None]).squeeze(1) * keep, lse * keep, entropy * keep]
+    at = lp.gather(1, y.clamp(min=0).long()[:, None]).squeeze(1)
+    out = [v.masked_fill(skip, 0.0) for v in (at, lse, entropy)]
     if case["top_k"]:
         # a stable sort keeps equal values in the order of their ids
         order = z.float().sort(dim=1, descending=True, stable=True).indices[:, :case["top_k"]]
         val = lp.gather(1, order)
-        none = torch.isinf(val) | (keep == 0)[:, None]
+        none = torch.isinf(val) | skip[:, None]
         out += [val.masked_fill(none, float("-inf")), order.masked_fill(none, -1).to(torch.int32)]
     return out
 
