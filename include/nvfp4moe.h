@@ -528,6 +528,82 @@ nvfp4_status moe_expert_backward(const void* dout, const void* x, const float* w
 nvfp4_status moe_backward_workspace_layout(int64_t T, int32_t k, int32_t E, int64_t H, int64_t I,
                                            int64_t layout_out[18]);
 
+/* ---------------------------------------------------------------- rows of logits */
+
+/* The operators of a learner's step on the student's logits ("The 4-bitter Lesson...",
+ * reinforcement learning of a model whose experts run in W4A4: the learner needs the log
+ * probabilities of the rollout's tokens and their gradient; "Low-Bit Precision Training Is
+ * Ready for Production...", §"The Cross-Engine Alignment Problem": a token's log probability
+ * must not depend on the batch that it is computed in).  The pages give no interface; these
+ * formulas are this library's.
+ * For every call of this section:
+ *   logits: device [T, ld] of `dtype`, the first V of each row are used; any ld >= V, aligned
+ *     to its element (odd vocabularies and views are fine).  1 <= V <= 2^20, T <= 2^24.
+ *   c = scale * logits, scale finite and > 0 (1 / temperature); lse = ln sum_j exp(c_j);
+ *   p_j = exp(c_j - lse).  Statistics are float32.
+ *   A logit of -inf excludes its token: p = 0, gradient 0, never an alternative.  The type's
+ *   lowest value is a value like any other.  NaN or +inf makes the row's results NaN.
+ *   A row's bits depend on its logits, V and scale alone: not on T, its place or its address. */
+typedef enum { NVFP4_ACT_BF16 = 0, NVFP4_ACT_F32 = 1, NVFP4_ACT_F16 = 2 } nvfp4_act_dtype;
+
+/* Log probabilities of given tokens, entropy and the best alternatives, in one pass.
+ *   targets: device int32 [T] or NULL; logprob: device float [T], c_target - lse (given with
+ *     targets, and only then).  A target equal to ignore_index makes the row's logprob, lse
+ *     and entropy 0 and its list empty; the row is not read.  Any other target outside
+ *     [0, V) sets NVFP4_ERR_DEVICE_STATUS and gives NaN.
+ *   lse: device float [T]; entropy: device float [T] or NULL, -sum_j p_j ln p_j.
+ *   top_k: 0 .. 128, at most V; top_logprob: device float [T, top_k], top_ids: device int32
+ *     [T, top_k]: the tokens with the largest logits, best first, equal ones by lower id;
+ *     places beyond the allowed tokens hold -inf and -1.
+ *   A row whose tokens are all excluded has lse = -inf, logprob = -inf, entropy = 0. */
+nvfp4_status token_logprobs(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                            const int32_t* targets, int32_t ignore_index, float scale, int32_t top_k,
+                            float* logprob, float* lse, float* entropy, float* top_logprob, int32_t* top_ids,
+                            void* stream);
+
+/* The gradient of sum_t dlogprob[t] logprob[t] + dentropy[t] entropy[t]:
+ *   dlogits[t, j] = scale (dlogprob (1[j = target] - p_j) - dentropy p_j (ln p_j + entropy)),
+ * zero in ignored rows, in rows without an allowed token, in rows with lse < -1e30 (nothing but a
+ * mask's lowest values, whose p a float32 lse no longer holds) and at excluded tokens.  p_j is
+ * recomputed from lse and carries its rounding, 2^-24 |lse| relatively.
+ *   lse, entropy: the forward's; targets and dlogprob, entropy and dentropy: device or NULL
+ *     (dlogprob needs targets, dentropy needs entropy).  A target that the forward refused
+ *     adds nothing.
+ *   dlogits: device [T, ldd] of `dtype`, rounded once; it may be `logits` itself (ldd = ld),
+ *     else it must not overlap it. */
+nvfp4_status token_logprobs_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                     const int32_t* targets, int32_t ignore_index, float scale, const float* lse,
+                                     const float* entropy, const float* dlogprob, const float* dentropy,
+                                     void* dlogits, int64_t ldd, void* stream);
+
+/* Distillation from a teacher's top logits: the cross entropy of the teacher's distribution
+ * and the student's, less the teacher's entropy (the forward Kullback-Leibler divergence).
+ *   teacher_ids: device int32 [T, K], distinct in a row, -1 = no entry; teacher_values:
+ *     device float [T, K]; 1 <= K <= 128.  token_logprobs' lists fit.
+ *   tail == 0: q = softmax of the listed values (logits or log probabilities).
+ *     loss = sum_i q_i (ln q_i - ln p_i).
+ *   tail != 0: the values are log probabilities over the whole vocabulary; q_i = exp(value)
+ *     and q_r = max(0, 1 - sum q) is the mass of the unlisted tokens, compared as one:
+ *     loss = sum_i q_i (ln q_i - ln p_i) + q_r (ln q_r - ln p_r), p_r = sum of the unlisted p
+ *     (left out where no unlisted token is allowed).
+ *   loss: device float [T]; lse: device float [T] or NULL.
+ *   A row without entries has loss 0 and lse 0 and is not read.  An id outside [-1, V), or
+ *   twice in a row, sets NVFP4_ERR_DEVICE_STATUS, gives the loss NaN and the gradient 0.
+ *   A listed token that the student excludes and q > 0 give the loss +inf. */
+nvfp4_status distill_topk(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                          const int32_t* teacher_ids, const float* teacher_values, int32_t K, int tail,
+                          float scale, float* loss, float* lse, void* stream);
+
+/* The same loss and its gradient in one call (nothing of the forward is needed):
+ *   dlogits[t, j] = dloss[t] dloss_t/dlogits_tj, rounded once to `dtype`:
+ *     scale dloss (p_j - q_j) at listed tokens; elsewhere scale dloss p_j, and with the tail
+ *     scale dloss p_j (1 - q_r / p_r); 0 at excluded tokens.
+ *   dloss: device float [T] or NULL (ones).  dlogits as in token_logprobs_backward. */
+nvfp4_status distill_topk_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,
+                                   const int32_t* teacher_ids, const float* teacher_values, int32_t K, int tail,
+                                   float scale, const float* dloss, float* loss, float* lse, void* dlogits,
+                                   int64_t ldd, void* stream);
+
 /* Byte offsets of the forward's intermediates inside its workspace, in this order:
  * [0] counts int32[E], [1] offsets int32[E+1], [2] padded_offsets int32[E+1],
  * [3] inv int32[T*k], [4] perm int32[M_cap],

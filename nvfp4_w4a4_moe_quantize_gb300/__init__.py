@@ -29,6 +29,7 @@ __all__ = [
     "SF_SWIZZLED_128x4", "SF_ROWMAJOR",
     "NVFP4MoEWeightsT", "moe_prepare_weights_backward", "moe_expert_backward", "moe_backward_workspace",
     "moe_backward_workspace_layout",
+    "token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward",
 ]
 
 SCALE_PER_TENSOR, SCALE_PER_ROW, SCALE_PER_GROUP = 0, 1, 2
@@ -37,9 +38,11 @@ SF_SWIZZLED_128x4, SF_ROWMAJOR = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 OP_QUANTIZE, OP_PREPARE_WEIGHTS, OP_MOE_FORWARD, OP_MOE_PERMUTE, OP_QUANTIZE_T = 0, 1, 2, 3, 4
 OP_MOE_BACKWARD, OP_PREPARE_WEIGHTS_T = 5, 6
+ACT_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 _lib = None
 _vp, _i64, _i32, _u64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 class Status:
@@ -106,6 +109,14 @@ _SIGS = {
                                            ctypes.POINTER(_WeightsT), _vp, _sz, _u64, _vp, _vp, _vp, _vp, _vp, _sz,
                                            _vp]),
     "moe_backward_workspace_layout": (ctypes.c_int, [_i64, _i32, _i32, _i64, _i64, ctypes.POINTER(_i64)]),
+    "token_logprobs": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i32, _f32, _i32, _vp, _vp, _vp, _vp,
+                                      _vp, _vp]),
+    "token_logprobs_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i32, _f32, _vp, _vp, _vp,
+                                               _vp, _vp, _i64, _vp]),
+    "distill_topk": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _i32, ctypes.c_int, _f32, _vp, _vp,
+                                    _vp]),
+    "distill_topk_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _i32, ctypes.c_int, _f32,
+                                             _vp, _vp, _vp, _vp, _i64, _vp]),
 }
 
 
@@ -592,3 +603,115 @@ def moe_expert_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, we
                                    _p(dx), _p(dw), _p(dw13), _p(dw2), _p(workspace), workspace.numel(),
                                    _stream(stream)), "moe_expert_backward")
     return dx, dw, dw13, dw2
+
+
+# --------------------------------------------------------------------------- rows of logits
+
+def _rows_2d(t: torch.Tensor, what: str) -> torch.Tensor:
+    """A [rows, cols] CUDA tensor of an activation type whose columns are adjacent."""
+    if t.dim() != 2 or t.dtype not in ACT_DTYPES:
+        raise ValueError(f"{what} must be a 2-D BF16, float16 or float32 tensor")
+    _dev(t)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return t
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _per_row(t, rows: int, dtype, like: torch.Tensor, what: str, cols: int | None = None):
+    """Checks a [rows] (or [rows, cols]) companion of `like`; None passes.  Returns it dense."""
+    if t is None:
+        return None
+    shape = (rows,) if cols is None else (rows, cols)
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != like.device:
+        raise ValueError(f"{what} must be {dtype} {list(shape)} on {like.device}")
+    return t.contiguous()
+
+
+def _like_rows(out, like: torch.Tensor, what: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError(f"{what} must have the shape, type and device of its input")
+    return _rows_2d(out, what)
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
+                   ignore_index: int = -100, entropy: bool = True, stream=None):
+    """Log probabilities of given tokens, entropy and top alternatives of logits [T, V] (BF16,
+    float16 or float32; rows may be strided).  Returns (logprob, lse, entropy, top_logprobs,
+    top_ids): float32 [T], [T], [T], [T, top_k] and int32 [T, top_k], None for what was not
+    asked.  targets: int32 [T]; a row whose target is ignore_index is skipped (zeros)."""
+    lib = load()
+    T, V = _rows_2d(logits, "logits").shape
+    dev = logits.device
+    targets = _per_row(targets, T, torch.int32, logits, "targets")
+    f = dict(dtype=torch.float32, device=dev)
+    logprob = torch.empty(T, **f) if targets is not None else None
+    lse = torch.empty(T, **f)
+    ent = torch.empty(T, **f) if entropy else None
+    top_lp = torch.empty(T, top_k, **f) if top_k > 0 else None
+    top_ids = torch.empty(T, top_k, dtype=torch.int32, device=dev) if top_k > 0 else None
+    _check(lib.token_logprobs(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(targets), ignore_index,
+                              scale, top_k, _p(logprob), _p(lse), _p(ent), _p(top_lp), _p(top_ids), _stream(stream)),
+           "token_logprobs")
+    return logprob, lse, ent, top_lp, top_ids
+
+
+def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, targets: torch.Tensor | None = None,
+                            dlogprob: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
+                            dentropy: torch.Tensor | None = None, scale: float = 1.0, ignore_index: int = -100,
+                            out: torch.Tensor | None = None, stream=None):
+    """dlogits [T, V] of sum(dlogprob * logprob + dentropy * entropy), with the forward's lse and
+    entropy (all float32 [T]).  out may be the logits themselves."""
+    lib = load()
+    T, V = _rows_2d(logits, "logits").shape
+    targets = _per_row(targets, T, torch.int32, logits, "targets")
+    rows = [_per_row(t, T, torch.float32, logits, n) for t, n in
+            ((lse, "lse"), (entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy"))]
+    out = _like_rows(out, logits, "out")
+    _check(lib.token_logprobs_backward(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(targets),
+                                       ignore_index, scale, *(_p(r) for r in rows), _p(out), _pitch(out),
+                                       _stream(stream)), "token_logprobs_backward")
+    return out
+
+
+def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values: torch.Tensor, tail: bool = True,
+                 scale: float = 1.0, stream=None):
+    """Distillation loss of logits [T, V] against a teacher's top entries (ids int32 [T, K], -1 =
+    none; values float32 [T, K]).  tail: the values are log probabilities over the whole
+    vocabulary and the unlisted tokens count as one; else q = softmax(values).  Returns
+    (loss, lse), float32 [T]."""
+    lib = load()
+    T, V = _rows_2d(logits, "logits").shape
+    K = teacher_ids.shape[-1]
+    ids = _per_row(teacher_ids, T, torch.int32, logits, "teacher_ids", K)
+    values = _per_row(teacher_values, T, torch.float32, logits, "teacher_values", K)
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    _check(lib.distill_topk(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(ids), _p(values), K,
+                            int(tail), scale, _p(loss), _p(lse), _stream(stream)), "distill_topk")
+    return loss, lse
+
+
+def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values: torch.Tensor,
+                          dloss: torch.Tensor | None = None, tail: bool = True, scale: float = 1.0,
+                          out: torch.Tensor | None = None, stream=None):
+    """The loss of distill_topk and dlogits [T, V] = dloss * dloss/dlogits in one call (dloss
+    float32 [T], None: ones; nothing of the forward is needed).  out may be the logits
+    themselves.  Returns (loss, dlogits)."""
+    lib = load()
+    T, V = _rows_2d(logits, "logits").shape
+    K = teacher_ids.shape[-1]
+    ids = _per_row(teacher_ids, T, torch.int32, logits, "teacher_ids", K)
+    values = _per_row(teacher_values, T, torch.float32, logits, "teacher_values", K)
+    dloss = _per_row(dloss, T, torch.float32, logits, "dloss")
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    out = _like_rows(out, logits, "out")
+    _check(lib.distill_topk_backward(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(ids), _p(values), K,
+                                     int(tail), scale, _p(dloss), _p(loss), None, _p(out), _pitch(out),
+                                     _stream(stream)), "distill_topk_backward")
+    return loss, out

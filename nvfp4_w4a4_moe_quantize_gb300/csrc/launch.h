@@ -11,6 +11,7 @@ namespace nvfp4 {
 enum : int { kScopeTensor = 0, kScopeRow = 1, kScopeGroup = 2 };
 enum : int { kRoundRNE = 0, kRoundSR = 1 };
 enum : int { kMapIdentity = 0, kMapInterleave = 1 };
+enum : int { kActBF16 = 0, kActF32 = 1, kActF16 = 2 };
 
 struct QuantArgs {
   const __nv_bfloat16* x;  // input rows [rows, ld]
@@ -197,6 +198,22 @@ cudaError_t launch_swiglu_backward(const void* gu, const void* dh, int64_t rows,
 cudaError_t launch_swiglu_quant(const void* d, const int32_t* perm, int64_t rows, const int32_t* nrows_dev,
                                 int64_t I, int64_t Ip, void* h_out, uint8_t* hq, uint8_t* hsf, float* gh,
                                 cudaStream_t s);
+
+// Rows of logits (logprobs.cu, distill.cu): 1 <= V <= 2^20, at most 128 alternatives or
+// teacher entries; pointers aligned to their element.
+// targets, logprob, entropy nullable; k = 0: no alternatives.
+cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                  const int32_t* targets, int32_t ignore, float scale, int k, float* logprob,
+                                  float* lse, float* entropy, float* top_logprob, int32_t* top_ids, cudaStream_t s);
+// targets with dlogprob, and entropy with dentropy, nullable.
+cudaError_t launch_token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                           const int32_t* targets, int32_t ignore, float scale, const float* lse,
+                                           const float* entropy, const float* dlogprob, const float* dentropy,
+                                           void* dlogits, int64_t ldd, cudaStream_t s);
+// dlogits nullable: the loss alone.  dloss (nullable: ones), lse nullable.
+cudaError_t launch_distill_topk(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int32_t* ids,
+                                const float* values, int K, bool tail, float scale, const float* dloss, float* loss,
+                                float* lse, void* dlogits, int64_t ldd, cudaStream_t s);
 
 constexpr int64_t kPermuteChunk = 256;    // (token, j) entries per warp in the permute
 inline int64_t permute_chunks(int64_t entries) { return (entries + kPermuteChunk - 1) / kPermuteChunk; }

@@ -1,0 +1,414 @@
+// Log probabilities of given tokens, entropy and the top alternatives of rows of logits, and
+// their backward.
+//
+//   c = scale z,  lse = ln sum exp(c),  logprob = c_y - lse,  H = lse - sum p c,  p = exp(c - lse)
+//   dz = scale (g (1[j = y] - p) - h p (ln p + H))
+//
+// Forward: one pass over the row with a running maximum (vocab.cuh).
+// The top k come out of the same pass.  Every thread remembers, for each slice, its best value
+// and the first chunk that held it (a cell).  The k-th best of the threads' best is a lower
+// bound of the k-th best of the row, so only cells that reach it can hold one of the top k;
+// their few chunks are read again (from L2) and every element that reaches the bound becomes a
+// candidate, ranked by (value, lowest id).  A sort or a heap over the row is not needed, and
+// no atomic decides an order: a candidate's key is its value and id.
+#include "launch.h"
+#include "pdl.cuh"
+#include "status.cuh"
+#include "vocab.cuh"
+
+namespace nvfp4 {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kKeep = 1024;                              // candidates kept from round to round
+constexpr int kCandidates = kKeep + kVocabThreads * 8;   // a round adds at most 8 a thread
+
+// Order of the values as unsigned words; -0 counts as 0.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
+}
+// Larger value first, then the lower position.
+__device__ __forceinline__ uint64_t order_key(float v, uint32_t pos) {
+  return (static_cast<uint64_t>(order_bits(v)) << 32) | (0xffffffffu - pos);
+}
+
+struct LogprobSmem {
+  Stats part[kMaxSlices][kVocabWarps];
+  int count, cells;
+  uint64_t bound;
+};
+struct TopSmem {
+  float best[kMaxSlices][kVocabThreads];       // a cell's best value, -inf: nothing there
+  int chunk[kMaxSlices][kVocabThreads];        // the first chunk that holds it
+  uint16_t cell[kMaxSlices * kVocabThreads];   // cells that reach the bound
+  uint64_t key[kCandidates];
+  uint64_t sorted[kMaxList];
+  uint64_t lists[kMaxSlices][kMaxList];        // the cluster's lists (first CTA)
+  int sizes[kMaxSlices];
+};
+
+// The best min(n, k) of key[0 .. n) in order into out; returns how many.  Keys differ, so a
+// key's rank is the number of larger ones.
+__device__ __forceinline__ int rank_keys(const uint64_t* key, int n, int k, uint64_t* out) {
+  for (int i = threadIdx.x; i < n; i += kVocabThreads) {
+    const uint64_t mine = key[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += key[j] > mine;
+    if (rank < k) out[rank] = mine;
+  }
+  __syncthreads();
+  return min(n, k);
+}
+
+// The k-th largest (value, first chunk) over the threads' best cells; one warp, 8 threads'
+// cells a lane.  0 when fewer than k threads hold anything.
+__device__ __forceinline__ uint64_t list_bound(const TopSmem& t, int slices, int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t val[kVocabWarps];
+  uint32_t chunk[kVocabWarps];
+#pragma unroll
+  for (int w = 0; w < kVocabWarps; ++w) {
+    const int i = w * 32 + lane;
+    float b = t.best[0][i];
+    int c = t.chunk[0][i];
+    for (int s = 1; s < slices; ++s)
+      if (t.best[s][i] > b) {
+        b = t.best[s][i];
+        c = t.chunk[s][i];
+      }
+    val[w] = b > -INFINITY ? order_bits(b) : 0u;
+    chunk[w] = static_cast<uint32_t>(c);
+  }
+  // the largest value that k of them reach, bit by bit
+  uint32_t v = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t next = v | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kVocabWarps; ++w) n += val[w] >= next;
+    if (__reduce_add_sync(0xffffffffu, n) >= k) v = next;
+  }
+  if (v == 0) return 0;
+  // of those equal to it, the (k - larger) lowest chunks: the smallest chunk bound that keeps k
+  int over = 0;
+#pragma unroll
+  for (int w = 0; w < kVocabWarps; ++w) over += val[w] > v;
+  over = __reduce_add_sync(0xffffffffu, over);
+  uint32_t c = 0xfffffu;
+  for (int bit = 19; bit >= 0; --bit) {
+    const uint32_t next = c & ~(1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kVocabWarps; ++w) n += val[w] == v && chunk[w] <= next;
+    if (over + __reduce_add_sync(0xffffffffu, n) >= k) c = next;
+  }
+  return (static_cast<uint64_t>(v) << 32) | (0xffffffffu - (8 * c + 7));
+}
+
+struct LogprobArgs {
+  const void* logits;
+  int64_t ld;
+  int V;
+  const int32_t* targets;
+  int32_t ignore;
+  float scale;
+  int k;
+  float *logprob, *lse, *entropy, *top_logprob;
+  int32_t* top_ids;
+  int* status;
+};
+
+// One row a cluster; a cluster is one CTA that runs the row's slices in turn, or one CTA a
+// slice.
+template <typename E, bool kEntropy, bool kTop>
+__global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const LogprobArgs a) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  __shared__ LogprobSmem sm;
+  TopSmem& top = *reinterpret_cast<TopSmem*>(dyn);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  const int64_t t = blockIdx.x / ctas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t y = a.targets != nullptr ? a.targets[t] : 0;
+  if (a.targets != nullptr && y == a.ignore) {   // the same in every CTA of the cluster
+    if (rank == 0) {
+      if (tid == 0) {
+        a.logprob[t] = 0.f;
+        a.lse[t] = 0.f;
+        if (kEntropy) a.entropy[t] = 0.f;
+      }
+      if (kTop)
+        for (int i = tid; i < a.k; i += kVocabThreads) {
+          a.top_logprob[t * a.k + i] = -INFINITY;
+          a.top_ids[t * a.k + i] = -1;
+        }
+    }
+    return;
+  }
+  const Row<E> row(static_cast<const E*>(a.logits), a.ld, t, a.V);
+  const int slices = vocab_slices(a.V);
+  const float c1 = a.scale * kLog2e;
+  const int s0 = ctas == 1 ? 0 : rank, s1 = ctas == 1 ? slices : rank + 1;
+  if (ctas > 1) cluster.sync();   // every CTA of the cluster has started: its shared memory may be written
+  Stats(*part)[kVocabWarps] = ctas == 1 ? sm.part : cluster.map_shared_rank(sm.part, 0);
+  if (kTop && tid == 0) sm.count = sm.cells = 0;
+  for (int s = s0; s < s1; ++s) {
+    int first, last;
+    slice_range(a.V, slices, s, first, last);
+    Stats st = empty_stats();
+    float best = -INFINITY;
+    int at = 0;
+    for_chunks(row, first, last, [&](int c, const float(&v)[8]) {
+      const float cm = accumulate<kEntropy>(st, v, c1);
+      if (kTop && cm > best) {
+        best = cm;
+        at = c;
+      }
+    });
+    st = warp_merge<kEntropy>(st, c1);
+    if (lane == 0) part[s][warp] = st;
+    if (kTop) {
+      top.best[s - s0][tid] = best;
+      top.chunk[s - s0][tid] = at;
+    }
+  }
+  int found = 0;
+  if (kTop) {
+    const int mine = s1 - s0;
+    __syncthreads();
+    if (warp == 0) {
+      const uint64_t b = list_bound(top, mine, a.k);
+      if (lane == 0) sm.bound = b;
+    }
+    __syncthreads();
+    const uint64_t bound = sm.bound;
+    for (int s = 0; s < mine; ++s)
+      if (top.best[s][tid] > -INFINITY && order_key(top.best[s][tid], 8 * top.chunk[s][tid]) >= bound)
+        top.cell[atomicAdd(&sm.cells, 1)] = static_cast<uint16_t>(s * kVocabThreads + tid);
+    __syncthreads();
+    // each round every warp reads up to 32 chunks of one cell
+    const int cells = sm.cells;
+    int per = 0;
+    {
+      int first, last;
+      slice_range(a.V, slices, s0, first, last);
+      per = (last - first + kVocabThreads - 1) / kVocabThreads;   // the first slice is the longest
+    }
+    const int groups = (per + 31) / 32, items = cells * groups;
+    for (int base = 0; base < items; base += kVocabWarps) {
+      const int item = base + warp;
+      if (item < items) {
+        const int cell = top.cell[item / groups];
+        int first, last;
+        slice_range(a.V, slices, s0 + cell / kVocabThreads, first, last);
+        const int c = first + cell % kVocabThreads + ((item % groups) * 32 + lane) * kVocabThreads;
+        if (c < last) {
+          float v[8];
+          row.get(c, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t key = order_key(v[i], 8 * c + i);
+            if (v[i] > -INFINITY && key >= bound) top.key[atomicAdd(&sm.count, 1)] = key;
+          }
+        }
+      }
+      __syncthreads();
+      const int n = sm.count;
+      __syncthreads();      // everyone has read it before the next round counts on
+      if (n > kKeep) {      // keep the best k, so that the next round has room
+        rank_keys(top.key, n, a.k, top.sorted);
+        if (tid < a.k) top.key[tid] = top.sorted[tid];
+        if (tid == 0) sm.count = a.k;
+        __syncthreads();
+      }
+    }
+    found = rank_keys(top.key, sm.count, a.k, top.sorted);
+    if (ctas > 1) {   // push the list into the first CTA
+      TopSmem* lead = cluster.map_shared_rank(&top, 0);
+      if (tid < found) lead->lists[rank][tid] = top.sorted[tid];
+      if (tid == 0) lead->sizes[rank] = found;
+    }
+  }
+  if (ctas > 1) {
+    cluster.sync();
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+  const Stats st = join_slices<kEntropy>(sm.part, slices, c1);   // every warp, the same bits
+  const float ln_s = logf(st.s);
+  const bool none = st.s == 0.f;   // every token excluded
+  if (tid == 0) {
+    if (a.targets != nullptr) {
+      float lp = -INFINITY;
+      if (y < 0 || y >= a.V) {
+        set_status(a.status, kStatusBadInput);
+        lp = NAN;
+      } else if (!none) {
+        lp = fmaf(to_f32(row.p[y]) - st.m, a.scale, -ln_s);
+      }
+      a.logprob[t] = lp;
+    }
+    a.lse[t] = none ? -INFINITY : fmaf(st.m, a.scale, ln_s);
+    if (kEntropy) {
+      const float h = ln_s - kLn2 * (st.u / st.s);
+      a.entropy[t] = none || h < 0.f ? 0.f : h;   // round-off below 0
+    }
+  }
+  if (kTop) {
+    const uint64_t* list = top.sorted;
+    if (ctas > 1) {
+      // merge the sorted lists: a key's rank is its place in its own list plus the larger
+      // keys of every other
+      for (int i = tid; i < ctas * kMaxList; i += kVocabThreads) {
+        const int l = i / kMaxList, p = i % kMaxList;
+        if (p >= top.sizes[l]) continue;
+        const uint64_t mine = top.lists[l][p];
+        int r = p;
+        for (int o = 0; o < ctas && r < a.k; ++o) {
+          if (o == l) continue;
+          int lo = 0, hi = top.sizes[o];
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (top.lists[o][mid] > mine) lo = mid + 1;
+            else hi = mid;
+          }
+          r += lo;
+        }
+        if (r < a.k) top.key[r] = mine;
+      }
+      found = 0;
+      for (int l = 0; l < ctas; ++l) found += top.sizes[l];
+      found = min(found, a.k);
+      list = top.key;
+      __syncthreads();
+    }
+    for (int i = tid; i < a.k; i += kVocabThreads) {
+      float lp = -INFINITY;
+      int32_t id = -1;
+      if (i < found) {
+        lp = fmaf(order_value(static_cast<uint32_t>(list[i] >> 32)) - st.m, a.scale, -ln_s);
+        id = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(list[i]));
+      }
+      a.top_logprob[t * a.k + i] = lp;
+      a.top_ids[t * a.k + i] = id;
+    }
+  }
+}
+
+template <typename E, bool kEntropy, bool kTop>
+cudaError_t launch_forward(const LogprobArgs& a, int64_t T, cudaStream_t s) {
+  static std::atomic<bool> smem_set[64];
+  const int slices = vocab_slices(a.V);
+  // few rows: a row's slices side by side in a cluster, until the rows alone fill the GPU
+  const int ctas = T < 4 * num_sms() ? slices : 1;
+  const int smem = kTop ? static_cast<int>(sizeof(TopSmem)) : 0;
+  auto kernel = token_logprobs_kernel<E, kEntropy, kTop>;
+  if (smem > 0) {
+    const cudaError_t e = set_smem_attr_once(smem_set, reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(T * ctas));
+  cfg.blockDim = dim3(kVocabThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename E>
+cudaError_t forward_dtype(const LogprobArgs& a, int64_t T, cudaStream_t s) {
+  if (a.k > 0) return a.entropy ? launch_forward<E, true, true>(a, T, s) : launch_forward<E, false, true>(a, T, s);
+  return a.entropy ? launch_forward<E, true, false>(a, T, s) : launch_forward<E, false, false>(a, T, s);
+}
+
+struct LogprobBackwardArgs {
+  const void* logits;
+  int64_t ld;
+  int V;
+  const int32_t* targets;
+  int32_t ignore;
+  float scale;
+  const float *lse, *entropy, *dlogprob, *dentropy;
+  void* dlogits;
+  int64_t ldd;
+  int tiles;
+};
+
+constexpr int kBackwardTile = 16384;   // elements of a row a CTA
+
+template <typename E, bool kEntropy>
+__global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(const LogprobBackwardArgs a) {
+  const int64_t t = blockIdx.x / a.tiles;
+  const int lo = static_cast<int>(blockIdx.x % a.tiles) * kBackwardTile, hi = min(a.V, lo + kBackwardTile);
+  const E* z = static_cast<const E*>(a.logits) + t * a.ld;
+  E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
+  const int32_t y = a.targets != nullptr ? a.targets[t] : -1;
+  const float lse = a.lse[t];
+  // a target that the forward refused adds nothing
+  const float g = a.dlogprob != nullptr && y >= 0 && y < a.V ? a.dlogprob[t] : 0.f;
+  const float h = kEntropy ? a.dentropy[t] : 0.f;
+  // nothing to learn from the row: ignored, or nothing above the lowest values (a lse of that
+  // size has lost ln s, and p with it)
+  const bool skip = (a.targets != nullptr && y == a.ignore) || lse < -1e30f;
+  const float c1 = a.scale * kLog2e, l1 = -lse * kLog2e;
+  // with t = log2 p:  dz = p (A + B t), + scale g at the target
+  const float A = -a.scale * (g + (kEntropy ? h * a.entropy[t] : 0.f)), B = -a.scale * h * kLn2;
+  map_range(z, out, lo, hi, threadIdx.x, kVocabThreads, [&](int e0, float(&v)[8]) {
+    const int at = y - e0;
+    const float zy = a.scale * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool hit = i == at && v[i] > -INFINITY;
+      const float lt = fmaf(v[i], c1, l1);
+      const float p = ex2(lt);
+      float d = kEntropy ? p * fmaf(B, fmaxf(lt, -1e30f), A) : p * A;
+      if (hit) d += zy;
+      v[i] = skip ? 0.f : d;
+    }
+  });
+}
+
+template <typename E>
+cudaError_t backward_dtype(const LogprobBackwardArgs& a, int64_t T, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(T * a.tiles));
+  if (a.dentropy != nullptr) token_logprobs_backward_kernel<E, true><<<grid, kVocabThreads, 0, s>>>(a);
+  else token_logprobs_backward_kernel<E, false><<<grid, kVocabThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                  const int32_t* targets, int32_t ignore, float scale, int k, float* logprob,
+                                  float* lse, float* entropy, float* top_logprob, int32_t* top_ids, cudaStream_t s) {
+  LogprobArgs a{logits, ld, static_cast<int>(V), targets, ignore, scale, k, logprob, lse, entropy, top_logprob,
+                top_ids, device_status_ptr()};
+  if (dtype == kActBF16) return forward_dtype<__nv_bfloat16>(a, T, s);
+  if (dtype == kActF16) return forward_dtype<__half>(a, T, s);
+  return forward_dtype<float>(a, T, s);
+}
+
+cudaError_t launch_token_logprobs_backward(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld,
+                                           const int32_t* targets, int32_t ignore, float scale, const float* lse,
+                                           const float* entropy, const float* dlogprob, const float* dentropy,
+                                           void* dlogits, int64_t ldd, cudaStream_t s) {
+  LogprobBackwardArgs a{logits, ld, static_cast<int>(V), targets, ignore, scale, lse, entropy, dlogprob, dentropy,
+                        dlogits, ldd, static_cast<int>((V + kBackwardTile - 1) / kBackwardTile)};
+  if (dtype == kActBF16) return backward_dtype<__nv_bfloat16>(a, T, s);
+  if (dtype == kActF16) return backward_dtype<__half>(a, T, s);
+  return backward_dtype<float>(a, T, s);
+}
+
+}  // namespace nvfp4
