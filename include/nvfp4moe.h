@@ -124,7 +124,8 @@ enum {
   NVFP4_OP_MOE_PERMUTE = 3,     /* args: T, k, E */
   NVFP4_OP_QUANTIZE_T = 4,      /* args: batches * C (rows of the transpose), R */
   NVFP4_OP_MOE_BACKWARD = 5,    /* args: T, k, E, H, I */
-  NVFP4_OP_PREPARE_WEIGHTS_T = 6 /* args: E */
+  NVFP4_OP_PREPARE_WEIGHTS_T = 6, /* args: E */
+  NVFP4_OP_NORM_BACKWARD = 7    /* args: T, gate_rows (0: none or one number a row), -, H */
 };
 size_t nvfp4_workspace_size(int op, int64_t T_or_rows, int64_t k_or_cols, int64_t E,
                             int64_t H, int64_t I);
@@ -603,6 +604,54 @@ nvfp4_status distill_topk_backward(const void* logits, nvfp4_act_dtype dtype, in
                                    const int32_t* teacher_ids, const float* teacher_values, int32_t K, int tail,
                                    float scale, const float* dloss, float* loss, float* lse, void* dlogits,
                                    int64_t ldd, void* stream);
+
+/* ---------------------------------------------------------------- norms around the block */
+
+/* RMS norms before and after the expert block, fused with the block's gate and the scale of
+ * the residual ("Low-Bit Precision Training Is Ready for Production...", §"What W4A4 GEMM
+ * Actually Changes": only the expert layers run in 4 bits; the norms around them stay in
+ * high precision).  The pages give no formulas; these are this library's.
+ *   in:   n = x rstd(x) weight,  rstd(v) = 1 / sqrt(mean(v^2) + eps)
+ *   out:  r = residual_scale x + gate (y rstd(y) weight), y the block's output;
+ *         n = r rstd(r) next_weight, r as it is stored: the next block's input norm
+ * x, y, r, n and their gradients: device [T, H] of `dtype`, inputs with a row pitch ld >= H,
+ * outputs dense; any alignment of the element.  Parameters and statistics are float32:
+ * weight, next_weight [H]; rstd [T].
+ *   gate: device float, NULL; [T] (gate_rows = 0), one number a row; or [gate_rows, H], each
+ *     row serving T / gate_rows consecutive rows (T % gate_rows == 0, gate_rows <= 8192).
+ *   1 <= H <= 8192, eps > 0.  Sums are float32 in an order that H fixes: a row's bits do not
+ *   depend on the batch.  Outputs must not overlap inputs; n may not be r. */
+nvfp4_status moe_norm_in(const void* x, int64_t ldx, nvfp4_act_dtype dtype, int64_t T, int64_t H,
+                         const float* weight, float eps, void* n, float* rstd, void* stream);
+
+/*   dx = dresidual + (the norm's gradient for dn), rounded once; dweight [H] = sum_t dn x rstd.
+ *   dresidual: the gradient that reaches x along the residual, or NULL.
+ *   workspace: nvfp4_workspace_size(NVFP4_OP_NORM_BACKWARD, T, 0, 0, H, 0) bytes, 16-byte
+ *   aligned.  dweight is overwritten.  Deterministic (no atomics). */
+nvfp4_status moe_norm_in_backward(const void* dn, int64_t lddn, const void* dresidual, int64_t lddr,
+                                  const void* x, int64_t ldx, const float* rstd, nvfp4_act_dtype dtype, int64_t T,
+                                  int64_t H, const float* weight, void* dx, float* dweight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*   next_weight NULL: r alone (n and rstd_r are not written).  rstd_y, rstd_r: device float [T]. */
+nvfp4_status moe_norm_out(const void* x, int64_t ldx, const void* y, int64_t ldy, nvfp4_act_dtype dtype, int64_t T,
+                          int64_t H, const float* weight, const float* gate, int64_t gate_rows,
+                          float residual_scale, const float* next_weight, float eps, void* r, void* n,
+                          float* rstd_y, float* rstd_r, void* stream);
+
+/* With d = dr + (the next norm's gradient for dn at r):
+ *   dx = residual_scale d;  dy: the gradient of gate (y rstd_y weight);
+ *   dweight [H], dnext_weight [H], dgate [T] or [gate_rows, H], float32, overwritten.
+ *   dr may be NULL (zero) when dn is given; dn, r, rstd_r, next_weight and dnext_weight are
+ *   given together or not at all (next_weight decides); dgate is given with gate.
+ *   workspace: nvfp4_workspace_size(NVFP4_OP_NORM_BACKWARD, T, gate_rows, 0, H, 0) bytes. */
+nvfp4_status moe_norm_out_backward(const void* dr, int64_t lddr, const void* dn, int64_t lddn, const void* r,
+                                   int64_t ldr, const void* y, int64_t ldy, const float* rstd_y,
+                                   const float* rstd_r, nvfp4_act_dtype dtype, int64_t T, int64_t H,
+                                   const float* weight, const float* gate, int64_t gate_rows,
+                                   float residual_scale, const float* next_weight, void* dx, void* dy,
+                                   float* dweight, float* dgate, float* dnext_weight, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* Byte offsets of the forward's intermediates inside its workspace, in this order:
  * [0] counts int32[E], [1] offsets int32[E+1], [2] padded_offsets int32[E+1],

@@ -30,6 +30,7 @@ __all__ = [
     "NVFP4MoEWeightsT", "moe_prepare_weights_backward", "moe_expert_backward", "moe_backward_workspace",
     "moe_backward_workspace_layout",
     "token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward",
+    "moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
 ]
 
 SCALE_PER_TENSOR, SCALE_PER_ROW, SCALE_PER_GROUP = 0, 1, 2
@@ -37,7 +38,7 @@ ROUND_RNE, ROUND_STOCHASTIC = 0, 1
 SF_SWIZZLED_128x4, SF_ROWMAJOR = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 OP_QUANTIZE, OP_PREPARE_WEIGHTS, OP_MOE_FORWARD, OP_MOE_PERMUTE, OP_QUANTIZE_T = 0, 1, 2, 3, 4
-OP_MOE_BACKWARD, OP_PREPARE_WEIGHTS_T = 5, 6
+OP_MOE_BACKWARD, OP_PREPARE_WEIGHTS_T, OP_NORM_BACKWARD = 5, 6, 7
 ACT_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 _lib = None
@@ -117,6 +118,13 @@ _SIGS = {
                                     _vp]),
     "distill_topk_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _i32, ctypes.c_int, _f32,
                                              _vp, _vp, _vp, _vp, _i64, _vp]),
+    "moe_norm_in": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _i64, _i64, _vp, _f32, _vp, _vp, _vp]),
+    "moe_norm_in_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_int, _i64, _i64, _vp, _vp,
+                                            _vp, _vp, _sz, _vp]),
+    "moe_norm_out": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, _vp, _i64, _f32, _vp, _f32,
+                                    _vp, _vp, _vp, _vp, _vp]),
+    "moe_norm_out_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_int, _i64,
+                                             _i64, _vp, _vp, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -715,3 +723,120 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
                                      int(tail), scale, _p(dloss), _p(loss), None, _p(out), _pitch(out),
                                      _stream(stream)), "distill_topk_backward")
     return loss, out
+
+
+# --------------------------------------------------------------------------- norms around the block
+
+def _norm_rows(t, like: torch.Tensor | None, what: str):
+    """A [T, H] activation like `like`; None passes."""
+    if t is None:
+        return None
+    _rows_2d(t, what)
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} must have the shape, type and device of the other activations")
+    return t
+
+
+def _norm_gate(gate, like: torch.Tensor):
+    """gate as (dense tensor or None, gate_rows): [T] is one number a row, [G, H] G gate rows."""
+    if gate is None:
+        return None, 0
+    T, H = like.shape
+    if gate.dim() == 1:
+        return _per_row(gate, T, torch.float32, like, "gate"), 0
+    return _per_row(gate, gate.shape[0], torch.float32, like, "gate", H), gate.shape[0]
+
+
+def _norm_workspace(T: int, gate_rows: int, H: int, device) -> torch.Tensor:
+    n = int(load().nvfp4_workspace_size(OP_NORM_BACKWARD, T, gate_rows, 0, H, 0))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _pitch_or_0(t) -> int:
+    return 0 if t is None else _pitch(t)
+
+
+def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, stream=None):
+    """The norm before the block: n = x * rstd(x) * weight of x [T, H] (weight float32 [H]).
+    Returns (n [T, H], rstd float32 [T])."""
+    lib = load()
+    T, H = _rows_2d(x, "x").shape
+    weight = _per_row(weight, H, torch.float32, x, "weight")
+    n = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check(lib.moe_norm_in(_p(x), _pitch(x), ACT_DTYPES[x.dtype], T, H, _p(weight), eps, _p(n), _p(rstd),
+                           _stream(stream)), "moe_norm_in")
+    return n, rstd
+
+
+def moe_norm_in_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                         dresidual: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of moe_norm_in: (dx [T, H] = dresidual + the norm's gradient, dweight float32 [H])."""
+    lib = load()
+    T, H = _rows_2d(x, "x").shape
+    dn, dresidual = _norm_rows(dn, x, "dn"), _norm_rows(dresidual, x, "dresidual")
+    rstd = _per_row(rstd, T, torch.float32, x, "rstd")
+    weight = _per_row(weight, H, torch.float32, x, "weight")
+    dx = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    dweight = torch.empty(H, dtype=torch.float32, device=x.device)
+    ws = _norm_workspace(T, 0, H, x.device) if workspace is None else workspace
+    _check(lib.moe_norm_in_backward(_p(dn), _pitch(dn), _p(dresidual), _pitch_or_0(dresidual), _p(x), _pitch(x), _p(rstd),
+                                    ACT_DTYPES[x.dtype], T, H, _p(weight), _p(dx), _p(dweight), _p(ws), ws.numel(),
+                                    _stream(stream)), "moe_norm_in_backward")
+    return dx, dweight
+
+
+def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: torch.Tensor | None = None,
+                 residual_scale: float = 1.0, next_weight: torch.Tensor | None = None, eps: float = 1e-6, stream=None):
+    """The norm after the block: r = residual_scale * x + gate * (y * rstd(y) * weight), and with
+    next_weight the next block's input norm n = r * rstd(r) * next_weight.  gate: None, float32
+    [T] (one number a row) or [G, H] (each row serves T / G consecutive rows).  Returns
+    (r, n, rstd_y, rstd_r); n and rstd_r are None without next_weight."""
+    lib = load()
+    T, H = _rows_2d(x, "x").shape
+    y = _norm_rows(y, x, "y")
+    weight = _per_row(weight, H, torch.float32, x, "weight")
+    next_weight = _per_row(next_weight, H, torch.float32, x, "next_weight")
+    gate, gate_rows = _norm_gate(gate, x)
+    r = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    rstd_y = torch.empty(T, dtype=torch.float32, device=x.device)
+    n = torch.empty_like(r) if next_weight is not None else None
+    rstd_r = torch.empty_like(rstd_y) if next_weight is not None else None
+    _check(lib.moe_norm_out(_p(x), _pitch(x), _p(y), _pitch(y), ACT_DTYPES[x.dtype], T, H, _p(weight), _p(gate), gate_rows,
+                            residual_scale, _p(next_weight), eps, _p(r), _p(n), _p(rstd_y), _p(rstd_r),
+                            _stream(stream)), "moe_norm_out")
+    return r, n, rstd_y, rstd_r
+
+
+def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torch.Tensor, weight: torch.Tensor,
+                          gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                          dn: torch.Tensor | None = None, r: torch.Tensor | None = None,
+                          rstd_r: torch.Tensor | None = None, next_weight: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of moe_norm_out from dr (and dn, with r, rstd_r and next_weight): (dx, dy [T, H],
+    dweight [H], dgate like gate, dnext_weight [H]); the last two None where there is none."""
+    lib = load()
+    T, H = _rows_2d(y, "y").shape
+    if len({t is None for t in (dn, rstd_r, next_weight)}) != 1 or (dn is not None and r is None):
+        raise ValueError("dn, r, rstd_r and next_weight are given together")
+    if dn is None:
+        r = None      # only the next norm's gradient reads it
+    if dr is None and dn is None:
+        raise ValueError("no gradient arrives: give dr, dn or both")
+    dr, dn, r = _norm_rows(dr, y, "dr"), _norm_rows(dn, y, "dn"), _norm_rows(r, y, "r")
+    rstd_y, rstd_r = (_per_row(t, T, torch.float32, y, n) for t, n in ((rstd_y, "rstd_y"), (rstd_r, "rstd_r")))
+    weight = _per_row(weight, H, torch.float32, y, "weight")
+    next_weight = _per_row(next_weight, H, torch.float32, y, "next_weight")
+    gate, gate_rows = _norm_gate(gate, y)
+    f = dict(dtype=torch.float32, device=y.device)
+    dx, dy = (torch.empty(T, H, dtype=y.dtype, device=y.device) for _ in range(2))
+    dweight = torch.empty(H, **f)
+    dgate = torch.empty(gate.shape, **f) if gate is not None else None
+    dnext = torch.empty(H, **f) if next_weight is not None else None
+    ws = _norm_workspace(T, gate_rows, H, y.device) if workspace is None else workspace
+    _check(lib.moe_norm_out_backward(_p(dr), _pitch_or_0(dr), _p(dn), _pitch_or_0(dn), _p(r), _pitch_or_0(r), _p(y),
+                                     _pitch(y), _p(rstd_y), _p(rstd_r), ACT_DTYPES[y.dtype], T, H, _p(weight), _p(gate),
+                                     gate_rows, residual_scale, _p(next_weight), _p(dx), _p(dy), _p(dweight),
+                                     _p(dgate), _p(dnext), _p(ws), ws.numel(), _stream(stream)),
+           "moe_norm_out_backward")
+    return dx, dy, dweight, dgate, dnext

@@ -215,6 +215,22 @@ cudaError_t launch_distill_topk(const void* logits, int dtype, int64_t T, int64_
                                 const float* values, int K, bool tail, float scale, const float* dloss, float* loss,
                                 float* lse, void* dlogits, int64_t ldd, cudaStream_t s);
 
+// Norms around the block (block_norm.cu), 1 <= H <= 8192.  y null: r is x, only n is written.
+// next_weight null: no n.  gate null, one number a row (gate_rows = 0) or gate_rows rows of H.
+cudaError_t launch_block_norm(const void* x, int64_t ldx, const void* y, int64_t ldy, int dtype, int64_t T, int64_t H,
+                              const float* weight, const float* gate, int64_t gate_rows, float alpha,
+                              const float* next_weight, float eps, void* r, void* n, float* rstd_y, float* rstd_r,
+                              cudaStream_t s);
+// Ranges of rows a gate row whose sums meet in the second kernel; partial holds
+// 2 * max(gate_rows, 1) * block_norm_parts * H floats.
+int64_t block_norm_parts(int64_t T, int64_t gate_rows);
+cudaError_t launch_block_norm_backward(const void* dr, int64_t lddr, const void* dn, int64_t lddn, const void* r,
+                                       int64_t ldr, const void* y, int64_t ldy, int dtype, int64_t T, int64_t H,
+                                       const float* rstd_y, const float* rstd_r, const float* weight,
+                                       const float* gate, int64_t gate_rows, float alpha, const float* next_weight,
+                                       void* dx, void* dy, float* dweight, float* dgate, float* dnext, float* partial,
+                                       cudaStream_t s);
+
 constexpr int64_t kPermuteChunk = 256;    // (token, j) entries per warp in the permute
 inline int64_t permute_chunks(int64_t entries) { return (entries + kPermuteChunk - 1) / kPermuteChunk; }
 

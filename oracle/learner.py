@@ -89,3 +89,43 @@ def distill(z, ids, values, tail=True, scale=1.0):
         grad[t][j] -= q
     grad[np.isneginf(z)] = 0.0
     return loss, grad * scale, lse
+
+
+def gate_rows(gate, T):
+    """The gate as [T, 1] or [T, H]: None, one number a row, or rows that serve T / G rows each."""
+    if gate is None:
+        return np.ones((T, 1))
+    gate = np.asarray(gate, np.float64)
+    return gate[:, None] if gate.ndim == 1 else np.repeat(gate, T // gate.shape[0], axis=0)
+
+
+def rstd(x, eps):
+    x = np.asarray(x, np.float64)
+    return 1.0 / np.sqrt((x * x).mean(1) + eps)
+
+
+def norm_out(x, y, weight, gate=None, alpha=1.0, eps=1e-6):
+    y = np.asarray(y, np.float64)
+    return alpha * np.asarray(x, np.float64) + gate_rows(gate, y.shape[0]) * (y * rstd(y, eps)[:, None] * weight)
+
+
+def norm_backward(du, x, r):
+    """Gradient at x of xhat = x r(x), for the gradient du at xhat, with r = rstd(x) given."""
+    xhat = x * r[:, None]
+    return r[:, None] * (du - xhat * (du * xhat).mean(1, keepdims=True))
+
+
+def norm_out_backward(dr, y, rstd_y, weight, gate=None, alpha=1.0, dn=None, r=None, rstd_r=None, next_weight=None):
+    """(dx, dy, dweight, dgate or None, dnext or None)."""
+    T, H = y.shape
+    d = np.zeros((T, H)) if dr is None else np.asarray(dr, np.float64)
+    dnext = dgate = None
+    if dn is not None:
+        d = d + norm_backward(dn * next_weight, r, rstd_r)
+        dnext = (dn * r * rstd_r[:, None]).sum(0)
+    g, yhat = gate_rows(gate, T), y * rstd_y[:, None]
+    dy = norm_backward(d * g * weight, y, rstd_y)
+    if gate is not None:
+        full = d * weight * yhat
+        dgate = full.sum(1) if np.ndim(gate) == 1 else full.reshape(len(gate), -1, H).sum(1)
+    return alpha * d, dy, (d * g * yhat).sum(0), dgate, dnext

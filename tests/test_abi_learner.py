@@ -80,3 +80,47 @@ def test_distill_checks(lib):
     assert b(ldd=64) == INVALID and b(out=N) == INVALID and b(loss=N) == INVALID and b(dloss=P2) == INVALID
     assert b(out=ctypes.c_void_p(0x10000 + 16)) == INVALID
     assert f(T=0) == OK and b(T=0) == OK
+
+
+def test_norm_checks(lib):
+    big = 1 << 40
+
+    def fin(x=P, ldx=64, dtype=BF16, T=4, H=64, w=P, eps=1e-6, n=Q, rstd=P):
+        return lib.moe_norm_in(x, ldx, dtype, T, H, w, eps, n, rstd, N)
+
+    def fout(ldy=64, gate=N, gate_rows=0, alpha=1.0, nxt=P, n=Q, rr=P, T=4, w=P):
+        return lib.moe_norm_out(P, 64, P, ldy, BF16, T, 64, w, gate, gate_rows, alpha, nxt, 1e-6, Q, n, P, rr, N)
+
+    def bin_(dn=P, ld=64, x=P, w=P, dx=Q, dw=P, ws=P, n=big):
+        return lib.moe_norm_in_backward(dn, ld, N, 0, x, 64, P, BF16, 4, 64, w, dx, dw, ws, n, N)
+
+    def bout(dr=P, dn=P, r=P, rr=P, gate=N, gate_rows=0, nxt=P, dg=N, dnext=P, ws=P, n=big, lddn=64):
+        return lib.moe_norm_out_backward(dr, 64, dn, lddn, r, 64, P, 64, P, rr, BF16, 4, 64, P, gate, gate_rows, 1.0,
+                                         nxt, Q, Q, P, dg, dnext, ws, n, N)
+
+    assert fin(dtype=9) == INVALID and fin(T=-1) == INVALID and fin(H=0) == INVALID and fin(ldx=63) == INVALID
+    assert fin(eps=0.0) == INVALID and fin(eps=math.nan) == INVALID
+    assert fin(H=8193, ldx=9000) == UNSUPPORTED
+    assert fin(x=P1) == INVALID and fin(n=N) == INVALID and fin(w=N) == INVALID and fin(rstd=N) == INVALID
+    assert fin(T=0) == OK
+    assert fout(ldy=60) == INVALID and fout(alpha=math.inf) == INVALID and fout(w=N) == INVALID
+    assert fout(gate_rows=2) == INVALID                          # gate rows without a gate
+    assert fout(gate=P, gate_rows=3) == INVALID                  # 4 rows do not split into 3
+    assert fout(gate=P, gate_rows=-1) == INVALID and fout(gate=P1) == INVALID
+    assert fout(n=N) == INVALID and fout(rr=N) == INVALID        # given with next_weight
+    assert fout(T=0) == OK
+    assert bin_(dn=N) == INVALID and bin_(ld=10) == INVALID and bin_(dw=N) == INVALID and bin_(dx=N) == INVALID
+    assert bin_(ws=N) == L.Status.WORKSPACE and bin_(n=100) == L.Status.WORKSPACE
+    assert bout(dn=N) == INVALID and bout(r=N) == INVALID and bout(rr=N) == INVALID and bout(dnext=N) == INVALID
+    assert bout(dr=N, nxt=N) == INVALID                          # no gradient arrives
+    assert bout(gate=P) == INVALID and bout(gate=P, gate_rows=3, dg=P) == INVALID
+    assert bout(lddn=3) == INVALID
+    assert bout(ws=P2) == L.Status.WORKSPACE and bout(n=0) == L.Status.WORKSPACE
+
+
+def test_norm_workspace(lib):
+    size = lambda T, g, H: lib.nvfp4_workspace_size(L.OP_NORM_BACKWARD, T, g, 0, H, 0)
+    assert size(1, 0, 64) == 512                                 # one range of rows, two sums of 64 floats
+    assert size(5, 5, 64) == 5 * 512
+    assert size(0, 0, 64) == 0 and size(4, 0, 0) == 0
+    assert size(1 << 20, 0, 2048) <= 16 << 20

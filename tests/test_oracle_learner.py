@@ -74,3 +74,25 @@ def test_distill_is_zero_at_the_teacher():
     loss, grad, _ = O.distill(z, ids, v, True)
     np.testing.assert_allclose(loss, 0.0, atol=1e-14)
     np.testing.assert_allclose(grad, 0.0, atol=1e-14)
+
+
+@pytest.mark.parametrize("kind", ["none", "token", "rows"])
+def test_norm_gradients_by_differences(kind):
+    rng = np.random.default_rng(4)
+    T, H, eps, alpha = 6, 5, 1e-3, 0.7
+    x, y, w, wn = rng.normal(size=(T, H)), rng.normal(size=(T, H)), rng.normal(size=H), rng.normal(size=H)
+    gate = {"none": None, "token": rng.normal(size=T), "rows": rng.normal(size=(3, H))}[kind]
+    cr, cn = rng.normal(size=(T, H)), rng.normal(size=(T, H))
+
+    def f(x=x, y=y, w=w, gate=gate, wn=wn):
+        r = O.norm_out(x, y, w, gate, alpha, eps)
+        return np.sum(cr * r) + np.sum(cn * r * O.rstd(r, eps)[:, None] * wn)
+
+    r = O.norm_out(x, y, w, gate, alpha, eps)
+    dx, dy, dw, dg, dnext = O.norm_out_backward(cr, y, O.rstd(y, eps), w, gate, alpha, cn, r, O.rstd(r, eps), wn)
+    np.testing.assert_allclose(dx, _differences(lambda v: f(x=v), x), atol=1e-7)
+    np.testing.assert_allclose(dy, _differences(lambda v: f(y=v), y), atol=1e-7)
+    np.testing.assert_allclose(dw, _differences(lambda v: f(w=v), w), atol=1e-7)
+    np.testing.assert_allclose(dnext, _differences(lambda v: f(wn=v), wn), atol=1e-7)
+    if gate is not None:
+        np.testing.assert_allclose(dg, _differences(lambda v: f(gate=v), gate), atol=1e-7)
