@@ -588,7 +588,7 @@ nvfp4_status token_logprobs_backward(const void* logits, nvfp4_act_dtype dtype, 
  *     loss = sum_i q_i (ln q_i - ln p_i) + q_r (ln q_r - ln p_r), p_r = sum of the unlisted p
  *     (left out where no unlisted token is allowed).
  *   loss: device float [T]; lse: device float [T] or NULL.
- *   A row without entries has loss 0 and lse 0 and is not read.  An id outside [-1, V), or
+ *   A row without entries has loss 0 and lse 0.  An id outside [-1, V), or
  *   twice in a row, sets NVFP4_ERR_DEVICE_STATUS, gives the loss NaN and the gradient 0.
  *   A listed token that the student excludes and q > 0 give the loss +inf. */
 nvfp4_status distill_topk(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,

@@ -177,6 +177,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The operators on rows run for a few microseconds on small batches, so their host side
+# counts: addresses pass as plain integers, and the current stream's handle is asked for
+# without building a Stream object (0.1 instead of 2.9 us).
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(t: torch.Tensor, stream=None) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
 def _dev(t):
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
@@ -619,8 +630,9 @@ def _rows_2d(t: torch.Tensor, what: str) -> torch.Tensor:
     """A [rows, cols] CUDA tensor of an activation type whose columns are adjacent."""
     if t.dim() != 2 or t.dtype not in ACT_DTYPES:
         raise ValueError(f"{what} must be a 2-D BF16, float16 or float32 tensor")
-    _dev(t)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{what} must have unit column stride")
     return t
 
@@ -629,13 +641,13 @@ def _pitch(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-def _per_row(t, rows: int, dtype, like: torch.Tensor, what: str, cols: int | None = None):
-    """Checks a [rows] (or [rows, cols]) companion of `like`; None passes.  Returns it dense."""
+def _per_row(t, shape: tuple, dtype, dev: int, what: str):
+    """Checks a companion of the rows (targets, statistics, weights) on device number `dev`; None
+    passes.  Returns it dense."""
     if t is None:
         return None
-    shape = (rows,) if cols is None else (rows, cols)
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != like.device:
-        raise ValueError(f"{what} must be {dtype} {list(shape)} on {like.device}")
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be {dtype} {list(shape)} on the device of the rows")
     return t.contiguous()
 
 
@@ -647,6 +659,11 @@ def _like_rows(out, like: torch.Tensor, what: str) -> torch.Tensor:
     return _rows_2d(out, what)
 
 
+def _floats(n: int, T: int, dev: torch.device) -> tuple:
+    """n float32 [T] outputs (rows of one allocation)."""
+    return torch.empty((n, T), dtype=torch.float32, device=dev).unbind(0)
+
+
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
                    ignore_index: int = -100, entropy: bool = True, stream=None):
     """Log probabilities of given tokens, entropy and top alternatives of logits [T, V] (BF16,
@@ -655,17 +672,17 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     asked.  targets: int32 [T]; a row whose target is ignore_index is skipped (zeros)."""
     lib = load()
     T, V = _rows_2d(logits, "logits").shape
-    dev = logits.device
-    targets = _per_row(targets, T, torch.int32, logits, "targets")
-    f = dict(dtype=torch.float32, device=dev)
-    logprob = torch.empty(T, **f) if targets is not None else None
-    lse = torch.empty(T, **f)
-    ent = torch.empty(T, **f) if entropy else None
-    top_lp = torch.empty(T, top_k, **f) if top_k > 0 else None
-    top_ids = torch.empty(T, top_k, dtype=torch.int32, device=dev) if top_k > 0 else None
-    _check(lib.token_logprobs(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(targets), ignore_index,
-                              scale, top_k, _p(logprob), _p(lse), _p(ent), _p(top_lp), _p(top_ids), _stream(stream)),
-           "token_logprobs")
+    dev, index = logits.device, logits.get_device()
+    targets = _per_row(targets, (T,), torch.int32, index, "targets")
+    outs = list(_floats(1 + (targets is not None) + bool(entropy), T, dev))
+    lse = outs.pop()
+    logprob = outs.pop() if targets is not None else None
+    ent = outs.pop() if entropy else None
+    top_lp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
+    top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
+    _check(lib.token_logprobs(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _ptr(targets),
+                              ignore_index, scale, top_k, _ptr(logprob), lse.data_ptr(), _ptr(ent), _ptr(top_lp),
+                              _ptr(top_ids), _stream_of(logits, stream)), "token_logprobs")
     return logprob, lse, ent, top_lp, top_ids
 
 
@@ -677,13 +694,17 @@ def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, targets: to
     entropy (all float32 [T]).  out may be the logits themselves."""
     lib = load()
     T, V = _rows_2d(logits, "logits").shape
-    targets = _per_row(targets, T, torch.int32, logits, "targets")
-    rows = [_per_row(t, T, torch.float32, logits, n) for t, n in
-            ((lse, "lse"), (entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy"))]
+    index = logits.get_device()
+    targets = _per_row(targets, (T,), torch.int32, index, "targets")
+    lse = _per_row(lse, (T,), torch.float32, index, "lse")
+    entropy = _per_row(entropy, (T,), torch.float32, index, "entropy")
+    dlogprob = _per_row(dlogprob, (T,), torch.float32, index, "dlogprob")
+    dentropy = _per_row(dentropy, (T,), torch.float32, index, "dentropy")
     out = _like_rows(out, logits, "out")
-    _check(lib.token_logprobs_backward(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(targets),
-                                       ignore_index, scale, *(_p(r) for r in rows), _p(out), _pitch(out),
-                                       _stream(stream)), "token_logprobs_backward")
+    _check(lib.token_logprobs_backward(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _ptr(targets),
+                                       ignore_index, scale, _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy),
+                                       out.data_ptr(), _pitch(out), _stream_of(logits, stream)),
+           "token_logprobs_backward")
     return out
 
 
@@ -695,13 +716,13 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     (loss, lse), float32 [T]."""
     lib = load()
     T, V = _rows_2d(logits, "logits").shape
-    K = teacher_ids.shape[-1]
-    ids = _per_row(teacher_ids, T, torch.int32, logits, "teacher_ids", K)
-    values = _per_row(teacher_values, T, torch.float32, logits, "teacher_values", K)
-    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
-    _check(lib.distill_topk(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(ids), _p(values), K,
-                            int(tail), scale, _p(loss), _p(lse), _stream(stream)), "distill_topk")
+    index, K = logits.get_device(), teacher_ids.shape[-1]
+    ids = _per_row(teacher_ids, (T, K), torch.int32, index, "teacher_ids")
+    values = _per_row(teacher_values, (T, K), torch.float32, index, "teacher_values")
+    loss, lse = _floats(2, T, logits.device)
+    _check(lib.distill_topk(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), ids.data_ptr(),
+                            values.data_ptr(), K, tail, scale, loss.data_ptr(), lse.data_ptr(),
+                            _stream_of(logits, stream)), "distill_topk")
     return loss, lse
 
 
@@ -713,38 +734,36 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     themselves.  Returns (loss, dlogits)."""
     lib = load()
     T, V = _rows_2d(logits, "logits").shape
-    K = teacher_ids.shape[-1]
-    ids = _per_row(teacher_ids, T, torch.int32, logits, "teacher_ids", K)
-    values = _per_row(teacher_values, T, torch.float32, logits, "teacher_values", K)
-    dloss = _per_row(dloss, T, torch.float32, logits, "dloss")
+    index, K = logits.get_device(), teacher_ids.shape[-1]
+    ids = _per_row(teacher_ids, (T, K), torch.int32, index, "teacher_ids")
+    values = _per_row(teacher_values, (T, K), torch.float32, index, "teacher_values")
+    dloss = _per_row(dloss, (T,), torch.float32, index, "dloss")
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     out = _like_rows(out, logits, "out")
-    _check(lib.distill_topk_backward(_p(logits), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _p(ids), _p(values), K,
-                                     int(tail), scale, _p(dloss), _p(loss), None, _p(out), _pitch(out),
-                                     _stream(stream)), "distill_topk_backward")
+    _check(lib.distill_topk_backward(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), ids.data_ptr(),
+                                     values.data_ptr(), K, tail, scale, _ptr(dloss), loss.data_ptr(), None,
+                                     out.data_ptr(), _pitch(out), _stream_of(logits, stream)), "distill_topk_backward")
     return loss, out
 
 
 # --------------------------------------------------------------------------- norms around the block
 
-def _norm_rows(t, like: torch.Tensor | None, what: str):
+def _norm_rows(t, like: torch.Tensor, what: str):
     """A [T, H] activation like `like`; None passes."""
     if t is None:
         return None
-    _rows_2d(t, what)
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{what} must have the shape, type and device of the other activations")
-    return t
+    return _rows_2d(t, what)
 
 
-def _norm_gate(gate, like: torch.Tensor):
+def _norm_gate(gate, T: int, H: int, index: int):
     """gate as (dense tensor or None, gate_rows): [T] is one number a row, [G, H] G gate rows."""
     if gate is None:
         return None, 0
-    T, H = like.shape
     if gate.dim() == 1:
-        return _per_row(gate, T, torch.float32, like, "gate"), 0
-    return _per_row(gate, gate.shape[0], torch.float32, like, "gate", H), gate.shape[0]
+        return _per_row(gate, (T,), torch.float32, index, "gate"), 0
+    return _per_row(gate, (gate.shape[0], H), torch.float32, index, "gate"), gate.shape[0]
 
 
 def _norm_workspace(T: int, gate_rows: int, H: int, device) -> torch.Tensor:
@@ -761,11 +780,11 @@ def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, stream
     Returns (n [T, H], rstd float32 [T])."""
     lib = load()
     T, H = _rows_2d(x, "x").shape
-    weight = _per_row(weight, H, torch.float32, x, "weight")
-    n = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    weight = _per_row(weight, (H,), torch.float32, x.get_device(), "weight")
+    n = torch.empty((T, H), dtype=x.dtype, device=x.device)
     rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    _check(lib.moe_norm_in(_p(x), _pitch(x), ACT_DTYPES[x.dtype], T, H, _p(weight), eps, _p(n), _p(rstd),
-                           _stream(stream)), "moe_norm_in")
+    _check(lib.moe_norm_in(x.data_ptr(), _pitch(x), ACT_DTYPES[x.dtype], T, H, weight.data_ptr(), eps, n.data_ptr(),
+                           rstd.data_ptr(), _stream_of(x, stream)), "moe_norm_in")
     return n, rstd
 
 
@@ -774,15 +793,17 @@ def moe_norm_in_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, 
     """Gradients of moe_norm_in: (dx [T, H] = dresidual + the norm's gradient, dweight float32 [H])."""
     lib = load()
     T, H = _rows_2d(x, "x").shape
+    index = x.get_device()
     dn, dresidual = _norm_rows(dn, x, "dn"), _norm_rows(dresidual, x, "dresidual")
-    rstd = _per_row(rstd, T, torch.float32, x, "rstd")
-    weight = _per_row(weight, H, torch.float32, x, "weight")
-    dx = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    rstd = _per_row(rstd, (T,), torch.float32, index, "rstd")
+    weight = _per_row(weight, (H,), torch.float32, index, "weight")
+    dx = torch.empty((T, H), dtype=x.dtype, device=x.device)
     dweight = torch.empty(H, dtype=torch.float32, device=x.device)
     ws = _norm_workspace(T, 0, H, x.device) if workspace is None else workspace
-    _check(lib.moe_norm_in_backward(_p(dn), _pitch(dn), _p(dresidual), _pitch_or_0(dresidual), _p(x), _pitch(x), _p(rstd),
-                                    ACT_DTYPES[x.dtype], T, H, _p(weight), _p(dx), _p(dweight), _p(ws), ws.numel(),
-                                    _stream(stream)), "moe_norm_in_backward")
+    _check(lib.moe_norm_in_backward(dn.data_ptr(), _pitch(dn), _ptr(dresidual), _pitch_or_0(dresidual), x.data_ptr(),
+                                    _pitch(x), rstd.data_ptr(), ACT_DTYPES[x.dtype], T, H, weight.data_ptr(),
+                                    dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel(),
+                                    _stream_of(x, stream)), "moe_norm_in_backward")
     return dx, dweight
 
 
@@ -794,17 +815,22 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     (r, n, rstd_y, rstd_r); n and rstd_r are None without next_weight."""
     lib = load()
     T, H = _rows_2d(x, "x").shape
+    dev, index = x.device, x.get_device()
     y = _norm_rows(y, x, "y")
-    weight = _per_row(weight, H, torch.float32, x, "weight")
-    next_weight = _per_row(next_weight, H, torch.float32, x, "next_weight")
-    gate, gate_rows = _norm_gate(gate, x)
-    r = torch.empty(T, H, dtype=x.dtype, device=x.device)
-    rstd_y = torch.empty(T, dtype=torch.float32, device=x.device)
-    n = torch.empty_like(r) if next_weight is not None else None
-    rstd_r = torch.empty_like(rstd_y) if next_weight is not None else None
-    _check(lib.moe_norm_out(_p(x), _pitch(x), _p(y), _pitch(y), ACT_DTYPES[x.dtype], T, H, _p(weight), _p(gate), gate_rows,
-                            residual_scale, _p(next_weight), eps, _p(r), _p(n), _p(rstd_y), _p(rstd_r),
-                            _stream(stream)), "moe_norm_out")
+    weight = _per_row(weight, (H,), torch.float32, index, "weight")
+    next_weight = _per_row(next_weight, (H,), torch.float32, index, "next_weight")
+    gate, gate_rows = _norm_gate(gate, T, H, index)
+    r = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if next_weight is None:
+        n = rstd_r = None
+        rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        n = torch.empty((T, H), dtype=x.dtype, device=dev)
+        rstd_y, rstd_r = _floats(2, T, dev)
+    _check(lib.moe_norm_out(x.data_ptr(), _pitch(x), y.data_ptr(), _pitch(y), ACT_DTYPES[x.dtype], T, H,
+                            weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight), eps,
+                            r.data_ptr(), _ptr(n), rstd_y.data_ptr(), _ptr(rstd_r), _stream_of(x, stream)),
+           "moe_norm_out")
     return r, n, rstd_y, rstd_r
 
 
@@ -817,26 +843,28 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
     dweight [H], dgate like gate, dnext_weight [H]); the last two None where there is none."""
     lib = load()
     T, H = _rows_2d(y, "y").shape
+    dev, index = y.device, y.get_device()
     if len({t is None for t in (dn, rstd_r, next_weight)}) != 1 or (dn is not None and r is None):
         raise ValueError("dn, r, rstd_r and next_weight are given together")
     if dn is None:
         r = None      # only the next norm's gradient reads it
-    if dr is None and dn is None:
-        raise ValueError("no gradient arrives: give dr, dn or both")
+        if dr is None:
+            raise ValueError("no gradient arrives: give dr, dn or both")
     dr, dn, r = _norm_rows(dr, y, "dr"), _norm_rows(dn, y, "dn"), _norm_rows(r, y, "r")
-    rstd_y, rstd_r = (_per_row(t, T, torch.float32, y, n) for t, n in ((rstd_y, "rstd_y"), (rstd_r, "rstd_r")))
-    weight = _per_row(weight, H, torch.float32, y, "weight")
-    next_weight = _per_row(next_weight, H, torch.float32, y, "next_weight")
-    gate, gate_rows = _norm_gate(gate, y)
-    f = dict(dtype=torch.float32, device=y.device)
-    dx, dy = (torch.empty(T, H, dtype=y.dtype, device=y.device) for _ in range(2))
-    dweight = torch.empty(H, **f)
-    dgate = torch.empty(gate.shape, **f) if gate is not None else None
-    dnext = torch.empty(H, **f) if next_weight is not None else None
-    ws = _norm_workspace(T, gate_rows, H, y.device) if workspace is None else workspace
-    _check(lib.moe_norm_out_backward(_p(dr), _pitch_or_0(dr), _p(dn), _pitch_or_0(dn), _p(r), _pitch_or_0(r), _p(y),
-                                     _pitch(y), _p(rstd_y), _p(rstd_r), ACT_DTYPES[y.dtype], T, H, _p(weight), _p(gate),
-                                     gate_rows, residual_scale, _p(next_weight), _p(dx), _p(dy), _p(dweight),
-                                     _p(dgate), _p(dnext), _p(ws), ws.numel(), _stream(stream)),
-           "moe_norm_out_backward")
+    rstd_y = _per_row(rstd_y, (T,), torch.float32, index, "rstd_y")
+    rstd_r = _per_row(rstd_r, (T,), torch.float32, index, "rstd_r")
+    weight = _per_row(weight, (H,), torch.float32, index, "weight")
+    next_weight = _per_row(next_weight, (H,), torch.float32, index, "next_weight")
+    gate, gate_rows = _norm_gate(gate, T, H, index)
+    dx = torch.empty((T, H), dtype=y.dtype, device=dev)
+    dy = torch.empty((T, H), dtype=y.dtype, device=dev)
+    dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
+    dnext = torch.empty(H, dtype=torch.float32, device=dev) if next_weight is not None else None
+    ws = _norm_workspace(T, gate_rows, H, dev) if workspace is None else workspace
+    _check(lib.moe_norm_out_backward(_ptr(dr), _pitch_or_0(dr), _ptr(dn), _pitch_or_0(dn), _ptr(r), _pitch_or_0(r),
+                                     y.data_ptr(), _pitch(y), rstd_y.data_ptr(), _ptr(rstd_r), ACT_DTYPES[y.dtype], T, H,
+                                     weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight),
+                                     dx.data_ptr(), dy.data_ptr(), dweight.data_ptr(), _ptr(dgate), _ptr(dnext),
+                                     ws.data_ptr(), ws.numel(), _stream_of(y, stream)), "moe_norm_out_backward")
     return dx, dy, dweight, dgate, dnext

@@ -9,10 +9,17 @@
 // With the tail, the sum over the tokens outside S is taken on its own, with its own running
 // maximum (a bitmap of S in shared memory, one byte a chunk, leaves them out): 1 - sum_S p
 // would cancel when the student's mass lies on S.  lse then is that of the two parts.
-// The gradient is 2^((z - m) scale log2 e) times one number of the row, and on S a value that is written
-// over it afterwards.  The row is read twice, the second time from L2: the CTAs of a row are
-// one cluster, so few rows are in flight and they stay there.
+// The gradient is 2^((z - m) scale log2 e) times one number of the row, and on S a value that
+// is written over it afterwards.
+// One warp of each CTA reduces the list to a few sums while the row arrives; the row's
+// maximum enters them afterwards, so nothing but scalars follows the exchange.
+// With the gradient, a row's slices are a cluster, a CTA each, and a slice stays in shared memory
+// between the sum and the gradient: the row is read once.  A slice too long for that is
+// read again.
+#include <type_traits>
+
 #include "launch.h"
+#include "ptx.cuh"
 #include "status.cuh"
 #include "vocab.cuh"
 
@@ -36,10 +43,20 @@ struct DistillArgs {
   int* status;
 };
 
+// The list of a row, and its sums.  mz is the maximum of its logits, s = sum 2^((z - mz) c1),
+// A = sum q ln q, B = sum q (z - mz), Q = sum q.
+struct ListSmem {
+  int id[kMaxList];
+  float q[kMaxList], z[kMaxList];
+  float mz, s, A, B, Q;
+  int live, bad;
+};
 struct DistillSmem {
   Stats part[kMaxSlices][kVocabWarps];
-  int id[kMaxList];
-  float red[4][kVocabWarps];
+  int twice[kMaxSlices];   // a slice found an id of the list twice
+  ListSmem list;
+  uint64_t arrived;
+  int abort;
 };
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -52,36 +69,139 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// Over the block, the same bits in every thread.
-__device__ __forceinline__ float block_max(float x, float* red) {
-  x = warp_max(x);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = red[0];
+
+// One warp: reads row t's list, marks those of its ids that lie in [lo, hi) in `listed`, which
+// every thread of the CTA has cleared before `sync`, and leaves the sums in sm.
+template <typename E, bool kTail, typename Sync>
+__device__ __forceinline__ void reduce_list(const DistillArgs& a, const E* z, int64_t t, int lo, int hi,
+                                            unsigned* listed, ListSmem& sm, int& twice, Sync&& sync) {
+  constexpr int N = kMaxList / 32;
+  const int lane = threadIdx.x & 31;
+  const float c1 = a.scale * kLog2e;
+  int id[N];
+  float v[N], zi[N];
+  bool bad = false, live = false;
 #pragma unroll
-  for (int w = 1; w < kVocabWarps; ++w) x = fmaxf(x, red[w]);
-  __syncthreads();
-  return x;
-}
-__device__ __forceinline__ float block_sum(float x, float* red) {
-  x = warp_sum(x);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = red[0];
+  for (int j = 0; j < N; ++j) {
+    const int i = lane + 32 * j;
+    id[j] = i < a.K ? a.ids[t * a.K + i] : -1;
+    v[j] = i < a.K ? a.values[t * a.K + i] : -INFINITY;
+    if (id[j] < 0 || id[j] >= a.V) {
+      bad |= id[j] != -1;
+      id[j] = -1;
+      v[j] = -INFINITY;
+    }
+    zi[j] = id[j] >= 0 ? to_f32(z[id[j]]) : -INFINITY;
+    live |= kTail ? id[j] >= 0 : !(v[j] == -INFINITY);   // NaN lives
+  }
+  sync();
+  bool again = false;
+  float mv = -INFINITY, mz = -FLT_MAX;
 #pragma unroll
-  for (int w = 1; w < kVocabWarps; ++w) x += red[w];
-  __syncthreads();
-  return x;
+  for (int j = 0; j < N; ++j) {
+    if (id[j] >= lo && id[j] < hi) {
+      const unsigned bit = 1u << ((id[j] - lo) & 31);
+      again |= (atomicOr(listed + ((id[j] - lo) >> 5), bit) & bit) != 0;
+    }
+    mv = fmaxf(mv, v[j]);
+    mz = fmaxf(mz, zi[j]);
+  }
+  mz = warp_max(mz);
+  if (!kTail) mv = warp_max(mv);
+  float e[N], esum = 0.f, s = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    e[j] = id[j] >= 0 ? expf(kTail ? v[j] : v[j] - mv) : 0.f;
+    esum += e[j];
+    if (!(zi[j] == -INFINITY)) s += ex2((zi[j] - mz) * c1);
+  }
+  esum = warp_sum(esum);
+  const float ln_e = kTail ? 0.f : logf(esum);
+  float A = 0.f, B = 0.f, Q = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float q = kTail ? e[j] : e[j] / esum;
+    if (q != 0.f) {   // 0 ln 0 = 0
+      A += q * (kTail ? v[j] : v[j] - mv - ln_e);
+      B += q * (zi[j] - mz);
+    }
+    Q += q;
+    const int i = lane + 32 * j;
+    sm.id[i] = id[j];
+    sm.q[i] = q;
+    sm.z[i] = zi[j];
+  }
+  s = warp_sum(s);
+  A = warp_sum(A);
+  B = warp_sum(B);
+  Q = warp_sum(Q);
+  const int any_bad = __any_sync(0xffffffffu, bad), any_live = __any_sync(0xffffffffu, live);
+  const int any_twice = __any_sync(0xffffffffu, again);
+  if (lane == 0) {
+    sm.mz = mz;
+    sm.s = s;
+    sm.A = A;
+    sm.B = B;
+    sm.Q = Q;
+    sm.bad = any_bad;
+    sm.live = any_live;
+    twice = any_twice;
+  }
 }
 
-template <typename E, bool kTail, bool kGrad>
+// What the row's sums give: the loss, and the gradient as coef 2^((z - mb) c1), lp(z) = ln p.
+struct RowResult {
+  float loss, lse, mb, coef;
+  float m, ln_s;
+};
+template <bool kTail>
+__device__ __forceinline__ RowResult finish_row(Stats st, const ListSmem& l, float scale, float c1) {
+  RowResult r;
+  const bool rest = st.s != 0.f;   // some token outside the list is allowed (NaN counts)
+  r.mb = st.m;
+  float tail = 0.f;
+  if (kTail) {
+    const float rest_s = st.s, ln_rest = rest ? logf(st.s) : -INFINITY;
+    r.m = fmaxf(l.mz, st.m);
+    rebase<false>(st, r.m, c1);
+    st.s += l.s == 0.f ? 0.f : ex2((l.mz - r.m) * c1) * l.s;
+    r.ln_s = logf(st.s);
+    const float lr = rest ? fmaf(r.mb - r.m, scale, ln_rest - r.ln_s) : -INFINITY;   // ln p_r
+    const float qr = fmaxf(0.f, 1.f - l.Q);
+    r.coef = rest ? (expf(lr) - qr) / rest_s : 0.f;
+    if (rest && qr > 0.f) tail = qr * (logf(qr) - lr);
+  } else {
+    r.m = st.m;
+    r.ln_s = logf(st.s);
+    r.coef = rest ? 1.f / st.s : 0.f;
+  }
+  // sum q (ln q - ln p) with ln p = scale (z - m) - ln s; a student without any allowed token
+  // has p = 0 everywhere
+  if (l.Q == 0.f) r.loss = tail;
+  else if (st.s == 0.f) r.loss = INFINITY;
+  else r.loss = l.A - scale * (l.B + l.Q * (l.mz - r.m)) + r.ln_s * l.Q + tail;
+  r.lse = fmaf(r.m, scale, r.ln_s);
+  return r;
+}
+
+template <bool kTail>
+__device__ __forceinline__ void leave_out(float (&v)[8], uint32_t bits) {
+  if (kTail && bits != 0)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (bits >> i & 1) v[i] = -INFINITY;
+}
+
+// The loss alone.
+template <typename E, bool kTail>
 __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const DistillArgs a) {
-  extern __shared__ __align__(16) uint8_t listed[];   // kTail: a byte a chunk of this CTA's slices
+  extern __shared__ __align__(16) uint8_t listed[];   // a byte a chunk of this CTA's slices
   __shared__ DistillSmem sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int64_t t = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (ctas > 1) cluster.barrier_arrive();   // met below, before anything is written to another CTA
   const Row<E> row(static_cast<const E*>(a.logits), a.ld, t, a.V);
   const int slices = vocab_slices(a.V);
   const float c1 = a.scale * kLog2e;
@@ -89,163 +209,237 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const Disti
   int first, end, unused;
   slice_range(a.V, slices, s0, first, unused);
   slice_range(a.V, slices, s1 - 1, unused, end);
-
-  // the teacher's list: an entry a thread (every CTA of the row computes the same)
-  int id = -1;
-  float tv = -INFINITY;
-  bool bad = false;
-  if (tid < a.K) {
-    id = a.ids[t * a.K + tid];
-    tv = a.values[t * a.K + tid];
-    bad = id < -1 || id >= a.V;
-    if (bad || id == -1) {
-      id = -1;
-      tv = -INFINITY;
-    }
-  }
-  if (tid < kMaxList) sm.id[tid] = id;
-  if (kTail)
-    for (int i = tid; 16 * i < end - first; i += kVocabThreads)
-      reinterpret_cast<uint4*>(listed)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; 16 * i < end - first; i += kVocabThreads)
+    reinterpret_cast<uint4*>(listed)[i] = make_uint4(0, 0, 0, 0);
+  if (warp == 0)
+    reduce_list<E, kTail>(a, row.p, t, 8 * first, 8 * end, reinterpret_cast<unsigned*>(listed), sm.list,
+                          sm.twice[rank], [] { __syncthreads(); });
+  else
+    __syncthreads();
   __syncthreads();
-  if (id >= 0)
-    for (int j = 0; j < tid; ++j) bad |= sm.id[j] == id;
-  bad = __syncthreads_or(bad);                     // an id outside [0, V) or twice in the row
-  const bool live = __syncthreads_or(tv > -INFINITY || (kTail && id >= 0) || tv != tv);
-  const E* z = row.p;
-  const int lo = 8 * first, hi = min(a.V, 8 * end);
-  E* out = kGrad ? static_cast<E*>(a.dlogits) + t * a.ldd : nullptr;
-  if (bad || !live) {   // nothing to learn from the row; a bad row's loss is NaN
-    if (rank == 0 && tid == 0) {
-      if (bad) set_status(a.status, kStatusBadInput);
-      a.loss[t] = bad ? NAN : 0.f;
-      if (a.lse != nullptr) a.lse[t] = 0.f;
+  if (ctas > 1) cluster.barrier_wait();
+  const ListSmem& l = sm.list;
+  const bool dead = l.bad || !l.live;
+  if (!dead)
+    for (int s = s0; s < s1; ++s) {
+      int f, e;
+      slice_range(a.V, slices, s, f, e);
+      Stats st = empty_stats();
+      for_chunks(row, f, e, [&](int c, float(&v)[8]) {
+        leave_out<kTail>(v, listed[c - first]);
+        accumulate<false>(st, v, c1);
+      });
+      st = warp_merge<false>(st, c1);
+      if (lane == 0) *(ctas == 1 ? &sm.part[s][warp] : cluster.map_shared_rank(&sm.part[s][warp], 0)) = st;
     }
-    if (kGrad)
-      for (int e = lo + tid; e < hi; e += kVocabThreads) store_one(out + e, 0.f);
-    return;
-  }
-  if (ctas > 1) cluster.sync();   // every CTA of the cluster has started: its shared memory may be written
-  if (kTail && id >= lo && id < hi)
-    atomicOr(reinterpret_cast<unsigned*>(listed) + ((id - lo) >> 5), 1u << ((id - lo) & 31));
-  const float zi = id >= 0 ? to_f32(z[id]) : -INFINITY;
-  __syncthreads();
-
-  // one pass over the row (the tokens outside the list, with the tail)
-  for (int s = s0; s < s1; ++s) {
-    int f, l;
-    slice_range(a.V, slices, s, f, l);
-    Stats st = empty_stats();
-    for_chunks(row, f, l, [&](int c, float(&v)[8]) {
-      if (kTail) {
-        const uint32_t b = listed[c - first];
-        if (b != 0)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (b >> i & 1) v[i] = -INFINITY;
-      }
-      accumulate<false>(st, v, c1);
-    });
-    st = warp_merge<false>(st, c1);
-    if (lane == 0)
-      for (int r = 0; r < (kGrad ? ctas : 1); ++r) {   // the gradient needs the sums in every CTA
-        Stats(*part)[kVocabWarps] = ctas == 1 ? sm.part : cluster.map_shared_rank(sm.part, r);
-        part[s][warp] = st;
-      }
-  }
   if (ctas > 1) {
+    if (tid == 0 && rank != 0) *cluster.map_shared_rank(&sm.twice[rank], 0) = sm.twice[rank];
     cluster.sync();
-    if (!kGrad && rank != 0) return;
+    if (rank != 0) return;
   } else {
     __syncthreads();
   }
-  Stats st = join_slices<false>(sm.part, slices, c1);
-
-  // Probabilities outside the list are k1 2^((c - mb) log2 e): mb is a maximum and k1 holds the
-  // sum, so that rows of a mask's lowest values keep their digits.
-  float mb, coef, m, ln_s, q, lq, qr = 0.f, lr = 0.f;   // lse = scale m + ln_s;  lr = ln p_r
-  const bool rest = st.s != 0.f;   // some token outside the list is allowed (NaN counts)
-  if (kTail) {
-    mb = st.m;
-    float on_m = -FLT_MAX, on_s = 0.f;
-    if (zi > -INFINITY || zi != zi) {
-      on_m = zi;
-      on_s = zi < INFINITY ? 1.f : NAN;
-    }
-    // the list's own sum, over the block
-    const float ln_rest = rest ? logf(st.s) : -INFINITY;
-    m = fmaxf(block_max(on_m, sm.red[0]), st.m);
-    const float sum = block_sum(on_s == 0.f ? 0.f : ex2((on_m - m) * c1) * on_s, sm.red[1]);
-    const float rest_s = st.s;
-    rebase<false>(st, m, c1);
-    ln_s = logf(st.s + sum);
-    lr = rest ? fmaf(mb - m, a.scale, ln_rest - ln_s) : -INFINITY;
-    q = id >= 0 ? expf(tv) : 0.f;
-    lq = tv;
-    qr = fmaxf(0.f, 1.f - block_sum(q, sm.red[2]));
-    coef = rest ? (expf(lr) - qr) / rest_s : 0.f;
-  } else {
-    mb = m = st.m;
-    ln_s = logf(st.s);
-    const float mt = block_max(tv, sm.red[0]);
-    const float e = id >= 0 ? expf(tv - mt) : 0.f;
-    const float sum = block_sum(e, sm.red[2]);
-    q = e / sum;
-    lq = tv - mt - logf(sum);
-    coef = rest ? 1.f / st.s : 0.f;
-  }
-  const float lp = zi == -INFINITY ? -INFINITY : fmaf(zi - m, a.scale, -ln_s);
-  const float term = id >= 0 && q != 0.f ? q * (lq - lp) : 0.f;
-  float loss = block_sum(term, sm.red[3]);
-  if (kTail && rest && qr > 0.f) loss += qr * (logf(qr) - lr);
-  if (rank == 0 && tid == 0) {
-    a.loss[t] = loss;
-    if (a.lse != nullptr) a.lse[t] = fmaf(m, a.scale, ln_s);
-  }
-  if (kGrad) {
-    const float w = a.scale * (a.dloss != nullptr ? a.dloss[t] : 1.f);
-    const float k1 = w * coef;
-    map_range(z, out, lo, hi, tid, kVocabThreads, [&](int, float(&v)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = k1 * ex2((v[i] - mb) * c1);
-    });
-    __syncthreads();
-    if (id >= lo && id < hi) store_one(out + id, zi == -INFINITY ? 0.f : w * (expf(lp) - q));
+  if (warp != 0) return;
+  bool bad = l.bad;
+  for (int r = 0; r < ctas; ++r) bad |= sm.twice[r] != 0;
+  RowResult r{0.f, 0.f};
+  if (!dead) r = finish_row<kTail>(join_slices<false>(sm.part, slices, c1), l, a.scale, c1);
+  if (lane == 0) {
+    if (bad) set_status(a.status, kStatusBadInput);
+    a.loss[t] = bad ? NAN : r.loss;
+    if (a.lse != nullptr) a.lse[t] = bad ? 0.f : r.lse;
   }
 }
 
-template <typename E, bool kTail, bool kGrad>
-cudaError_t launch(const DistillArgs& a, int64_t T, cudaStream_t s) {
-  static std::atomic<bool> smem_set[64];
-  const int slices = vocab_slices(a.V);
-  const int ctas = kGrad || T < 4 * num_sms() ? slices : 1;
-  const int chunks = (a.V + 7) / 8;
-  const int bytes = kTail ? (ctas == 1 ? chunks : (chunks + slices - 1) / slices) : 0;
-  const int smem = (bytes + 15) / 16 * 16;
-  auto kernel = distill_topk_kernel<E, kTail, kGrad>;
-  if (kTail) {
-    const cudaError_t e =
-        set_smem_attr_once(smem_set, reinterpret_cast<const void*>(kernel), static_cast<int>(kMaxVocab / 8));
-    if (e != cudaSuccess) return e;
+// A CTA's slice of a row in shared memory: element e of [lo, hi) lies at at(e), as far from a
+// 16-byte boundary as in global memory.
+template <typename E>
+struct Stage {
+  const char* mem;   // 16-byte aligned, 16 spare bytes at both ends
+  int lo, hi;
+  uint32_t lead;     // the slice's offset from a 16-byte boundary
+  __device__ __forceinline__ const char* at(int e) const { return mem + lead + (e - lo) * static_cast<int>(sizeof(E)); }
+  // Starts the copy: whole 16-byte words by one bulk copy, the ends by the first threads.
+  __device__ __forceinline__ void fetch(const E* z, uint64_t* bar) const {
+    const int bytes = (hi - lo) * static_cast<int>(sizeof(E));
+    const char* g = reinterpret_cast<const char*>(z + lo);
+    char* s = const_cast<char*>(mem) + lead;
+    const int head = min(bytes, static_cast<int>((16u - lead) & 15u)), body = (bytes - head) & ~15;
+    if (threadIdx.x == 0) {
+      mbar_arrive_expect_tx(bar, body);
+      if (body > 0) bulk_load(s + head, g + head, body, bar);
+    }
+    const int h = head / sizeof(E), tl = (bytes - head - body) / sizeof(E);
+    const int i = static_cast<int>(threadIdx.x) - 32;   // another warp than the one that issues the copy
+    const int e = i < h ? lo + i : hi - tl + i - h;
+    if (i >= 0 && i < h + tl) *reinterpret_cast<E*>(const_cast<char*>(at(e))) = z[e];
   }
+  // Elements [e, e + 8).
+  __device__ __forceinline__ void get(int e, float (&v)[8]) const {
+    constexpr int Q = Chunk<E>::kQ;
+    const char* p = at(e);
+    const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const uint4* w = reinterpret_cast<const uint4*>(p - shift);
+    Chunk<E> c;
+    if (shift == 0) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) c.q[i] = w[i];
+    } else {
+      c = join_words<E>([&](int i) { return w[i]; }, shift);
+    }
+    unpack8(c, v);
+  }
+};
+
+template <typename E, bool kTail, bool kStage>
+__global__ void __launch_bounds__(kVocabThreads) distill_topk_backward_kernel(const DistillArgs a, int stage_bytes) {
+  extern __shared__ __align__(128) uint8_t dyn[];   // kStage: the slice; then a byte a chunk of it
+  __shared__ DistillSmem sm;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  const int64_t t = blockIdx.x / ctas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (ctas > 1) cluster.barrier_arrive();   // met below, before anything is written to another CTA
+  const Row<E> row(static_cast<const E*>(a.logits), a.ld, t, a.V);
+  const E* z = row.p;
+  uint8_t* listed = dyn + stage_bytes;
+  const float c1 = a.scale * kLog2e;
+  int first, end;
+  slice_range(a.V, ctas, rank, first, end);
+  const int lo = min(a.V, 8 * first), hi = min(a.V, 8 * end);
+  Stage<E> stage{reinterpret_cast<const char*>(dyn) + 16, lo, hi,
+                 static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z + lo)) & 15u};
+  if (kStage) {
+    if (tid == 0) {
+      mbar_init(&sm.arrived, 1);
+      fence_mbar_init();
+      sm.abort = 0;
+    }
+    stage.fetch(z, &sm.arrived);   // its first thread made the barrier
+  }
+  for (int i = tid; 16 * i < end - first; i += kVocabThreads)
+    reinterpret_cast<uint4*>(listed)[i] = make_uint4(0, 0, 0, 0);
+  if (warp == kVocabWarps - 1)
+    reduce_list<E, kTail>(a, z, t, lo, hi, reinterpret_cast<unsigned*>(listed), sm.list, sm.twice[rank],
+                          [] { __syncthreads(); });
+  else
+    __syncthreads();
+  __syncthreads();
+  const ListSmem& l = sm.list;
+  if (kStage) mbar_wait(&sm.arrived, 0, a.status, &sm.abort);   // (a copy that never came leaves a status)
+  bool dead = l.bad || !l.live;
+  Stats st = empty_stats();
+  if (!dead) {
+    if (kStage) {
+      for (int c = first + tid; c < end; c += kVocabThreads) {
+        float v[8];
+        stage.get(8 * c, v);
+        if (8 * c + 8 > a.V)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (8 * c + i >= a.V) v[i] = -INFINITY;
+        leave_out<kTail>(v, listed[c - first]);
+        accumulate<false>(st, v, c1);
+      }
+    } else {
+      for_chunks(row, first, end, [&](int c, float(&v)[8]) {
+        leave_out<kTail>(v, listed[c - first]);
+        accumulate<false>(st, v, c1);
+      });
+    }
+    st = warp_merge<false>(st, c1);
+  }
+  if (ctas > 1) {
+    cluster.barrier_wait();
+    if (lane < ctas) {
+      *cluster.map_shared_rank(&sm.part[rank][warp], lane) = st;
+      if (warp == 0 && lane != rank) *cluster.map_shared_rank(&sm.twice[rank], lane) = sm.twice[rank];
+    }
+    cluster.sync();
+  } else {
+    if (lane == 0) sm.part[0][warp] = st;
+    __syncthreads();
+  }
+  bool bad = l.bad;
+  for (int r = 0; r < ctas; ++r) bad |= sm.twice[r] != 0;
+  RowResult r{0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (!dead) r = finish_row<kTail>(join_slices<false>(sm.part, ctas, c1), l, a.scale, c1);
+  dead |= bad;
+  if (rank == 0 && tid == 0) {
+    if (bad) set_status(a.status, kStatusBadInput);
+    a.loss[t] = bad ? NAN : r.loss;
+    if (a.lse != nullptr) a.lse[t] = bad ? 0.f : r.lse;
+  }
+  const float w = a.scale * (a.dloss != nullptr ? a.dloss[t] : 1.f);
+  const float k1 = w * r.coef;
+  E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
+  const auto gradient = [&](int, float(&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = dead ? 0.f : k1 * ex2((v[i] - r.mb) * c1);
+  };
+  if (kStage)
+    map_chunks(out, lo, hi, tid, kVocabThreads, [&](int e, float(&v)[8]) { stage.get(e, v); },
+               [&](int e) { return to_f32(*reinterpret_cast<const E*>(stage.at(e))); }, gradient);
+  else
+    map_range(z, out, lo, hi, tid, kVocabThreads, gradient);
+  if (dead) return;
+  __syncthreads();   // the listed tokens' values go over the others
+  if (tid < kMaxList) {
+    const int id = l.id[tid];
+    const float zi = l.z[tid];
+    if (id >= lo && id < hi)
+      store_one(out + id, zi == -INFINITY ? 0.f : w * (expf(fmaf(zi - r.m, a.scale, -r.ln_s)) - l.q[tid]));
+  }
+}
+
+template <typename K>
+cudaError_t launch(K kernel, std::atomic<bool>* smem_set, int smem_max, int64_t ctas, int cluster, int smem,
+                   cudaStream_t s, const DistillArgs& a, int stage) {
+  const cudaError_t e = set_smem_attr_once(smem_set, reinterpret_cast<const void*>(kernel), smem_max);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(T * ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kVocabThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.x = cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  if constexpr (std::is_invocable_v<K, DistillArgs, int>) return cudaLaunchKernelEx(&cfg, kernel, a, stage);
+  else return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+constexpr int kMaxSmem = 200 * 1024;   // a slice and its bitmap
+
+template <typename E, bool kTail>
+cudaError_t forward(const DistillArgs& a, int64_t T, cudaStream_t s) {
+  static std::atomic<bool> set[64];
+  const int slices = vocab_slices(a.V), chunks = (a.V + 7) / 8;
+  const int ctas = T < 4 * num_sms() ? slices : 1;
+  const int bytes = ctas == 1 ? chunks : (chunks + slices - 1) / slices;
+  return launch(distill_topk_kernel<E, kTail>, set, static_cast<int>(kMaxVocab / 8), T * ctas, ctas,
+                (bytes + 15) / 16 * 16, s, a, 0);
+}
+
+template <typename E, bool kTail>
+cudaError_t backward(const DistillArgs& a, int64_t T, cudaStream_t s) {
+  static std::atomic<bool> set[2][64];
+  const int slices = vocab_slices(a.V), per = ((a.V + 7) / 8 + slices - 1) / slices;
+  const int bits = (per + 15) / 16 * 16;
+  const int64_t slice = static_cast<int64_t>(per) * 8 * sizeof(E) + 48;   // 16 spare bytes at both ends, 16 for its offset
+  if (slice + bits <= kMaxSmem)
+    return launch(distill_topk_backward_kernel<E, kTail, true>, set[0], kMaxSmem, T * slices, slices,
+                  static_cast<int>(slice) + bits, s, a, static_cast<int>(slice));
+  return launch(distill_topk_backward_kernel<E, kTail, false>, set[1], kMaxSmem, T * slices, slices, bits, s, a, 0);
 }
 
 template <typename E>
 cudaError_t dispatch(const DistillArgs& a, int64_t T, bool tail, cudaStream_t s) {
-  if (a.dlogits != nullptr) return tail ? launch<E, true, true>(a, T, s) : launch<E, false, true>(a, T, s);
-  return tail ? launch<E, true, false>(a, T, s) : launch<E, false, false>(a, T, s);
+  if (a.dlogits != nullptr) return tail ? backward<E, true>(a, T, s) : backward<E, false>(a, T, s);
+  return tail ? forward<E, true>(a, T, s) : forward<E, false>(a, T, s);
 }
 
 }  // namespace

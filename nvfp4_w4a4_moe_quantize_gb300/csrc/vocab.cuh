@@ -80,6 +80,38 @@ __device__ __forceinline__ void unpack8(const Chunk<float>& c, float (&v)[8]) {
   }
 }
 
+// 8 elements that begin `shift` > 0 bytes into 16-byte words, word(0) the first.
+template <int S, int N, int M>
+__device__ __forceinline__ void funnel(const uint32_t (&w)[N], uint32_t (&o)[M], uint32_t bits) {
+#pragma unroll
+  for (int i = 0; i < M; ++i) o[i] = __funnelshift_r(w[i + S], w[i + S + 1], bits);
+}
+template <typename E, typename Word>
+__device__ __forceinline__ Chunk<E> join_words(Word&& word, uint32_t shift) {
+  constexpr int Q = Chunk<E>::kQ;
+  uint32_t w[4 * Q + 5], o[4 * Q];
+#pragma unroll
+  for (int i = 0; i <= Q; ++i) {
+    const uint4 q = word(i);
+    w[4 * i] = q.x;
+    w[4 * i + 1] = q.y;
+    w[4 * i + 2] = q.z;
+    w[4 * i + 3] = q.w;
+  }
+  w[4 * Q + 4] = 0;
+  const uint32_t bits = (shift & 3u) * 8u;
+  switch (shift >> 2) {
+    case 0: funnel<0>(w, o, bits); break;
+    case 1: funnel<1>(w, o, bits); break;
+    case 2: funnel<2>(w, o, bits); break;
+    default: funnel<3>(w, o, bits); break;
+  }
+  Chunk<E> r;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) r.q[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  return r;
+}
+
 // One row and how to read it.  `shift` is the row's byte offset from a 16-byte boundary.
 template <typename E>
 struct Row {
@@ -104,33 +136,7 @@ struct Row {
       for (int i = 0; i < Q; ++i) r.q[i] = load16(b + 16 * i);
       return r;
     }
-    b -= shift;
-    uint32_t w[4 * Q + 5];
-#pragma unroll
-    for (int i = 0; i <= Q; ++i) {
-      const uint4 q = load16(b + 16 * i);
-      w[4 * i] = q.x;
-      w[4 * i + 1] = q.y;
-      w[4 * i + 2] = q.z;
-      w[4 * i + 3] = q.w;
-    }
-    w[4 * Q + 4] = 0;
-    const uint32_t bits = (shift & 3u) * 8u;
-    uint32_t o[4 * Q];
-    switch (shift >> 2) {
-      case 0: join<0>(w, o, bits); break;
-      case 1: join<1>(w, o, bits); break;
-      case 2: join<2>(w, o, bits); break;
-      default: join<3>(w, o, bits); break;
-    }
-#pragma unroll
-    for (int i = 0; i < Q; ++i) r.q[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    return r;
-  }
-  template <int S, int N, int M>
-  static __device__ __forceinline__ void join(const uint32_t (&w)[N], uint32_t (&o)[M], uint32_t bits) {
-#pragma unroll
-    for (int i = 0; i < M; ++i) o[i] = __funnelshift_r(w[i + S], w[i + S + 1], bits);
+    return join_words<E>([&](int i) { return load16(b - shift + 16 * i); }, shift);
   }
   // Any chunk that begins inside the row; places past its end read as -inf (excluded).
   __device__ __forceinline__ void get(int c, float (&v)[8]) const {
@@ -278,37 +284,22 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// out[e] = f(e, z[e]) for e in [lo, hi) of a row, by `threads` threads of which this is
-// number `tid`.  The chunks are cut on the output's 16-byte boundaries, so that stores are
-// whole; z is read in one piece where it is aligned with the output, else one by one.  out
-// may be z itself: a thread reads its elements before it writes them.
-template <typename E, typename F>
-__device__ __forceinline__ void map_range(const E* z, E* out, int lo, int hi, int tid, int threads, F&& f) {
+// out[e] = f(e, value(e)) for e in [lo, hi) of a row, by `threads` threads of which this is
+// number `tid`: eight(e, v) gives the values of [e, e + 8), one(e) a single one.  The chunks are
+// cut on the output's 16-byte boundaries, so that stores are whole.
+template <typename E, typename Eight, typename One, typename F>
+__device__ __forceinline__ void map_chunks(E* out, int lo, int hi, int tid, int threads, Eight&& eight, One&& one,
+                                           F&& f) {
   const uint32_t so = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out + lo)) & 15u;
-  const uint32_t sz = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z + lo)) & 15u;
   const int head = min(hi - lo, static_cast<int>((16u - so) & 15u) / static_cast<int>(sizeof(E)));
   const int body = (hi - lo - head) >> 3;
   const int tail = lo + head + 8 * body;
-  const bool same = so == sz;
   constexpr int kAhead = 2;
   for (int c = tid; c < body; c += kAhead * threads) {
-    Chunk<E> raw[kAhead];
     float v[kAhead][8];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int e = lo + head + 8 * (c + k * threads);
-      if (c + k * threads < body) {
-        if (same) {
-#pragma unroll
-          for (int i = 0; i < Chunk<E>::kQ; ++i)
-            raw[k].q[i] = load16(reinterpret_cast<const char*>(z + e) + 16 * i);
-          unpack8(raw[k], v[k]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = to_f32(z[e + i]);
-        }
-      }
-    }
+    for (int k = 0; k < kAhead; ++k)
+      if (c + k * threads < body) eight(lo + head + 8 * (c + k * threads), v[k]);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int e = lo + head + 8 * (c + k * threads);
@@ -322,12 +313,34 @@ __device__ __forceinline__ void map_range(const E* z, E* out, int lo, int hi, in
   if (tid < head || (tid >= 8 && tid - 8 < hi - tail)) {
     const int e = tid < head ? lo + tid : tail + tid - 8;
     float v[8];
-    v[0] = to_f32(z[e]);
+    v[0] = one(e);
 #pragma unroll
     for (int i = 1; i < 8; ++i) v[i] = -INFINITY;
     f(e, v);
     store_one(out + e, v[0]);
   }
+}
+
+// The same with the values of z in global memory: z is read in whole words where it is aligned
+// with the output, else one by one.  out may be z itself: a thread reads its elements before it
+// writes them.
+template <typename E, typename F>
+__device__ __forceinline__ void map_range(const E* z, E* out, int lo, int hi, int tid, int threads, F&& f) {
+  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(z)) & 15u) == 0;
+  map_chunks(
+      out, lo, hi, tid, threads,
+      [&](int e, float(&v)[8]) {
+        if (same) {
+          Chunk<E> c;
+#pragma unroll
+          for (int i = 0; i < Chunk<E>::kQ; ++i) c.q[i] = load16(reinterpret_cast<const char*>(z + e) + 16 * i);
+          unpack8(c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = to_f32(z[e + i]);
+        }
+      },
+      [&](int e) { return to_f32(z[e]); }, f);
 }
 
 }  // namespace nvfp4

@@ -379,6 +379,30 @@ def test_distill(cuda_lib, T, V, K, tail, dtype):
 
 
 @pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,V", [("f32", 300007), ("bf16", 1 << 20), ("f32", (1 << 20) - 3)])
+def test_distill_long_rows(cuda_lib, tail, dtype, V):
+    """Slices that fill the shared memory, and slices that do not fit into it; in place too."""
+    z, rng = logits(2, V, V)
+    ids, val = teacher(2, V, 100, rng)
+    zt = store(z, dtype, lead=1)
+    _, d = check_distill(cuda_lib, zt, ids, val, tail)
+    keep = d.clone()
+    cuda_lib.distill_topk_backward(zt, torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), tail=tail, out=zt)
+    assert torch.equal(zt, keep)
+
+
+def test_distill_student_without_tokens(cuda_lib):
+    z = np.full((2, 5000), -np.inf)
+    z[1, 7] = 1.0
+    ids = np.array([[7, 9], [7, -1]], np.int32)
+    val = np.log(np.array([[0.5, 0.25], [1.0, 1.0]])).astype(np.float32)
+    for tail in (False, True):
+        loss, d = cuda_lib.distill_topk_backward(store(z, "f32"), torch.from_numpy(ids).cuda(),
+                                                 torch.from_numpy(val).cuda(), tail=tail)
+        assert loss.tolist() == [float("inf"), 0.0] and not d.any()
+
+
+@pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("pad,lead", [(0, 0), (3, 5)])
 def test_distill_masks_and_in_place(cuda_lib, tail, dtype, pad, lead):
