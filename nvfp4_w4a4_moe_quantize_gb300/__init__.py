@@ -659,11 +659,6 @@ def _like_rows(out, like: torch.Tensor, what: str) -> torch.Tensor:
     return _rows_2d(out, what)
 
 
-def _floats(n: int, T: int, dev: torch.device) -> tuple:
-    """n float32 [T] outputs (rows of one allocation)."""
-    return torch.empty((n, T), dtype=torch.float32, device=dev).unbind(0)
-
-
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
                    ignore_index: int = -100, entropy: bool = True, stream=None):
     """Log probabilities of given tokens, entropy and top alternatives of logits [T, V] (BF16,
@@ -674,10 +669,9 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     T, V = _rows_2d(logits, "logits").shape
     dev, index = logits.device, logits.get_device()
     targets = _per_row(targets, (T,), torch.int32, index, "targets")
-    outs = list(_floats(1 + (targets is not None) + bool(entropy), T, dev))
-    lse = outs.pop()
-    logprob = outs.pop() if targets is not None else None
-    ent = outs.pop() if entropy else None
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    logprob = torch.empty(T, dtype=torch.float32, device=dev) if targets is not None else None
+    ent = torch.empty(T, dtype=torch.float32, device=dev) if entropy else None
     top_lp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
     top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
     _check(lib.token_logprobs(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _ptr(targets),
@@ -719,7 +713,8 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     index, K = logits.get_device(), teacher_ids.shape[-1]
     ids = _per_row(teacher_ids, (T, K), torch.int32, index, "teacher_ids")
     values = _per_row(teacher_values, (T, K), torch.float32, index, "teacher_values")
-    loss, lse = _floats(2, T, logits.device)
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
     _check(lib.distill_topk(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), ids.data_ptr(),
                             values.data_ptr(), K, tail, scale, loss.data_ptr(), lse.data_ptr(),
                             _stream_of(logits, stream)), "distill_topk")
@@ -821,12 +816,9 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     next_weight = _per_row(next_weight, (H,), torch.float32, index, "next_weight")
     gate, gate_rows = _norm_gate(gate, T, H, index)
     r = torch.empty((T, H), dtype=x.dtype, device=dev)
-    if next_weight is None:
-        n = rstd_r = None
-        rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
-    else:
-        n = torch.empty((T, H), dtype=x.dtype, device=dev)
-        rstd_y, rstd_r = _floats(2, T, dev)
+    rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
+    n = torch.empty((T, H), dtype=x.dtype, device=dev) if next_weight is not None else None
+    rstd_r = torch.empty(T, dtype=torch.float32, device=dev) if next_weight is not None else None
     _check(lib.moe_norm_out(x.data_ptr(), _pitch(x), y.data_ptr(), _pitch(y), ACT_DTYPES[x.dtype], T, H,
                             weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight), eps,
                             r.data_ptr(), _ptr(n), rstd_y.data_ptr(), _ptr(rstd_r), _stream_of(x, stream)),

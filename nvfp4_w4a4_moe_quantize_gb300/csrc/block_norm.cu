@@ -26,56 +26,80 @@ inline int group_threads(int64_t H) {
   return g;
 }
 
-template <typename E, bool kVec>
-struct RowIo {
-  // chunk j of this thread: elements [e, e + 8)
-  static __device__ __forceinline__ void load(const E* row, int e, int H, float (&v)[8]) {
-    if (kVec) {
-      if (e < H) {
-        Chunk<E> c;
-#pragma unroll
-        for (int i = 0; i < Chunk<E>::kQ; ++i) c.q[i] = load16(reinterpret_cast<const char*>(row + e) + 16 * i);
-        unpack8(c, v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = e + i < H ? to_f32(row[e + i]) : 0.f;
-    }
-  }
-  static __device__ __forceinline__ void store(E* row, int e, int H, const float (&v)[8]) {
-    if (kVec) {
-      if (e < H) store8(row + e, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (e + i < H) store_one(row + e + i, v[i]);
-    }
-  }
+// 8 values as pairs: elements [e, e + 8) of a row, zero beyond it.  kVec: the rows are 16-byte
+// aligned and whole chunks; else element by element.
+struct Eight {
+  F2 p[4];
 };
-// float32 parameters (weights, gates): 16-byte aligned rows or element by element
-template <bool kVec>
-__device__ __forceinline__ void load_param(const float* row, int e, int H, float (&v)[8]) {
-  if (kVec) {
-    if (e < H) {
-      const float4 a = *reinterpret_cast<const float4*>(row + e), b = *reinterpret_cast<const float4*>(row + e + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
+template <typename E, bool kVec>
+__device__ __forceinline__ Chunk<E> load_chunk(const E* row, int e, int H) {
+  Chunk<E> c;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
+  for (int i = 0; i < 4 * Chunk<E>::kQ; ++i) c.w[i] = 0;
+  if (kVec) {
+    if (e < H)
+#pragma unroll
+      for (int i = 0; i < Chunk<E>::kQ; ++i) c.set(i, load16(reinterpret_cast<const char*>(row + e) + 16 * i));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = e + i < H ? row[e + i] : 0.f;
+    for (int i = 0; i < 8; ++i)
+      if (e + i < H) c.put(i, row[e + i]);
+  }
+  return c;
+}
+template <typename E>
+__device__ __forceinline__ Eight pairs(const Chunk<E>& c) {
+  Eight v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p[i] = c.pair(i);
+  return v;
+}
+template <typename E, bool kVec>
+__device__ __forceinline__ void store_chunk(E* row, int e, int H, const Eight& v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2(v.p[i]);
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
+  }
+  if (kVec) {
+    if (e < H) store8(row + e, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e + i < H) store_one(row + e + i, f[i]);
   }
 }
+// A float32 parameter (a gate row), likewise.
+template <bool kVec>
+__device__ __forceinline__ Eight load_param(const float* row, int e, int H) {
+  return pairs(load_chunk<float, kVec>(row, e, H));
+}
+// 8 floats of shared memory (the weights, zero-padded to whole chunks).
+__device__ __forceinline__ Eight shared8(const float* p) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(p + 4);
+  return {{a.x, a.y, b.x, b.y}};
+}
+__device__ __forceinline__ float pair_sum(F2 p) {
+  const float2 f = unpack2(p);
+  return f.x + f.y;
+}
 
-__device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) { return to_f32(__float2bfloat16_rn(v)); }
-__device__ __forceinline__ float round_to(float v, const __half*) { return to_f32(__float2half_rn(v)); }
-__device__ __forceinline__ float round_to(float v, const float*) { return v; }
+// The value as the type stores it.
+__device__ __forceinline__ F2 round_pair(F2 v, const __nv_bfloat16*) {
+  const float2 f = unpack2(v);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+  return pack2(Packed<__nv_bfloat16>::low(w), Packed<__nv_bfloat16>::high(w));
+}
+__device__ __forceinline__ F2 round_pair(F2 v, const __half*) {
+  const float2 f = unpack2(v);
+  const __half2 h = __floats2half2_rn(f.x, f.y);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+  return pack2(Packed<__half>::low(w), Packed<__half>::high(w));
+}
+__device__ __forceinline__ F2 round_pair(F2 v, const float*) { return v; }
 
 // Sum over the group's threads, the same bits in each.  red: two floats a warp of the CTA,
 // used in turn, so one barrier a sum is enough.
@@ -109,69 +133,86 @@ struct NormArgs {
   float *rstd_y, *rstd_r;
 };
 
+// The weights in shared memory, padded with zeros to the threads' chunks.
+__device__ __forceinline__ void stage_weight(float* dst, const float* w, int H, int padded) {
+  for (int i = threadIdx.x; i < padded; i += blockDim.x) dst[i] = w != nullptr && i < H ? w[i] : 0.f;
+}
+
 // kBranch: r = alpha x + gate norm(y); else r is x itself and is not written.
+// The weights live in shared memory, so that a thread needs few registers and enough rows are
+// in flight: 1024 threads an SM hold 64 bytes each of the rows they wait for.
 template <typename E, bool kBranch, bool kNext, bool kVec>
-__global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) float weights[];
   __shared__ float red[32];
   const int G = a.group, groups = blockDim.x / G, group = threadIdx.x / G, tid = threadIdx.x % G;
+  const int padded = 8 * kChunks * G;
+  float *w = weights, *wn = weights + (kBranch ? padded : 0);
+  if (kBranch) stage_weight(w, a.weight, a.H, padded);
+  if (kNext) stage_weight(wn, a.next_weight, a.H, padded);
+  __syncthreads();
   GroupSum sum{red, G, group, 0};
-  using Io = RowIo<E, kVec>;
-  float w[kChunks][8], wn[kChunks][8];
-#pragma unroll
-  for (int j = 0; j < kChunks; ++j) {
-    const int e = 8 * (tid + j * G);
-    if (kBranch) load_param<kVec>(a.weight, e, a.H, w[j]);
-    if (kNext) load_param<kVec>(a.next_weight, e, a.H, wn[j]);
-  }
   const float inv_h = 1.f / a.H;
+  const bool per_token = a.gate != nullptr && a.rows_per_gate == 0;
+  const F2 alpha = pack2(a.alpha, a.alpha);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group; t < a.T;
        t += static_cast<int64_t>(gridDim.x) * groups) {
-    float x[kChunks][8], y[kChunks][8];
+    Chunk<E> xr[kChunks], yr[kChunks];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
       const int e = 8 * (tid + j * G);
-      if (kBranch) Io::load(static_cast<const E*>(a.y) + t * a.ldy, e, a.H, y[j]);
-      Io::load(static_cast<const E*>(a.x) + t * a.ldx, e, a.H, x[j]);
+      if (kBranch) yr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.y) + t * a.ldy, e, a.H);
+      xr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.x) + t * a.ldx, e, a.H);
     }
+    Eight x[kChunks];
     if (kBranch) {
-      float ss = 0.f;
+      F2 ss = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[j][i], y[j][i], ss);
-      const float rstd = rsqrtf(fmaf(sum(ss), inv_h, a.eps));
+        for (int i = 0; i < 4; ++i) ss = fma2(yr[j].pair(i), yr[j].pair(i), ss);
+      const float rstd = rsqrtf(fmaf(sum(pair_sum(ss)), inv_h, a.eps));
       if (tid == 0) a.rstd_y[t] = rstd;
-      const bool per_token = a.gate != nullptr && a.rows_per_gate == 0;
       const float f = per_token ? rstd * a.gate[t] : rstd;
+      const F2 ff = pack2(f, f);
       const float* grow = a.gate != nullptr && !per_token ? a.gate + t / a.rows_per_gate * a.H : nullptr;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
         const int e = 8 * (tid + j * G);
-        float g[8];
-        if (grow != nullptr) load_param<kVec>(grow, e, a.H, g);
+        const Eight wj = shared8(w + e);
+        Eight y;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float b = y[j][i] * f * w[j][i];
-          if (grow != nullptr) b *= g[i];
-          x[j][i] = round_to(fmaf(a.alpha, x[j][i], b), static_cast<const E*>(nullptr));
+        for (int i = 0; i < 4; ++i) y.p[i] = mul2(mul2(yr[j].pair(i), ff), wj.p[i]);
+        if (grow != nullptr) {
+          const Eight g = load_param<kVec>(grow, e, a.H);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], g.p[i]);
         }
-        Io::store(static_cast<E*>(a.r) + t * a.H, e, a.H, x[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[j].p[i] = round_pair(fma2(alpha, xr[j].pair(i), y.p[i]), static_cast<const E*>(nullptr));
+        store_chunk<E, kVec>(static_cast<E*>(a.r) + t * a.H, e, a.H, x[j]);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) x[j] = pairs(xr[j]);
     }
     if (kNext) {
-      float ss = 0.f;
+      F2 ss = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[j][i], x[j][i], ss);
-      const float rstd = rsqrtf(fmaf(sum(ss), inv_h, a.eps));
+        for (int i = 0; i < 4; ++i) ss = fma2(x[j].p[i], x[j].p[i], ss);
+      const float rstd = rsqrtf(fmaf(sum(pair_sum(ss)), inv_h, a.eps));
       if (tid == 0) a.rstd_r[t] = rstd;
+      const F2 rr = pack2(rstd, rstd);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
         const int e = 8 * (tid + j * G);
+        const Eight wj = shared8(wn + e);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[j][i] = x[j][i] * rstd * wn[j][i];
-        Io::store(static_cast<E*>(a.n) + t * a.H, e, a.H, x[j]);
+        for (int i = 0; i < 4; ++i) x[j].p[i] = mul2(mul2(x[j].p[i], rr), wj.p[i]);
+        store_chunk<E, kVec>(static_cast<E*>(a.n) + t * a.H, e, a.H, x[j]);
       }
     }
   }
@@ -196,95 +237,103 @@ struct NormBackwardArgs {
 //   sums over rows: d yhat (per-token: times the gate), dn rhat
 template <typename E, bool kBranch, bool kNext, bool kVec>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBackwardArgs a) {
-  extern __shared__ float cols[];
+  extern __shared__ __align__(16) float weights[];   // w, w'; at the end the groups' column sums
   __shared__ float red[32];
   const int G = a.group, groups = blockDim.x / G, group = threadIdx.x / G, tid = threadIdx.x % G;
+  const int padded = 8 * kChunks * G;
+  float *w = weights, *wn = weights + (kBranch ? padded : 0);
+  if (kBranch) stage_weight(w, a.weight, a.H, padded);
+  if (kNext) stage_weight(wn, a.next_weight, a.H, padded);
+  __syncthreads();
   GroupSum sum{red, G, group, 0};
-  using Io = RowIo<E, kVec>;
   const int64_t seg = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
   const int64_t per = (a.segment + a.parts - 1) / a.parts;
   const int64_t row0 = seg * a.segment + part * per;
   const int64_t row1 = seg * a.segment + (part * per + per < a.segment ? part * per + per : a.segment);
   const bool per_token = a.gate != nullptr && a.rows_per_gate == 0;
   const float* grow = a.gate != nullptr && !per_token ? a.gate + seg * a.H : nullptr;
-  float acc_w[kChunks][8], acc_n[kChunks][8];
+  Eight acc_w[kChunks], acc_n[kChunks];
 #pragma unroll
   for (int j = 0; j < kChunks; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc_w[j][i] = acc_n[j][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc_w[j].p[i] = acc_n[j].p[i] = 0;
   const float inv_h = 1.f / a.H;
+  const F2 alpha = pack2(a.alpha, a.alpha);
   for (int64_t t = row0 + group; t < row1; t += groups) {
-    float d[kChunks][8], dn[kChunks][8], r[kChunks][8], y[kChunks][8];
+    Chunk<E> dr[kChunks], dnr[kChunks], rr[kChunks], yr[kChunks];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
       const int e = 8 * (tid + j * G);
       if (kNext) {
-        Io::load(static_cast<const E*>(a.dn) + t * a.lddn, e, a.H, dn[j]);
-        Io::load(static_cast<const E*>(a.r) + t * a.ldr, e, a.H, r[j]);
+        dnr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.dn) + t * a.lddn, e, a.H);
+        rr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.r) + t * a.ldr, e, a.H);
       }
-      if (a.dr != nullptr) {
-        Io::load(static_cast<const E*>(a.dr) + t * a.lddr, e, a.H, d[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[j][i] = 0.f;
-      }
-      if (kBranch) Io::load(static_cast<const E*>(a.y) + t * a.ldy, e, a.H, y[j]);
+      dr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.dr) + t * a.lddr, e, a.dr != nullptr ? a.H : 0);
+      if (kBranch) yr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.y) + t * a.ldy, e, a.H);
     }
+    Eight d[kChunks];
     if (kNext) {
       const float rstd = a.rstd_r[t];
-      float dot = 0.f;
+      const F2 rs = pack2(rstd, rstd);
+      F2 dot = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        float wn[8];
-        load_param<kVec>(a.next_weight, 8 * (tid + j * G), a.H, wn);
+        const Eight wj = shared8(wn + 8 * (tid + j * G));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          r[j][i] *= rstd;
-          acc_n[j][i] = fmaf(dn[j][i], r[j][i], acc_n[j][i]);
-          dn[j][i] *= wn[i];
-          dot = fmaf(dn[j][i], r[j][i], dot);
+        for (int i = 0; i < 4; ++i) {
+          const F2 rhat = mul2(rr[j].pair(i), rs), dn = dnr[j].pair(i);
+          acc_n[j].p[i] = fma2(dn, rhat, acc_n[j].p[i]);
+          d[j].p[i] = mul2(dn, wj.p[i]);
+          dot = fma2(d[j].p[i], rhat, dot);
         }
       }
-      const float m = sum(dot) * inv_h;
+      const float m = -sum(pair_sum(dot)) * inv_h * rstd;   // times r, not rhat, below
+      const F2 mm = pack2(m, m);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[j][i] = fmaf(rstd, fmaf(-m, r[j][i], dn[j][i]), d[j][i]);
+        for (int i = 0; i < 4; ++i)
+          d[j].p[i] = fma2(rs, fma2(mm, rr[j].pair(i), d[j].p[i]), dr[j].pair(i));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) d[j] = pairs(dr[j]);
     }
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      float v[8];
+      Eight v;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = a.alpha * d[j][i];
-      Io::store(static_cast<E*>(a.dx) + t * a.H, 8 * (tid + j * G), a.H, v);
+      for (int i = 0; i < 4; ++i) v.p[i] = mul2(alpha, d[j].p[i]);
+      store_chunk<E, kVec>(static_cast<E*>(a.dx) + t * a.H, 8 * (tid + j * G), a.H, v);
     }
     if (kBranch) {
       const float rstd = a.rstd_y[t];
       const float gt = per_token ? a.gate[t] : 1.f;
-      float dot = 0.f;
+      const F2 rs = pack2(rstd, rstd), gg = pack2(gt, gt);
+      F2 dot = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
         const int e = 8 * (tid + j * G);
-        float w[8], g[8];
-        load_param<kVec>(a.weight, e, a.H, w);
-        if (grow != nullptr) load_param<kVec>(grow, e, a.H, g);
+        const Eight wj = shared8(w + e);
+        Eight g;
+        if (grow != nullptr) g = load_param<kVec>(grow, e, a.H);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[j][i] *= rstd;
-          acc_w[j][i] = fmaf(gt * d[j][i], y[j][i], acc_w[j][i]);
-          d[j][i] *= w[i];
-          if (grow != nullptr) d[j][i] *= g[i];
-          dot = fmaf(d[j][i], y[j][i], dot);
+        for (int i = 0; i < 4; ++i) {
+          const F2 yhat = mul2(yr[j].pair(i), rs);
+          acc_w[j].p[i] = fma2(mul2(gg, d[j].p[i]), yhat, acc_w[j].p[i]);
+          d[j].p[i] = mul2(d[j].p[i], wj.p[i]);
+          if (grow != nullptr) d[j].p[i] = mul2(d[j].p[i], g.p[i]);
+          dot = fma2(d[j].p[i], yhat, dot);
         }
       }
-      const float s = sum(dot);   // the token gate's gradient; the mean below times the gate
+      const float s = sum(pair_sum(dot));   // the token gate's gradient; the mean below times the gate
       if (per_token && tid == 0) a.dgate_token[t] = s;
-      const float m = s * inv_h, f = rstd * gt;
+      const float m = -s * inv_h * rstd, f = rstd * gt;
+      const F2 mm = pack2(m, m), ff = pack2(f, f);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[j][i] = f * fmaf(-m, y[j][i], d[j][i]);
-        Io::store(static_cast<E*>(a.dy) + t * a.H, 8 * (tid + j * G), a.H, d[j]);
+        for (int i = 0; i < 4; ++i) d[j].p[i] = mul2(ff, fma2(mm, yr[j].pair(i), d[j].p[i]));
+        store_chunk<E, kVec>(static_cast<E*>(a.dy) + t * a.H, 8 * (tid + j * G), a.H, d[j]);
       }
     }
   }
@@ -296,14 +345,13 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
 #pragma unroll
     for (int j = 0; j < kChunks; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 8 * (tid + j * G) + i;
-        if (e < a.H) cols[group * a.H + e] = which == 0 ? acc_w[j][i] : acc_n[j][i];
-      }
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<F2*>(weights + group * padded + 8 * (tid + j * G) + 2 * i) =
+            which == 0 ? acc_w[j].p[i] : acc_n[j].p[i];
     __syncthreads();
     for (int e = threadIdx.x; e < a.H; e += blockDim.x) {
-      float s = cols[e];
-      for (int g = 1; g < groups; ++g) s += cols[g * a.H + e];
+      float s = weights[e];
+      for (int g = 1; g < groups; ++g) s += weights[g * padded + e];
       out[e] = s;
     }
   }
@@ -316,36 +364,51 @@ struct NormReduceArgs {
   float *dweight, *dgate, *dnext;                 // nullable
 };
 
-// CTA (b, s): 32 columns, by 8 threads each.  s = 0: the weights' gradients over all ranges;
-// s > 0: the gradient of gate row s - 1.
-__global__ void __launch_bounds__(256) block_norm_reduce_kernel(const NormReduceArgs a) {
-  __shared__ float red[8][33];
+constexpr int kReduceSlices = 16;
+
+// CTA (b, s): 32 columns, a warp a slice of the ranges.  s = 0, 1: the two weights' gradients over all
+// ranges; s > 1: the gradient of gate row s - 2.
+__global__ void __launch_bounds__(32 * kReduceSlices) block_norm_reduce_kernel(const NormReduceArgs a) {
+  __shared__ float red[kReduceSlices][32];
   const int blocks = (a.H + 31) / 32, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int e = static_cast<int>(blockIdx.x % blocks) * 32 + lane;
   const int64_t s = blockIdx.x / blocks;
-  const int64_t first = s == 0 ? 0 : (s - 1) * a.parts, count = s == 0 ? a.segments * a.parts : a.parts;
-  for (int which = 0; which < 2; ++which) {
-    float* out = which == 1 ? a.dnext : (s == 0 ? a.dweight : a.dgate + (s - 1) * a.H);
-    if ((which == 1 && s > 0) || out == nullptr) continue;
-    const float* src = which == 0 ? a.part_w : a.part_n;
-    float v = 0.f;
-    if (e < a.H)
-      for (int64_t p = slice; p < count; p += 8) {
-        const float x = src[(first + p) * a.H + e];
-        v = which == 0 && s == 0 && a.gate != nullptr ? fmaf(a.gate[p / a.parts * a.H + e], x, v) : v + x;
-      }
-    red[slice][lane] = v;
-    __syncthreads();
-    if (slice == 0 && e < a.H) {
-      for (int i = 1; i < 8; ++i) v += red[i][lane];
-      out[e] = which == 0 && s > 0 ? v * a.weight[e] : v;
+  float* out = s == 0 ? a.dweight : s == 1 ? a.dnext : a.dgate + (s - 2) * a.H;
+  if (out == nullptr) return;
+  const float* src = s == 1 ? a.part_n : a.part_w;
+  const int64_t first = s < 2 ? 0 : (s - 2) * a.parts, count = s < 2 ? a.segments * a.parts : a.parts;
+  const bool gated = s == 0 && a.gate != nullptr;
+  float v = 0.f;
+  if (e < a.H) {
+#pragma unroll 8
+    for (int64_t p = slice; p < count; p += kReduceSlices) {
+      const float x = src[(first + p) * a.H + e];
+      v = gated ? fmaf(a.gate[p / a.parts * a.H + e], x, v) : v + x;
     }
-    __syncthreads();
+  }
+  red[slice][lane] = v;
+  __syncthreads();
+  if (slice == 0 && e < a.H) {
+#pragma unroll
+    for (int i = 1; i < kReduceSlices; ++i) v += red[i][lane];
+    out[e] = s > 1 ? v * a.weight[e] : v;
   }
 }
 
 bool rows_aligned(const void* p, int64_t ld, int e) {
   return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * e % 16 == 0);
+}
+
+// Launches with more than 48 KB of shared memory (H > 4096: two weights of 32 KB) need the limit raised.
+template <typename Args>
+cudaError_t start(void (*kernel)(Args), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args& a) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<grid, threads, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename E>
@@ -356,10 +419,11 @@ cudaError_t forward(const NormArgs& a, cudaStream_t s) {
                    rows_aligned(a.next_weight, a.H, 4) &&
                    (a.rows_per_gate == 0 || rows_aligned(a.gate, a.H, 4));
   const int threads = a.group > kNormThreads ? a.group : kNormThreads, groups = threads / a.group;
-  const int64_t want = (a.T + groups - 1) / groups, most = static_cast<int64_t>(num_sms()) * 8;
+  const int64_t want = (a.T + groups - 1) / groups, most = static_cast<int64_t>(num_sms()) * (1024 / threads);
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
   const bool branch = a.y != nullptr, next = a.next_weight != nullptr;
-#define NVFP4_NORM(B, N, V) block_norm_kernel<E, B, N, V><<<grid, threads, 0, s>>>(a)
+  const size_t smem = sizeof(float) * 8 * kChunks * a.group * ((branch ? 1 : 0) + (next ? 1 : 0));   // at most 64 KB
+#define NVFP4_NORM(B, N, V) return start(block_norm_kernel<E, B, N, V>, grid, threads, smem, s, a)
   if (vec) {
     if (branch && next) NVFP4_NORM(true, true, true);
     else if (branch) NVFP4_NORM(true, false, true);
@@ -370,7 +434,6 @@ cudaError_t forward(const NormArgs& a, cudaStream_t s) {
     else NVFP4_NORM(false, true, false);
   }
 #undef NVFP4_NORM
-  return cudaGetLastError();
 }
 
 template <typename E>
@@ -383,9 +446,11 @@ cudaError_t backward(const NormBackwardArgs& a, int64_t segments, float* dweight
                    rows_aligned(a.next_weight, a.H, 4) && (a.rows_per_gate == 0 || rows_aligned(a.gate, a.H, 4));
   const int threads = a.group > kNormThreads ? a.group : kNormThreads, groups = threads / a.group;
   const dim3 grid(static_cast<unsigned>(segments * a.parts));
-  const size_t smem = sizeof(float) * groups * a.H;   // at most 256 / G * 16 G floats: 16 KB, 32 KB for G = 512
   const bool branch = a.y != nullptr, next = a.next_weight != nullptr;
-#define NVFP4_NORM(B, N, V) block_norm_backward_kernel<E, B, N, V><<<grid, threads, smem, s>>>(a)
+  const int rows = (branch ? 1 : 0) + (next ? 1 : 0);   // of shared memory: the weights, later the groups' sums
+  const size_t smem = sizeof(float) * 8 * kChunks * a.group * (rows > groups ? rows : groups);
+  cudaError_t err;
+#define NVFP4_NORM(B, N, V) err = start(block_norm_backward_kernel<E, B, N, V>, grid, threads, smem, s, a)
   if (vec) {
     if (branch && next) NVFP4_NORM(true, true, true);
     else if (branch) NVFP4_NORM(true, false, true);
@@ -396,16 +461,16 @@ cudaError_t backward(const NormBackwardArgs& a, int64_t segments, float* dweight
     else NVFP4_NORM(false, true, false);
   }
 #undef NVFP4_NORM
-  cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   NormReduceArgs ra{a.part_w, a.part_n, a.weight, a.rows_per_gate > 0 ? a.gate : nullptr, a.H, segments, a.parts,
                     dweight, a.rows_per_gate > 0 ? dgate : nullptr, dnext};
   const int64_t blocks = (a.H + 31) / 32;
-  block_norm_reduce_kernel<<<static_cast<unsigned>(blocks * (1 + (ra.gate != nullptr ? segments : 0))), 256, 0, s>>>(ra);
+  block_norm_reduce_kernel<<<static_cast<unsigned>(blocks * (2 + (ra.gate != nullptr ? segments : 0))),
+                             32 * kReduceSlices, 0, s>>>(ra);
   return cudaGetLastError();
 }
 
-constexpr int64_t kNormParts = 608;   // ranges of rows in all, unless there are more gate rows
+constexpr int64_t kNormParts = 304;   // ranges of rows in all, unless there are more gate rows
 
 }  // namespace
 

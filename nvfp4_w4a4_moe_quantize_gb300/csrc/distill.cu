@@ -51,12 +51,18 @@ struct ListSmem {
   float mz, s, A, B, Q;
   int live, bad;
 };
+// What the row's sums give: the loss, and the gradient as coef 2^((z - mb) c1), lp(z) = ln p.
+struct RowResult {
+  float loss, lse, mb, coef;
+  float m, ln_s;
+};
 struct DistillSmem {
   Stats part[kMaxSlices][kVocabWarps];
   int twice[kMaxSlices];   // a slice found an id of the list twice
   ListSmem list;
+  RowResult result;
   uint64_t arrived;
-  int abort;
+  int abort, dead;
 };
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -149,11 +155,6 @@ __device__ __forceinline__ void reduce_list(const DistillArgs& a, const E* z, in
   }
 }
 
-// What the row's sums give: the loss, and the gradient as coef 2^((z - mb) c1), lp(z) = ln p.
-struct RowResult {
-  float loss, lse, mb, coef;
-  float m, ln_s;
-};
 template <bool kTail>
 __device__ __forceinline__ RowResult finish_row(Stats st, const ListSmem& l, float scale, float c1) {
   RowResult r;
@@ -184,12 +185,19 @@ __device__ __forceinline__ RowResult finish_row(Stats st, const ListSmem& l, flo
   return r;
 }
 
-template <bool kTail>
-__device__ __forceinline__ void leave_out(float (&v)[8], uint32_t bits) {
-  if (kTail && bits != 0)
+// The listed tokens of a batch, four bytes of the bitmap 256 apart, become -inf.
+template <bool kTail, typename E>
+__device__ __forceinline__ void leave_out(Chunk<E> (&raw)[4], const uint8_t* listed, int chunks_left) {
+  if constexpr (kTail) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (bits >> i & 1) v[i] = -INFINITY;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t bits = k * kVocabThreads < chunks_left ? listed[k * kVocabThreads] : 0;
+      if (bits != 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (bits >> i & 1) raw[k].leave_out(i);
+    }
+  }
 }
 
 // The loss alone.
@@ -224,12 +232,12 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const Disti
     for (int s = s0; s < s1; ++s) {
       int f, e;
       slice_range(a.V, slices, s, f, e);
-      Stats st = empty_stats();
-      for_chunks(row, f, e, [&](int c, float(&v)[8]) {
-        leave_out<kTail>(v, listed[c - first]);
-        accumulate<false>(st, v, c1);
+      Running<E, false> run;
+      for_batches(row, f, e, [&](int c, Chunk<E>(&raw)[4]) {
+        leave_out<kTail>(raw, listed + (c - first), e - c);
+        run.add(raw, c1);
       });
-      st = warp_merge<false>(st, c1);
+      const Stats st = run.warp(c1);
       if (lane == 0) *(ctas == 1 ? &sm.part[s][warp] : cluster.map_shared_rank(&sm.part[s][warp], 0)) = st;
     }
   if (ctas > 1) {
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const Disti
   bool bad = l.bad;
   for (int r = 0; r < ctas; ++r) bad |= sm.twice[r] != 0;
   RowResult r{0.f, 0.f};
-  if (!dead) r = finish_row<kTail>(join_slices<false>(sm.part, slices, c1), l, a.scale, c1);
+  if (!dead) r = finish_row<kTail>(Running<E, false>::join_slices(sm.part, slices, c1), l, a.scale, c1);
   if (lane == 0) {
     if (bad) set_status(a.status, kStatusBadInput);
     a.loss[t] = bad ? NAN : r.loss;
@@ -275,19 +283,16 @@ struct Stage {
     if (i >= 0 && i < h + tl) *reinterpret_cast<E*>(const_cast<char*>(at(e))) = z[e];
   }
   // Elements [e, e + 8).
-  __device__ __forceinline__ void get(int e, float (&v)[8]) const {
+  __device__ __forceinline__ Chunk<E> get(int e) const {
     constexpr int Q = Chunk<E>::kQ;
     const char* p = at(e);
     const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
     const uint4* w = reinterpret_cast<const uint4*>(p - shift);
+    if (shift != 0) return join_words<E>([&](int i) { return w[i]; }, shift);
     Chunk<E> c;
-    if (shift == 0) {
 #pragma unroll
-      for (int i = 0; i < Q; ++i) c.q[i] = w[i];
-    } else {
-      c = join_words<E>([&](int i) { return w[i]; }, shift);
-    }
-    unpack8(c, v);
+    for (int i = 0; i < Q; ++i) c.set(i, w[i]);
+    return c;
   }
 };
 
@@ -330,24 +335,29 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_backward_kernel(co
   bool dead = l.bad || !l.live;
   Stats st = empty_stats();
   if (!dead) {
+    Running<E, false> run;
     if (kStage) {
-      for (int c = first + tid; c < end; c += kVocabThreads) {
-        float v[8];
-        stage.get(8 * c, v);
-        if (8 * c + 8 > a.V)
+      for (int c = first + tid; c < end; c += 4 * kVocabThreads) {
+        Chunk<E> raw[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (8 * c + i >= a.V) v[i] = -INFINITY;
-        leave_out<kTail>(v, listed[c - first]);
-        accumulate<false>(st, v, c1);
+        for (int k = 0; k < 4; ++k) {
+          const int ck = c + k * kVocabThreads;
+          raw[k] = ck < end ? stage.get(8 * ck) : Chunk<E>::none();
+          if (ck < end && 8 * ck + 8 > a.V)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (8 * ck + i >= a.V) raw[k].leave_out(i);
+        }
+        leave_out<kTail>(raw, listed + (c - first), end - c);
+        run.add(raw, c1);
       }
     } else {
-      for_chunks(row, first, end, [&](int c, float(&v)[8]) {
-        leave_out<kTail>(v, listed[c - first]);
-        accumulate<false>(st, v, c1);
+      for_batches(row, first, end, [&](int c, Chunk<E>(&raw)[4]) {
+        leave_out<kTail>(raw, listed + (c - first), end - c);
+        run.add(raw, c1);
       });
     }
-    st = warp_merge<false>(st, c1);
+    st = run.warp(c1);
   }
   if (ctas > 1) {
     cluster.barrier_wait();
@@ -360,28 +370,49 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_backward_kernel(co
     if (lane == 0) sm.part[0][warp] = st;
     __syncthreads();
   }
-  bool bad = l.bad;
-  for (int r = 0; r < ctas; ++r) bad |= sm.twice[r] != 0;
-  RowResult r{0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (!dead) r = finish_row<kTail>(join_slices<false>(sm.part, ctas, c1), l, a.scale, c1);
-  dead |= bad;
-  if (rank == 0 && tid == 0) {
-    if (bad) set_status(a.status, kStatusBadInput);
-    a.loss[t] = bad ? NAN : r.loss;
-    if (a.lse != nullptr) a.lse[t] = bad ? 0.f : r.lse;
+  // one warp finishes the row's scalars for the CTA
+  if (warp == 0) {
+    bool bad = l.bad;
+    for (int r = 0; r < ctas; ++r) bad |= sm.twice[r] != 0;
+    RowResult r{0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (!dead) r = finish_row<kTail>(Running<E, false>::join_slices(sm.part, ctas, c1), l, a.scale, c1);
+    if (bad) {
+      r.loss = NAN;
+      r.lse = 0.f;
+    }
+    if (lane == 0) {
+      sm.result = r;
+      sm.dead = dead || bad;
+      if (rank == 0) {
+        if (bad) set_status(a.status, kStatusBadInput);
+        a.loss[t] = r.loss;
+        if (a.lse != nullptr) a.lse[t] = r.lse;
+      }
+    }
   }
+  __syncthreads();
+  const RowResult r = sm.result;
+  dead = sm.dead;
   const float w = a.scale * (a.dloss != nullptr ? a.dloss[t] : 1.f);
-  const float k1 = w * r.coef;
   E* out = static_cast<E*>(a.dlogits) + t * a.ldd;
+  const F2 minus = pack2(-r.mb, -r.mb), cc = pack2(c1, c1), kk = pack2(w * r.coef, w * r.coef);
   const auto gradient = [&](int, float(&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = dead ? 0.f : k1 * ex2((v[i] - r.mb) * c1);
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2(mul2(add2(pack2(v[2 * i], v[2 * i + 1]), minus), cc));
+      const float2 d = unpack2(mul2(pack2(ex2(x.x), ex2(x.y)), kk));
+      v[2 * i] = d.x;
+      v[2 * i + 1] = d.y;
+    }
+    if (dead)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
   };
   if (kStage)
-    map_chunks(out, lo, hi, tid, kVocabThreads, [&](int e, float(&v)[8]) { stage.get(e, v); },
-               [&](int e) { return to_f32(*reinterpret_cast<const E*>(stage.at(e))); }, gradient);
+    map_chunks<E, 2>(out, lo, hi, [&](int e) { return stage.get(e); },
+                     [&](int e) { return *reinterpret_cast<const E*>(stage.at(e)); }, gradient);
   else
-    map_range(z, out, lo, hi, tid, kVocabThreads, gradient);
+    map_row<E, 2>(z, a.V, out, lo, hi, gradient);
   if (dead) return;
   __syncthreads();   // the listed tokens' values go over the others
   if (tid < kMaxList) {

@@ -160,17 +160,19 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
   for (int s = s0; s < s1; ++s) {
     int first, last;
     slice_range(a.V, slices, s, first, last);
-    Stats st = empty_stats();
+    Running<E, kEntropy> run;
     float best = -INFINITY;
     int at = 0;
-    for_chunks(row, first, last, [&](int c, const float(&v)[8]) {
-      const float cm = accumulate<kEntropy>(st, v, c1);
+    for_batches(row, first, last, [&](int c, const Chunk<E>(&raw)[4]) {
+      const float cm = run.add(raw, c1);
       if (kTop && cm > best) {
         best = cm;
-        at = c;
+#pragma unroll
+        for (int i = 3; i >= 0; --i)   // the first of the four that holds it
+          if (raw[i].max() == cm) at = c + i * kVocabThreads;
       }
     });
-    st = warp_merge<kEntropy>(st, c1);
+    const Stats st = run.warp(c1);
     if (lane == 0) part[s][warp] = st;
     if (kTop) {
       top.best[s - s0][tid] = best;
@@ -191,32 +193,34 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
       if (top.best[s][tid] > -INFINITY && order_key(top.best[s][tid], 8 * top.chunk[s][tid]) >= bound)
         top.cell[atomicAdd(&sm.cells, 1)] = static_cast<uint16_t>(s * kVocabThreads + tid);
     __syncthreads();
-    // each round every warp reads up to 32 chunks of one cell
+    // the cells' chunks, a thread each
     const int cells = sm.cells;
-    int per = 0;
-    {
-      int first, last;
-      slice_range(a.V, slices, s0, first, last);
-      per = (last - first + kVocabThreads - 1) / kVocabThreads;   // the first slice is the longest
-    }
-    const int groups = (per + 31) / 32, items = cells * groups;
-    for (int base = 0; base < items; base += kVocabWarps) {
-      const int item = base + warp;
+    int begin, stop;
+    slice_range(a.V, slices, s0, begin, stop);   // the first slice is the longest
+    const int per = (stop - begin + kVocabThreads - 1) / kVocabThreads, items = cells * per;
+    const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
+    for (int base = 0; base < items; base += kVocabThreads) {
+      const int item = base + tid;
       if (item < items) {
-        const int cell = top.cell[item / groups];
+        const int cell = top.cell[item / per];
         int first, last;
         slice_range(a.V, slices, s0 + cell / kVocabThreads, first, last);
-        const int c = first + cell % kVocabThreads + ((item % groups) * 32 + lane) * kVocabThreads;
+        const int c = first + cell % kVocabThreads + (item % per) * kVocabThreads;
         if (c < last) {
-          float v[8];
-          row.get(c, v);
+          const Chunk<E> raw = row.get(c);
+          if (raw.max() >= floor) {
+            float v[8];
+            unpack8(raw, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t key = order_key(v[i], 8 * c + i);
-            if (v[i] > -INFINITY && key >= bound) top.key[atomicAdd(&sm.count, 1)] = key;
+            for (int i = 0; i < 8; ++i)
+              if (v[i] >= floor && v[i] > -INFINITY) {
+                const uint64_t key = order_key(v[i], 8 * c + i);
+                if (key >= bound) top.key[atomicAdd(&sm.count, 1)] = key;
+              }
           }
         }
       }
+      if (base + kVocabThreads >= items) break;
       __syncthreads();
       const int n = sm.count;
       __syncthreads();      // everyone has read it before the next round counts on
@@ -227,6 +231,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
         __syncthreads();
       }
     }
+    __syncthreads();
     found = rank_keys(top.key, sm.count, a.k, top.sorted);
     if (ctas > 1) {   // push the list into the first CTA
       TopSmem* lead = cluster.map_shared_rank(&top, 0);
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
   } else {
     __syncthreads();
   }
-  const Stats st = join_slices<kEntropy>(sm.part, slices, c1);   // every warp, the same bits
+  const Stats st = Running<E, kEntropy>::join_slices(sm.part, slices, c1);   // every warp, the same bits
   const float ln_s = logf(st.s);
   const bool none = st.s == 0.f;   // every token excluded
   if (tid == 0) {
@@ -365,18 +370,27 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(
   const float c1 = a.scale * kLog2e, l1 = -lse * kLog2e;
   // with t = log2 p:  dz = p (A + B t), + scale g at the target
   const float A = -a.scale * (g + (kEntropy ? h * a.entropy[t] : 0.f)), B = -a.scale * h * kLn2;
-  map_range(z, out, lo, hi, threadIdx.x, kVocabThreads, [&](int e0, float(&v)[8]) {
-    const int at = y - e0;
-    const float zy = a.scale * g;
+  const F2 cc = pack2(c1, c1), ll = pack2(l1, l1), aa = pack2(A, A), bb = pack2(B, B);
+  const float zy = a.scale * g;
+  map_row<E, 4>(z, a.V, out, lo, hi, [&](int e0, float(&v)[8]) {
+    const unsigned at = y - e0;
+    const float zt = at < 8 ? to_f32(z[min(y, a.V - 1)]) : 0.f;   // before it may be overwritten
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool hit = i == at && v[i] > -INFINITY;
-      const float lt = fmaf(v[i], c1, l1);
-      const float p = ex2(lt);
-      float d = kEntropy ? p * fmaf(B, fmaxf(lt, -1e30f), A) : p * A;
-      if (hit) d += zy;
-      v[i] = skip ? 0.f : d;
+    for (int i = 0; i < 4; ++i) {
+      const float2 lt = unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), cc, ll));
+      const F2 p = pack2(ex2(lt.x), ex2(lt.y));
+      const F2 f = kEntropy ? fma2(bb, pack2(fmaxf(lt.x, -1e30f), fmaxf(lt.y, -1e30f)), aa) : aa;
+      const float2 d = unpack2(mul2(p, f));
+      v[2 * i] = d.x;
+      v[2 * i + 1] = d.y;
     }
+    if (at < 8 && zt > -INFINITY)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i == at) v[i] += zy;
+    if (skip)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
   });
 }
 

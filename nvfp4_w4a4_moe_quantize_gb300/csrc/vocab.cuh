@@ -3,9 +3,13 @@
 //
 // A row of V logits is cut into chunks of 8 consecutive elements by element number, and the
 // chunks into vocab_slices(V) slices; thread i of a slice's 256 threads takes chunks i, i + 256,
-// ... of the slice.  The cut depends on V alone -- not on the number of rows, not on whether
-// the slices of a row run one after the other in one CTA or side by side in a cluster, and
-// not on the row's address -- and so do a row's bits.
+// ... of the slice, four at a time (a batch).  The cut depends on V alone -- not on the number
+// of rows, not on whether the slices of a row run one after the other in one CTA or side by
+// side in a cluster, and not on the row's address -- and so do a row's bits.
+//
+// These kernels are bound by instructions as much as by HBM: at 6.8 TB/s an SM receives a BF16
+// element every 11.6 issue slots / 32.  So float32 arithmetic runs on pairs (add, mul and fma
+// .f32x2), maxima on packed words, and the running maximum is met once a batch of 32 elements.
 #pragma once
 #include <cfloat>
 #include <cooperative_groups.h>
@@ -43,40 +47,124 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return q;
 }
 
+// Pairs of float32.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// What the kernels know of an element type: -inf in a packed word, the larger of two packed
+// words, and the pairs and the maximum of a word.
 template <typename E>
-struct Chunk {
-  static constexpr int kQ = sizeof(E) / 2;   // 16-byte words of 8 elements
-  uint4 q[kQ];
+struct Packed;
+template <>
+struct Packed<__nv_bfloat16> {
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+};
+template <>
+struct Packed<__half> {
+  static constexpr uint32_t kNegInf = 0xfc00fc00u;
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float low(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __high2float(*reinterpret_cast<const __half2*>(&w)); }
 };
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
-__device__ __forceinline__ void unpack8(const Chunk<__nv_bfloat16>& c, float (&v)[8]) {
-  const uint32_t w[4] = {c.q[0].x, c.q[0].y, c.q[0].z, c.q[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 8 consecutive elements as they lie in memory.
+template <typename E>
+struct Chunk {
+  static constexpr int kQ = sizeof(E) / 2;   // 16-byte words
+  uint32_t w[4 * kQ];
+  __device__ __forceinline__ void set(int i, uint4 q) {
+    w[4 * i] = q.x;
+    w[4 * i + 1] = q.y;
+    w[4 * i + 2] = q.z;
+    w[4 * i + 3] = q.w;
   }
-}
-__device__ __forceinline__ void unpack8(const Chunk<__half>& c, float (&v)[8]) {
-  const uint32_t w[4] = {c.q[0].x, c.q[0].y, c.q[0].z, c.q[0].w};
+  __device__ __forceinline__ F2 pair(int i) const {   // elements 2i, 2i + 1
+    if constexpr (sizeof(E) == 4) return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else return pack2(Packed<E>::low(w[i]), Packed<E>::high(w[i]));
+  }
+  __device__ __forceinline__ float max() const {
+    if constexpr (sizeof(E) == 4) {
+      float m = __uint_as_float(w[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+      return m;
+    } else {
+      const uint32_t m = max_word();
+      return fmaxf(Packed<E>::low(m), Packed<E>::high(m));
+    }
+  }
+  __device__ __forceinline__ uint32_t max_word() const {
+    return Packed<E>::max(Packed<E>::max(w[0], w[1]), Packed<E>::max(w[2], w[3]));
+  }
+  // element i (known at compile time) becomes -inf
+  __device__ __forceinline__ void leave_out(int i) {
+    if constexpr (sizeof(E) == 4) w[i] = 0xff800000u;
+    else w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | (Packed<E>::kNegInf & 0xffff0000u)
+                          : (w[i / 2] & 0xffff0000u) | (Packed<E>::kNegInf & 0xffffu);
+  }
+  __device__ __forceinline__ void put(int i, E v) {
+    if constexpr (sizeof(E) == 4) w[i] = __float_as_uint(v);
+    else {
+      const uint32_t h = *reinterpret_cast<const uint16_t*>(&v);
+      w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | (h << 16) : (w[i / 2] & 0xffff0000u) | h;
+    }
+  }
+  static __device__ __forceinline__ Chunk none() {
+    Chunk c;
+#pragma unroll
+    for (int i = 0; i < 4 * kQ; ++i) {
+      if constexpr (sizeof(E) == 4) c.w[i] = 0xff800000u;
+      else c.w[i] = Packed<E>::kNegInf;
+    }
+    return c;
+  }
+};
+template <typename E>
+__device__ __forceinline__ void unpack8(const Chunk<E>& c, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    const float2 f = unpack2(c.pair(i));
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void unpack8(const Chunk<float>& c, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    v[4 * i] = __uint_as_float(c.q[i].x);
-    v[4 * i + 1] = __uint_as_float(c.q[i].y);
-    v[4 * i + 2] = __uint_as_float(c.q[i].z);
-    v[4 * i + 3] = __uint_as_float(c.q[i].w);
   }
 }
 
@@ -108,7 +196,7 @@ __device__ __forceinline__ Chunk<E> join_words(Word&& word, uint32_t shift) {
   }
   Chunk<E> r;
 #pragma unroll
-  for (int i = 0; i < Q; ++i) r.q[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  for (int i = 0; i < 4 * Q; ++i) r.w[i] = o[i];
   return r;
 }
 
@@ -128,30 +216,29 @@ struct Row {
     return last <= V && (shift == 0 || c > 0);
   }
   __device__ __forceinline__ Chunk<E> load_inner(int c) const {
-    constexpr int Q = Chunk<E>::kQ;
-    Chunk<E> r;
     const char* b = reinterpret_cast<const char*>(p + 8 * static_cast<int64_t>(c));
     if (shift == 0) {
+      Chunk<E> r;
 #pragma unroll
-      for (int i = 0; i < Q; ++i) r.q[i] = load16(b + 16 * i);
+      for (int i = 0; i < Chunk<E>::kQ; ++i) r.set(i, load16(b + 16 * i));
       return r;
     }
     return join_words<E>([&](int i) { return load16(b - shift + 16 * i); }, shift);
   }
   // Any chunk that begins inside the row; places past its end read as -inf (excluded).
-  __device__ __forceinline__ void get(int c, float (&v)[8]) const {
-    if (inner(c)) {
-      unpack8(load_inner(c), v);
-      return;
-    }
+  __device__ __forceinline__ Chunk<E> get(int c) const {
+    if (inner(c)) return load_inner(c);
+    Chunk<E> r = Chunk<E>::none();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 8 * c + i < V ? to_f32(p[8 * c + i]) : -INFINITY;
+    for (int i = 0; i < 8; ++i)
+      if (8 * c + i < V) r.put(i, p[8 * c + i]);
+    return r;
   }
 };
 
 // ---------------------------------------------------------------- softmax statistics
 
-// Over a set of logits z with c1 = scale * log2(e), t = (z - m) c1 and m their running
+// Over a set of logits z with c1 = scale * log2(e), t = (z - m) c1 and m their
 // maximum: s = sum 2^t and u = sum 2^t t.  m starts at the lowest float, so a set of -inf
 // alone has s = 0 and a set of the lowest values is still uniform.  A NaN or +inf logit
 // makes s (and u) NaN.
@@ -168,57 +255,83 @@ __device__ __forceinline__ void rebase(Stats& a, float m, float c1) {
   a.s = r * a.s;
   a.m = m;
 }
-template <bool kEntropy>
-__device__ __forceinline__ Stats merge(Stats a, Stats b, float c1) {
-  const float m = fmaxf(a.m, b.m);
-  rebase<kEntropy>(a, m, c1);
-  rebase<kEntropy>(b, m, c1);
-  a.s += b.s;
-  if (kEntropy) a.u += b.u;
-  return a;
-}
-template <bool kEntropy>
-__device__ __forceinline__ float accumulate(Stats& a, const float (&v)[8], float c1) {
-  float cm = v[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) cm = fmaxf(cm, v[i]);
-  if (cm > a.m) rebase<kEntropy>(a, cm, c1);
-  float s = 0.f, u = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = (v[i] - a.m) * c1;
-    const float e = ex2(t);
-    s += e;
-    if (kEntropy) u = fmaf(e, fmaxf(t, -1000.f), u);   // an excluded token adds 0, not 0 * inf
-  }
-  a.s += s;
-  if (kEntropy) a.u += u;
-  return cm;
-}
-template <bool kEntropy>
-__device__ __forceinline__ Stats warp_merge(Stats a, float c1) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Stats b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.u = kEntropy ? __shfl_xor_sync(0xffffffffu, a.u, o) : 0.f;
-    a = merge<kEntropy>(a, b, c1);
-  }
-  return a;
-}
 
-// The slices of a row join here: part[slice][warp], filled by every CTA of the row in the
-// shared memory of the cluster's first CTA (or of each CTA).  Called by one warp; every lane
-// returns the row's statistics.
-template <bool kEntropy>
-__device__ __forceinline__ Stats join_slices(const Stats (*part)[kVocabWarps], int slices, float c1) {
-  const int lane = threadIdx.x & 31;
-  const Stats* flat = &part[0][0];
-  Stats a = lane < slices * kVocabWarps ? flat[lane] : empty_stats();
-  if (lane + 32 < slices * kVocabWarps) a = merge<kEntropy>(a, flat[lane + 32], c1);
-  return warp_merge<kEntropy>(a, c1);
-}
+// A thread's running sums: s and u of its even and odd elements.
+template <typename E, bool kEntropy>
+struct Running {
+  float m = -FLT_MAX;
+  F2 s = 0, u = 0;
+  // Four chunks; returns their maximum.
+  __device__ __forceinline__ float add(const Chunk<E> (&raw)[4], float c1) {
+    float cm;
+    if constexpr (sizeof(E) == 4) {
+      cm = fmaxf(fmaxf(raw[0].max(), raw[1].max()), fmaxf(raw[2].max(), raw[3].max()));
+    } else {
+      const uint32_t w = Packed<E>::max(Packed<E>::max(raw[0].max_word(), raw[1].max_word()),
+                                        Packed<E>::max(raw[2].max_word(), raw[3].max_word()));
+      cm = fmaxf(Packed<E>::low(w), Packed<E>::high(w));
+    }
+    if (cm > m) {
+      const float d = fmaxf((m - cm) * c1, -1000.f);
+      const float r = ex2(d);
+      const F2 rr = pack2(r, r);
+      if (kEntropy) u = mul2(rr, fma2(pack2(d, d), s, u));
+      s = mul2(rr, s);
+      m = cm;
+    }
+    const F2 minus = pack2(-m, -m), cc = pack2(c1, c1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      F2 e[4];
+      F2 x = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = unpack2(mul2(add2(raw[k].pair(i), minus), cc));
+        e[i] = pack2(ex2(t.x), ex2(t.y));
+        if (kEntropy) {   // an excluded token adds 0, not 0 * inf
+          const F2 tt = pack2(fmaxf(t.x, -1000.f), fmaxf(t.y, -1000.f));
+          x = i == 0 ? mul2(e[i], tt) : fma2(e[i], tt, x);
+        }
+      }
+      s = add2(s, add2(add2(e[0], e[1]), add2(e[2], e[3])));
+      if (kEntropy) u = add2(u, x);
+    }
+    return cm;
+  }
+  // The warp's statistics, the same in every lane.
+  __device__ __forceinline__ Stats warp(float c1) const {
+    const float2 ss = unpack2(s), uu = unpack2(u);
+    Stats a{m, ss.x + ss.y, kEntropy ? uu.x + uu.y : 0.f};
+    return warp_join(a, c1);
+  }
+  static __device__ __forceinline__ Stats warp_join(Stats a, float c1) {
+    float top;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(a.m));
+    rebase<kEntropy>(a, top, c1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+      if (kEntropy) a.u += __shfl_xor_sync(0xffffffffu, a.u, o);
+    }
+    return a;
+  }
+  // The slices of a row join here: part[slice][warp], in the shared memory of the CTA.  Called by
+  // one warp; every lane returns the row's statistics.
+  static __device__ __forceinline__ Stats join_slices(const Stats (*part)[kVocabWarps], int slices, float c1) {
+    const int lane = threadIdx.x & 31;
+    const Stats* flat = &part[0][0];
+    Stats a = lane < slices * kVocabWarps ? flat[lane] : empty_stats();
+    if (lane + 32 < slices * kVocabWarps) {
+      Stats b = flat[lane + 32];
+      const float m = fmaxf(a.m, b.m);
+      rebase<kEntropy>(a, m, c1);
+      rebase<kEntropy>(b, m, c1);
+      a.s += b.s;
+      a.u += b.u;
+    }
+    return warp_join(a, c1);
+  }
+};
 
 // The chunks [first, last) of a slice.
 __device__ __forceinline__ void slice_range(int V, int slices, int slice, int& first, int& last) {
@@ -227,31 +340,22 @@ __device__ __forceinline__ void slice_range(int V, int slices, int slice, int& f
   last = min(chunks, first + per);
 }
 
-// Calls f(chunk number, 8 values) for this thread's chunks of [first, last), in order, with
-// four loads in flight.
+// Calls f(c, raw) for this thread's batches of [first, last), in order: raw[i] is chunk
+// c + 256 i, -inf beyond the slice.  The four loads of a batch are in flight together.
 template <typename E, typename F>
-__device__ __forceinline__ void for_chunks(const Row<E>& row, int first, int last, F&& f) {
-  constexpr int kAhead = 4;
-  int c = first + threadIdx.x;
-  while (c < last) {
-    const int end = c + (kAhead - 1) * kVocabThreads;
+__device__ __forceinline__ void for_batches(const Row<E>& row, int first, int last, F&& f) {
+  for (int c = first + threadIdx.x; c < last; c += 4 * kVocabThreads) {
+    const int end = c + 3 * kVocabThreads;
+    Chunk<E> raw[4];
     if (end < last && row.inner(c) && row.inner(end)) {
-      Chunk<E> raw[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) raw[i] = row.load_inner(c + i * kVocabThreads);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        float v[8];
-        unpack8(raw[i], v);
-        f(c + i * kVocabThreads, v);
-      }
-      c += kAhead * kVocabThreads;
+      for (int i = 0; i < 4; ++i) raw[i] = row.load_inner(c + i * kVocabThreads);
     } else {
-      float v[8];
-      row.get(c, v);
-      f(c, v);
-      c += kVocabThreads;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        raw[i] = c + i * kVocabThreads < last ? row.get(c + i * kVocabThreads) : Chunk<E>::none();
     }
+    f(c, raw);
   }
 }
 
@@ -284,36 +388,37 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// out[e] = f(e, value(e)) for e in [lo, hi) of a row, by `threads` threads of which this is
-// number `tid`: eight(e, v) gives the values of [e, e + 8), one(e) a single one.  The chunks are
-// cut on the output's 16-byte boundaries, so that stores are whole.
-template <typename E, typename Eight, typename One, typename F>
-__device__ __forceinline__ void map_chunks(E* out, int lo, int hi, int tid, int threads, Eight&& eight, One&& one,
-                                           F&& f) {
+// out[e] = f(e, value(e)) for e in [lo, hi) of a row, by the CTA's threads: eight(e) gives the
+// chunk of [e, e + 8), one(e) a single element.  The chunks are cut on the output's 16-byte
+// boundaries, so that stores are whole; kAhead of them are read before the first is
+// written.
+template <typename E, int kAhead, typename Eight, typename One, typename F>
+__device__ __forceinline__ void map_chunks(E* out, int lo, int hi, Eight&& eight, One&& one, F&& f) {
+  const int tid = threadIdx.x;
   const uint32_t so = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out + lo)) & 15u;
   const int head = min(hi - lo, static_cast<int>((16u - so) & 15u) / static_cast<int>(sizeof(E)));
   const int body = (hi - lo - head) >> 3;
-  const int tail = lo + head + 8 * body;
-  constexpr int kAhead = 2;
-  for (int c = tid; c < body; c += kAhead * threads) {
-    float v[kAhead][8];
+  const int base = lo + head, tail = base + 8 * body;
+  for (int c = tid; c < body; c += kAhead * kVocabThreads) {
+    Chunk<E> raw[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (c + k * threads < body) eight(lo + head + 8 * (c + k * threads), v[k]);
+      if (c + k * kVocabThreads < body) raw[k] = eight(base + 8 * (c + k * kVocabThreads));
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int e = lo + head + 8 * (c + k * threads);
-      if (c + k * threads < body) {
-        f(e, v[k]);
-        store8(out + e, v[k]);
+    for (int k = 0; k < kAhead; ++k)
+      if (c + k * kVocabThreads < body) {
+        const int e = base + 8 * (c + k * kVocabThreads);
+        float v[8];
+        unpack8(raw[k], v);
+        f(e, v);
+        store8(out + e, v);
       }
-    }
   }
   // the ends, at most 7 elements each
   if (tid < head || (tid >= 8 && tid - 8 < hi - tail)) {
     const int e = tid < head ? lo + tid : tail + tid - 8;
     float v[8];
-    v[0] = one(e);
+    v[0] = to_f32(one(e));
 #pragma unroll
     for (int i = 1; i < 8; ++i) v[i] = -INFINITY;
     f(e, v);
@@ -321,26 +426,42 @@ __device__ __forceinline__ void map_chunks(E* out, int lo, int hi, int tid, int 
   }
 }
 
-// The same with the values of z in global memory: z is read in whole words where it is aligned
-// with the output, else one by one.  out may be z itself: a thread reads its elements before it
-// writes them.
-template <typename E, typename F>
-__device__ __forceinline__ void map_range(const E* z, E* out, int lo, int hi, int tid, int threads, F&& f) {
-  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(z)) & 15u) == 0;
-  map_chunks(
-      out, lo, hi, tid, threads,
-      [&](int e, float(&v)[8]) {
-        if (same) {
+// The same with the values in the row z[0, V) of global memory.  Where z and out are not
+// equally far from a 16-byte boundary, z's words are joined by funnel shifts (inside the
+// row; its ends are read one by one).  out may be z itself: a thread then reads its own
+// elements alone, before it writes them.
+template <typename E, int kAhead, typename F>
+__device__ __forceinline__ void map_row(const E* z, int V, E* out, int lo, int hi, F&& f) {
+  constexpr int Q = Chunk<E>::kQ;
+  const auto one = [&](int e) { return z[e]; };
+  // the shift of every chunk: out + e is on a boundary
+  const uint32_t shift =
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(z) - reinterpret_cast<uintptr_t>(out)) & 15u;
+  if (shift == 0) {
+    map_chunks<E, kAhead>(
+        out, lo, hi,
+        [&](int e) {
           Chunk<E> c;
 #pragma unroll
-          for (int i = 0; i < Chunk<E>::kQ; ++i) c.q[i] = load16(reinterpret_cast<const char*>(z + e) + 16 * i);
-          unpack8(c, v);
-        } else {
+          for (int i = 0; i < Q; ++i) c.set(i, load16(reinterpret_cast<const char*>(z + e) + 16 * i));
+          return c;
+        },
+        one, f);
+    return;
+  }
+  const int before = shift / sizeof(E), after = static_cast<int>((16 - shift) / sizeof(E));
+  map_chunks<E, 2>(
+      out, lo, hi,
+      [&](int e) {
+        if (e >= before && e + 8 + after <= V)
+          return join_words<E>(
+              [&](int i) { return load16(reinterpret_cast<const char*>(z + e) - shift + 16 * i); }, shift);
+        Chunk<E> c = Chunk<E>::none();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = to_f32(z[e + i]);
-        }
+        for (int i = 0; i < 8; ++i) c.put(i, z[e + i]);
+        return c;
       },
-      [&](int e) { return to_f32(z[e]); }, f);
+      one, f);
 }
 
 }  // namespace nvfp4
