@@ -233,9 +233,9 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const Disti
       int f, e;
       slice_range(a.V, slices, s, f, e);
       Running<E, false> run;
-      for_batches(row, f, e, [&](int c, Chunk<E>(&raw)[4]) {
-        leave_out<kTail>(raw, listed + (c - first), e - c);
-        run.add(raw, c1);
+      for_batches(row, f, e, [&](int c, Chunk<E>(&raw)[4], int left) {
+        leave_out<kTail>(raw, listed + (c - first), left);
+        run.add(raw, left, c1);
       });
       const Stats st = run.warp(c1);
       if (lane == 0) *(ctas == 1 ? &sm.part[s][warp] : cluster.map_shared_rank(&sm.part[s][warp], 0)) = st;
@@ -349,12 +349,12 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_backward_kernel(co
               if (8 * ck + i >= a.V) raw[k].leave_out(i);
         }
         leave_out<kTail>(raw, listed + (c - first), end - c);
-        run.add(raw, c1);
+        run.add(raw, end - c, c1);
       }
     } else {
-      for_batches(row, first, end, [&](int c, Chunk<E>(&raw)[4]) {
-        leave_out<kTail>(raw, listed + (c - first), end - c);
-        run.add(raw, c1);
+      for_batches(row, first, end, [&](int c, Chunk<E>(&raw)[4], int left) {
+        leave_out<kTail>(raw, listed + (c - first), left);
+        run.add(raw, left, c1);
       });
     }
     st = run.warp(c1);

@@ -21,8 +21,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kKeep = 1024;                              // candidates kept from round to round
-constexpr int kCandidates = kKeep + kVocabThreads * 8;   // a round adds at most 8 a thread
+constexpr int kCandidates = 1024;   // room for candidates; few more than k are usual
+constexpr int kKeep = 512;          // when they do not fit: kept from round to round,
+constexpr int kRound = 64;          // and chunks read a round, at most 8 candidates each
+static_assert(kKeep + 8 * kRound <= kCandidates && kMaxList <= kKeep, "a round has to fit");
+static_assert(kMaxSlices * kMaxList <= kCandidates, "the lists of a cluster have to fit");
 
 // Order of the values as unsigned words; -0 counts as 0.
 __device__ __forceinline__ uint32_t order_bits(float v) {
@@ -46,31 +49,44 @@ struct TopSmem {
   float best[kMaxSlices][kVocabThreads];       // a cell's best value, -inf: nothing there
   int chunk[kMaxSlices][kVocabThreads];        // the first chunk that holds it
   uint16_t cell[kMaxSlices * kVocabThreads];   // cells that reach the bound
-  uint64_t key[kCandidates];
+  alignas(16) uint64_t key[kCandidates + 8];
   uint64_t sorted[kMaxList];
   uint64_t lists[kMaxSlices][kMaxList];        // the cluster's lists (first CTA)
   int sizes[kMaxSlices];
 };
 
 // The best min(n, k) of key[0 .. n) in order into out; returns how many.  Keys differ, so a
-// key's rank is the number of larger ones.
-__device__ __forceinline__ int rank_keys(const uint64_t* key, int n, int k, uint64_t* out) {
+// key's rank is the number of larger ones.  key has room for 8 more than n.
+__device__ __forceinline__ int rank_keys(uint64_t* key, int n, int k, uint64_t* out) {
+  if (threadIdx.x < 8) key[n + threadIdx.x] = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += kVocabThreads) {
     const uint64_t mine = key[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += key[j] > mine;
+    for (int j = 0; j < n; j += 8) {
+      ulonglong2 two[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) two[x] = reinterpret_cast<const ulonglong2*>(key + j)[x];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) rank += (two[x].x > mine) + (two[x].y > mine);
+    }
     if (rank < k) out[rank] = mine;
   }
   __syncthreads();
   return min(n, k);
 }
 
-// The k-th largest (value, first chunk) over the threads' best cells; one warp, 8 threads'
-// cells a lane.  0 when fewer than k threads hold anything.
+// A lower bound of the row's k-th best key, from the threads' best cells; one warp, 8 threads' cells
+// a lane.  0 when fewer than k threads hold anything.
+//   The values are searched bit by bit for a bound that at least k threads reach, until hardly
+//   more do: every bit costs the warp a vote, and a few candidates too many cost less.  Where
+//   many share one value (a plateau), the lowest chunks are searched for in the same way.
 __device__ __forceinline__ uint64_t list_bound(const TopSmem& t, int slices, int k) {
   const int lane = threadIdx.x & 31;
   uint32_t val[kVocabWarps];
   uint32_t chunk[kVocabWarps];
+  uint32_t hi = 0, lo = 0xffffffffu;
+  int n = 0;
 #pragma unroll
   for (int w = 0; w < kVocabWarps; ++w) {
     const int i = w * 32 + lane;
@@ -83,29 +99,42 @@ __device__ __forceinline__ uint64_t list_bound(const TopSmem& t, int slices, int
       }
     val[w] = b > -INFINITY ? order_bits(b) : 0u;
     chunk[w] = static_cast<uint32_t>(c);
+    n += val[w] != 0;
+    hi = max(hi, val[w]);
+    lo = val[w] != 0 ? min(lo, val[w]) : lo;
   }
-  // the largest value that k of them reach, bit by bit
-  uint32_t v = 0;
-  for (int bit = 31; bit >= 0; --bit) {
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (n < k) return 0;
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  // v: what n threads reach; bits that all values share are settled
+  int bit = 31 - __clz(hi ^ lo);
+  uint32_t v = bit < 0 ? hi : hi & ~((2u << bit) - 1u);
+  if (bit == 31) v = 0;
+  const int enough = k + (k >> 3) + 4;
+  for (; bit >= 0 && n > enough; --bit) {
     const uint32_t next = v | (1u << bit);
-    int n = 0;
+    int m = 0;
 #pragma unroll
-    for (int w = 0; w < kVocabWarps; ++w) n += val[w] >= next;
-    if (__reduce_add_sync(0xffffffffu, n) >= k) v = next;
+    for (int w = 0; w < kVocabWarps; ++w) m += val[w] >= next;
+    m = __reduce_add_sync(0xffffffffu, m);
+    if (m >= k) {
+      v = next;
+      n = m;
+    }
   }
-  if (v == 0) return 0;
-  // of those equal to it, the (k - larger) lowest chunks: the smallest chunk bound that keeps k
-  int over = 0;
+  if (n <= 2 * enough) return static_cast<uint64_t>(v) << 32;
+  int over = 0;   // v is exact here: every bit was searched
 #pragma unroll
   for (int w = 0; w < kVocabWarps; ++w) over += val[w] > v;
   over = __reduce_add_sync(0xffffffffu, over);
   uint32_t c = 0xfffffu;
-  for (int bit = 19; bit >= 0; --bit) {
-    const uint32_t next = c & ~(1u << bit);
-    int n = 0;
+  for (int b = 19; b >= 0; --b) {
+    const uint32_t next = c & ~(1u << b);
+    int m = 0;
 #pragma unroll
-    for (int w = 0; w < kVocabWarps; ++w) n += val[w] == v && chunk[w] <= next;
-    if (over + __reduce_add_sync(0xffffffffu, n) >= k) c = next;
+    for (int w = 0; w < kVocabWarps; ++w) m += val[w] == v && chunk[w] <= next;
+    if (over + __reduce_add_sync(0xffffffffu, m) >= k) c = next;
   }
   return (static_cast<uint64_t>(v) << 32) | (0xffffffffu - (8 * c + 7));
 }
@@ -134,6 +163,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int64_t t = blockIdx.x / ctas;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (ctas > 1) cluster.barrier_arrive();   // met below, before another CTA's shared memory is written
   const int32_t y = a.targets != nullptr ? a.targets[t] : 0;
   if (a.targets != nullptr && y == a.ignore) {   // the same in every CTA of the cluster
     if (rank == 0) {
@@ -148,13 +178,14 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
           a.top_ids[t * a.k + i] = -1;
         }
     }
+    if (ctas > 1) cluster.barrier_wait();
     return;
   }
   const Row<E> row(static_cast<const E*>(a.logits), a.ld, t, a.V);
   const int slices = vocab_slices(a.V);
   const float c1 = a.scale * kLog2e;
   const int s0 = ctas == 1 ? 0 : rank, s1 = ctas == 1 ? slices : rank + 1;
-  if (ctas > 1) cluster.sync();   // every CTA of the cluster has started: its shared memory may be written
+  const float zy = rank == 0 && tid == 0 && a.targets != nullptr && y >= 0 && y < a.V ? to_f32(row.p[y]) : 0.f;
   Stats(*part)[kVocabWarps] = ctas == 1 ? sm.part : cluster.map_shared_rank(sm.part, 0);
   if (kTop && tid == 0) sm.count = sm.cells = 0;
   for (int s = s0; s < s1; ++s) {
@@ -163,8 +194,8 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
     Running<E, kEntropy> run;
     float best = -INFINITY;
     int at = 0;
-    for_batches(row, first, last, [&](int c, const Chunk<E>(&raw)[4]) {
-      const float cm = run.add(raw, c1);
+    for_batches(row, first, last, [&](int c, const Chunk<E>(&raw)[4], int left) {
+      const float cm = run.add(raw, left, c1);
       if (kTop && cm > best) {
         best = cm;
 #pragma unroll
@@ -173,6 +204,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
       }
     });
     const Stats st = run.warp(c1);
+    if (ctas > 1) cluster.barrier_wait();   // once: one slice a CTA
     if (lane == 0) part[s][warp] = st;
     if (kTop) {
       top.best[s - s0][tid] = best;
@@ -194,44 +226,63 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
         top.cell[atomicAdd(&sm.cells, 1)] = static_cast<uint16_t>(s * kVocabThreads + tid);
     __syncthreads();
     // the cells' chunks, a thread each
-    const int cells = sm.cells;
     int begin, stop;
     slice_range(a.V, slices, s0, begin, stop);   // the first slice is the longest
-    const int per = (stop - begin + kVocabThreads - 1) / kVocabThreads, items = cells * per;
+    const int per = (stop - begin + kVocabThreads - 1) / kVocabThreads, items = sm.cells * per;
     const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
-    for (int base = 0; base < items; base += kVocabThreads) {
-      const int item = base + tid;
-      if (item < items) {
-        const int cell = top.cell[item / per];
-        int first, last;
-        slice_range(a.V, slices, s0 + cell / kVocabThreads, first, last);
-        const int c = first + cell % kVocabThreads + (item % per) * kVocabThreads;
-        if (c < last) {
-          const Chunk<E> raw = row.get(c);
-          if (raw.max() >= floor) {
-            float v[8];
-            unpack8(raw, v);
+    const auto chunk_of = [&](int item) {   // -1: beyond the slice
+      if (item >= items) return -1;
+      const int cell = top.cell[item / per];
+      int first, last;
+      slice_range(a.V, slices, s0 + cell / kVocabThreads, first, last);
+      const int c = first + cell % kVocabThreads + (item % per) * kVocabThreads;
+      return c < last ? c : -1;
+    };
+    const auto collect = [&](int c, const Chunk<E>& raw) {
+      if (c < 0 || !(raw.max() >= floor)) return;
+      float v[8];
+      unpack8(raw, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (v[i] >= floor && v[i] > -INFINITY) {
-                const uint64_t key = order_key(v[i], 8 * c + i);
-                if (key >= bound) top.key[atomicAdd(&sm.count, 1)] = key;
-              }
+      for (int i = 0; i < 8; ++i)
+        if (v[i] >= floor && v[i] > -INFINITY) {
+          const uint64_t key = order_key(v[i], 8 * c + i);
+          if (key >= bound) {
+            const int at = atomicAdd(&sm.count, 1);
+            if (at < kCandidates) top.key[at] = key;
           }
         }
+    };
+    for (int base = tid; base < items; base += 4 * kVocabThreads) {
+      int c[4];
+      Chunk<E> raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = chunk_of(base + i * kVocabThreads);
+        if (c[i] >= 0) raw[i] = row.get(c[i]);
       }
-      if (base + kVocabThreads >= items) break;
-      __syncthreads();
-      const int n = sm.count;
-      __syncthreads();      // everyone has read it before the next round counts on
-      if (n > kKeep) {      // keep the best k, so that the next round has room
-        rank_keys(top.key, n, a.k, top.sorted);
-        if (tid < a.k) top.key[tid] = top.sorted[tid];
-        if (tid == 0) sm.count = a.k;
-        __syncthreads();
-      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) collect(c[i], raw[i]);
     }
     __syncthreads();
+    if (sm.count > kCandidates) {   // too many (most of the large values lie in few cells): again, in rounds
+      __syncthreads();
+      if (tid == 0) sm.count = 0;
+      for (int base = 0; base < items; base += kRound) {
+        __syncthreads();
+        const int c = tid < kRound ? chunk_of(base + tid) : -1;
+        Chunk<E> raw;
+        if (c >= 0) raw = row.get(c);
+        collect(c, raw);
+        __syncthreads();
+        const int n = sm.count;
+        if (n > kKeep) {            // keep the best k, so that the next round has room
+          rank_keys(top.key, n, a.k, top.sorted);
+          if (tid < a.k) top.key[tid] = top.sorted[tid];
+          if (tid == 0) sm.count = a.k;
+        }
+      }
+      __syncthreads();
+    }
     found = rank_keys(top.key, sm.count, a.k, top.sorted);
     if (ctas > 1) {   // push the list into the first CTA
       TopSmem* lead = cluster.map_shared_rank(&top, 0);
@@ -255,7 +306,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
         set_status(a.status, kStatusBadInput);
         lp = NAN;
       } else if (!none) {
-        lp = fmaf(to_f32(row.p[y]) - st.m, a.scale, -ln_s);
+        lp = fmaf(zy - st.m, a.scale, -ln_s);
       }
       a.logprob[t] = lp;
     }
@@ -266,39 +317,30 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
     }
   }
   if (kTop) {
-    const uint64_t* list = top.sorted;
     if (ctas > 1) {
-      // merge the sorted lists: a key's rank is its place in its own list plus the larger
-      // keys of every other
+      // Merge the sorted lists.  If every list has k / ctas keys, k of them reach the smallest of
+      // those lists' (k / ctas)-th keys, so few others remain to be ranked.
+      const int share = (a.k + ctas - 1) / ctas;
+      uint64_t least = ~uint64_t(0);
+      for (int l = 0; l < ctas; ++l) {
+        const uint64_t key = top.sizes[l] < share ? 0 : top.lists[l][share - 1];
+        least = key < least ? key : least;
+      }
+      if (tid == 0) sm.count = 0;
+      __syncthreads();
       for (int i = tid; i < ctas * kMaxList; i += kVocabThreads) {
         const int l = i / kMaxList, p = i % kMaxList;
-        if (p >= top.sizes[l]) continue;
-        const uint64_t mine = top.lists[l][p];
-        int r = p;
-        for (int o = 0; o < ctas && r < a.k; ++o) {
-          if (o == l) continue;
-          int lo = 0, hi = top.sizes[o];
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (top.lists[o][mid] > mine) lo = mid + 1;
-            else hi = mid;
-          }
-          r += lo;
-        }
-        if (r < a.k) top.key[r] = mine;
+        if (p < top.sizes[l] && top.lists[l][p] >= least) top.key[atomicAdd(&sm.count, 1)] = top.lists[l][p];
       }
-      found = 0;
-      for (int l = 0; l < ctas; ++l) found += top.sizes[l];
-      found = min(found, a.k);
-      list = top.key;
       __syncthreads();
+      found = rank_keys(top.key, sm.count, a.k, top.sorted);
     }
     for (int i = tid; i < a.k; i += kVocabThreads) {
       float lp = -INFINITY;
       int32_t id = -1;
       if (i < found) {
-        lp = fmaf(order_value(static_cast<uint32_t>(list[i] >> 32)) - st.m, a.scale, -ln_s);
-        id = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(list[i]));
+        lp = fmaf(order_value(static_cast<uint32_t>(top.sorted[i] >> 32)) - st.m, a.scale, -ln_s);
+        id = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(top.sorted[i]));
       }
       a.top_logprob[t * a.k + i] = lp;
       a.top_ids[t * a.k + i] = id;

@@ -261,8 +261,9 @@ template <typename E, bool kEntropy>
 struct Running {
   float m = -FLT_MAX;
   F2 s = 0, u = 0;
-  // Four chunks; returns their maximum.
-  __device__ __forceinline__ float add(const Chunk<E> (&raw)[4], float c1) {
+  // Four chunks, of which `left` counts 256 for each that is not the filling beyond the slice
+  // (-inf, which adds 0 and is skipped); returns their maximum.
+  __device__ __forceinline__ float add(const Chunk<E> (&raw)[4], int left, float c1) {
     float cm;
     if constexpr (sizeof(E) == 4) {
       cm = fmaxf(fmaxf(raw[0].max(), raw[1].max()), fmaxf(raw[2].max(), raw[3].max()));
@@ -282,6 +283,7 @@ struct Running {
     const F2 minus = pack2(-m, -m), cc = pack2(c1, c1);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      if (k > 0 && k * kVocabThreads >= left) break;
       F2 e[4];
       F2 x = 0;
 #pragma unroll
@@ -340,8 +342,8 @@ __device__ __forceinline__ void slice_range(int V, int slices, int slice, int& f
   last = min(chunks, first + per);
 }
 
-// Calls f(c, raw) for this thread's batches of [first, last), in order: raw[i] is chunk
-// c + 256 i, -inf beyond the slice.  The four loads of a batch are in flight together.
+// Calls f(c, raw, last - c) for this thread's batches of [first, last), in order: raw[i] is
+// chunk c + 256 i, -inf beyond the slice.  The four loads of a batch are in flight together.
 template <typename E, typename F>
 __device__ __forceinline__ void for_batches(const Row<E>& row, int first, int last, F&& f) {
   for (int c = first + threadIdx.x; c < last; c += 4 * kVocabThreads) {
@@ -355,7 +357,7 @@ __device__ __forceinline__ void for_batches(const Row<E>& row, int first, int la
       for (int i = 0; i < 4; ++i)
         raw[i] = c + i * kVocabThreads < last ? row.get(c + i * kVocabThreads) : Chunk<E>::none();
     }
-    f(c, raw);
+    f(c, raw, last - c);
   }
 }
 

@@ -160,6 +160,11 @@ def test_candidates_beyond_one_round(cuda_lib):
     zz[:, hot, :] += 40.0
     check_forward(cuda_lib, store(z, "f32"), np.array([0, V - 1], np.int32), 1.0, 128)
     check_forward(cuda_lib, store(z, "bf16"), np.array([0, V - 1], np.int32), 1.0, 128)
+    # the same with one CTA a row
+    V, T = 40000, 640
+    z = rng.normal(0.0, 1.0, (T, V))
+    z.reshape(T, V // 8, 8)[:, (np.arange(V // 8) % 256) < 100, :] += 40.0
+    check_forward(cuda_lib, store(z, "f32"), np.zeros(T, np.int32), 1.0, 128)
 
 
 def test_not_a_number_rows(cuda_lib):
