@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
         best = cm;
 #pragma unroll
         for (int i = 3; i >= 0; --i)   // the first of the four that holds it
-          if (raw[i].max() == cm) at = c + i * kVocabThreads;
+          if (i * kVocabThreads < left && raw[i].max() == cm) at = c + i * kVocabThreads;
       }
     });
     const Stats st = run.warp(c1);
@@ -230,26 +230,32 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
     slice_range(a.V, slices, s0, begin, stop);   // the first slice is the longest
     const int per = (stop - begin + kVocabThreads - 1) / kVocabThreads, items = sm.cells * per;
     const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
-    const auto chunk_of = [&](int item) {   // -1: beyond the slice
+    const unsigned inverse = 0xffffffffu / per + 1;   // item / per by a multiplication: item * per < 2^32
+    const auto chunk_of = [&](int item) {             // -1: beyond the slice
       if (item >= items) return -1;
-      const int cell = top.cell[item / per];
+      const int q = per == 1 ? item : static_cast<int>(__umulhi(item, inverse));
+      const int cell = top.cell[q];
       int first, last;
       slice_range(a.V, slices, s0 + cell / kVocabThreads, first, last);
-      const int c = first + cell % kVocabThreads + (item % per) * kVocabThreads;
+      const int c = first + cell % kVocabThreads + (item - q * per) * kVocabThreads;
       return c < last ? c : -1;
     };
+    // the elements that reach the bound, one count a chunk
     const auto collect = [&](int c, const Chunk<E>& raw) {
       if (c < 0 || !(raw.max() >= floor)) return;
       float v[8];
       unpack8(raw, v);
+      unsigned hit = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (v[i] >= floor && v[i] > -INFINITY) {
-          const uint64_t key = order_key(v[i], 8 * c + i);
-          if (key >= bound) {
-            const int at = atomicAdd(&sm.count, 1);
-            if (at < kCandidates) top.key[at] = key;
-          }
+        if (v[i] >= floor && v[i] > -INFINITY && order_key(v[i], 8 * c + i) >= bound) hit |= 1u << i;
+      if (hit == 0) return;
+      int at = atomicAdd(&sm.count, __popc(hit));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (hit >> i & 1) {
+          if (at < kCandidates) top.key[at] = order_key(v[i], 8 * c + i);
+          ++at;
         }
     };
     for (int base = tid; base < items; base += 4 * kVocabThreads) {
@@ -414,12 +420,12 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(
   const float A = -a.scale * (g + (kEntropy ? h * a.entropy[t] : 0.f)), B = -a.scale * h * kLn2;
   const F2 cc = pack2(c1, c1), ll = pack2(l1, l1), aa = pack2(A, A), bb = pack2(B, B);
   const float zy = a.scale * g;
-  map_row<E, 4>(z, a.V, out, lo, hi, [&](int e0, float(&v)[8]) {
+  map_row<E, 4>(z, a.V, out, lo, hi, [&](int e0, const Chunk<E>& z8, float(&v)[8]) {
     const unsigned at = y - e0;
     const float zt = at < 8 ? to_f32(z[min(y, a.V - 1)]) : 0.f;   // before it may be overwritten
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 lt = unpack2(fma2(pack2(v[2 * i], v[2 * i + 1]), cc, ll));
+      const float2 lt = unpack2(fma2(z8.pair(i), cc, ll));
       const F2 p = pack2(ex2(lt.x), ex2(lt.y));
       const F2 f = kEntropy ? fma2(bb, pack2(fmaxf(lt.x, -1e30f), fmaxf(lt.y, -1e30f)), aa) : aa;
       const float2 d = unpack2(mul2(p, f));

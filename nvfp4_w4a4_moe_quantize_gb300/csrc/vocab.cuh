@@ -14,6 +14,7 @@
 #include <cfloat>
 #include <cooperative_groups.h>
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -87,6 +88,11 @@ struct Packed<__nv_bfloat16> {
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
+  static __device__ __forceinline__ float minus(uint16_t h, float m) {   // h - m, h widened on the way
+    float r;
+    asm("sub.rn.f32.bf16 %0, %1, %2;" : "=f"(r) : "h"(h), "f"(m));
+    return r;
+  }
   static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 };
@@ -96,6 +102,11 @@ struct Packed<__half> {
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float minus(uint16_t h, float m) {
+    float r;
+    asm("sub.rn.f32.f16 %0, %1, %2;" : "=f"(r) : "h"(h), "f"(m));
     return r;
   }
   static __device__ __forceinline__ float low(uint32_t w) { return __low2float(*reinterpret_cast<const __half2*>(&w)); }
@@ -120,6 +131,11 @@ struct Chunk {
   __device__ __forceinline__ F2 pair(int i) const {   // elements 2i, 2i + 1
     if constexpr (sizeof(E) == 4) return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     else return pack2(Packed<E>::low(w[i]), Packed<E>::high(w[i]));
+  }
+  __device__ __forceinline__ F2 pair_minus(int i, float m) const {   // the pair less m, rounded once
+    if constexpr (sizeof(E) == 4) return add2(pair(i), pack2(-m, -m));
+    else return pack2(Packed<E>::minus(static_cast<uint16_t>(w[i] & 0xffffu), m),
+                      Packed<E>::minus(static_cast<uint16_t>(w[i] >> 16), m));
   }
   __device__ __forceinline__ float max() const {
     if constexpr (sizeof(E) == 4) {
@@ -261,15 +277,19 @@ template <typename E, bool kEntropy>
 struct Running {
   float m = -FLT_MAX;
   F2 s = 0, u = 0;
-  // Four chunks, of which `left` counts 256 for each that is not the filling beyond the slice
-  // (-inf, which adds 0 and is skipped); returns their maximum.
+  // Four chunks, 256 apart; only those of them that begin fewer than `left` chunks on count.
+  // Returns their maximum.
   __device__ __forceinline__ float add(const Chunk<E> (&raw)[4], int left, float c1) {
     float cm;
     if constexpr (sizeof(E) == 4) {
-      cm = fmaxf(fmaxf(raw[0].max(), raw[1].max()), fmaxf(raw[2].max(), raw[3].max()));
+      cm = raw[0].max();
+#pragma unroll
+      for (int k = 1; k < 4; ++k) cm = fmaxf(cm, k * kVocabThreads < left ? raw[k].max() : -INFINITY);
     } else {
-      const uint32_t w = Packed<E>::max(Packed<E>::max(raw[0].max_word(), raw[1].max_word()),
-                                        Packed<E>::max(raw[2].max_word(), raw[3].max_word()));
+      uint32_t w = raw[0].max_word();
+#pragma unroll
+      for (int k = 1; k < 4; ++k)
+        w = Packed<E>::max(w, k * kVocabThreads < left ? raw[k].max_word() : Packed<E>::kNegInf);
       cm = fmaxf(Packed<E>::low(w), Packed<E>::high(w));
     }
     if (cm > m) {
@@ -280,7 +300,7 @@ struct Running {
       s = mul2(rr, s);
       m = cm;
     }
-    const F2 minus = pack2(-m, -m), cc = pack2(c1, c1);
+    const F2 cc = pack2(c1, c1);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (k > 0 && k * kVocabThreads >= left) break;
@@ -288,7 +308,7 @@ struct Running {
       F2 x = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 t = unpack2(mul2(add2(raw[k].pair(i), minus), cc));
+        const float2 t = unpack2(mul2(raw[k].pair_minus(i, m), cc));
         e[i] = pack2(ex2(t.x), ex2(t.y));
         if (kEntropy) {   // an excluded token adds 0, not 0 * inf
           const F2 tt = pack2(fmaxf(t.x, -1000.f), fmaxf(t.y, -1000.f));
@@ -307,9 +327,24 @@ struct Running {
     return warp_join(a, c1);
   }
   static __device__ __forceinline__ Stats warp_join(Stats a, float c1) {
+    rebase<kEntropy>(a, warp_top(a.m), c1);
+    return warp_add(a);
+  }
+  // Of two sets a lane.
+  static __device__ __forceinline__ Stats join_two(Stats a, Stats b, float c1) {
+    const float m = warp_top(fmaxf(a.m, b.m));
+    rebase<kEntropy>(a, m, c1);
+    rebase<kEntropy>(b, m, c1);
+    a.s += b.s;
+    a.u += b.u;
+    return warp_add(a);
+  }
+  static __device__ __forceinline__ float warp_top(float m) {
     float top;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(a.m));
-    rebase<kEntropy>(a, top, c1);
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+    return top;
+  }
+  static __device__ __forceinline__ Stats warp_add(Stats a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
@@ -322,40 +357,31 @@ struct Running {
   static __device__ __forceinline__ Stats join_slices(const Stats (*part)[kVocabWarps], int slices, float c1) {
     const int lane = threadIdx.x & 31;
     const Stats* flat = &part[0][0];
-    Stats a = lane < slices * kVocabWarps ? flat[lane] : empty_stats();
-    if (lane + 32 < slices * kVocabWarps) {
-      Stats b = flat[lane + 32];
-      const float m = fmaxf(a.m, b.m);
-      rebase<kEntropy>(a, m, c1);
-      rebase<kEntropy>(b, m, c1);
-      a.s += b.s;
-      a.u += b.u;
-    }
-    return warp_join(a, c1);
+    return join_two(lane < slices * kVocabWarps ? flat[lane] : empty_stats(),
+                    lane + 32 < slices * kVocabWarps ? flat[lane + 32] : empty_stats(), c1);
   }
 };
 
 // The chunks [first, last) of a slice.
 __device__ __forceinline__ void slice_range(int V, int slices, int slice, int& first, int& last) {
-  const int chunks = (V + 7) >> 3, per = (chunks + slices - 1) / slices;
+  const int chunks = (V + 7) >> 3, per = (chunks + slices - 1) >> (__ffs(slices) - 1);   // 1, 2, 4 or 8 slices
   first = min(chunks, slice * per);
   last = min(chunks, first + per);
 }
 
 // Calls f(c, raw, last - c) for this thread's batches of [first, last), in order: raw[i] is
-// chunk c + 256 i, -inf beyond the slice.  The four loads of a batch are in flight together.
+// chunk c + 256 i, and where that lies beyond the slice some chunk of it.  The four loads of a
+// batch are in flight together.
 template <typename E, typename F>
 __device__ __forceinline__ void for_batches(const Row<E>& row, int first, int last, F&& f) {
   for (int c = first + threadIdx.x; c < last; c += 4 * kVocabThreads) {
-    const int end = c + 3 * kVocabThreads;
     Chunk<E> raw[4];
-    if (end < last && row.inner(c) && row.inner(end)) {
+    if (row.inner(c) && row.inner(last - 1)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = row.load_inner(c + i * kVocabThreads);
+      for (int i = 0; i < 4; ++i) raw[i] = row.load_inner(min(c + i * kVocabThreads, last - 1));
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        raw[i] = c + i * kVocabThreads < last ? row.get(c + i * kVocabThreads) : Chunk<E>::none();
+      for (int i = 0; i < 4; ++i) raw[i] = row.get(min(c + i * kVocabThreads, last - 1));
     }
     f(c, raw, last - c);
   }
@@ -390,41 +416,41 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// out[e] = f(e, value(e)) for e in [lo, hi) of a row, by the CTA's threads: eight(e) gives the
-// chunk of [e, e + 8), one(e) a single element.  The chunks are cut on the output's 16-byte
-// boundaries, so that stores are whole; kAhead of them are read before the first is
-// written.
+// out[e] = f(e, value(e)) for e in [lo, hi) of a row, by the first 256 threads: eight(e) gives the
+// chunk of [e, e + 8), one(e) a single element, f(e, chunk, v) the eight results.  The chunks are
+// cut on the output's 16-byte boundaries, so that stores are whole; kAhead of them are read
+// before the first is written.
 template <typename E, int kAhead, typename Eight, typename One, typename F>
 __device__ __forceinline__ void map_chunks(E* out, int lo, int hi, Eight&& eight, One&& one, F&& f) {
+  constexpr int kStep = 8 * kVocabThreads;
   const int tid = threadIdx.x;
   const uint32_t so = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out + lo)) & 15u;
   const int head = min(hi - lo, static_cast<int>((16u - so) & 15u) / static_cast<int>(sizeof(E)));
-  const int body = (hi - lo - head) >> 3;
-  const int base = lo + head, tail = base + 8 * body;
-  for (int c = tid; c < body; c += kAhead * kVocabThreads) {
-    Chunk<E> raw[kAhead];
+  const int base = lo + head, tail = base + ((hi - base) & ~7);
+  const auto some = [&](int e, auto n) {
+    constexpr int N = decltype(n)::value;
+    Chunk<E> raw[N];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (c + k * kVocabThreads < body) raw[k] = eight(base + 8 * (c + k * kVocabThreads));
+    for (int k = 0; k < N; ++k) raw[k] = eight(e + k * kStep);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (c + k * kVocabThreads < body) {
-        const int e = base + 8 * (c + k * kVocabThreads);
-        float v[8];
-        unpack8(raw[k], v);
-        f(e, v);
-        store8(out + e, v);
-      }
-  }
+    for (int k = 0; k < N; ++k) {
+      float v[8];
+      f(e + k * kStep, raw[k], v);
+      store8(out + e + k * kStep, v);
+    }
+  };
+  int e = base + 8 * tid;
+  for (; e + (kAhead - 1) * kStep < tail; e += kAhead * kStep) some(e, std::integral_constant<int, kAhead>());
+  if (kAhead > 1)
+    for (; e < tail; e += kStep) some(e, std::integral_constant<int, 1>());
   // the ends, at most 7 elements each
   if (tid < head || (tid >= 8 && tid - 8 < hi - tail)) {
-    const int e = tid < head ? lo + tid : tail + tid - 8;
+    const int at = tid < head ? lo + tid : tail + tid - 8;
+    Chunk<E> c = Chunk<E>::none();
+    c.put(0, one(at));
     float v[8];
-    v[0] = to_f32(one(e));
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v[i] = -INFINITY;
-    f(e, v);
-    store_one(out + e, v[0]);
+    f(at, c, v);
+    store_one(out + at, v[0]);
   }
 }
 

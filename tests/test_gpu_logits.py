@@ -396,6 +396,27 @@ def test_distill_long_rows(cuda_lib, tail, dtype, V):
     assert torch.equal(zt, keep)
 
 
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,T,V", [("bf16", 2500, 8200), ("f16", 1900, 20003), ("f32", 700, 33001), ("f32", 2000, 16400)])
+def test_distill_many_rows(cuda_lib, tail, dtype, T, V):
+    """Several rows a cluster, several slices a CTA: every row equals the same row alone."""
+    z, rng = logits(64, V, V + T)
+    ids, val = teacher(64, V, 37, rng, short=True)
+    pick = torch.from_numpy(rng.integers(0, 64, T)).cuda()
+    zt, it, vt = store(z, dtype), torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda()
+    w = torch.ones(T, device="cuda")
+    few_loss, few = cuda_lib.distill_topk_backward(zt, it, vt, w[:64], tail)
+    check_distill(cuda_lib, zt, ids, val, tail)
+    many = torch.full((T, V + 5), -1.0, dtype=DT[dtype], device="cuda")
+    many[:, :V] = zt[pick]
+    for x in (many[:, :V], many[:, :V].contiguous()):
+        loss, d = cuda_lib.distill_topk_backward(x, it[pick], vt[pick], w, tail)
+        assert torch.equal(loss, few_loss[pick]) and torch.equal(d, few[pick])
+    cuda_lib.distill_topk_backward(many[:, :V], it[pick], vt[pick], w, tail, out=many[:, :V])
+    assert torch.equal(many[:, :V], few[pick]) and (many[:, V:] == -1).all()
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
 def test_distill_student_without_tokens(cuda_lib):
     z = np.full((2, 5000), -np.inf)
     z[1, 7] = 1.0
