@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const Disti
   const Row<E> row(static_cast<const E*>(a.logits), a.ld, t, a.V);
   const int slices = vocab_slices(a.V);
   const float c1 = a.scale * kLog2e;
-  const int s0 = ctas == 1 ? 0 : rank, s1 = ctas == 1 ? slices : rank + 1;
+  const int s0 = rank * (slices / ctas), s1 = s0 + slices / ctas;
   int first, end, unused;
   slice_range(a.V, slices, s0, first, unused);
   slice_range(a.V, slices, s1 - 1, unused, end);
@@ -653,41 +653,83 @@ template <typename E, bool kTail>
 cudaError_t forward(const DistillArgs& a, int64_t T, cudaStream_t s) {
   static std::atomic<bool> set[64];
   const int slices = vocab_slices(a.V), chunks = (a.V + 7) / 8;
-  const int ctas = T < 4 * num_sms() ? slices : 1;
+  int ctas = 1;
+  while (ctas < slices && T * ctas < 4 * num_sms()) ctas *= 2;   // as the log probabilities
   const int words = slices / ctas * Marks::slice_words((chunks + slices - 1) / slices);
   return launch(distill_topk_kernel<E, kTail>, set, kMaxSmem, T * ctas, ctas, kVocabThreads, 4 * words, s, a);
 }
 
-constexpr int kStageAim = 36 * 1024;     // two of them, three CTAs an SM
+constexpr int kStageAim = 66 * 1024;     // shared memory of a CTA; three CTAs fit on an SM
+
+// Clusters of `cluster` CTAs that the GPU holds at a time (some SMs stay free where a cluster does not fit
+// into what is left of a GPC: 51 clusters of 8 on 152 SMs of 3 CTAs).  The answer of the last
+// configuration is kept.
+template <typename... Params>
+int resident_clusters(void (*kernel)(Params...), std::atomic<uint64_t>* memo, int cluster, int threads, int smem) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool kept = dev >= 0 && dev < 64;
+  const uint64_t key = (static_cast<uint64_t>(smem) << 32) | (static_cast<uint64_t>(cluster) << 24);
+  const uint64_t last = kept ? memo[dev].load(std::memory_order_relaxed) : 0;
+  if ((last & 0xffffffffff000000ull) == key && (last & 0xffffffull) != 0) return static_cast<int>(last & 0xffffffull);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster * 4096));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+  if (kept) memo[dev].store(key | static_cast<uint64_t>(n), std::memory_order_relaxed);
+  return n;
+}
 
 template <typename E, bool kTail>
 cudaError_t backward(const DistillArgs& a, int64_t T, cudaStream_t s) {
   static std::atomic<bool> set[2][64];
+  static std::atomic<uint64_t> memo[64];
   const int slices = vocab_slices(a.V), per = ((a.V + 7) / 8 + slices - 1) / slices;
-  // slices a CTA: one while there are few rows; else as many as a stage of the size aimed at takes
-  int mine = 1;
-  const auto stage_bytes = [&](int n) {   // 16 spare bytes at both ends, 16 for the slice's offset
+  const auto stage_bytes = [&](int n) {   // 16 spare bytes at both ends, 16 for the part's offset
     return static_cast<int64_t>(n) * per * 8 * sizeof(E) + 48;
   };
-  while (T >= 2 * num_sms() && 2 * mine <= slices && stage_bytes(2 * mine) <= kStageAim) mine *= 2;
+  // Slices a CTA: as many as a stage of the size aimed at takes, so that the work of a row that does not
+  // grow with V is shared by few CTAs, while there are rows enough to fill the GPU.
+  // (2048 x 131072 BF16, two slices a CTA 197 us, one 279 us, four 292 us.)
+  int mine = 1;
+  while (2 * mine <= slices && stage_bytes(2 * mine) <= kStageAim && T * (slices / (2 * mine)) >= 3 * num_sms())
+    mine *= 2;
   const int ctas = slices / mine;
   BackwardPlan plan{};
   plan.T = T;
   plan.stage_bytes = static_cast<int>(stage_bytes(mine));
-  // rows a cluster: several, while that leaves a dozen CTAs an SM
-  const int64_t rows = T * ctas / (12 * num_sms());
-  plan.rows = static_cast<int>(rows < 1 ? 1 : rows > 8 ? 8 : rows);
-  plan.stages = plan.rows > 1 && stage_bytes(mine) <= kStageAim ? 2 : 1;
-  const int64_t clusters = (T + plan.rows - 1) / plan.rows;
-  const int64_t smem = plan.stages * stage_bytes(mine);
-  if (smem <= kMaxSmem)
-    return launch(distill_topk_backward_kernel<E, kTail, true>, set[0], kMaxSmem, clusters * ctas, ctas,
-                  kBackwardThreads, static_cast<int>(smem), s, a, plan);
+  plan.stages = 2 * stage_bytes(mine) <= kStageAim ? 2 : 1;
+  int64_t smem = plan.stages * stage_bytes(mine);
+  if (smem <= kMaxSmem) {
+    // Rows a cluster: all of them in one wave if that takes at most eight (1000 x 50021 float16: 5 rows
+    // 61 us, 2 rows 66 us), else two, which the hardware balances (eight where the next row's
+    // slices arrive in a second stage).
+    const auto kernel = distill_topk_backward_kernel<E, kTail, true>;
+    cudaError_t e = set_smem_attr_once(set[0], reinterpret_cast<const void*>(kernel), kMaxSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t resident = resident_clusters(kernel, memo, ctas, kBackwardThreads, static_cast<int>(smem));
+    plan.rows = static_cast<int>(T <= 8 * resident ? (T + resident - 1) / resident : plan.stages == 2 ? 8 : 2);
+    if (plan.rows == 1) {
+      plan.stages = 1;
+      smem = stage_bytes(mine);
+    }
+    return launch(kernel, set[0], kMaxSmem, (T + plan.rows - 1) / plan.rows * ctas, ctas, kBackwardThreads,
+                  static_cast<int>(smem), s, a, plan);
+  }
+  plan.rows = 1;
   plan.stages = 1;
   plan.stage_bytes = 0;
   const int marks = 2 * 4 * mine * Marks::slice_words(per);   // of two rows
-  return launch(distill_topk_backward_kernel<E, kTail, false>, set[1], kMaxSmem, clusters * ctas, ctas,
-                kBackwardThreads, marks, s, a, plan);
+  return launch(distill_topk_backward_kernel<E, kTail, false>, set[1], kMaxSmem, T * ctas, ctas, kBackwardThreads, marks,
+                s, a, plan);
 }
 
 template <typename E>

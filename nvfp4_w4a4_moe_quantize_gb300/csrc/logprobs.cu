@@ -152,10 +152,9 @@ struct LogprobArgs {
   int* status;
 };
 
-// One row a cluster; a cluster is one CTA that runs the row's slices in turn, or one CTA a
-// slice.
+// One row a cluster of 1, 2, 4 or 8 CTAs; a CTA runs its part of the row's slices in turn.
 template <typename E, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kVocabThreads, sizeof(E) == 4 ? 4 : kTop ? 5 : 6) token_logprobs_kernel(const LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ LogprobSmem sm;
   TopSmem& top = *reinterpret_cast<TopSmem*>(dyn);
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
   const Row<E> row(static_cast<const E*>(a.logits), a.ld, t, a.V);
   const int slices = vocab_slices(a.V);
   const float c1 = a.scale * kLog2e;
-  const int s0 = ctas == 1 ? 0 : rank, s1 = ctas == 1 ? slices : rank + 1;
+  const int mine = slices / ctas, s0 = rank * mine, s1 = s0 + mine;
   const float zy = rank == 0 && tid == 0 && a.targets != nullptr && y >= 0 && y < a.V ? to_f32(row.p[y]) : 0.f;
   Stats(*part)[kVocabWarps] = ctas == 1 ? sm.part : cluster.map_shared_rank(sm.part, 0);
   if (kTop && tid == 0) sm.count = sm.cells = 0;
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
       }
     });
     const Stats st = run.warp(c1);
-    if (ctas > 1) cluster.barrier_wait();   // once: one slice a CTA
+    if (ctas > 1 && s == s0) cluster.barrier_wait();
     if (lane == 0) part[s][warp] = st;
     if (kTop) {
       top.best[s - s0][tid] = best;
@@ -213,7 +212,6 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
   }
   int found = 0;
   if (kTop) {
-    const int mine = s1 - s0;
     __syncthreads();
     if (warp == 0) {
       const uint64_t b = list_bound(top, mine, a.k);
@@ -240,7 +238,8 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
       const int c = first + cell % kVocabThreads + (item - q * per) * kVocabThreads;
       return c < last ? c : -1;
     };
-    // the elements that reach the bound, one count a chunk
+    // the elements that reach the bound, one count a chunk; its lower half matters on a plateau alone
+    const bool plateau = static_cast<uint32_t>(bound) != 0;
     const auto collect = [&](int c, const Chunk<E>& raw) {
       if (c < 0 || !(raw.max() >= floor)) return;
       float v[8];
@@ -248,15 +247,22 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_kernel(const Log
       unsigned hit = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (v[i] >= floor && v[i] > -INFINITY && order_key(v[i], 8 * c + i) >= bound) hit |= 1u << i;
+        if (v[i] >= floor && v[i] > -INFINITY) hit |= 1u << i;
+      if (plateau)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (order_key(v[i], 8 * c + i) < bound) hit &= ~(1u << i);
       if (hit == 0) return;
       int at = atomicAdd(&sm.count, __popc(hit));
+      do {   // mostly one
+        const int i = __ffs(hit) - 1;
+        hit &= hit - 1;
+        float x = v[0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (hit >> i & 1) {
-          if (at < kCandidates) top.key[at] = order_key(v[i], 8 * c + i);
-          ++at;
-        }
+        for (int j = 1; j < 8; ++j) x = j == i ? v[j] : x;
+        if (at < kCandidates) top.key[at] = order_key(x, 8 * c + i);
+        ++at;
+      } while (hit != 0);
     };
     for (int base = tid; base < items; base += 4 * kVocabThreads) {
       int c[4];
@@ -358,8 +364,9 @@ template <typename E, bool kEntropy, bool kTop>
 cudaError_t launch_forward(const LogprobArgs& a, int64_t T, cudaStream_t s) {
   static std::atomic<bool> smem_set[64];
   const int slices = vocab_slices(a.V);
-  // few rows: a row's slices side by side in a cluster, until the rows alone fill the GPU
-  const int ctas = T < 4 * num_sms() ? slices : 1;
+  // few rows: a row's slices in a cluster, over as many CTAs as it takes to fill the GPU
+  int ctas = 1;
+  while (ctas < slices && T * ctas < 4 * num_sms()) ctas *= 2;
   const int smem = kTop ? static_cast<int>(sizeof(TopSmem)) : 0;
   auto kernel = token_logprobs_kernel<E, kEntropy, kTop>;
   if (smem > 0) {
