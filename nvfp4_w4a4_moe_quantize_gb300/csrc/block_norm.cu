@@ -4,13 +4,18 @@
 //   n = x rstd(x) w                                    rstd(x) = 1 / sqrt(mean(x^2) + eps)
 //   r = a x + gate (y rstd(y) w);   n' = r rstd(r) w'  (r as it is stored)
 //
-// A row stays in registers between its reductions: x and y are read once, r and n' written
-// once.  A row belongs to a group of G threads, G a function of H alone, two chunks of 8
-// elements a thread; sums run in that fixed order, so a row's bits do not depend on the batch.
+// A row stays on the SM between its reductions: x and y are read once, r and n' written
+// once.  A row belongs to a group of G threads, G a function of H alone, 16 elements a
+// thread; sums run in an order that H fixes, so a row's bits do not depend on the batch.
+// What bounds these kernels is HBM, if enough bytes are on their way: a group's next rows arrive in
+// shared memory by bulk copies while it works on one, and the weights stay there.  Rows
+// that are not 16-byte aligned are read from global memory element by element.
 // Backward: a CTA takes a range of rows of one gate row and keeps the column sums of the
 // weights' and gate's gradients in registers; the ranges' sums are added by a second kernel
 // in a fixed order (no atomics).
 #include "launch.h"
+#include "ptx.cuh"
+#include "status.cuh"
 #include "vocab.cuh"
 
 namespace nvfp4 {
@@ -26,25 +31,46 @@ inline int group_threads(int64_t H) {
   return g;
 }
 
-// 8 values as pairs: elements [e, e + 8) of a row, zero beyond it.  kVec: the rows are 16-byte
-// aligned and whole chunks; else element by element.
+// 8 values as pairs.
 struct Eight {
   F2 p[4];
 };
+
+// The elements of a thread's chunk: first, first + step, ... (8 of them, below H).  Where H is a
+// multiple of 8 they are neighbours, else a group apart, so that single reads coalesce.
+struct Places {
+  int first, step, H;
+};
+__device__ __forceinline__ Places places(int tid, int j, int G, int H) {
+  return H % 8 == 0 ? Places{8 * (tid + j * G), 1, H} : Places{tid + 8 * j * G, G, H};
+}
+
+// kVec: rows are 16-byte aligned and whole chunks of neighbours.
 template <typename E, bool kVec>
-__device__ __forceinline__ Chunk<E> load_chunk(const E* row, int e, int H) {
+__device__ __forceinline__ Chunk<E> load_chunk(const E* row, const Places& at) {
   Chunk<E> c;
 #pragma unroll
   for (int i = 0; i < 4 * Chunk<E>::kQ; ++i) c.w[i] = 0;
   if (kVec) {
-    if (e < H)
+    if (at.first < at.H)
 #pragma unroll
-      for (int i = 0; i < Chunk<E>::kQ; ++i) c.set(i, load16(reinterpret_cast<const char*>(row + e) + 16 * i));
+      for (int i = 0; i < Chunk<E>::kQ; ++i) c.set(i, load16(reinterpret_cast<const char*>(row + at.first) + 16 * i));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e + i < H) c.put(i, row[e + i]);
+      if (at.first + i * at.step < at.H) c.put(i, row[at.first + i * at.step]);
   }
+  return c;
+}
+template <typename E>
+__device__ __forceinline__ Chunk<E> stage_chunk(const char* row, const Places& at) {
+  Chunk<E> c;
+#pragma unroll
+  for (int i = 0; i < 4 * Chunk<E>::kQ; ++i) c.w[i] = 0;
+  if (at.first < at.H)
+#pragma unroll
+    for (int i = 0; i < Chunk<E>::kQ; ++i)
+      c.set(i, reinterpret_cast<const uint4*>(row + at.first * sizeof(E))[i]);
   return c;
 }
 template <typename E>
@@ -55,7 +81,7 @@ __device__ __forceinline__ Eight pairs(const Chunk<E>& c) {
   return v;
 }
 template <typename E, bool kVec>
-__device__ __forceinline__ void store_chunk(E* row, int e, int H, const Eight& v) {
+__device__ __forceinline__ void store_chunk(E* row, const Places& at, const Eight& v) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -64,22 +90,35 @@ __device__ __forceinline__ void store_chunk(E* row, int e, int H, const Eight& v
     f[2 * i + 1] = x.y;
   }
   if (kVec) {
-    if (e < H) store8(row + e, f);
+    if (at.first < at.H) store8(row + at.first, f);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e + i < H) store_one(row + e + i, f[i]);
+      if (at.first + i * at.step < at.H) store_one(row + at.first + i * at.step, f[i]);
   }
 }
 // A float32 parameter (a gate row), likewise.
 template <bool kVec>
-__device__ __forceinline__ Eight load_param(const float* row, int e, int H) {
-  return pairs(load_chunk<float, kVec>(row, e, H));
+__device__ __forceinline__ Eight load_param(const float* row, const Places& at) {
+  return pairs(load_chunk<float, kVec>(row, at));
 }
-// 8 floats of shared memory (the weights, zero-padded to whole chunks).
-__device__ __forceinline__ Eight shared8(const float* p) {
-  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(p + 4);
-  return {{a.x, a.y, b.x, b.y}};
+// The weights, in shared memory and zero beyond H.
+template <bool kVec>
+__device__ __forceinline__ Eight shared8(const float* w, const Places& at) {
+  Eight v;
+  if (kVec) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(w + at.first);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(w + at.first + 4);
+    v.p[0] = a.x;
+    v.p[1] = a.y;
+    v.p[2] = b.x;
+    v.p[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v.p[i] = pack2(w[at.first + 2 * i * at.step], w[at.first + (2 * i + 1) * at.step]);
+  }
+  return v;
 }
 __device__ __forceinline__ float pair_sum(F2 p) {
   const float2 f = unpack2(p);
@@ -106,6 +145,9 @@ __device__ __forceinline__ F2 round_pair(F2 v, const float*) { return v; }
 struct GroupSum {
   float* red;
   int threads, group, turn;
+  __device__ __forceinline__ void sync() const {
+    if (threads > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+  }
   __device__ float operator()(float x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -114,7 +156,7 @@ struct GroupSum {
     float* r = red + turn * 16;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) r[warp] = x;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(threads) : "memory");
+    sync();
     const int w0 = group * warps;
     float s = r[w0];
     for (int w = 1; w < warps; ++w) s += r[w0 + w];
@@ -122,15 +164,44 @@ struct GroupSum {
   }
 };
 
+// A group's rows on their way into shared memory: `stages` rows of N arrays each.
+constexpr int kMaxStages = 4;
+template <int N>
+struct Ring {
+  char* mem;            // this group's
+  uint64_t* bars;
+  int stages, row_bytes;
+  int at = 0, parity = 0;
+  __device__ __forceinline__ char* array(int i) const { return mem + (at * N + i) * row_bytes; }
+  // One thread: starts row number k (k = 0, 1, ... of the group) of the arrays that are given.
+  __device__ __forceinline__ void start(int stage, const void* const (&rows)[N]) const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += rows[i] != nullptr;
+    mbar_arrive_expect_tx(&bars[stage], n * row_bytes);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (rows[i] != nullptr) bulk_load(mem + (stage * N + i) * row_bytes, rows[i], row_bytes, &bars[stage]);
+  }
+  __device__ __forceinline__ void wait(int* status, int* abort) const { mbar_wait(&bars[at], parity, status, abort); }
+  __device__ __forceinline__ void next() {
+    if (++at == stages) {
+      at = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 struct NormArgs {
   const void *x, *y;
   int64_t ldx, ldy, T;
-  int H, group;
+  int H, group, stages;
   const float *weight, *gate, *next_weight;
   int64_t rows_per_gate;   // 0: gate is one number a row
   float alpha, eps;
   void *r, *n;
   float *rstd_y, *rstd_r;
+  int* status;
 };
 
 // The weights in shared memory, padded with zeros to the threads' chunks.
@@ -139,15 +210,39 @@ __device__ __forceinline__ void stage_weight(float* dst, const float* w, int H, 
 }
 
 // kBranch: r = alpha x + gate norm(y); else r is x itself and is not written.
-// The weights live in shared memory, so that a thread needs few registers and enough rows are
-// in flight: 1024 threads an SM hold 64 bytes each of the rows they wait for.
+// kVec: the rows come through the ring; else from global memory, element by element.
 template <typename E, bool kBranch, bool kNext, bool kVec>
 __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
-  extern __shared__ __align__(16) float weights[];
+  constexpr int N = kBranch ? 2 : 1;
+  extern __shared__ __align__(128) float weights[];
   __shared__ float red[32];
+  __shared__ uint64_t bars[8 * kMaxStages];
+  __shared__ int abort;
   const int G = a.group, groups = blockDim.x / G, group = threadIdx.x / G, tid = threadIdx.x % G;
   const int padded = 8 * kChunks * G;
   float *w = weights, *wn = weights + (kBranch ? padded : 0);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * groups + group;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * groups;
+  const auto x_row = [&](int64_t t) { return static_cast<const E*>(a.x) + t * a.ldx; };
+  const auto y_row = [&](int64_t t) { return static_cast<const E*>(a.y) + t * a.ldy; };
+  const int row_bytes = a.H * static_cast<int>(sizeof(E));
+  Ring<N> ring{reinterpret_cast<char*>(weights + padded * ((kBranch ? 1 : 0) + (kNext ? 1 : 0))) +
+                   static_cast<int64_t>(group) * a.stages * N * row_bytes,
+               bars + group * kMaxStages, a.stages, row_bytes};
+  const auto start = [&](int stage, int64_t t) {
+    if constexpr (kBranch) ring.start(stage, {y_row(t), x_row(t)});
+    else ring.start(stage, {x_row(t)});
+  };
+  if (kVec) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 8 * kMaxStages; ++i) mbar_init(&bars[i], 1);
+      fence_mbar_init();
+      abort = 0;
+    }
+    __syncthreads();
+    if (tid == 0)
+      for (int k = 0; k < a.stages && t0 + k * stride < a.T; ++k) start(k, t0 + k * stride);
+  }
   if (kBranch) stage_weight(w, a.weight, a.H, padded);
   if (kNext) stage_weight(wn, a.next_weight, a.H, padded);
   __syncthreads();
@@ -155,15 +250,22 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
   const float inv_h = 1.f / a.H;
   const bool per_token = a.gate != nullptr && a.rows_per_gate == 0;
   const F2 alpha = pack2(a.alpha, a.alpha);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * groups + group; t < a.T;
-       t += static_cast<int64_t>(gridDim.x) * groups) {
+  for (int64_t t = t0; t < a.T; t += stride) {
     Chunk<E> xr[kChunks], yr[kChunks];
+    if (kVec) ring.wait(a.status, &abort);
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const int e = 8 * (tid + j * G);
-      if (kBranch) yr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.y) + t * a.ldy, e, a.H);
-      xr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.x) + t * a.ldx, e, a.H);
+      const Places at = places(tid, j, G, a.H);
+      if (kBranch) yr[j] = kVec ? stage_chunk<E>(ring.array(0), at) : load_chunk<E, false>(y_row(t), at);
+      xr[j] = kVec ? stage_chunk<E>(ring.array(N - 1), at) : load_chunk<E, false>(x_row(t), at);
     }
+    // once the group has read a row, its place is free for the one after the next
+    const auto refill = [&] {
+      if (!kVec) return;
+      if (G == 32) __syncwarp();
+      if (tid == 0 && t + a.stages * stride < a.T) start(ring.at, t + a.stages * stride);
+      ring.next();
+    };
     Eight x[kChunks];
     if (kBranch) {
       F2 ss = 0;
@@ -172,26 +274,27 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) ss = fma2(yr[j].pair(i), yr[j].pair(i), ss);
       const float rstd = rsqrtf(fmaf(sum(pair_sum(ss)), inv_h, a.eps));
+      refill();
       if (tid == 0) a.rstd_y[t] = rstd;
       const float f = per_token ? rstd * a.gate[t] : rstd;
       const F2 ff = pack2(f, f);
       const float* grow = a.gate != nullptr && !per_token ? a.gate + t / a.rows_per_gate * a.H : nullptr;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const int e = 8 * (tid + j * G);
-        const Eight wj = shared8(w + e);
+        const Places at = places(tid, j, G, a.H);
+        const Eight wj = shared8<kVec>(w, at);
         Eight y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) y.p[i] = mul2(mul2(yr[j].pair(i), ff), wj.p[i]);
         if (grow != nullptr) {
-          const Eight g = load_param<kVec>(grow, e, a.H);
+          const Eight g = load_param<kVec>(grow, at);
 #pragma unroll
           for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], g.p[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           x[j].p[i] = round_pair(fma2(alpha, xr[j].pair(i), y.p[i]), static_cast<const E*>(nullptr));
-        store_chunk<E, kVec>(static_cast<E*>(a.r) + t * a.H, e, a.H, x[j]);
+        store_chunk<E, kVec>(static_cast<E*>(a.r) + t * a.H, at, x[j]);
       }
     } else {
 #pragma unroll
@@ -204,15 +307,16 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) ss = fma2(x[j].p[i], x[j].p[i], ss);
       const float rstd = rsqrtf(fmaf(sum(pair_sum(ss)), inv_h, a.eps));
+      if (!kBranch) refill();
       if (tid == 0) a.rstd_r[t] = rstd;
       const F2 rr = pack2(rstd, rstd);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const int e = 8 * (tid + j * G);
-        const Eight wj = shared8(wn + e);
+        const Places at = places(tid, j, G, a.H);
+        const Eight wj = shared8<kVec>(wn, at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[j].p[i] = mul2(mul2(x[j].p[i], rr), wj.p[i]);
-        store_chunk<E, kVec>(static_cast<E*>(a.n) + t * a.H, e, a.H, x[j]);
+        store_chunk<E, kVec>(static_cast<E*>(a.n) + t * a.H, at, x[j]);
       }
     }
   }
@@ -221,7 +325,7 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
 struct NormBackwardArgs {
   const void *dr, *dn, *r, *y;   // dr nullable
   int64_t lddr, lddn, ldr, ldy, T;
-  int H, group;
+  int H, group, stages;
   const float *rstd_y, *rstd_r, *weight, *gate, *next_weight;
   int64_t rows_per_gate;
   float alpha;
@@ -229,6 +333,7 @@ struct NormBackwardArgs {
   float* dgate_token;            // one number a row (per-token gates)
   float *part_w, *part_n;        // [parts, H]: sums over a range of rows
   int64_t segment, parts;        // rows that share a gate row; ranges a segment
+  int* status;
 };
 
 // With d the gradient at r:
@@ -237,19 +342,45 @@ struct NormBackwardArgs {
 //   sums over rows: d yhat (per-token: times the gate), dn rhat
 template <typename E, bool kBranch, bool kNext, bool kVec>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBackwardArgs a) {
-  extern __shared__ __align__(16) float weights[];   // w, w'; at the end the groups' column sums
+  constexpr int N = 1 + (kBranch ? 1 : 0) + (kNext ? 2 : 0);
+  constexpr int kDr = 0, kY = 1, kDn = kBranch ? 2 : 1, kR = kDn + 1;   // arrays of the ring
+  extern __shared__ __align__(128) float weights[];   // w, w'; at the end the groups' column sums
   __shared__ float red[32];
+  __shared__ uint64_t bars[8 * kMaxStages];
+  __shared__ int abort;
   const int G = a.group, groups = blockDim.x / G, group = threadIdx.x / G, tid = threadIdx.x % G;
   const int padded = 8 * kChunks * G;
   float *w = weights, *wn = weights + (kBranch ? padded : 0);
+  const int64_t seg = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int64_t per = (a.segment + a.parts - 1) / a.parts;
+  const int64_t row0 = seg * a.segment + part * per + group;
+  const int64_t row1 = seg * a.segment + (part * per + per < a.segment ? part * per + per : a.segment);
+  const auto row_of = [&](const void* p, int64_t ld, int64_t t) { return static_cast<const E*>(p) + t * ld; };
+  const int row_bytes = a.H * static_cast<int>(sizeof(E));
+  Ring<N> ring{reinterpret_cast<char*>(weights + padded * ((kBranch ? 1 : 0) + (kNext ? 1 : 0))) +
+                   static_cast<int64_t>(group) * a.stages * N * row_bytes,
+               bars + group * kMaxStages, a.stages, row_bytes};
+  const auto start = [&](int stage, int64_t t) {
+    const void* dr = a.dr != nullptr ? row_of(a.dr, a.lddr, t) : nullptr;
+    if constexpr (kBranch && kNext)
+      ring.start(stage, {dr, row_of(a.y, a.ldy, t), row_of(a.dn, a.lddn, t), row_of(a.r, a.ldr, t)});
+    else if constexpr (kBranch) ring.start(stage, {dr, row_of(a.y, a.ldy, t)});
+    else ring.start(stage, {dr, row_of(a.dn, a.lddn, t), row_of(a.r, a.ldr, t)});
+  };
+  if (kVec) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 8 * kMaxStages; ++i) mbar_init(&bars[i], 1);
+      fence_mbar_init();
+      abort = 0;
+    }
+    __syncthreads();
+    if (tid == 0)
+      for (int k = 0; k < a.stages && row0 + k * groups < row1; ++k) start(k, row0 + k * groups);
+  }
   if (kBranch) stage_weight(w, a.weight, a.H, padded);
   if (kNext) stage_weight(wn, a.next_weight, a.H, padded);
   __syncthreads();
   GroupSum sum{red, G, group, 0};
-  const int64_t seg = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-  const int64_t per = (a.segment + a.parts - 1) / a.parts;
-  const int64_t row0 = seg * a.segment + part * per;
-  const int64_t row1 = seg * a.segment + (part * per + per < a.segment ? part * per + per : a.segment);
   const bool per_token = a.gate != nullptr && a.rows_per_gate == 0;
   const float* grow = a.gate != nullptr && !per_token ? a.gate + seg * a.H : nullptr;
   Eight acc_w[kChunks], acc_n[kChunks];
@@ -259,18 +390,11 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
     for (int i = 0; i < 4; ++i) acc_w[j].p[i] = acc_n[j].p[i] = 0;
   const float inv_h = 1.f / a.H;
   const F2 alpha = pack2(a.alpha, a.alpha);
-  for (int64_t t = row0 + group; t < row1; t += groups) {
-    Chunk<E> dr[kChunks], dnr[kChunks], rr[kChunks], yr[kChunks];
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      const int e = 8 * (tid + j * G);
-      if (kNext) {
-        dnr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.dn) + t * a.lddn, e, a.H);
-        rr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.r) + t * a.ldr, e, a.H);
-      }
-      dr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.dr) + t * a.lddr, e, a.dr != nullptr ? a.H : 0);
-      if (kBranch) yr[j] = load_chunk<E, kVec>(static_cast<const E*>(a.y) + t * a.ldy, e, a.H);
-    }
+  for (int64_t t = row0; t < row1; t += groups) {
+    const auto get = [&](int array, const void* p, int64_t ld, const Places& at) {
+      return kVec ? stage_chunk<E>(ring.array(array), at) : load_chunk<E, false>(row_of(p, ld, t), at);
+    };
+    if (kVec) ring.wait(a.status, &abort);
     Eight d[kChunks];
     if (kNext) {
       const float rstd = a.rstd_r[t];
@@ -278,44 +402,55 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
       F2 dot = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const Eight wj = shared8(wn + 8 * (tid + j * G));
+        const Places at = places(tid, j, G, a.H);
+        const Chunk<E> dn = get(kDn, a.dn, a.lddn, at), r = get(kR, a.r, a.ldr, at);
+        const Eight wj = shared8<kVec>(wn, at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const F2 rhat = mul2(rr[j].pair(i), rs), dn = dnr[j].pair(i);
-          acc_n[j].p[i] = fma2(dn, rhat, acc_n[j].p[i]);
-          d[j].p[i] = mul2(dn, wj.p[i]);
+          const F2 rhat = mul2(r.pair(i), rs);
+          acc_n[j].p[i] = fma2(dn.pair(i), rhat, acc_n[j].p[i]);
+          d[j].p[i] = mul2(dn.pair(i), wj.p[i]);
           dot = fma2(d[j].p[i], rhat, dot);
         }
       }
       const float m = -sum(pair_sum(dot)) * inv_h * rstd;   // times r, not rhat, below
       const F2 mm = pack2(m, m);
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j)
+      for (int j = 0; j < kChunks; ++j) {
+        const Places at = places(tid, j, G, a.H);
+        const Chunk<E> r = get(kR, a.r, a.ldr, at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          d[j].p[i] = fma2(rs, fma2(mm, rr[j].pair(i), d[j].p[i]), dr[j].pair(i));
+        for (int i = 0; i < 4; ++i) d[j].p[i] = mul2(rs, fma2(mm, r.pair(i), d[j].p[i]));
+        if (a.dr != nullptr) {
+          const Chunk<E> dr = get(kDr, a.dr, a.lddr, at);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[j].p[i] = add2(d[j].p[i], dr.pair(i));
+        }
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j) d[j] = pairs(dr[j]);
+      for (int j = 0; j < kChunks; ++j) d[j] = pairs(get(kDr, a.dr, a.lddr, places(tid, j, G, a.H)));
     }
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      Eight v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v.p[i] = mul2(alpha, d[j].p[i]);
-      store_chunk<E, kVec>(static_cast<E*>(a.dx) + t * a.H, 8 * (tid + j * G), a.H, v);
-    }
+    Chunk<E> yr[kChunks];
+    float s = 0.f;
+    const float rstd_y = kBranch ? a.rstd_y[t] : 0.f, gt = kBranch && per_token ? a.gate[t] : 1.f;
     if (kBranch) {
-      const float rstd = a.rstd_y[t];
-      const float gt = per_token ? a.gate[t] : 1.f;
-      const F2 rs = pack2(rstd, rstd), gg = pack2(gt, gt);
+      const F2 rs = pack2(rstd_y, rstd_y);
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) yr[j] = get(kY, a.y, a.ldy, places(tid, j, G, a.H));
+      // dx, and then d becomes v / gate
       F2 dot = 0;
+      const F2 gg = pack2(gt, gt);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const int e = 8 * (tid + j * G);
-        const Eight wj = shared8(w + e);
+        const Places at = places(tid, j, G, a.H);
+        Eight v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.p[i] = mul2(alpha, d[j].p[i]);
+        store_chunk<E, kVec>(static_cast<E*>(a.dx) + t * a.H, at, v);
+        const Eight wj = shared8<kVec>(w, at);
         Eight g;
-        if (grow != nullptr) g = load_param<kVec>(grow, e, a.H);
+        if (grow != nullptr) g = load_param<kVec>(grow, at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F2 yhat = mul2(yr[j].pair(i), rs);
@@ -325,15 +460,31 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
           dot = fma2(d[j].p[i], yhat, dot);
         }
       }
-      const float s = sum(pair_sum(dot));   // the token gate's gradient; the mean below times the gate
+      s = sum(pair_sum(dot));   // the token gate's gradient; the mean below times the gate
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        Eight v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.p[i] = mul2(alpha, d[j].p[i]);
+        store_chunk<E, kVec>(static_cast<E*>(a.dx) + t * a.H, places(tid, j, G, a.H), v);
+      }
+      if (kVec) sum.sync();
+    }
+    if (kVec) {   // the group has read the row: its place is free
+      if (G == 32) __syncwarp();
+      if (tid == 0 && t + a.stages * groups < row1) start(ring.at, t + a.stages * groups);
+      ring.next();
+    }
+    if (kBranch) {
       if (per_token && tid == 0) a.dgate_token[t] = s;
-      const float m = -s * inv_h * rstd, f = rstd * gt;
+      const float m = -s * inv_h * rstd_y, f = rstd_y * gt;
       const F2 mm = pack2(m, m), ff = pack2(f, f);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[j].p[i] = mul2(ff, fma2(mm, yr[j].pair(i), d[j].p[i]));
-        store_chunk<E, kVec>(static_cast<E*>(a.dy) + t * a.H, 8 * (tid + j * G), a.H, d[j]);
+        store_chunk<E, kVec>(static_cast<E*>(a.dy) + t * a.H, places(tid, j, G, a.H), d[j]);
       }
     }
   }
@@ -343,11 +494,15 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
     float* out = (which == 0 ? a.part_w : a.part_n) + static_cast<int64_t>(blockIdx.x) * a.H;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j)
+    for (int j = 0; j < kChunks; ++j) {
+      const Places at = places(tid, j, G, a.H);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<F2*>(weights + group * padded + 8 * (tid + j * G) + 2 * i) =
-            which == 0 ? acc_w[j].p[i] : acc_n[j].p[i];
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2(which == 0 ? acc_w[j].p[i] : acc_n[j].p[i]);
+        weights[group * padded + at.first + 2 * i * at.step] = v.x;
+        weights[group * padded + at.first + (2 * i + 1) * at.step] = v.y;
+      }
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < a.H; e += blockDim.x) {
       float s = weights[e];
@@ -399,68 +554,73 @@ bool rows_aligned(const void* p, int64_t ld, int e) {
   return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * e % 16 == 0);
 }
 
-// Launches with more than 48 KB of shared memory (H > 4096: two weights of 32 KB) need the limit raised.
 template <typename Args>
-cudaError_t start(void (*kernel)(Args), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args& a) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+cudaError_t start(void (*kernel)(Args), std::atomic<bool>* smem_set, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                  const Args& a) {
+  const cudaError_t e = set_smem_attr_once(smem_set, reinterpret_cast<const void*>(kernel), 208 * 1024);
+  if (e != cudaSuccess) return e;
   kernel<<<grid, threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename E>
-cudaError_t forward(const NormArgs& a, cudaStream_t s) {
-  const int e = sizeof(E);
-  const bool vec = a.H % 8 == 0 && rows_aligned(a.x, a.ldx, e) && rows_aligned(a.y, a.ldy, e) &&
-                   rows_aligned(a.r, a.H, e) && rows_aligned(a.n, a.H, e) && rows_aligned(a.weight, a.H, 4) &&
-                   rows_aligned(a.next_weight, a.H, 4) &&
-                   (a.rows_per_gate == 0 || rows_aligned(a.gate, a.H, 4));
+// Stages of a ring whose rows take `row` bytes a group: what `budget` bytes of shared memory leave, one at
+// least (the largest: two weights of 8192 floats and four float32 rows, 192 KB).
+int ring_stages(size_t weights, size_t row, int groups, size_t budget) {
+  const size_t n = budget > weights ? (budget - weights) / (row * groups) : 0;
+  return n < 1 ? 1 : n > kMaxStages ? kMaxStages : static_cast<int>(n);
+}
+
+template <typename E, bool kBranch, bool kNext>
+cudaError_t forward_kernel(NormArgs& a, bool vec, cudaStream_t s) {
+  static std::atomic<bool> set[2][64];
   const int threads = a.group > kNormThreads ? a.group : kNormThreads, groups = threads / a.group;
   const int64_t want = (a.T + groups - 1) / groups, most = static_cast<int64_t>(num_sms()) * (1024 / threads);
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-  const bool branch = a.y != nullptr, next = a.next_weight != nullptr;
-  const size_t smem = sizeof(float) * 8 * kChunks * a.group * ((branch ? 1 : 0) + (next ? 1 : 0));   // at most 64 KB
-#define NVFP4_NORM(B, N, V) return start(block_norm_kernel<E, B, N, V>, grid, threads, smem, s, a)
-  if (vec) {
-    if (branch && next) NVFP4_NORM(true, true, true);
-    else if (branch) NVFP4_NORM(true, false, true);
-    else NVFP4_NORM(false, true, true);
-  } else {
-    if (branch && next) NVFP4_NORM(true, true, false);
-    else if (branch) NVFP4_NORM(true, false, false);
-    else NVFP4_NORM(false, true, false);
-  }
-#undef NVFP4_NORM
+  const size_t weights = sizeof(float) * 8 * kChunks * a.group * ((kBranch ? 1 : 0) + (kNext ? 1 : 0));
+  if (!vec) return start(block_norm_kernel<E, kBranch, kNext, false>, set[0], grid, threads, weights, s, a);
+  const size_t row = static_cast<size_t>(a.H) * sizeof(E) * (kBranch ? 2 : 1);
+  a.stages = ring_stages(weights, row, groups, 216 * 1024 / (1024 / threads));
+  return start(block_norm_kernel<E, kBranch, kNext, true>, set[1], grid, threads, weights + a.stages * row * groups, s, a);
 }
 
 template <typename E>
-cudaError_t backward(const NormBackwardArgs& a, int64_t segments, float* dweight, float* dgate, float* dnext,
+cudaError_t forward(NormArgs a, cudaStream_t s) {
+  const int e = sizeof(E);
+  const bool vec = a.H % 8 == 0 && rows_aligned(a.x, a.ldx, e) && rows_aligned(a.y, a.ldy, e) &&
+                   rows_aligned(a.r, a.H, e) && rows_aligned(a.n, a.H, e) &&
+                   (a.rows_per_gate == 0 || rows_aligned(a.gate, a.H, 4));
+  if (a.y == nullptr) return forward_kernel<E, false, true>(a, vec, s);
+  return a.next_weight != nullptr ? forward_kernel<E, true, true>(a, vec, s) : forward_kernel<E, true, false>(a, vec, s);
+}
+
+template <typename E, bool kBranch, bool kNext>
+cudaError_t backward_kernel(NormBackwardArgs& a, bool vec, int64_t segments, cudaStream_t s) {
+  static std::atomic<bool> set[2][64];
+  const int threads = a.group > kNormThreads ? a.group : kNormThreads, groups = threads / a.group;
+  const dim3 grid(static_cast<unsigned>(segments * a.parts));
+  const size_t unit = sizeof(float) * 8 * kChunks * a.group;
+  const size_t weights = unit * ((kBranch ? 1 : 0) + (kNext ? 1 : 0));
+  const size_t sums = unit * groups;   // the groups' column sums, at the end
+  if (!vec)
+    return start(block_norm_backward_kernel<E, kBranch, kNext, false>, set[0], grid, threads,
+                 weights > sums ? weights : sums, s, a);
+  const size_t row = static_cast<size_t>(a.H) * sizeof(E) * (1 + (kBranch ? 1 : 0) + (kNext ? 2 : 0));
+  a.stages = ring_stages(weights, row, groups, 108 * 1024);
+  const size_t smem = weights + a.stages * row * groups;
+  return start(block_norm_backward_kernel<E, kBranch, kNext, true>, set[1], grid, threads, smem > sums ? smem : sums, s, a);
+}
+
+template <typename E>
+cudaError_t backward(NormBackwardArgs a, int64_t segments, float* dweight, float* dgate, float* dnext,
                      cudaStream_t s) {
   const int e = sizeof(E);
   const bool vec = a.H % 8 == 0 && rows_aligned(a.dr, a.lddr, e) && rows_aligned(a.dn, a.lddn, e) &&
                    rows_aligned(a.r, a.ldr, e) && rows_aligned(a.y, a.ldy, e) && rows_aligned(a.dx, a.H, e) &&
-                   rows_aligned(a.dy, a.H, e) && rows_aligned(a.weight, a.H, 4) &&
-                   rows_aligned(a.next_weight, a.H, 4) && (a.rows_per_gate == 0 || rows_aligned(a.gate, a.H, 4));
-  const int threads = a.group > kNormThreads ? a.group : kNormThreads, groups = threads / a.group;
-  const dim3 grid(static_cast<unsigned>(segments * a.parts));
-  const bool branch = a.y != nullptr, next = a.next_weight != nullptr;
-  const int rows = (branch ? 1 : 0) + (next ? 1 : 0);   // of shared memory: the weights, later the groups' sums
-  const size_t smem = sizeof(float) * 8 * kChunks * a.group * (rows > groups ? rows : groups);
-  cudaError_t err;
-#define NVFP4_NORM(B, N, V) err = start(block_norm_backward_kernel<E, B, N, V>, grid, threads, smem, s, a)
-  if (vec) {
-    if (branch && next) NVFP4_NORM(true, true, true);
-    else if (branch) NVFP4_NORM(true, false, true);
-    else NVFP4_NORM(false, true, true);
-  } else {
-    if (branch && next) NVFP4_NORM(true, true, false);
-    else if (branch) NVFP4_NORM(true, false, false);
-    else NVFP4_NORM(false, true, false);
-  }
-#undef NVFP4_NORM
+                   rows_aligned(a.dy, a.H, e) && (a.rows_per_gate == 0 || rows_aligned(a.gate, a.H, 4));
+  const bool next = a.next_weight != nullptr;
+  const cudaError_t err = a.y == nullptr ? backward_kernel<E, false, true>(a, vec, segments, s)
+                          : next         ? backward_kernel<E, true, true>(a, vec, segments, s)
+                                         : backward_kernel<E, true, false>(a, vec, segments, s);
   if (err != cudaSuccess) return err;
   NormReduceArgs ra{a.part_w, a.part_n, a.weight, a.rows_per_gate > 0 ? a.gate : nullptr, a.H, segments, a.parts,
                     dweight, a.rows_per_gate > 0 ? dgate : nullptr, dnext};
@@ -485,8 +645,8 @@ cudaError_t launch_block_norm(const void* x, int64_t ldx, const void* y, int64_t
                               const float* weight, const float* gate, int64_t gate_rows, float alpha,
                               const float* next_weight, float eps, void* r, void* n, float* rstd_y, float* rstd_r,
                               cudaStream_t s) {
-  NormArgs a{x, y, ldx, ldy, T, static_cast<int>(H), group_threads(H), weight, gate, next_weight,
-             gate_rows > 0 ? T / gate_rows : 0, alpha, eps, r, n, rstd_y, rstd_r};
+  NormArgs a{x, y, ldx, ldy, T, static_cast<int>(H), group_threads(H), 1, weight, gate, next_weight,
+             gate_rows > 0 ? T / gate_rows : 0, alpha, eps, r, n, rstd_y, rstd_r, device_status_ptr()};
   if (dtype == kActBF16) return forward<__nv_bfloat16>(a, s);
   if (dtype == kActF16) return forward<__half>(a, s);
   return forward<float>(a, s);
@@ -500,10 +660,10 @@ cudaError_t launch_block_norm_backward(const void* dr, int64_t lddr, const void*
                                        cudaStream_t s) {
   const int64_t segments = gate_rows > 0 ? gate_rows : 1, parts = block_norm_parts(T, gate_rows);
   NormBackwardArgs a{dr,     dn,    r,    y,    lddr,        lddn,
-                     ldr,    ldy,   T,    static_cast<int>(H), group_threads(H), rstd_y,
+                     ldr,    ldy,   T,    static_cast<int>(H), group_threads(H), 1, rstd_y,
                      rstd_r, weight, gate, next_weight, gate_rows > 0 ? T / gate_rows : 0, alpha,
                      dx,     dy,    gate_rows > 0 ? nullptr : dgate, partial, partial + segments * parts * H,
-                     T / segments, parts};
+                     T / segments, parts, device_status_ptr()};
   if (dtype == kActBF16) return backward<__nv_bfloat16>(a, segments, dweight, dgate, dnext, s);
   if (dtype == kActF16) return backward<__half>(a, segments, dweight, dgate, dnext, s);
   return backward<float>(a, segments, dweight, dgate, dnext, s);

@@ -219,15 +219,17 @@ __global__ void __launch_bounds__(kVocabThreads, sizeof(E) == 4 ? 4 : kTop ? 5 :
     }
     __syncthreads();
     const uint64_t bound = sm.bound;
+    const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
+    const bool plateau = static_cast<uint32_t>(bound) != 0;   // the key's lower half matters there alone
     for (int s = 0; s < mine; ++s)
-      if (top.best[s][tid] > -INFINITY && order_key(top.best[s][tid], 8 * top.chunk[s][tid]) >= bound)
+      if (top.best[s][tid] >= floor && top.best[s][tid] > -INFINITY &&
+          (!plateau || order_key(top.best[s][tid], 8 * top.chunk[s][tid]) >= bound))
         top.cell[atomicAdd(&sm.cells, 1)] = static_cast<uint16_t>(s * kVocabThreads + tid);
     __syncthreads();
     // the cells' chunks, a thread each
     int begin, stop;
     slice_range(a.V, slices, s0, begin, stop);   // the first slice is the longest
     const int per = (stop - begin + kVocabThreads - 1) / kVocabThreads, items = sm.cells * per;
-    const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
     const unsigned inverse = 0xffffffffu / per + 1;   // item / per by a multiplication: item * per < 2^32
     const auto chunk_of = [&](int item) {             // -1: beyond the slice
       if (item >= items) return -1;
@@ -238,8 +240,7 @@ __global__ void __launch_bounds__(kVocabThreads, sizeof(E) == 4 ? 4 : kTop ? 5 :
       const int c = first + cell % kVocabThreads + (item - q * per) * kVocabThreads;
       return c < last ? c : -1;
     };
-    // the elements that reach the bound, one count a chunk; its lower half matters on a plateau alone
-    const bool plateau = static_cast<uint32_t>(bound) != 0;
+    // the elements that reach the bound, one count a chunk
     const auto collect = [&](int c, const Chunk<E>& raw) {
       if (c < 0 || !(raw.max() >= floor)) return;
       float v[8];

@@ -376,9 +376,9 @@ template <typename E, typename F>
 __device__ __forceinline__ void for_batches(const Row<E>& row, int first, int last, F&& f) {
   for (int c = first + threadIdx.x; c < last; c += 4 * kVocabThreads) {
     Chunk<E> raw[4];
-    if (row.inner(c) && row.inner(last - 1)) {
+    if (c + 3 * kVocabThreads < last && row.inner(c) && row.inner(c + 3 * kVocabThreads)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = row.load_inner(min(c + i * kVocabThreads, last - 1));
+      for (int i = 0; i < 4; ++i) raw[i] = row.load_inner(c + i * kVocabThreads);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw[i] = row.get(min(c + i * kVocabThreads, last - 1));
