@@ -267,7 +267,7 @@ size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t E, int64_t H, 
       return align256(8u * (size_t)(a > 1 ? a : 1)) + align256(8u * (size_t)((a > 1 ? a : 1) + 1));
     case NVFP4_OP_NORM_BACKWARD:       // column sums of two weights over ranges of rows
       if (a <= 0 || b < 0 || H <= 0) return 0;
-      return align256(8u * (size_t)(b > 0 ? b : 1) * (size_t)block_norm_parts(a, b) * (size_t)H);
+      return align256(8u * (size_t)(b > 0 ? b : 1) * (size_t)block_norm_parts(a, b, H) * (size_t)H);
     default:
       return 0;
   }

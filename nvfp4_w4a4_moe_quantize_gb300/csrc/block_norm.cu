@@ -14,6 +14,7 @@
 // weights' and gate's gradients in registers; the ranges' sums are added by a second kernel
 // in a fixed order (no atomics).
 #include "launch.h"
+#include "pdl.cuh"
 #include "ptx.cuh"
 #include "status.cuh"
 #include "vocab.cuh"
@@ -80,23 +81,6 @@ __device__ __forceinline__ Eight pairs(const Chunk<E>& c) {
   for (int i = 0; i < 4; ++i) v.p[i] = c.pair(i);
   return v;
 }
-template <typename E, bool kVec>
-__device__ __forceinline__ void store_chunk(E* row, const Places& at, const Eight& v) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = unpack2(v.p[i]);
-    f[2 * i] = x.x;
-    f[2 * i + 1] = x.y;
-  }
-  if (kVec) {
-    if (at.first < at.H) store8(row + at.first, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (at.first + i * at.step < at.H) store_one(row + at.first + i * at.step, f[i]);
-  }
-}
 // A float32 parameter (a gate row), likewise.
 template <bool kVec>
 __device__ __forceinline__ Eight load_param(const float* row, const Places& at) {
@@ -125,20 +109,43 @@ __device__ __forceinline__ float pair_sum(F2 p) {
   return f.x + f.y;
 }
 
-// The value as the type stores it.
-__device__ __forceinline__ F2 round_pair(F2 v, const __nv_bfloat16*) {
-  const float2 f = unpack2(v);
-  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-  return pack2(Packed<__nv_bfloat16>::low(w), Packed<__nv_bfloat16>::high(w));
+// Pairs as the type stores them.
+template <typename E>
+__device__ __forceinline__ Chunk<E> stored(const Eight& v) {
+  Chunk<E> c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2(v.p[i]);
+    if constexpr (sizeof(E) == 4) {
+      c.w[2 * i] = __float_as_uint(f.x);
+      c.w[2 * i + 1] = __float_as_uint(f.y);
+    } else if constexpr (std::is_same_v<E, __half>) {
+      const __half2 h = __floats2half2_rn(f.x, f.y);
+      c.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      c.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return c;
 }
-__device__ __forceinline__ F2 round_pair(F2 v, const __half*) {
-  const float2 f = unpack2(v);
-  const __half2 h = __floats2half2_rn(f.x, f.y);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-  return pack2(Packed<__half>::low(w), Packed<__half>::high(w));
+template <typename E, bool kVec>
+__device__ __forceinline__ void store_chunk(E* row, const Places& at, const Chunk<E>& c) {
+  if (kVec) {
+    if (at.first < at.H)
+#pragma unroll
+      for (int i = 0; i < Chunk<E>::kQ; ++i)
+        reinterpret_cast<uint4*>(row + at.first)[i] = make_uint4(c.w[4 * i], c.w[4 * i + 1], c.w[4 * i + 2], c.w[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (at.first + i * at.step < at.H) row[at.first + i * at.step] = c.get(i);
+  }
 }
-__device__ __forceinline__ F2 round_pair(F2 v, const float*) { return v; }
+template <typename E, bool kVec>
+__device__ __forceinline__ void store_chunk(E* row, const Places& at, const Eight& v) {
+  store_chunk<E, kVec>(row, at, stored<E>(v));
+}
 
 // Sum over the group's threads, the same bits in each.  red: two floats a warp of the CTA,
 // used in turn, so one barrier a sum is enough.
@@ -266,7 +273,6 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
       if (tid == 0 && t + a.stages * stride < a.T) start(ring.at, t + a.stages * stride);
       ring.next();
     };
-    Eight x[kChunks];
     if (kBranch) {
       F2 ss = 0;
 #pragma unroll
@@ -292,20 +298,17 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
           for (int i = 0; i < 4; ++i) y.p[i] = mul2(y.p[i], g.p[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[j].p[i] = round_pair(fma2(alpha, xr[j].pair(i), y.p[i]), static_cast<const E*>(nullptr));
-        store_chunk<E, kVec>(static_cast<E*>(a.r) + t * a.H, at, x[j]);
+        for (int i = 0; i < 4; ++i) y.p[i] = fma2(alpha, xr[j].pair(i), y.p[i]);
+        xr[j] = stored<E>(y);
+        store_chunk<E, kVec>(static_cast<E*>(a.r) + t * a.H, at, xr[j]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kChunks; ++j) x[j] = pairs(xr[j]);
     }
     if (kNext) {
       F2 ss = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ss = fma2(x[j].p[i], x[j].p[i], ss);
+        for (int i = 0; i < 4; ++i) ss = fma2(xr[j].pair(i), xr[j].pair(i), ss);
       const float rstd = rsqrtf(fmaf(sum(pair_sum(ss)), inv_h, a.eps));
       if (!kBranch) refill();
       if (tid == 0) a.rstd_r[t] = rstd;
@@ -314,9 +317,10 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
       for (int j = 0; j < kChunks; ++j) {
         const Places at = places(tid, j, G, a.H);
         const Eight wj = shared8<kVec>(wn, at);
+        Eight v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[j].p[i] = mul2(mul2(x[j].p[i], rr), wj.p[i]);
-        store_chunk<E, kVec>(static_cast<E*>(a.n) + t * a.H, at, x[j]);
+        for (int i = 0; i < 4; ++i) v.p[i] = mul2(mul2(xr[j].pair(i), rr), wj.p[i]);
+        store_chunk<E, kVec>(static_cast<E*>(a.n) + t * a.H, at, v);
       }
     }
   }
@@ -525,6 +529,7 @@ constexpr int kReduceSlices = 16;
 // ranges; s > 1: the gradient of gate row s - 2.
 __global__ void __launch_bounds__(32 * kReduceSlices) block_norm_reduce_kernel(const NormReduceArgs a) {
   __shared__ float red[kReduceSlices][32];
+  grid_dep_sync();   // launched beside the kernel that writes the sums
   const int blocks = (a.H + 31) / 32, lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int e = static_cast<int>(blockIdx.x % blocks) * 32 + lane;
   const int64_t s = blockIdx.x / blocks;
@@ -579,7 +584,8 @@ cudaError_t forward_kernel(NormArgs& a, bool vec, cudaStream_t s) {
   const size_t weights = sizeof(float) * 8 * kChunks * a.group * ((kBranch ? 1 : 0) + (kNext ? 1 : 0));
   if (!vec) return start(block_norm_kernel<E, kBranch, kNext, false>, set[0], grid, threads, weights, s, a);
   const size_t row = static_cast<size_t>(a.H) * sizeof(E) * (kBranch ? 2 : 1);
-  a.stages = ring_stages(weights, row, groups, 216 * 1024 / (1024 / threads));
+  // (32768 x 2048 BF16: one stage 88 us, two 91 us; wider rows have one in either case)
+  a.stages = ring_stages(weights, row, groups, 36 * 1024);
   return start(block_norm_kernel<E, kBranch, kNext, true>, set[1], grid, threads, weights + a.stages * row * groups, s, a);
 }
 
@@ -605,7 +611,7 @@ cudaError_t backward_kernel(NormBackwardArgs& a, bool vec, int64_t segments, cud
     return start(block_norm_backward_kernel<E, kBranch, kNext, false>, set[0], grid, threads,
                  weights > sums ? weights : sums, s, a);
   const size_t row = static_cast<size_t>(a.H) * sizeof(E) * (1 + (kBranch ? 1 : 0) + (kNext ? 2 : 0));
-  a.stages = ring_stages(weights, row, groups, 108 * 1024);
+  a.stages = ring_stages(weights, row, groups, threads > kNormThreads ? 200 * 1024 : 108 * 1024);   // one or two CTAs an SM
   const size_t smem = weights + a.stages * row * groups;
   return start(block_norm_backward_kernel<E, kBranch, kNext, true>, set[1], grid, threads, smem > sums ? smem : sums, s, a);
 }
@@ -625,18 +631,20 @@ cudaError_t backward(NormBackwardArgs a, int64_t segments, float* dweight, float
   NormReduceArgs ra{a.part_w, a.part_n, a.weight, a.rows_per_gate > 0 ? a.gate : nullptr, a.H, segments, a.parts,
                     dweight, a.rows_per_gate > 0 ? dgate : nullptr, dnext};
   const int64_t blocks = (a.H + 31) / 32;
-  block_norm_reduce_kernel<<<static_cast<unsigned>(blocks * (2 + (ra.gate != nullptr ? segments : 0))),
-                             32 * kReduceSlices, 0, s>>>(ra);
-  return cudaGetLastError();
+  return launch_pdl(true, block_norm_reduce_kernel,
+                    dim3(static_cast<unsigned>(blocks * (2 + (ra.gate != nullptr ? segments : 0)))),
+                    dim3(32 * kReduceSlices), 0, s, ra);
 }
 
-constexpr int64_t kNormParts = 304;   // ranges of rows in all, unless there are more gate rows
+// Ranges of rows in all, unless there are more gate rows: the CTAs that 152 SMs hold (two an SM, one where a
+// group is 512 threads).
+int64_t norm_parts(int64_t H) { return group_threads(H) > kNormThreads ? 152 : 304; }
 
 }  // namespace
 
-int64_t block_norm_parts(int64_t T, int64_t gate_rows) {
+int64_t block_norm_parts(int64_t T, int64_t gate_rows, int64_t H) {
   const int64_t segments = gate_rows > 0 ? gate_rows : 1, rows = T / segments;
-  int64_t parts = kNormParts / segments;
+  int64_t parts = norm_parts(H) / segments;
   if (parts > rows) parts = rows;
   return parts > 0 ? parts : 1;
 }
@@ -658,7 +666,7 @@ cudaError_t launch_block_norm_backward(const void* dr, int64_t lddr, const void*
                                        const float* gate, int64_t gate_rows, float alpha, const float* next_weight,
                                        void* dx, void* dy, float* dweight, float* dgate, float* dnext, float* partial,
                                        cudaStream_t s) {
-  const int64_t segments = gate_rows > 0 ? gate_rows : 1, parts = block_norm_parts(T, gate_rows);
+  const int64_t segments = gate_rows > 0 ? gate_rows : 1, parts = block_norm_parts(T, gate_rows, H);
   NormBackwardArgs a{dr,     dn,    r,    y,    lddr,        lddn,
                      ldr,    ldy,   T,    static_cast<int>(H), group_threads(H), 1, rstd_y,
                      rstd_r, weight, gate, next_weight, gate_rows > 0 ? T / gate_rows : 0, alpha,

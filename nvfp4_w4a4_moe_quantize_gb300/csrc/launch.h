@@ -223,7 +223,7 @@ cudaError_t launch_block_norm(const void* x, int64_t ldx, const void* y, int64_t
                               cudaStream_t s);
 // Ranges of rows a gate row whose sums meet in the second kernel; partial holds
 // 2 * max(gate_rows, 1) * block_norm_parts * H floats.
-int64_t block_norm_parts(int64_t T, int64_t gate_rows);
+int64_t block_norm_parts(int64_t T, int64_t gate_rows, int64_t H);
 cudaError_t launch_block_norm_backward(const void* dr, int64_t lddr, const void* dn, int64_t lddn, const void* r,
                                        int64_t ldr, const void* y, int64_t ldy, int dtype, int64_t T, int64_t H,
                                        const float* rstd_y, const float* rstd_r, const float* weight,

@@ -164,6 +164,13 @@ struct Chunk {
       w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | (h << 16) : (w[i / 2] & 0xffff0000u) | h;
     }
   }
+  __device__ __forceinline__ E get(int i) const {
+    if constexpr (sizeof(E) == 4) return __uint_as_float(w[i]);
+    else {
+      const uint16_t h = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+      return *reinterpret_cast<const E*>(&h);
+    }
+  }
   static __device__ __forceinline__ Chunk none() {
     Chunk c;
 #pragma unroll

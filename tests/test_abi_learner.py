@@ -123,4 +123,5 @@ def test_norm_workspace(lib):
     assert size(1, 0, 64) == 512                                 # one range of rows, two sums of 64 floats
     assert size(5, 5, 64) == 5 * 512
     assert size(0, 0, 64) == 0 and size(4, 0, 0) == 0
-    assert size(1 << 20, 0, 2048) <= 16 << 20
+    assert size(1 << 20, 0, 2048) == 304 * 2 * 2048 * 4          # the ranges that the GPU takes at a time
+    assert size(1 << 20, 0, 8192) == 152 * 2 * 8192 * 4
