@@ -5,12 +5,12 @@
 //   dz = scale (g (1[j = y] - p) - h p (ln p + H))
 //
 // Forward: one pass over the row with a running maximum (vocab.cuh).
-// The top k come out of the same pass.  Every thread remembers, for each slice, its best value
-// and the first chunk that held it (a cell).  The k-th best of the threads' best is a lower
-// bound of the k-th best of the row, so only cells that reach it can hold one of the top k;
-// their few chunks are read again (from L2) and every element that reaches the bound becomes a
-// candidate, ranked by (value, lowest id).  A sort or a heap over the row is not needed, and
-// no atomic decides an order: a candidate's key is its value and id.
+// The top k come out of the same pass.  Every thread leaves the maximum of each of its batches of 32
+// elements (a cell).  The k-th best of the threads' own maxima is a lower bound of the k-th best
+// of the row, so only cells that reach it can hold one of the top k; their few chunks are
+// read again (from L2) and every element that reaches the bound becomes a candidate, ranked by
+// (value, lowest id).  A sort or a heap over the row is not needed, and no atomic decides an
+// order: a candidate's key is its value and id.
 #include "launch.h"
 #include "pdl.cuh"
 #include "status.cuh"
@@ -23,8 +23,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kCandidates = 1024;   // room for candidates; few more than k are usual
 constexpr int kKeep = 512;          // when they do not fit: kept from round to round,
-constexpr int kRound = 64;          // and chunks read a round, at most 8 candidates each
-static_assert(kKeep + 8 * kRound <= kCandidates && kMaxList <= kKeep, "a round has to fit");
+constexpr int kRound = 16;          // and batches read a round, at most 32 candidates each
+constexpr int kMaxCells = 16;       // a thread
+static_assert(kKeep + 32 * kRound <= kCandidates && kMaxList <= kKeep, "a round has to fit");
 static_assert(kMaxSlices * kMaxList <= kCandidates, "the lists of a cluster have to fit");
 
 // Order of the values as unsigned words; -0 counts as 0.
@@ -46,18 +47,69 @@ struct LogprobSmem {
   uint64_t bound;
 };
 struct TopSmem {
-  float best[kMaxSlices][kVocabThreads];       // a cell's best value, -inf: nothing there
-  int chunk[kMaxSlices][kVocabThreads];        // the first chunk that holds it
-  uint16_t cell[kMaxSlices * kVocabThreads];   // cells that reach the bound
+  float best[kMaxCells][kVocabThreads];       // a cell's best value, -inf: nothing there
+  float thread_best[kVocabThreads];
+  uint16_t cell[kMaxCells * kVocabThreads];   // cells that reach the bound
   alignas(16) uint64_t key[kCandidates + 8];
   uint64_t sorted[kMaxList];
-  uint64_t lists[kMaxSlices][kMaxList];        // the cluster's lists (first CTA)
+  uint64_t lists[kMaxSlices][kMaxList];       // the cluster's lists (first CTA)
   int sizes[kMaxSlices];
 };
 
+// A CTA's slices [s0, s0 + mine) as cells: cell number s * per_slice + b of a thread is its batches
+// [b * batches, (b + 1) * batches) of slice s0 + s.
+struct Cells {
+  int V, slices, s0, batches, per_slice;
+  __device__ Cells(int V_, int slices_, int s0_, int mine) : V(V_), slices(slices_), s0(s0_) {
+    int first, last;
+    slice_range(V, slices, 0, first, last);   // no slice is longer than the first
+    const int n = (last + 4 * kVocabThreads - 1) / (4 * kVocabThreads);
+    batches = (mine * n + kMaxCells - 1) / kMaxCells;
+    per_slice = (n + batches - 1) / batches;  // mine per_slice <= kMaxCells: 16 / mine is whole
+  }
+  // first chunk of batch j of a thread's cell; last: the end of its slice
+  __device__ __forceinline__ int chunk(int cell, int thread, int j, int& last) const {
+    const int s = cell / per_slice;
+    int first;
+    slice_range(V, slices, s0 + s, first, last);
+    return first + thread + ((cell - s * per_slice) * batches + j) * 4 * kVocabThreads;
+  }
+};
+
+// One key a thread, in descending order over the CTA: a bitonic network, exchanges between warps through buf.
+__device__ __forceinline__ uint64_t sort_keys(uint64_t x, uint64_t* buf) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int k = 2; k <= kVocabThreads; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2) {
+      uint64_t y;
+      if (j < 32) {
+        y = __shfl_xor_sync(0xffffffffu, x, j);
+      } else {
+        buf[tid] = x;
+        __syncthreads();
+        y = buf[tid ^ j];
+        __syncthreads();
+      }
+      const bool larger = ((tid & j) == 0) == ((tid & k) == 0);
+      x = (x > y) == larger ? x : y;
+    }
+  return x;
+}
+
 // The best min(n, k) of key[0 .. n) in order into out; returns how many.  Keys differ, so a
-// key's rank is the number of larger ones.  key has room for 8 more than n.
+// key's rank is the number of larger ones; that costs n steps a key, a sort 36, so the sort takes
+// over where a warp is not enough for the keys.  key has room for 8 more than n.
 __device__ __forceinline__ int rank_keys(uint64_t* key, int n, int k, uint64_t* out) {
+  if (n > 48 && n <= kVocabThreads) {
+    const uint64_t mine = threadIdx.x < n ? key[threadIdx.x] : 0;
+    __syncthreads();
+    const uint64_t x = sort_keys(mine, key);
+    if (threadIdx.x < min(n, k)) out[threadIdx.x] = x;
+    __syncthreads();
+    return min(n, k);
+  }
   if (threadIdx.x < 8) key[n + threadIdx.x] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kVocabThreads) {
@@ -76,29 +128,21 @@ __device__ __forceinline__ int rank_keys(uint64_t* key, int n, int k, uint64_t* 
   return min(n, k);
 }
 
-// A lower bound of the row's k-th best key, from the threads' best cells; one warp, 8 threads' cells
+// A lower bound of the row's k-th best key, from the threads' best values; one warp, 8 threads
 // a lane.  0 when fewer than k threads hold anything.
 //   The values are searched bit by bit for a bound that at least k threads reach, until hardly
 //   more do: every bit costs the warp a vote, and a few candidates too many cost less.  Where
-//   many share one value (a plateau), the lowest chunks are searched for in the same way.
-__device__ __forceinline__ uint64_t list_bound(const TopSmem& t, int slices, int k) {
+//   many share one value (a plateau), the lowest places are searched for in the same way: a
+//   thread has that value no later than in the last chunk of its first cell that reaches it.
+__device__ __forceinline__ uint64_t list_bound(const TopSmem& t, const Cells& cells, int n_cells, int k) {
   const int lane = threadIdx.x & 31;
   uint32_t val[kVocabWarps];
-  uint32_t chunk[kVocabWarps];
   uint32_t hi = 0, lo = 0xffffffffu;
   int n = 0;
 #pragma unroll
   for (int w = 0; w < kVocabWarps; ++w) {
-    const int i = w * 32 + lane;
-    float b = t.best[0][i];
-    int c = t.chunk[0][i];
-    for (int s = 1; s < slices; ++s)
-      if (t.best[s][i] > b) {
-        b = t.best[s][i];
-        c = t.chunk[s][i];
-      }
+    const float b = t.thread_best[w * 32 + lane];
     val[w] = b > -INFINITY ? order_bits(b) : 0u;
-    chunk[w] = static_cast<uint32_t>(c);
     n += val[w] != 0;
     hi = max(hi, val[w]);
     lo = val[w] != 0 ? min(lo, val[w]) : lo;
@@ -125,8 +169,15 @@ __device__ __forceinline__ uint64_t list_bound(const TopSmem& t, int slices, int
   }
   if (n <= 2 * enough) return static_cast<uint64_t>(v) << 32;
   int over = 0;   // v is exact here: every bit was searched
+  uint32_t chunk[kVocabWarps];
+  const float value = order_value(v);
 #pragma unroll
-  for (int w = 0; w < kVocabWarps; ++w) over += val[w] > v;
+  for (int w = 0; w < kVocabWarps; ++w) {
+    over += val[w] > v;
+    int q = 0, last;
+    while (q + 1 < n_cells && t.best[q][w * 32 + lane] != value) ++q;
+    chunk[w] = cells.chunk(q, w * 32 + lane, cells.batches - 1, last) + 3 * kVocabThreads;
+  }
   over = __reduce_add_sync(0xffffffffu, over);
   uint32_t c = 0xfffffu;
   for (int b = 19; b >= 0; --b) {
@@ -154,7 +205,7 @@ struct LogprobArgs {
 
 // One row a cluster of 1, 2, 4 or 8 CTAs; a CTA runs its part of the row's slices in turn.
 template <typename E, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kVocabThreads, sizeof(E) == 4 ? 4 : kTop ? 5 : 6) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6) token_logprobs_kernel(const LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ LogprobSmem sm;
   TopSmem& top = *reinterpret_cast<TopSmem*>(dyn);
@@ -187,105 +238,126 @@ __global__ void __launch_bounds__(kVocabThreads, sizeof(E) == 4 ? 4 : kTop ? 5 :
   const float zy = rank == 0 && tid == 0 && a.targets != nullptr && y >= 0 && y < a.V ? to_f32(row.p[y]) : 0.f;
   Stats(*part)[kVocabWarps] = ctas == 1 ? sm.part : cluster.map_shared_rank(sm.part, 0);
   if (kTop && tid == 0) sm.count = sm.cells = 0;
+  const Cells cells(a.V, slices, s0, mine);
+  const int n_cells = mine * cells.per_slice;
+  float thread_best = -INFINITY;
   for (int s = s0; s < s1; ++s) {
     int first, last;
     slice_range(a.V, slices, s, first, last);
     Running<E, kEntropy> run;
+    if (kTop)   // the cells that this thread does not reach
+      for (int q = 0; q < cells.per_slice; ++q) top.best[(s - s0) * cells.per_slice + q][tid] = -INFINITY;
     float best = -INFINITY;
-    int at = 0;
+    int q = (s - s0) * cells.per_slice, left_in_cell = cells.batches;
     for_batches(row, first, last, [&](int c, const Chunk<E>(&raw)[4], int left) {
       const float cm = run.add(raw, left, c1);
-      if (kTop && cm > best) {
-        best = cm;
-#pragma unroll
-        for (int i = 3; i >= 0; --i)   // the first of the four that holds it
-          if (i * kVocabThreads < left && raw[i].max() == cm) at = c + i * kVocabThreads;
+      if (kTop) {
+        best = fmaxf(best, cm);
+        top.best[q][tid] = best;
+        if (--left_in_cell == 0) {
+          thread_best = fmaxf(thread_best, best);
+          best = -INFINITY;
+          left_in_cell = cells.batches;
+          ++q;
+        }
       }
     });
+    if (kTop) thread_best = fmaxf(thread_best, best);
     const Stats st = run.warp(c1);
     if (ctas > 1 && s == s0) cluster.barrier_wait();
     if (lane == 0) part[s][warp] = st;
-    if (kTop) {
-      top.best[s - s0][tid] = best;
-      top.chunk[s - s0][tid] = at;
-    }
   }
   int found = 0;
   if (kTop) {
+    top.thread_best[tid] = thread_best;
     __syncthreads();
     if (warp == 0) {
-      const uint64_t b = list_bound(top, mine, a.k);
+      const uint64_t b = list_bound(top, cells, n_cells, a.k);
       if (lane == 0) sm.bound = b;
     }
     __syncthreads();
     const uint64_t bound = sm.bound;
     const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
     const bool plateau = static_cast<uint32_t>(bound) != 0;   // the key's lower half matters there alone
-    for (int s = 0; s < mine; ++s)
-      if (top.best[s][tid] >= floor && top.best[s][tid] > -INFINITY &&
-          (!plateau || order_key(top.best[s][tid], 8 * top.chunk[s][tid]) >= bound))
-        top.cell[atomicAdd(&sm.cells, 1)] = static_cast<uint16_t>(s * kVocabThreads + tid);
-    __syncthreads();
-    // the cells' chunks, a thread each
-    int begin, stop;
-    slice_range(a.V, slices, s0, begin, stop);   // the first slice is the longest
-    const int per = (stop - begin + kVocabThreads - 1) / kVocabThreads, items = sm.cells * per;
-    const unsigned inverse = 0xffffffffu / per + 1;   // item / per by a multiplication: item * per < 2^32
-    const auto chunk_of = [&](int item) {             // -1: beyond the slice
-      if (item >= items) return -1;
-      const int q = per == 1 ? item : static_cast<int>(__umulhi(item, inverse));
-      const int cell = top.cell[q];
-      int first, last;
-      slice_range(a.V, slices, s0 + cell / kVocabThreads, first, last);
-      const int c = first + cell % kVocabThreads + (item - q * per) * kVocabThreads;
-      return c < last ? c : -1;
-    };
-    // the elements that reach the bound, one count a chunk
-    const auto collect = [&](int c, const Chunk<E>& raw) {
-      if (c < 0 || !(raw.max() >= floor)) return;
-      float v[8];
-      unpack8(raw, v);
-      unsigned hit = 0;
+    // (one count a warp: many lanes at one counter would wait for each other)
+    const auto reserve = [&](int* counter, int n, int& total) {   // places [returned, returned + n) of the counter
+      int before = n;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (v[i] >= floor && v[i] > -INFINITY) hit |= 1u << i;
-      if (plateau)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (order_key(v[i], 8 * c + i) < bound) hit &= ~(1u << i);
-      if (hit == 0) return;
-      int at = atomicAdd(&sm.count, __popc(hit));
-      do {   // mostly one
-        const int i = __ffs(hit) - 1;
-        hit &= hit - 1;
-        float x = v[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) x = j == i ? v[j] : x;
-        if (at < kCandidates) top.key[at] = order_key(x, 8 * c + i);
-        ++at;
-      } while (hit != 0);
-    };
-    for (int base = tid; base < items; base += 4 * kVocabThreads) {
-      int c[4];
-      Chunk<E> raw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = chunk_of(base + i * kVocabThreads);
-        if (c[i] >= 0) raw[i] = row.get(c[i]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        before += lane >= o ? x : 0;
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) collect(c[i], raw[i]);
+      total = __shfl_sync(0xffffffffu, before, 31);
+      int base = 0;
+      if (lane == 0 && total > 0) base = atomicAdd(counter, total);
+      return __shfl_sync(0xffffffffu, base, 0) + before - n;
+    };
+    {
+      unsigned hit = 0;
+      if (thread_best >= floor && thread_best > -INFINITY)
+        for (int q = 0; q < n_cells; ++q)
+          if (top.best[q][tid] >= floor && top.best[q][tid] > -INFINITY) hit |= 1u << q;
+      int total, at = reserve(&sm.cells, __popc(hit), total);
+      for (; hit != 0; hit &= hit - 1)
+        top.cell[at++] = static_cast<uint16_t>((__ffs(hit) - 1) * kVocabThreads + tid);
     }
+    __syncthreads();
+    // the cells' batches, a thread each
+    const int items = sm.cells * cells.batches;
+    const auto read = [&](int item, Chunk<E>(&raw)[4], int& c) {
+      const int i = cells.batches == 1 ? item : item / cells.batches;
+      const int cell = top.cell[i];
+      int last;
+      c = cells.chunk(cell / kVocabThreads, cell % kVocabThreads, item - i * cells.batches, last);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        raw[k] = c + k * kVocabThreads < last ? row.get(c + k * kVocabThreads) : Chunk<E>::none();
+    };
+    // the elements that reach the bound; every lane of a warp calls it
+    const auto collect = [&](int item) {
+      Chunk<E> raw[4];
+      int c = 0;
+      unsigned hit = 0;   // a bit an element
+      if (item < items) {
+        read(item, raw, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (raw[k].max() >= floor) {
+            float v[8];
+            unpack8(raw[k], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (v[i] >= floor && v[i] > -INFINITY) hit |= 1u << (8 * k + i);
+            if (plateau)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (order_key(v[i], 8 * (c + k * kVocabThreads) + i) < bound) hit &= ~(1u << (8 * k + i));
+          }
+      }
+      int total, at = reserve(&sm.count, __popc(hit), total);
+      if (total == 0) return;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        while (hit >> (8 * k) & 255u) {   // mostly one
+          const int i = __ffs(hit >> (8 * k) & 255u) - 1;
+          hit &= ~(1u << (8 * k + i));
+          float v[8];
+          unpack8(raw[k], v);
+          float x = v[0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) x = j == i ? v[j] : x;
+          if (at < kCandidates) top.key[at] = order_key(x, 8 * (c + k * kVocabThreads) + i);
+          ++at;
+        }
+    };
+    for (int base = 0; base < items; base += kVocabThreads) collect(base + tid);
     __syncthreads();
     if (sm.count > kCandidates) {   // too many (most of the large values lie in few cells): again, in rounds
       __syncthreads();
       if (tid == 0) sm.count = 0;
       for (int base = 0; base < items; base += kRound) {
         __syncthreads();
-        const int c = tid < kRound ? chunk_of(base + tid) : -1;
-        Chunk<E> raw;
-        if (c >= 0) raw = row.get(c);
-        collect(c, raw);
+        if (warp == 0) collect(lane < kRound ? base + lane : items);
         __syncthreads();
         const int n = sm.count;
         if (n > kKeep) {            // keep the best k, so that the next round has room
