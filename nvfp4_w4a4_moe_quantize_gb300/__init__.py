@@ -749,7 +749,9 @@ def _norm_rows(t, like: torch.Tensor, what: str):
         return None
     if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{what} must have the shape, type and device of the other activations")
-    return _rows_2d(t, what)
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return t
 
 
 def _norm_gate(gate, T: int, H: int, index: int):

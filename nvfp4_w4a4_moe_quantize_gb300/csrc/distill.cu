@@ -439,7 +439,7 @@ __device__ __forceinline__ void bar_arrive(int id) {
 // their sums by asynchronous stores into each other's shared memory; the buffers alternate,
 // because a CTA may be one row ahead of another, and no more: it needs that one's sums to go on.
 template <typename E, bool kTail, bool kStage>
-__global__ void __launch_bounds__(kBackwardThreads, 3) distill_topk_backward_kernel(const DistillArgs a,
+__global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_kernel(const DistillArgs a,
                                                                                  const BackwardPlan plan) {
   constexpr int Q = Chunk<E>::kQ;
   extern __shared__ __align__(128) uint8_t dyn[];   // the stages, or the marks of two rows
@@ -659,74 +659,42 @@ cudaError_t forward(const DistillArgs& a, int64_t T, cudaStream_t s) {
   return launch(distill_topk_kernel<E, kTail>, set, kMaxSmem, T * ctas, ctas, kVocabThreads, 4 * words, s, a);
 }
 
-constexpr int kStageAim = 66 * 1024;     // shared memory of a CTA; three CTAs fit on an SM
-
-// Clusters of `cluster` CTAs that the GPU holds at a time (some SMs stay free where a cluster does not fit
-// into what is left of a GPC: 51 clusters of 8 on 152 SMs of 3 CTAs).  The answer of the last
-// configuration is kept.
-template <typename... Params>
-int resident_clusters(void (*kernel)(Params...), std::atomic<uint64_t>* memo, int cluster, int threads, int smem) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  const bool kept = dev >= 0 && dev < 64;
-  const uint64_t key = (static_cast<uint64_t>(smem) << 32) | (static_cast<uint64_t>(cluster) << 24);
-  const uint64_t last = kept ? memo[dev].load(std::memory_order_relaxed) : 0;
-  if ((last & 0xffffffffff000000ull) == key && (last & 0xffffffull) != 0) return static_cast<int>(last & 0xffffffull);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cluster * 4096));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
-  if (kept) memo[dev].store(key | static_cast<uint64_t>(n), std::memory_order_relaxed);
-  return n;
-}
+constexpr int kStageAim = 66 * 1024;     // of a CTA's stages; three CTAs fit on an SM
 
 template <typename E, bool kTail>
 cudaError_t backward(const DistillArgs& a, int64_t T, cudaStream_t s) {
   static std::atomic<bool> set[2][64];
-  static std::atomic<uint64_t> memo[64];
   const int slices = vocab_slices(a.V), per = ((a.V + 7) / 8 + slices - 1) / slices;
   const auto stage_bytes = [&](int n) {   // 16 spare bytes at both ends, 16 for the part's offset
     return static_cast<int64_t>(n) * per * 8 * sizeof(E) + 48;
   };
   // Slices a CTA: as many as a stage of the size aimed at takes, so that the work of a row that does not
   // grow with V is shared by few CTAs, while there are rows enough to fill the GPU.
-  // (2048 x 131072 BF16, two slices a CTA 197 us, one 279 us, four 292 us.)
+  // (2048 x 131072 BF16: two slices a CTA 199 us, one 238 us, four 328 us.)
   int mine = 1;
   while (2 * mine <= slices && stage_bytes(2 * mine) <= kStageAim && T * (slices / (2 * mine)) >= 3 * num_sms())
     mine *= 2;
   const int ctas = slices / mine;
   BackwardPlan plan{};
   plan.T = T;
-  plan.stage_bytes = static_cast<int>(stage_bytes(mine));
-  plan.stages = 2 * stage_bytes(mine) <= kStageAim ? 2 : 1;
-  int64_t smem = plan.stages * stage_bytes(mine);
-  if (smem <= kMaxSmem) {
-    // Rows a cluster: all of them in one wave if that takes at most eight (1000 x 50021 float16: 5 rows
-    // 61 us, 2 rows 66 us), else two, which the hardware balances (eight where the next row's
-    // slices arrive in a second stage).
-    const auto kernel = distill_topk_backward_kernel<E, kTail, true>;
-    cudaError_t e = set_smem_attr_once(set[0], reinterpret_cast<const void*>(kernel), kMaxSmem);
-    if (e != cudaSuccess) return e;
-    const int64_t resident = resident_clusters(kernel, memo, ctas, kBackwardThreads, static_cast<int>(smem));
-    plan.rows = static_cast<int>(T <= 8 * resident ? (T + resident - 1) / resident : plan.stages == 2 ? 8 : 2);
-    if (plan.rows == 1) {
-      plan.stages = 1;
-      smem = stage_bytes(mine);
-    }
-    return launch(kernel, set[0], kMaxSmem, (T + plan.rows - 1) / plan.rows * ctas, ctas, kBackwardThreads,
-                  static_cast<int>(smem), s, a, plan);
-  }
   plan.rows = 1;
   plan.stages = 1;
-  plan.stage_bytes = 0;
+  if (stage_bytes(mine) <= kMaxSmem) {
+    plan.stage_bytes = static_cast<int>(stage_bytes(mine));
+    // Rows a cluster: one, for the hardware to balance, two where there are clusters enough all the same
+    // (8192 x 131072 BF16: one 769 us, two 743 us, four 774 us; 1000 x 50021 float16: 54, 55, 59 us).  Where
+    // whole rows are so short that two stages fit, several, so that the next row arrives meanwhile
+    // (4096 x 8000 BF16: eight 39 us, one 47 us; longer rows do not gain).
+    if (T * ctas >= 16 * num_sms()) plan.rows = 2;
+    if (ctas == 1 && 2 * plan.stage_bytes <= kStageAim) {
+      const int64_t rows = T / (4 * num_sms());
+      plan.rows = static_cast<int>(rows < 1 ? 1 : rows > 8 ? 8 : rows);
+      plan.stages = plan.rows > 1 ? 2 : 1;
+    }
+    return launch(distill_topk_backward_kernel<E, kTail, true>, set[0], kMaxSmem,
+                  (T + plan.rows - 1) / plan.rows * ctas, ctas, kBackwardThreads, plan.stages * plan.stage_bytes, s, a,
+                  plan);
+  }
   const int marks = 2 * 4 * mine * Marks::slice_words(per);   // of two rows
   return launch(distill_topk_backward_kernel<E, kTail, false>, set[1], kMaxSmem, T * ctas, ctas, kBackwardThreads, marks,
                 s, a, plan);

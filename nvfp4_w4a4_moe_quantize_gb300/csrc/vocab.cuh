@@ -29,8 +29,8 @@ constexpr int64_t kMaxVocab = 1 << 20;        // ids stay exact in the 20-bit pa
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A slice holds at least 4096 elements (two chunks a thread): smaller ones leave threads idle.
-__host__ __device__ inline int vocab_slices(int64_t V) { return V >= 32768 ? 8 : V >= 16384 ? 4 : V >= 8192 ? 2 : 1; }
+// A slice holds at least 8192 elements, a batch of every thread: its sums are reduced over the warps once.
+__host__ __device__ inline int vocab_slices(int64_t V) { return V >= 65536 ? 8 : V >= 32768 ? 4 : V >= 16384 ? 2 : 1; }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

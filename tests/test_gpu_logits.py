@@ -24,7 +24,8 @@ TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2
 
 
 def eps(V):
-    return (V / 8 / 256 / min(8, max(1, V // 4096)) + 1 + 24 + 84) * U
+    slices = 8 if V >= 65536 else 4 if V >= 32768 else 2 if V >= 16384 else 1
+    return (V / 8 / 256 / slices + 1 + 24 + 84) * U
 
 
 def store(z, dtype, pad=0, lead=0):
