@@ -670,8 +670,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     dev, index = logits.device, logits.get_device()
     targets = _per_row(targets, (T,), torch.int32, index, "targets")
     lse = torch.empty(T, dtype=torch.float32, device=dev)
-    logprob = torch.empty(T, dtype=torch.float32, device=dev) if targets is not None else None
-    ent = torch.empty(T, dtype=torch.float32, device=dev) if entropy else None
+    logprob = torch.empty_like(lse) if targets is not None else None
+    ent = torch.empty_like(lse) if entropy else None
     top_lp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
     top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
     _check(lib.token_logprobs(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _ptr(targets),
@@ -714,7 +714,7 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     ids = _per_row(teacher_ids, (T, K), torch.int32, index, "teacher_ids")
     values = _per_row(teacher_values, (T, K), torch.float32, index, "teacher_values")
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
-    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty_like(loss)
     _check(lib.distill_topk(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), ids.data_ptr(),
                             values.data_ptr(), K, tail, scale, loss.data_ptr(), lse.data_ptr(),
                             _stream_of(logits, stream)), "distill_topk")
@@ -819,8 +819,8 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     gate, gate_rows = _norm_gate(gate, T, H, index)
     r = torch.empty((T, H), dtype=x.dtype, device=dev)
     rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
-    n = torch.empty((T, H), dtype=x.dtype, device=dev) if next_weight is not None else None
-    rstd_r = torch.empty(T, dtype=torch.float32, device=dev) if next_weight is not None else None
+    n = torch.empty_like(r) if next_weight is not None else None
+    rstd_r = torch.empty_like(rstd_y) if next_weight is not None else None
     _check(lib.moe_norm_out(x.data_ptr(), _pitch(x), y.data_ptr(), _pitch(y), ACT_DTYPES[x.dtype], T, H,
                             weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight), eps,
                             r.data_ptr(), _ptr(n), rstd_y.data_ptr(), _ptr(rstd_r), _stream_of(x, stream)),
@@ -851,10 +851,10 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
     next_weight = _per_row(next_weight, (H,), torch.float32, index, "next_weight")
     gate, gate_rows = _norm_gate(gate, T, H, index)
     dx = torch.empty((T, H), dtype=y.dtype, device=dev)
-    dy = torch.empty((T, H), dtype=y.dtype, device=dev)
+    dy = torch.empty_like(dx)
     dweight = torch.empty(H, dtype=torch.float32, device=dev)
     dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
-    dnext = torch.empty(H, dtype=torch.float32, device=dev) if next_weight is not None else None
+    dnext = torch.empty_like(dweight) if next_weight is not None else None
     ws = _norm_workspace(T, gate_rows, H, dev) if workspace is None else workspace
     _check(lib.moe_norm_out_backward(_ptr(dr), _pitch_or_0(dr), _ptr(dn), _pitch_or_0(dn), _ptr(r), _pitch_or_0(r),
                                      y.data_ptr(), _pitch(y), rstd_y.data_ptr(), _ptr(rstd_r), ACT_DTYPES[y.dtype], T, H,

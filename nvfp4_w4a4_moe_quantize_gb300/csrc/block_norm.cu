@@ -42,11 +42,11 @@ struct Eight {
 struct Places {
   int first, step, H;
 };
+template <bool kVec>   // rows are 16-byte aligned and whole chunks of neighbours
 __device__ __forceinline__ Places places(int tid, int j, int G, int H) {
-  return H % 8 == 0 ? Places{8 * (tid + j * G), 1, H} : Places{tid + 8 * j * G, G, H};
+  return kVec || H % 8 == 0 ? Places{8 * (tid + j * G), 1, H} : Places{tid + 8 * j * G, G, H};
 }
 
-// kVec: rows are 16-byte aligned and whole chunks of neighbours.
 template <typename E, bool kVec>
 __device__ __forceinline__ Chunk<E> load_chunk(const E* row, const Places& at) {
   Chunk<E> c;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
     if (kVec) ring.wait(a.status, &abort);
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const Places at = places(tid, j, G, a.H);
+      const Places at = places<kVec>(tid, j, G, a.H);
       if (kBranch) yr[j] = kVec ? stage_chunk<E>(ring.array(0), at) : load_chunk<E, false>(y_row(t), at);
       xr[j] = kVec ? stage_chunk<E>(ring.array(N - 1), at) : load_chunk<E, false>(x_row(t), at);
     }
@@ -282,12 +282,12 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
       const float rstd = rsqrtf(fmaf(sum(pair_sum(ss)), inv_h, a.eps));
       refill();
       if (tid == 0) a.rstd_y[t] = rstd;
-      const float f = per_token ? rstd * a.gate[t] : rstd;
+      const float f = per_token ? rstd * a.gate[t] : rstd;   // (read earlier, 90 instead of 88 us)
       const F2 ff = pack2(f, f);
       const float* grow = a.gate != nullptr && !per_token ? a.gate + t / a.rows_per_gate * a.H : nullptr;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const Places at = places(tid, j, G, a.H);
+        const Places at = places<kVec>(tid, j, G, a.H);
         const Eight wj = shared8<kVec>(w, at);
         Eight y;
 #pragma unroll
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(512, 2) block_norm_kernel(const NormArgs a) {
       const F2 rr = pack2(rstd, rstd);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const Places at = places(tid, j, G, a.H);
+        const Places at = places<kVec>(tid, j, G, a.H);
         const Eight wj = shared8<kVec>(wn, at);
         Eight v;
 #pragma unroll
@@ -394,19 +394,30 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
     for (int i = 0; i < 4; ++i) acc_w[j].p[i] = acc_n[j].p[i] = 0;
   const float inv_h = 1.f / a.H;
   const F2 alpha = pack2(a.alpha, a.alpha);
+  // a row's own numbers are read a row ahead
+  struct Scalars {
+    float rstd_r, rstd_y, gate;
+  };
+  const auto scalars = [&](int64_t t) {
+    return Scalars{kNext ? a.rstd_r[t] : 0.f, kBranch ? a.rstd_y[t] : 0.f, kBranch && per_token ? a.gate[t] : 1.f};
+  };
+  Scalars ahead{0.f, 0.f, 1.f};
+  if (row0 < row1) ahead = scalars(row0);
   for (int64_t t = row0; t < row1; t += groups) {
+    const Scalars own = ahead;
+    if (t + groups < row1) ahead = scalars(t + groups);
     const auto get = [&](int array, const void* p, int64_t ld, const Places& at) {
       return kVec ? stage_chunk<E>(ring.array(array), at) : load_chunk<E, false>(row_of(p, ld, t), at);
     };
     if (kVec) ring.wait(a.status, &abort);
     Eight d[kChunks];
     if (kNext) {
-      const float rstd = a.rstd_r[t];
+      const float rstd = own.rstd_r;
       const F2 rs = pack2(rstd, rstd);
       F2 dot = 0;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const Places at = places(tid, j, G, a.H);
+        const Places at = places<kVec>(tid, j, G, a.H);
         const Chunk<E> dn = get(kDn, a.dn, a.lddn, at), r = get(kR, a.r, a.ldr, at);
         const Eight wj = shared8<kVec>(wn, at);
 #pragma unroll
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
       const F2 mm = pack2(m, m);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const Places at = places(tid, j, G, a.H);
+        const Places at = places<kVec>(tid, j, G, a.H);
         const Chunk<E> r = get(kR, a.r, a.ldr, at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[j].p[i] = mul2(rs, fma2(mm, r.pair(i), d[j].p[i]));
@@ -433,21 +444,21 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j) d[j] = pairs(get(kDr, a.dr, a.lddr, places(tid, j, G, a.H)));
+      for (int j = 0; j < kChunks; ++j) d[j] = pairs(get(kDr, a.dr, a.lddr, places<kVec>(tid, j, G, a.H)));
     }
     Chunk<E> yr[kChunks];
     float s = 0.f;
-    const float rstd_y = kBranch ? a.rstd_y[t] : 0.f, gt = kBranch && per_token ? a.gate[t] : 1.f;
+    const float rstd_y = own.rstd_y, gt = own.gate;
     if (kBranch) {
       const F2 rs = pack2(rstd_y, rstd_y);
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j) yr[j] = get(kY, a.y, a.ldy, places(tid, j, G, a.H));
+      for (int j = 0; j < kChunks; ++j) yr[j] = get(kY, a.y, a.ldy, places<kVec>(tid, j, G, a.H));
       // dx, and then d becomes v / gate
       F2 dot = 0;
       const F2 gg = pack2(gt, gt);
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
-        const Places at = places(tid, j, G, a.H);
+        const Places at = places<kVec>(tid, j, G, a.H);
         Eight v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.p[i] = mul2(alpha, d[j].p[i]);
@@ -471,7 +482,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
         Eight v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.p[i] = mul2(alpha, d[j].p[i]);
-        store_chunk<E, kVec>(static_cast<E*>(a.dx) + t * a.H, places(tid, j, G, a.H), v);
+        store_chunk<E, kVec>(static_cast<E*>(a.dx) + t * a.H, places<kVec>(tid, j, G, a.H), v);
       }
       if (kVec) sum.sync();
     }
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
       for (int j = 0; j < kChunks; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[j].p[i] = mul2(ff, fma2(mm, yr[j].pair(i), d[j].p[i]));
-        store_chunk<E, kVec>(static_cast<E*>(a.dy) + t * a.H, places(tid, j, G, a.H), d[j]);
+        store_chunk<E, kVec>(static_cast<E*>(a.dy) + t * a.H, places<kVec>(tid, j, G, a.H), d[j]);
       }
     }
   }
@@ -499,7 +510,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormBack
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const Places at = places(tid, j, G, a.H);
+      const Places at = places<kVec>(tid, j, G, a.H);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 v = unpack2(which == 0 ? acc_w[j].p[i] : acc_n[j].p[i]);
