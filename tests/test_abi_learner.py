@@ -34,7 +34,7 @@ def test_token_logprobs_checks(lib):
     assert _forward(lib, ld=99) == INVALID
     assert _forward(lib, V=(1 << 20) + 1, ld=1 << 21) == UNSUPPORTED
     assert _forward(lib, T=(1 << 24) + 1) == UNSUPPORTED
-    for scale in (0.0, -1.0, math.inf, math.nan):
+    for scale in (0.0, -1.0, math.inf, math.nan, 3e38):
         assert _forward(lib, scale=scale) == INVALID
     assert _forward(lib, k=-1) == INVALID
     assert _forward(lib, k=101) == INVALID

@@ -168,6 +168,28 @@ def test_candidates_beyond_one_round(cuda_lib):
     check_forward(cuda_lib, store(z, "f32"), np.zeros(T, np.int32), 1.0, 128)
 
 
+@pytest.mark.parametrize("T", [2, 640])
+def test_few_threads_hold_everything(cuda_lib, T):
+    """All but 100 threads' chunks excluded: fewer threads than alternatives, many candidates each."""
+    V = 40000
+    rng = np.random.default_rng(T)
+    z = np.full((T, V), -np.inf)
+    hot = (np.arange(V // 8) % 256) < 100
+    z.reshape(T, V // 8, 8)[:, hot, :] = rng.normal(0.0, 1.0, (T, hot.sum(), 8))
+    check_forward(cuda_lib, store(z, "f16"), np.zeros(T, np.int32), 1.0, 128)
+
+
+def test_no_rows(cuda_lib):
+    z = torch.empty(0, 64, device="cuda")
+    i, f = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
+    got = cuda_lib.token_logprobs(z, i, top_k=3)
+    assert [t.shape for t in got] == [(0,), (0,), (0,), (0, 3), (0, 3)]
+    assert cuda_lib.token_logprobs_backward(z, f, i, f).shape == (0, 64)
+    ids, val = torch.empty(0, 4, dtype=torch.int32, device="cuda"), torch.empty(0, 4, device="cuda")
+    assert cuda_lib.distill_topk(z, ids, val)[0].shape == (0,)
+    assert cuda_lib.distill_topk_backward(z, ids, val)[1].shape == (0, 64)
+
+
 def test_not_a_number_rows(cuda_lib):
     z, _ = logits(3, 5000, 11)
     z[0, 4999] = np.nan
