@@ -32,6 +32,7 @@ constexpr int kKeep = 512;          // when they do not fit: kept from round to 
 constexpr int kRound = 16;          // and batches read a round, at most 32 candidates each
 constexpr int kMaxCells = 16;       // a thread
 static_assert(kKeep + 32 * kRound <= kCandidates && kMaxList <= kKeep, "a round has to fit");
+static_assert(sizeof(Stats) == 12, "a cluster's sums are 24 KB at most");
 static_assert(kMaxSlices * kMaxList <= kCandidates, "the lists of a cluster have to fit");
 
 // Order of the values as unsigned words; -0 counts as 0.
@@ -48,7 +49,7 @@ __device__ __forceinline__ uint64_t order_key(float v, uint32_t pos) {
 }
 
 struct LogprobSmem {
-  Stats part[kMaxSlices][kVocabWarps];
+  Stats part[kVocabWarps];
   int count, cells;
   uint64_t bound;
 };
@@ -212,9 +213,10 @@ struct LogprobArgs {
 // One row a cluster of 1, 2, 4 or 8 CTAs; a CTA runs its part of the row's slices in turn.
 template <typename E, bool kEntropy, bool kTop>
 __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6) token_logprobs_kernel(const LogprobArgs a) {
-  extern __shared__ __align__(16) uint8_t dyn[];
+  extern __shared__ __align__(16) uint8_t dyn[];   // TopSmem; a cluster's sums, by slice and thread
   __shared__ LogprobSmem sm;
   TopSmem& top = *reinterpret_cast<TopSmem*>(dyn);
+  Stats* slice_sums = reinterpret_cast<Stats*>(dyn + (kTop ? sizeof(TopSmem) : 0));
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int64_t t = blockIdx.x / ctas;
@@ -242,7 +244,9 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
   const float c1 = a.scale * kLog2e;
   const int mine = slices / ctas, s0 = rank * mine, s1 = s0 + mine;
   const float zy = rank == 0 && tid == 0 && a.targets != nullptr && y >= 0 && y < a.V ? to_f32(row.p[y]) : 0.f;
-  Stats(*part)[kVocabWarps] = ctas == 1 ? sm.part : cluster.map_shared_rank(sm.part, 0);
+  // A thread's sums of the slices are added in the slices' order, here or in the cluster's first CTA.
+  Stats row_sums = empty_stats();
+  Stats* lead_sums = ctas == 1 ? nullptr : cluster.map_shared_rank(slice_sums, 0);
   if (kTop && tid == 0) sm.count = sm.cells = 0;
   const Cells cells(a.V, slices, s0, mine);
   const int n_cells = mine * cells.per_slice;
@@ -269,9 +273,12 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
       }
     });
     if (kTop) thread_best = fmaxf(thread_best, best);
-    const Stats st = run.warp(c1);
-    if (ctas > 1 && s == s0) cluster.barrier_wait();
-    if (lane == 0) part[s][warp] = st;
+    if (ctas == 1) {
+      row_sums = Running<E, kEntropy>::join(row_sums, run.thread(), c1);
+    } else {
+      if (s == s0) cluster.barrier_wait();
+      lead_sums[s * kVocabThreads + tid] = run.thread();
+    }
   }
   int found = 0;
   if (kTop) {
@@ -384,10 +391,14 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
   if (ctas > 1) {
     cluster.sync();
     if (rank != 0) return;
-  } else {
-    __syncthreads();
+    for (int s = 0; s < slices; ++s)
+      row_sums = Running<E, kEntropy>::join(row_sums, slice_sums[s * kVocabThreads + tid], c1);
   }
-  const Stats st = Running<E, kEntropy>::join_slices(sm.part, slices, c1);   // every warp, the same bits
+  row_sums = Running<E, kEntropy>::warp_join(row_sums, c1);
+  if (lane == 0) sm.part[warp] = row_sums;
+  __syncthreads();
+  const Stats st =   // every warp, the same bits
+      Running<E, kEntropy>::warp_join(lane < kVocabWarps ? sm.part[lane] : empty_stats(), c1);
   const float ln_s = logf(st.s);
   const bool none = st.s == 0.f;   // every token excluded
   if (tid == 0) {
@@ -446,10 +457,11 @@ cudaError_t launch_forward(const LogprobArgs& a, int64_t T, cudaStream_t s) {
   // few rows: a row's slices in a cluster, over as many CTAs as it takes to fill the GPU
   int ctas = 1;
   while (ctas < slices && T * ctas < 4 * num_sms()) ctas *= 2;
-  const int smem = kTop ? static_cast<int>(sizeof(TopSmem)) : 0;
+  const int smem = (kTop ? static_cast<int>(sizeof(TopSmem)) : 0) +
+                   (ctas > 1 ? static_cast<int>(sizeof(Stats)) * slices * kVocabThreads : 0);
   auto kernel = token_logprobs_kernel<E, kEntropy, kTop>;
   if (smem > 0) {
-    const cudaError_t e = set_smem_attr_once(smem_set, reinterpret_cast<const void*>(kernel), smem);
+    const cudaError_t e = set_smem_attr_once(smem_set, reinterpret_cast<const void*>(kernel), 96 * 1024);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -83,6 +83,13 @@ struct Packed;
 template <>
 struct Packed<__nv_bfloat16> {
   static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static constexpr uint32_t kFar = 0xf149f149u;        // -1e30, twice
+  static constexpr float kFarValue = -9.95e29f;        // a little above
+  static __device__ __forceinline__ uint32_t clamp_far(uint32_t w) {   // at least kFar; NaN stays
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(kFar));
+    return r;
+  }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -99,6 +106,13 @@ struct Packed<__nv_bfloat16> {
 template <>
 struct Packed<__half> {
   static constexpr uint32_t kNegInf = 0xfc00fc00u;
+  static constexpr uint32_t kFar = 0xfbfffbffu;        // -65504, twice
+  static constexpr float kFarValue = -65504.f;
+  static __device__ __forceinline__ uint32_t clamp_far(uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(kFar));
+    return r;
+  }
   static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -307,31 +321,59 @@ struct Running {
       s = mul2(rr, s);
       m = cm;
     }
+    if constexpr (kEntropy && sizeof(E) == 2) {
+      // Excluded tokens far below the maximum: as a far, finite value they add 0 to s and u, without a
+      // clamp of every t.  2^-200 is 0 and kFar c1 finite.
+      if ((Packed<E>::kFarValue - m) * c1 < -200.f && c1 < 1e6f) {
+        sum<true>(raw, left, c1);
+        return cm;
+      }
+    }
+    sum<false>(raw, left, c1);
+    return cm;
+  }
+  template <bool kFar>
+  __device__ __forceinline__ void sum(const Chunk<E> (&raw)[4], int left, float c1) {
     const F2 cc = pack2(c1, c1);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (k > 0 && k * kVocabThreads >= left) break;
+      Chunk<E> c = raw[k];
+      if constexpr (kFar)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c.w[i] = Packed<E>::clamp_far(c.w[i]);
       F2 e[4];
       F2 x = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 t = unpack2(mul2(raw[k].pair_minus(i, m), cc));
+        const F2 tt = mul2(c.pair_minus(i, m), cc);
+        const float2 t = unpack2(tt);
         e[i] = pack2(ex2(t.x), ex2(t.y));
         if (kEntropy) {   // an excluded token adds 0, not 0 * inf
-          const F2 tt = pack2(fmaxf(t.x, -1000.f), fmaxf(t.y, -1000.f));
-          x = i == 0 ? mul2(e[i], tt) : fma2(e[i], tt, x);
+          const F2 tu = kFar ? tt : pack2(fmaxf(t.x, -1000.f), fmaxf(t.y, -1000.f));
+          x = i == 0 ? mul2(e[i], tu) : fma2(e[i], tu, x);
         }
       }
       s = add2(s, add2(add2(e[0], e[1]), add2(e[2], e[3])));
       if (kEntropy) u = add2(u, x);
     }
-    return cm;
+  }
+  __device__ __forceinline__ Stats thread() const {
+    const float2 ss = unpack2(s), uu = unpack2(u);
+    return {m, ss.x + ss.y, kEntropy ? uu.x + uu.y : 0.f};
   }
   // The warp's statistics, the same in every lane.
   __device__ __forceinline__ Stats warp(float c1) const {
-    const float2 ss = unpack2(s), uu = unpack2(u);
-    Stats a{m, ss.x + ss.y, kEntropy ? uu.x + uu.y : 0.f};
-    return warp_join(a, c1);
+    return warp_join(thread(), c1);
+  }
+  // One after the other (in this order).
+  static __device__ __forceinline__ Stats join(Stats a, Stats b, float c1) {
+    const float m = fmaxf(a.m, b.m);
+    rebase<kEntropy>(a, m, c1);
+    rebase<kEntropy>(b, m, c1);
+    a.s += b.s;
+    if (kEntropy) a.u += b.u;
+    return a;
   }
   static __device__ __forceinline__ Stats warp_join(Stats a, float c1) {
     rebase<kEntropy>(a, warp_top(a.m), c1);
