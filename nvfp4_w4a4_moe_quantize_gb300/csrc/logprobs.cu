@@ -135,66 +135,55 @@ __device__ __forceinline__ int rank_keys(uint64_t* key, int n, int k, uint64_t* 
   return min(n, k);
 }
 
-// A lower bound of the row's k-th best key, from the threads' best values; one warp, 8 threads
-// a lane.  0 when fewer than k threads hold anything.
+// A lower bound of the row's k-th best key, from the threads' best values (`mine`); the whole CTA.
+// 0 when fewer than k threads hold anything.
 //   The values are searched bit by bit for a bound that at least k threads reach, until hardly
-//   more do: every bit costs the warp a vote, and a few candidates too many cost less.  Where
-//   many share one value (a plateau), the lowest places are searched for in the same way: a
-//   thread has that value no later than in the last chunk of its first cell that reaches it.
-__device__ __forceinline__ uint64_t list_bound(const TopSmem& t, const Cells& cells, int n_cells, int k) {
-  const int lane = threadIdx.x & 31;
-  uint32_t val[kVocabWarps];
-  uint32_t hi = 0, lo = 0xffffffffu;
-  int n = 0;
-#pragma unroll
-  for (int w = 0; w < kVocabWarps; ++w) {
-    const float b = t.thread_best[w * 32 + lane];
-    val[w] = b > -INFINITY ? order_bits(b) : 0u;
-    n += val[w] != 0;
-    hi = max(hi, val[w]);
-    lo = val[w] != 0 ? min(lo, val[w]) : lo;
-  }
-  n = __reduce_add_sync(0xffffffffu, n);
+//   more do: every bit costs a vote of the CTA, and a few candidates too many cost less.
+__device__ __forceinline__ uint64_t list_bound(float mine, TopSmem& t, const Cells& cells, int n_cells, int k,
+                                               uint64_t* plateau) {
+  const uint32_t val = mine > -INFINITY ? order_bits(mine) : 0u;
+  t.thread_best[threadIdx.x] = mine;
+  int n = __syncthreads_count(val != 0);
   if (n < k) return 0;
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  // v: what n threads reach; bits that all values share are settled
-  int bit = 31 - __clz(hi ^ lo);
-  uint32_t v = bit < 0 ? hi : hi & ~((2u << bit) - 1u);
-  if (bit == 31) v = 0;
+  uint32_t v = 0;
   const int enough = k + (k >> 3) + 4;
-  for (; bit >= 0 && n > enough; --bit) {
+  for (int bit = 31; bit >= 0 && n > enough; --bit) {
     const uint32_t next = v | (1u << bit);
-    int m = 0;
-#pragma unroll
-    for (int w = 0; w < kVocabWarps; ++w) m += val[w] >= next;
-    m = __reduce_add_sync(0xffffffffu, m);
+    const int m = __syncthreads_count(val >= next);
     if (m >= k) {
       v = next;
       n = m;
     }
   }
   if (n <= 2 * enough) return static_cast<uint64_t>(v) << 32;
-  int over = 0;   // v is exact here: every bit was searched
-  uint32_t chunk[kVocabWarps];
-  const float value = order_value(v);
+  // Many share one value (a plateau; v is exact, every bit was searched): the lowest places are searched for
+  // in the same way, by one warp.  A thread has that value no later than in the last chunk of its
+  // first cell that reaches it.
+  if (threadIdx.x < 32) {
+    const float value = order_value(v);
+    uint32_t chunk[kVocabWarps];
+    int over = 0;
 #pragma unroll
-  for (int w = 0; w < kVocabWarps; ++w) {
-    over += val[w] > v;
-    int q = 0, last;
-    while (q + 1 < n_cells && t.best[q][w * 32 + lane] != value) ++q;
-    chunk[w] = cells.chunk(q, w * 32 + lane, cells.batches - 1, last) + 3 * kVocabThreads;
-  }
-  over = __reduce_add_sync(0xffffffffu, over);
-  uint32_t c = 0xfffffu;
-  for (int b = 19; b >= 0; --b) {
-    const uint32_t next = c & ~(1u << b);
-    int m = 0;
+    for (int w = 0; w < kVocabWarps; ++w) {
+      const int i = w * 32 + threadIdx.x;
+      over += t.thread_best[i] > value;
+      int q = 0, last;
+      while (q + 1 < n_cells && t.best[q][i] != value) ++q;
+      chunk[w] = t.thread_best[i] == value ? cells.chunk(q, i, cells.batches - 1, last) + 3 * kVocabThreads : ~0u;
+    }
+    over = __reduce_add_sync(0xffffffffu, over);
+    uint32_t c = 0xfffffu;
+    for (int b = 19; b >= 0; --b) {
+      const uint32_t next = c & ~(1u << b);
+      int m = 0;
 #pragma unroll
-    for (int w = 0; w < kVocabWarps; ++w) m += val[w] == v && chunk[w] <= next;
-    if (over + __reduce_add_sync(0xffffffffu, m) >= k) c = next;
+      for (int w = 0; w < kVocabWarps; ++w) m += chunk[w] <= next;
+      if (over + __reduce_add_sync(0xffffffffu, m) >= k) c = next;
+    }
+    if (threadIdx.x == 0) *plateau = (static_cast<uint64_t>(v) << 32) | (0xffffffffu - (8 * c + 7));
   }
-  return (static_cast<uint64_t>(v) << 32) | (0xffffffffu - (8 * c + 7));
+  __syncthreads();
+  return *plateau;
 }
 
 struct LogprobArgs {
@@ -280,16 +269,14 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
       lead_sums[s * kVocabThreads + tid] = run.thread();
     }
   }
+  if (ctas == 1) {   // (read after the list's barriers)
+    row_sums = Running<E, kEntropy>::warp_join(row_sums, c1);
+    if (lane == 0) sm.part[warp] = row_sums;
+    if (!kTop) __syncthreads();
+  }
   int found = 0;
   if (kTop) {
-    top.thread_best[tid] = thread_best;
-    __syncthreads();
-    if (warp == 0) {
-      const uint64_t b = list_bound(top, cells, n_cells, a.k);
-      if (lane == 0) sm.bound = b;
-    }
-    __syncthreads();
-    const uint64_t bound = sm.bound;
+    const uint64_t bound = list_bound(thread_best, top, cells, n_cells, a.k, &sm.bound);
     const float floor = bound == 0 ? -INFINITY : order_value(static_cast<uint32_t>(bound >> 32));
     const bool plateau = static_cast<uint32_t>(bound) != 0;   // the key's lower half matters there alone
     // (one count a warp: many lanes at one counter would wait for each other)
@@ -308,6 +295,7 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
     {
       unsigned hit = 0;
       if (thread_best >= floor && thread_best > -INFINITY)
+#pragma unroll 4
         for (int q = 0; q < n_cells; ++q)
           if (top.best[q][tid] >= floor && top.best[q][tid] > -INFINITY) hit |= 1u << q;
       int total, at = reserve(&sm.cells, __popc(hit), total);
@@ -393,10 +381,10 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
     if (rank != 0) return;
     for (int s = 0; s < slices; ++s)
       row_sums = Running<E, kEntropy>::join(row_sums, slice_sums[s * kVocabThreads + tid], c1);
+    row_sums = Running<E, kEntropy>::warp_join(row_sums, c1);
+    if (lane == 0) sm.part[warp] = row_sums;
+    __syncthreads();
   }
-  row_sums = Running<E, kEntropy>::warp_join(row_sums, c1);
-  if (lane == 0) sm.part[warp] = row_sums;
-  __syncthreads();
   const Stats st =   // every warp, the same bits
       Running<E, kEntropy>::warp_join(lane < kVocabWarps ? sm.part[lane] : empty_stats(), c1);
   const float ln_s = logf(st.s);
