@@ -503,6 +503,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_ker
     };
     if (kStage)
       for (int i = 0; i < plan.stages && i < n_rows; ++i) stage_of(i).fetch(z_of(i), bar_of(i));
+    // a single stage is free for the next row only at this one's end; till then L2 takes it (no further row:
+    // two ahead cost 815 us where one gives 709)
+    if (lane == 0 && kStage && plan.stages == 1 && n_rows > 1) prefetch_row(z_of(1), lo, hi);
     list.read(a, t0);
     list.gather(a, z_of(0));
     list.template reduce<!kStage>(c1, marks_of(0), sm.list[0]);
@@ -552,7 +555,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_ker
       if (more && plan.stages == 2) open_row(i + 1);
       bar_sync(kBarWritten);   // the row's stage is free
       if (more && plan.stages == 1) {
-        if (kStage) stage_of(i + 1).fetch(z_of(i + 1), bar_of(i + 1));
+        if (kStage) {
+          stage_of(i + 1).fetch(z_of(i + 1), bar_of(i + 1));
+          if (lane == 0 && i + 2 < n_rows) prefetch_row(z_of(i + 2), lo, hi);
+        }
         open_row(i + 1);
       }
     }
@@ -689,7 +695,7 @@ cudaError_t backward(const DistillArgs& a, int64_t T, cudaStream_t s) {
   if (stage_bytes(mine) <= kMaxSmem) {
     plan.stage_bytes = static_cast<int>(stage_bytes(mine));
     // Rows a cluster: one, for the hardware to balance, two where there are clusters enough all the same
-    // (8192 x 131072 BF16: one 769 us, two 743 us, four 774 us; 1000 x 50021 float16: 54, 55, 59 us).  Where
+    // (8192 x 131072 BF16: one 767 us, two 709 us, four 724 us; 1000 x 50021 float16: 54, 57, 57 us).  Where
     // whole rows are so short that two stages fit, several, so that the next row arrives meanwhile
     // (4096 x 8000 BF16: eight 39 us, one 47 us; longer rows do not gain).
     if (T * ctas >= 16 * num_sms()) plan.rows = 2;

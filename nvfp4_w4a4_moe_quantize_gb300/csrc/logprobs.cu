@@ -243,6 +243,11 @@ __global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
   for (int s = s0; s < s1; ++s) {
     int first, last;
     slice_range(a.V, slices, s, first, last);
+    if (tid == 0 && s + 1 < s1) {   // the next slice on its way into L2: more bytes than the registers can await
+      int f, l;
+      slice_range(a.V, slices, s + 1, f, l);
+      prefetch_row(row.p, min(a.V, 8 * f), min(a.V, 8 * l));
+    }
     Running<E, kEntropy> run;
     if (kTop)   // the cells that this thread does not reach
       for (int q = 0; q < cells.per_slice; ++q) top.best[(s - s0) * cells.per_slice + q][tid] = -INFINITY;

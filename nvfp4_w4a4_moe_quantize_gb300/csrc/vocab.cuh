@@ -411,6 +411,15 @@ struct Running {
   }
 };
 
+// Elements [lo, hi) of a row on their way from HBM into L2, in one request of one thread (whole 16-byte words).
+template <typename E>
+__device__ __forceinline__ void prefetch_row(const E* row, int lo, int hi) {
+  const uintptr_t a = (reinterpret_cast<uintptr_t>(row + lo) + 15u) & ~uintptr_t(15);
+  const uintptr_t b = reinterpret_cast<uintptr_t>(row + hi) & ~uintptr_t(15);
+  if (a < b)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(static_cast<uint32_t>(b - a)) : "memory");
+}
+
 // The chunks [first, last) of a slice.
 __device__ __forceinline__ void slice_range(int V, int slices, int slice, int& first, int& last) {
   const int chunks = (V + 7) >> 3, per = (chunks + slices - 1) >> (__ffs(slices) - 1);   // 1, 2, 4 or 8 slices
