@@ -626,19 +626,30 @@ def moe_expert_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, we
 
 # --------------------------------------------------------------------------- rows of logits
 
-def _rows_2d(t: torch.Tensor, what: str) -> torch.Tensor:
-    """A [rows, cols] CUDA tensor of an activation type whose columns are adjacent."""
-    if t.dim() != 2 or t.dtype not in ACT_DTYPES:
+def _rows(t: torch.Tensor, what: str) -> tuple:
+    """(rows, cols, type code, pitch) of a [rows, cols] CUDA tensor of an activation type whose
+    columns are adjacent."""
+    code = ACT_DTYPES.get(t.dtype)
+    if code is None or t.dim() != 2:
         raise ValueError(f"{what} must be a 2-D BF16, float16 or float32 tensor")
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    (rows, cols), (pitch, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
-    return t
+    return rows, cols, code, pitch if rows > 1 else max(cols, 1)
 
 
-def _pitch(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _rows_like(t, like: torch.Tensor, what: str) -> int:
+    """The pitch of rows that have the shape, type and device of `like`; 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what} must have the shape, type and device of the other rows")
+    (rows, cols), (pitch, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return pitch if rows > 1 else max(cols, 1)
 
 
 def _per_row(t, shape: tuple, dtype, dev: int, what: str):
@@ -651,14 +662,6 @@ def _per_row(t, shape: tuple, dtype, dev: int, what: str):
     return t.contiguous()
 
 
-def _like_rows(out, like: torch.Tensor, what: str) -> torch.Tensor:
-    if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
-        raise ValueError(f"{what} must have the shape, type and device of its input")
-    return _rows_2d(out, what)
-
-
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
                    ignore_index: int = -100, entropy: bool = True, stream=None):
     """Log probabilities of given tokens, entropy and top alternatives of logits [T, V] (BF16,
@@ -666,7 +669,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     top_ids): float32 [T], [T], [T], [T, top_k] and int32 [T, top_k], None for what was not
     asked.  targets: int32 [T]; a row whose target is ignore_index is skipped (zeros)."""
     lib = load()
-    T, V = _rows_2d(logits, "logits").shape
+    T, V, code, ld = _rows(logits, "logits")
     dev, index = logits.device, logits.get_device()
     targets = _per_row(targets, (T,), torch.int32, index, "targets")
     lse = torch.empty(T, dtype=torch.float32, device=dev)
@@ -674,7 +677,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     ent = torch.empty_like(lse) if entropy else None
     top_lp = torch.empty((T, top_k), dtype=torch.float32, device=dev) if top_k > 0 else None
     top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
-    _check(lib.token_logprobs(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _ptr(targets),
+    _check(lib.token_logprobs(logits.data_ptr(), code, T, V, ld, _ptr(targets),
                               ignore_index, scale, top_k, _ptr(logprob), lse.data_ptr(), _ptr(ent), _ptr(top_lp),
                               _ptr(top_ids), _stream_of(logits, stream)), "token_logprobs")
     return logprob, lse, ent, top_lp, top_ids
@@ -687,17 +690,19 @@ def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, targets: to
     """dlogits [T, V] of sum(dlogprob * logprob + dentropy * entropy), with the forward's lse and
     entropy (all float32 [T]).  out may be the logits themselves."""
     lib = load()
-    T, V = _rows_2d(logits, "logits").shape
+    T, V, code, ld = _rows(logits, "logits")
     index = logits.get_device()
     targets = _per_row(targets, (T,), torch.int32, index, "targets")
     lse = _per_row(lse, (T,), torch.float32, index, "lse")
     entropy = _per_row(entropy, (T,), torch.float32, index, "entropy")
     dlogprob = _per_row(dlogprob, (T,), torch.float32, index, "dlogprob")
     dentropy = _per_row(dentropy, (T,), torch.float32, index, "dentropy")
-    out = _like_rows(out, logits, "out")
-    _check(lib.token_logprobs_backward(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), _ptr(targets),
+    if out is None:
+        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    ldd = _rows_like(out, logits, "out")
+    _check(lib.token_logprobs_backward(logits.data_ptr(), code, T, V, ld, _ptr(targets),
                                        ignore_index, scale, _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy),
-                                       out.data_ptr(), _pitch(out), _stream_of(logits, stream)),
+                                       out.data_ptr(), ldd, _stream_of(logits, stream)),
            "token_logprobs_backward")
     return out
 
@@ -709,15 +714,14 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     vocabulary and the unlisted tokens count as one; else q = softmax(values).  Returns
     (loss, lse), float32 [T]."""
     lib = load()
-    T, V = _rows_2d(logits, "logits").shape
+    T, V, code, ld = _rows(logits, "logits")
     index, K = logits.get_device(), teacher_ids.shape[-1]
     ids = _per_row(teacher_ids, (T, K), torch.int32, index, "teacher_ids")
     values = _per_row(teacher_values, (T, K), torch.float32, index, "teacher_values")
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     lse = torch.empty_like(loss)
-    _check(lib.distill_topk(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), ids.data_ptr(),
-                            values.data_ptr(), K, tail, scale, loss.data_ptr(), lse.data_ptr(),
-                            _stream_of(logits, stream)), "distill_topk")
+    _check(lib.distill_topk(logits.data_ptr(), code, T, V, ld, ids.data_ptr(), values.data_ptr(), K, tail, scale,
+                            loss.data_ptr(), lse.data_ptr(), _stream_of(logits, stream)), "distill_topk")
     return loss, lse
 
 
@@ -728,31 +732,22 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     float32 [T], None: ones; nothing of the forward is needed).  out may be the logits
     themselves.  Returns (loss, dlogits)."""
     lib = load()
-    T, V = _rows_2d(logits, "logits").shape
+    T, V, code, ld = _rows(logits, "logits")
     index, K = logits.get_device(), teacher_ids.shape[-1]
     ids = _per_row(teacher_ids, (T, K), torch.int32, index, "teacher_ids")
     values = _per_row(teacher_values, (T, K), torch.float32, index, "teacher_values")
     dloss = _per_row(dloss, (T,), torch.float32, index, "dloss")
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
-    out = _like_rows(out, logits, "out")
-    _check(lib.distill_topk_backward(logits.data_ptr(), ACT_DTYPES[logits.dtype], T, V, _pitch(logits), ids.data_ptr(),
-                                     values.data_ptr(), K, tail, scale, _ptr(dloss), loss.data_ptr(), None,
-                                     out.data_ptr(), _pitch(out), _stream_of(logits, stream)), "distill_topk_backward")
+    if out is None:
+        out = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    ldd = _rows_like(out, logits, "out")
+    _check(lib.distill_topk_backward(logits.data_ptr(), code, T, V, ld, ids.data_ptr(), values.data_ptr(), K, tail,
+                                     scale, _ptr(dloss), loss.data_ptr(), None, out.data_ptr(), ldd,
+                                     _stream_of(logits, stream)), "distill_topk_backward")
     return loss, out
 
 
 # --------------------------------------------------------------------------- norms around the block
-
-def _norm_rows(t, like: torch.Tensor, what: str):
-    """A [T, H] activation like `like`; None passes."""
-    if t is None:
-        return None
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{what} must have the shape, type and device of the other activations")
-    if t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError(f"{what} must have unit column stride")
-    return t
-
 
 def _norm_gate(gate, T: int, H: int, index: int):
     """gate as (dense tensor or None, gate_rows): [T] is one number a row, [G, H] G gate rows."""
@@ -768,19 +763,15 @@ def _norm_workspace(T: int, gate_rows: int, H: int, device) -> torch.Tensor:
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
-def _pitch_or_0(t) -> int:
-    return 0 if t is None else _pitch(t)
-
-
 def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, stream=None):
     """The norm before the block: n = x * rstd(x) * weight of x [T, H] (weight float32 [H]).
     Returns (n [T, H], rstd float32 [T])."""
     lib = load()
-    T, H = _rows_2d(x, "x").shape
+    T, H, code, ldx = _rows(x, "x")
     weight = _per_row(weight, (H,), torch.float32, x.get_device(), "weight")
     n = torch.empty((T, H), dtype=x.dtype, device=x.device)
     rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    _check(lib.moe_norm_in(x.data_ptr(), _pitch(x), ACT_DTYPES[x.dtype], T, H, weight.data_ptr(), eps, n.data_ptr(),
+    _check(lib.moe_norm_in(x.data_ptr(), ldx, code, T, H, weight.data_ptr(), eps, n.data_ptr(),
                            rstd.data_ptr(), _stream_of(x, stream)), "moe_norm_in")
     return n, rstd
 
@@ -789,18 +780,17 @@ def moe_norm_in_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, 
                          dresidual: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Gradients of moe_norm_in: (dx [T, H] = dresidual + the norm's gradient, dweight float32 [H])."""
     lib = load()
-    T, H = _rows_2d(x, "x").shape
+    T, H, code, ldx = _rows(x, "x")
     index = x.get_device()
-    dn, dresidual = _norm_rows(dn, x, "dn"), _norm_rows(dresidual, x, "dresidual")
+    lddn, lddr = _rows_like(dn, x, "dn"), _rows_like(dresidual, x, "dresidual")
     rstd = _per_row(rstd, (T,), torch.float32, index, "rstd")
     weight = _per_row(weight, (H,), torch.float32, index, "weight")
     dx = torch.empty((T, H), dtype=x.dtype, device=x.device)
     dweight = torch.empty(H, dtype=torch.float32, device=x.device)
     ws = _norm_workspace(T, 0, H, x.device) if workspace is None else workspace
-    _check(lib.moe_norm_in_backward(dn.data_ptr(), _pitch(dn), _ptr(dresidual), _pitch_or_0(dresidual), x.data_ptr(),
-                                    _pitch(x), rstd.data_ptr(), ACT_DTYPES[x.dtype], T, H, weight.data_ptr(),
-                                    dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel(),
-                                    _stream_of(x, stream)), "moe_norm_in_backward")
+    _check(lib.moe_norm_in_backward(dn.data_ptr(), lddn, _ptr(dresidual), lddr, x.data_ptr(), ldx, rstd.data_ptr(),
+                                    code, T, H, weight.data_ptr(), dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), _stream_of(x, stream)), "moe_norm_in_backward")
     return dx, dweight
 
 
@@ -811,9 +801,9 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     [T] (one number a row) or [G, H] (each row serves T / G consecutive rows).  Returns
     (r, n, rstd_y, rstd_r); n and rstd_r are None without next_weight."""
     lib = load()
-    T, H = _rows_2d(x, "x").shape
+    T, H, code, ldx = _rows(x, "x")
     dev, index = x.device, x.get_device()
-    y = _norm_rows(y, x, "y")
+    ldy = _rows_like(y, x, "y")
     weight = _per_row(weight, (H,), torch.float32, index, "weight")
     next_weight = _per_row(next_weight, (H,), torch.float32, index, "next_weight")
     gate, gate_rows = _norm_gate(gate, T, H, index)
@@ -821,7 +811,7 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     rstd_y = torch.empty(T, dtype=torch.float32, device=dev)
     n = torch.empty_like(r) if next_weight is not None else None
     rstd_r = torch.empty_like(rstd_y) if next_weight is not None else None
-    _check(lib.moe_norm_out(x.data_ptr(), _pitch(x), y.data_ptr(), _pitch(y), ACT_DTYPES[x.dtype], T, H,
+    _check(lib.moe_norm_out(x.data_ptr(), ldx, y.data_ptr(), ldy, code, T, H,
                             weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight), eps,
                             r.data_ptr(), _ptr(n), rstd_y.data_ptr(), _ptr(rstd_r), _stream_of(x, stream)),
            "moe_norm_out")
@@ -836,15 +826,17 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
     """Gradients of moe_norm_out from dr (and dn, with r, rstd_r and next_weight): (dx, dy [T, H],
     dweight [H], dgate like gate, dnext_weight [H]); the last two None where there is none."""
     lib = load()
-    T, H = _rows_2d(y, "y").shape
+    T, H, code, ldy = _rows(y, "y")
     dev, index = y.device, y.get_device()
-    if len({t is None for t in (dn, rstd_r, next_weight)}) != 1 or (dn is not None and r is None):
-        raise ValueError("dn, r, rstd_r and next_weight are given together")
     if dn is None:
         r = None      # only the next norm's gradient reads it
+        if rstd_r is not None or next_weight is not None:
+            raise ValueError("dn, r, rstd_r and next_weight are given together")
         if dr is None:
             raise ValueError("no gradient arrives: give dr, dn or both")
-    dr, dn, r = _norm_rows(dr, y, "dr"), _norm_rows(dn, y, "dn"), _norm_rows(r, y, "r")
+    elif r is None or rstd_r is None or next_weight is None:
+        raise ValueError("dn, r, rstd_r and next_weight are given together")
+    lddr, lddn, ldr = _rows_like(dr, y, "dr"), _rows_like(dn, y, "dn"), _rows_like(r, y, "r")
     rstd_y = _per_row(rstd_y, (T,), torch.float32, index, "rstd_y")
     rstd_r = _per_row(rstd_r, (T,), torch.float32, index, "rstd_r")
     weight = _per_row(weight, (H,), torch.float32, index, "weight")
@@ -856,9 +848,9 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
     dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
     dnext = torch.empty_like(dweight) if next_weight is not None else None
     ws = _norm_workspace(T, gate_rows, H, dev) if workspace is None else workspace
-    _check(lib.moe_norm_out_backward(_ptr(dr), _pitch_or_0(dr), _ptr(dn), _pitch_or_0(dn), _ptr(r), _pitch_or_0(r),
-                                     y.data_ptr(), _pitch(y), rstd_y.data_ptr(), _ptr(rstd_r), ACT_DTYPES[y.dtype], T, H,
-                                     weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight),
-                                     dx.data_ptr(), dy.data_ptr(), dweight.data_ptr(), _ptr(dgate), _ptr(dnext),
-                                     ws.data_ptr(), ws.numel(), _stream_of(y, stream)), "moe_norm_out_backward")
+    _check(lib.moe_norm_out_backward(_ptr(dr), lddr, _ptr(dn), lddn, _ptr(r), ldr, y.data_ptr(), ldy, rstd_y.data_ptr(),
+                                     _ptr(rstd_r), code, T, H, weight.data_ptr(), _ptr(gate), gate_rows, residual_scale,
+                                     _ptr(next_weight), dx.data_ptr(), dy.data_ptr(), dweight.data_ptr(), _ptr(dgate),
+                                     _ptr(dnext), ws.data_ptr(), ws.numel(), _stream_of(y, stream)),
+           "moe_norm_out_backward")
     return dx, dy, dweight, dgate, dnext

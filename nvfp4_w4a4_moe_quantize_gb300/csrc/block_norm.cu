@@ -139,7 +139,8 @@ __device__ __forceinline__ void store_chunk(E* row, const Places& at, const Chun
     if (at.first < at.H)
 #pragma unroll
       for (int i = 0; i < Chunk<E>::kQ; ++i)
-        reinterpret_cast<uint4*>(row + at.first)[i] = make_uint4(c.w[4 * i], c.w[4 * i + 1], c.w[4 * i + 2], c.w[4 * i + 3]);
+        reinterpret_cast<uint4*>(row + at.first)[i] =
+            make_uint4(c.w[4 * i], c.w[4 * i + 1], c.w[4 * i + 2], c.w[4 * i + 3]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -601,7 +602,8 @@ cudaError_t forward_kernel(NormArgs& a, bool vec, cudaStream_t s) {
   const size_t row = static_cast<size_t>(a.H) * sizeof(E) * (kBranch ? 2 : 1);
   // (32768 x 2048 BF16: one stage 88 us, two 91 us; wider rows have one in either case)
   a.stages = ring_stages(weights, row, groups, 36 * 1024);
-  return start(block_norm_kernel<E, kBranch, kNext, true>, set[1], grid, threads, weights + a.stages * row * groups, s, a);
+  const size_t smem = weights + a.stages * row * groups;
+  return start(block_norm_kernel<E, kBranch, kNext, true>, set[1], grid, threads, smem, s, a);
 }
 
 template <typename E>
@@ -626,9 +628,10 @@ cudaError_t backward_kernel(NormBackwardArgs& a, bool vec, int64_t segments, cud
     return start(block_norm_backward_kernel<E, kBranch, kNext, false>, set[0], grid, threads,
                  weights > sums ? weights : sums, s, a);
   const size_t row = static_cast<size_t>(a.H) * sizeof(E) * (1 + (kBranch ? 1 : 0) + (kNext ? 2 : 0));
-  a.stages = ring_stages(weights, row, groups, threads > kNormThreads ? 200 * 1024 : 108 * 1024);   // one or two CTAs an SM
+  a.stages = ring_stages(weights, row, groups, threads > kNormThreads ? 200 * 1024 : 108 * 1024);   // 1 or 2 CTAs an SM
   const size_t smem = weights + a.stages * row * groups;
-  return start(block_norm_backward_kernel<E, kBranch, kNext, true>, set[1], grid, threads, smem > sums ? smem : sums, s, a);
+  return start(block_norm_backward_kernel<E, kBranch, kNext, true>, set[1], grid, threads, smem > sums ? smem : sums,
+               s, a);
 }
 
 template <typename E>

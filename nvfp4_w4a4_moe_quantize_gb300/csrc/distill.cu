@@ -16,7 +16,7 @@
 // The loss alone streams like the log probabilities; a bitmap of S in shared memory leaves the
 // listed tokens out.  With the gradient a row's slices lie in the shared memory of a cluster
 // between the sum and the gradient, so HBM sees the row read once and written once
-// (8192 x 131072 BF16, K = 64 with the tail: 738 us, 5.8 TB/s, 86% of a copy's rate; 1000 x 50021
+// (8192 x 131072 BF16, K = 64 with the tail: 706 us, 6.1 TB/s, 90% of a copy's rate; 1000 x 50021
 // float16, K = 100: 53 us, 3.8 TB/s).  What bounds it is the row's chain -- arrival, sum,
 // exchange, gradient -- of which an SM has three to four under way: warps wait at a barrier 5 of
 // 12 cycles, the issue slots are used to half.  Measured and not kept: the row read again from L2

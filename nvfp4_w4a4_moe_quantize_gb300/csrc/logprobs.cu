@@ -12,11 +12,11 @@
 // (value, lowest id).  A sort or a heap over the row is not needed, and no atomic decides an
 // order: a candidate's key is its value and id.
 //
-// Bound: HBM for the pass (8192 x 131072 BF16, a tenth of the rows ignored: 300 us, 6.4 TB/s of the
+// Bound: HBM for the pass (8192 x 131072 BF16, a tenth of the rows ignored: 288 us, 6.7 TB/s of the
 // rows read; backward 615 us, 6.9 TB/s read and written); what a list adds is latency at the end of
-// a row, hidden behind the other three CTAs of the SM in part (2048 x 131072: no list 95 us, 20
-// entries 124 us, 128 entries 139 us; of these the threads' bound costs 12, reading the cells
-// again 16, the sort 6).  One row is bound by latency: 131072 BF16 logits over the 8 CTAs
+// a row, hidden behind the other three CTAs of the SM in part (2048 x 131072: no list 93 us, 20
+// entries 120 us, 128 entries 135 us; of a row's 66000 cycles the bound takes 2400, the cells 1800, reading
+// them again 7200, the sort 2900).  One row is bound by latency: 131072 BF16 logits over the 8 CTAs
 // of a cluster with 20 entries 10 us.
 #include "launch.h"
 #include "status.cuh"
@@ -201,7 +201,8 @@ struct LogprobArgs {
 
 // One row a cluster of 1, 2, 4 or 8 CTAs; a CTA runs its part of the row's slices in turn.
 template <typename E, bool kEntropy, bool kTop>
-__global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kVocabThreads, kTop || sizeof(E) == 4 ? 4 : 6)
+    token_logprobs_kernel(const LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];   // TopSmem; a cluster's sums, by slice and thread
   __shared__ LogprobSmem sm;
   TopSmem& top = *reinterpret_cast<TopSmem*>(dyn);

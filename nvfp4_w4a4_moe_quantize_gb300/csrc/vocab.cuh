@@ -8,8 +8,9 @@
 // side in a cluster, and not on the row's address -- and so do a row's bits.
 //
 // These kernels are bound by instructions as much as by HBM: at 6.8 TB/s an SM receives 11.7 BF16
-// elements a cycle and issues 4 instructions for 32 lanes, so 11 an element are all it has.  So float32 arithmetic runs on pairs (add, mul and fma
-// .f32x2), maxima on packed words, and the running maximum is met once a batch of 32 elements.
+// elements a cycle and issues 4 instructions for 32 lanes, so 11 an element are all it has.  So
+// float32 arithmetic runs on pairs (add, mul and fma .f32x2), differences are taken from the 16-bit
+// type, maxima on packed words, and the running maximum is met once a batch of 32 elements.
 #pragma once
 #include <cfloat>
 #include <cooperative_groups.h>
