@@ -184,8 +184,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(t: torch.Tensor, stream=None) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _stream_of(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _on_stream(stream, call, args: dict):
+    """call(**args) as under torch.cuda.stream(stream): results, workspaces and dense copies are that
+    stream's memory too, since the current stream's memory would be handed out again while
+    the kernels still read it."""
+    with torch.cuda.stream(stream):
+        return call(**{**args, "stream": None})
 
 
 def _dev(t):
@@ -668,6 +676,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     float16 or float32; rows may be strided).  Returns (logprob, lse, entropy, top_logprobs,
     top_ids): float32 [T], [T], [T], [T, top_k] and int32 [T, top_k], None for what was not
     asked.  targets: int32 [T]; a row whose target is ignore_index is skipped (zeros)."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs, locals())
     lib = load()
     T, V, code, ld = _rows(logits, "logits")
     dev, index = logits.device, logits.get_device()
@@ -679,7 +689,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev) if top_k > 0 else None
     _check(lib.token_logprobs(logits.data_ptr(), code, T, V, ld, _ptr(targets),
                               ignore_index, scale, top_k, _ptr(logprob), lse.data_ptr(), _ptr(ent), _ptr(top_lp),
-                              _ptr(top_ids), _stream_of(logits, stream)), "token_logprobs")
+                              _ptr(top_ids), _stream_of(logits)), "token_logprobs")
     return logprob, lse, ent, top_lp, top_ids
 
 
@@ -689,6 +699,8 @@ def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, targets: to
                             out: torch.Tensor | None = None, stream=None):
     """dlogits [T, V] of sum(dlogprob * logprob + dentropy * entropy), with the forward's lse and
     entropy (all float32 [T]).  out may be the logits themselves."""
+    if stream is not None:
+        return _on_stream(stream, token_logprobs_backward, locals())
     lib = load()
     T, V, code, ld = _rows(logits, "logits")
     index = logits.get_device()
@@ -702,7 +714,7 @@ def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, targets: to
     ldd = _rows_like(out, logits, "out")
     _check(lib.token_logprobs_backward(logits.data_ptr(), code, T, V, ld, _ptr(targets),
                                        ignore_index, scale, _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy),
-                                       out.data_ptr(), ldd, _stream_of(logits, stream)),
+                                       out.data_ptr(), ldd, _stream_of(logits)),
            "token_logprobs_backward")
     return out
 
@@ -713,6 +725,8 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     none; values float32 [T, K]).  tail: the values are log probabilities over the whole
     vocabulary and the unlisted tokens count as one; else q = softmax(values).  Returns
     (loss, lse), float32 [T]."""
+    if stream is not None:
+        return _on_stream(stream, distill_topk, locals())
     lib = load()
     T, V, code, ld = _rows(logits, "logits")
     index, K = logits.get_device(), teacher_ids.shape[-1]
@@ -721,7 +735,7 @@ def distill_topk(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_values
     loss = torch.empty(T, dtype=torch.float32, device=logits.device)
     lse = torch.empty_like(loss)
     _check(lib.distill_topk(logits.data_ptr(), code, T, V, ld, ids.data_ptr(), values.data_ptr(), K, tail, scale,
-                            loss.data_ptr(), lse.data_ptr(), _stream_of(logits, stream)), "distill_topk")
+                            loss.data_ptr(), lse.data_ptr(), _stream_of(logits)), "distill_topk")
     return loss, lse
 
 
@@ -731,6 +745,8 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     """The loss of distill_topk and dlogits [T, V] = dloss * dloss/dlogits in one call (dloss
     float32 [T], None: ones; nothing of the forward is needed).  out may be the logits
     themselves.  Returns (loss, dlogits)."""
+    if stream is not None:
+        return _on_stream(stream, distill_topk_backward, locals())
     lib = load()
     T, V, code, ld = _rows(logits, "logits")
     index, K = logits.get_device(), teacher_ids.shape[-1]
@@ -743,7 +759,7 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     ldd = _rows_like(out, logits, "out")
     _check(lib.distill_topk_backward(logits.data_ptr(), code, T, V, ld, ids.data_ptr(), values.data_ptr(), K, tail,
                                      scale, _ptr(dloss), loss.data_ptr(), None, out.data_ptr(), ldd,
-                                     _stream_of(logits, stream)), "distill_topk_backward")
+                                     _stream_of(logits)), "distill_topk_backward")
     return loss, out
 
 
@@ -766,19 +782,23 @@ def _norm_workspace(T: int, gate_rows: int, H: int, device) -> torch.Tensor:
 def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, stream=None):
     """The norm before the block: n = x * rstd(x) * weight of x [T, H] (weight float32 [H]).
     Returns (n [T, H], rstd float32 [T])."""
+    if stream is not None:
+        return _on_stream(stream, moe_norm_in, locals())
     lib = load()
     T, H, code, ldx = _rows(x, "x")
     weight = _per_row(weight, (H,), torch.float32, x.get_device(), "weight")
     n = torch.empty((T, H), dtype=x.dtype, device=x.device)
     rstd = torch.empty(T, dtype=torch.float32, device=x.device)
     _check(lib.moe_norm_in(x.data_ptr(), ldx, code, T, H, weight.data_ptr(), eps, n.data_ptr(),
-                           rstd.data_ptr(), _stream_of(x, stream)), "moe_norm_in")
+                           rstd.data_ptr(), _stream_of(x)), "moe_norm_in")
     return n, rstd
 
 
 def moe_norm_in_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
                          dresidual: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Gradients of moe_norm_in: (dx [T, H] = dresidual + the norm's gradient, dweight float32 [H])."""
+    if stream is not None:
+        return _on_stream(stream, moe_norm_in_backward, locals())
     lib = load()
     T, H, code, ldx = _rows(x, "x")
     index = x.get_device()
@@ -790,7 +810,7 @@ def moe_norm_in_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, 
     ws = _norm_workspace(T, 0, H, x.device) if workspace is None else workspace
     _check(lib.moe_norm_in_backward(dn.data_ptr(), lddn, _ptr(dresidual), lddr, x.data_ptr(), ldx, rstd.data_ptr(),
                                     code, T, H, weight.data_ptr(), dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), _stream_of(x, stream)), "moe_norm_in_backward")
+                                    ws.numel(), _stream_of(x)), "moe_norm_in_backward")
     return dx, dweight
 
 
@@ -800,6 +820,8 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     next_weight the next block's input norm n = r * rstd(r) * next_weight.  gate: None, float32
     [T] (one number a row) or [G, H] (each row serves T / G consecutive rows).  Returns
     (r, n, rstd_y, rstd_r); n and rstd_r are None without next_weight."""
+    if stream is not None:
+        return _on_stream(stream, moe_norm_out, locals())
     lib = load()
     T, H, code, ldx = _rows(x, "x")
     dev, index = x.device, x.get_device()
@@ -813,7 +835,7 @@ def moe_norm_out(x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, gate: t
     rstd_r = torch.empty_like(rstd_y) if next_weight is not None else None
     _check(lib.moe_norm_out(x.data_ptr(), ldx, y.data_ptr(), ldy, code, T, H,
                             weight.data_ptr(), _ptr(gate), gate_rows, residual_scale, _ptr(next_weight), eps,
-                            r.data_ptr(), _ptr(n), rstd_y.data_ptr(), _ptr(rstd_r), _stream_of(x, stream)),
+                            r.data_ptr(), _ptr(n), rstd_y.data_ptr(), _ptr(rstd_r), _stream_of(x)),
            "moe_norm_out")
     return r, n, rstd_y, rstd_r
 
@@ -825,6 +847,8 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
                           workspace: torch.Tensor | None = None, stream=None):
     """Gradients of moe_norm_out from dr (and dn, with r, rstd_r and next_weight): (dx, dy [T, H],
     dweight [H], dgate like gate, dnext_weight [H]); the last two None where there is none."""
+    if stream is not None:
+        return _on_stream(stream, moe_norm_out_backward, locals())
     lib = load()
     T, H, code, ldy = _rows(y, "y")
     dev, index = y.device, y.get_device()
@@ -851,6 +875,6 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
     _check(lib.moe_norm_out_backward(_ptr(dr), lddr, _ptr(dn), lddn, _ptr(r), ldr, y.data_ptr(), ldy, rstd_y.data_ptr(),
                                      _ptr(rstd_r), code, T, H, weight.data_ptr(), _ptr(gate), gate_rows, residual_scale,
                                      _ptr(next_weight), dx.data_ptr(), dy.data_ptr(), dweight.data_ptr(), _ptr(dgate),
-                                     _ptr(dnext), ws.data_ptr(), ws.numel(), _stream_of(y, stream)),
+                                     _ptr(dnext), ws.data_ptr(), ws.numel(), _stream_of(y)),
            "moe_norm_out_backward")
     return dx, dy, dweight, dgate, dnext

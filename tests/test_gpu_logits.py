@@ -548,6 +548,33 @@ def test_another_stream_and_a_graph(cuda_lib):
         assert torch.equal(a, b)
 
 
+def test_copies_belong_to_the_given_stream(cuda_lib):
+    """Dense copies of strided companions are read on the given stream, after the call has returned:
+    nothing that the current stream allocates meanwhile may take their place."""
+    T, V, K = 64, 4001, 8
+    z, rng = logits(T, V, 5)
+    zt = store(z, "bf16")
+    y = torch.from_numpy(rng.integers(1, V, T).astype(np.int32)).cuda()
+    _, _, _, values, ids = cuda_lib.token_logprobs(zt, top_k=K)
+    strided = lambda t: torch.stack((t, t), -1)[..., 0]
+    y2, ids2, values2 = strided(y), strided(ids), strided(values)
+    assert not (y2.is_contiguous() or ids2.is_contiguous() or values2.is_contiguous())
+    want = cuda_lib.token_logprobs(zt, y2)[0], *cuda_lib.distill_topk_backward(zt, ids2, values2)
+    torch.zeros(T, dtype=torch.int32, device="cuda")   # every kernel has run once: loading one could wait
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)   # some 50 ms, in which the other stream gets its work done
+    lp = cuda_lib.token_logprobs(zt, y2, stream=s)[0]
+    got = lp, *cuda_lib.distill_topk_backward(zt, ids2, values2, None, True, 1.0, None, s)
+    others = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (T, T * K) for _ in range(64)]
+    assert not s.query()
+    s.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert not any(o.any() for o in others)
+
+
 def test_refusals(cuda_lib):
     z = torch.zeros(4, 64, device="cuda")
     y = torch.zeros(4, dtype=torch.int32, device="cuda")

@@ -177,6 +177,30 @@ def test_empty_batch(cuda_lib):
     assert not cuda_lib.moe_norm_in_backward(x, x, ry, w)[1].any()
 
 
+def test_norm_copies_belong_to_the_given_stream(cuda_lib):
+    """Dense copies of strided weights, read on the given stream after the call has returned."""
+    T, H = 64, 1024
+    x = torch.randn(T, H, device="cuda")
+    w = torch.rand(H, device="cuda") + 0.5
+    w2 = torch.stack((w, w), -1)[..., 0]
+    assert not w2.is_contiguous()
+    want, rstd = cuda_lib.moe_norm_in(x, w2)
+    want_back = cuda_lib.moe_norm_in_backward(x, x, rstd, w2)
+    torch.zeros(H, device="cuda")   # every kernel has run once: loading one could wait
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)   # some 50 ms, in which the other stream gets its work done
+    got = cuda_lib.moe_norm_in(x, w2, stream=s)[0]
+    got_back = cuda_lib.moe_norm_in_backward(x, x, rstd, w2, stream=s)
+    others = [torch.zeros(H, device="cuda") for _ in range(64)]
+    assert not s.query()
+    s.synchronize()
+    for a, b in zip((want, *want_back), (got, *got_back)):
+        assert torch.equal(a, b)
+    assert not any(o.any() for o in others)
+
+
 def test_norm_refusals(cuda_lib):
     x = torch.zeros(6, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, device="cuda")
