@@ -771,6 +771,8 @@ def _norm_gate(gate, T: int, H: int, index: int):
         return None, 0
     if gate.dim() == 1:
         return _per_row(gate, (T,), torch.float32, index, "gate"), 0
+    if gate.dim() != 2 or (gate.shape[0] == 0 and T > 0):
+        raise ValueError(f"gate must be [{T}] or [G, {H}] with G at least 1")
     return _per_row(gate, (gate.shape[0], H), torch.float32, index, "gate"), gate.shape[0]
 
 

@@ -219,3 +219,13 @@ def test_norm_refusals(cuda_lib):
                                                                                           device="cuda"))):
         with pytest.raises(cuda_lib.NVFP4Error):
             bad()
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (), (1, 6, 64)])
+def test_norm_gate_without_rows_is_refused(cuda_lib, shape):
+    x = torch.ones(6, 64, device="cuda")
+    w, gate = torch.ones(64, device="cuda"), torch.ones(shape, device="cuda")
+    with pytest.raises(ValueError):
+        cuda_lib.moe_norm_out(x, x, w, gate=gate)
+    with pytest.raises(ValueError):
+        cuda_lib.moe_norm_out_backward(x, x, torch.ones(6, device="cuda"), w, gate=gate)
