@@ -776,7 +776,11 @@ def _norm_gate(gate, T: int, H: int, index: int):
     return _per_row(gate, (gate.shape[0], H), torch.float32, index, "gate"), gate.shape[0]
 
 
-def _norm_workspace(T: int, gate_rows: int, H: int, device) -> torch.Tensor:
+def _norm_workspace(given, T: int, gate_rows: int, H: int, device) -> torch.Tensor:
+    if given is not None:
+        if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be dense uint8 on the device of the rows")
+        return given   # its size is checked with the other arguments
     n = int(load().nvfp4_workspace_size(OP_NORM_BACKWARD, T, gate_rows, 0, H, 0))
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
@@ -809,7 +813,7 @@ def moe_norm_in_backward(dn: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, 
     weight = _per_row(weight, (H,), torch.float32, index, "weight")
     dx = torch.empty((T, H), dtype=x.dtype, device=x.device)
     dweight = torch.empty(H, dtype=torch.float32, device=x.device)
-    ws = _norm_workspace(T, 0, H, x.device) if workspace is None else workspace
+    ws = _norm_workspace(workspace, T, 0, H, x.device)
     _check(lib.moe_norm_in_backward(dn.data_ptr(), lddn, _ptr(dresidual), lddr, x.data_ptr(), ldx, rstd.data_ptr(),
                                     code, T, H, weight.data_ptr(), dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(),
                                     ws.numel(), _stream_of(x)), "moe_norm_in_backward")
@@ -873,7 +877,7 @@ def moe_norm_out_backward(dr: torch.Tensor | None, y: torch.Tensor, rstd_y: torc
     dweight = torch.empty(H, dtype=torch.float32, device=dev)
     dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
     dnext = torch.empty_like(dweight) if next_weight is not None else None
-    ws = _norm_workspace(T, gate_rows, H, dev) if workspace is None else workspace
+    ws = _norm_workspace(workspace, T, gate_rows, H, dev)
     _check(lib.moe_norm_out_backward(_ptr(dr), lddr, _ptr(dn), lddn, _ptr(r), ldr, y.data_ptr(), ldy, rstd_y.data_ptr(),
                                      _ptr(rstd_r), code, T, H, weight.data_ptr(), _ptr(gate), gate_rows, residual_scale,
                                      _ptr(next_weight), dx.data_ptr(), dy.data_ptr(), dweight.data_ptr(), _ptr(dgate),

@@ -229,3 +229,20 @@ def test_norm_gate_without_rows_is_refused(cuda_lib, shape):
         cuda_lib.moe_norm_out(x, x, w, gate=gate)
     with pytest.raises(ValueError):
         cuda_lib.moe_norm_out_backward(x, x, torch.ones(6, device="cuda"), w, gate=gate)
+
+
+def test_norm_workspace_is_checked(cuda_lib):
+    """Only host-side refusals: memory of the host, another type's elements, bytes apart."""
+    x, w = torch.ones(6, 64, device="cuda"), torch.ones(64, device="cuda")
+    n = cuda_lib.load().nvfp4_workspace_size(cuda_lib.OP_NORM_BACKWARD, 6, 0, 0, 64, 0)
+    rstd = torch.ones(6, device="cuda")
+    for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(n, device="cuda"),
+                torch.empty(n, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError):
+            cuda_lib.moe_norm_in_backward(x, x, rstd, w, workspace=bad)
+        with pytest.raises(ValueError):
+            cuda_lib.moe_norm_out_backward(x, x, rstd, w, workspace=bad)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for a, b in zip(cuda_lib.moe_norm_in_backward(x, x, rstd, w, workspace=ws),
+                    cuda_lib.moe_norm_in_backward(x, x, rstd, w)):
+        assert torch.equal(a, b)
