@@ -371,9 +371,12 @@ struct Stage {
   __device__ __forceinline__ char* at(int e) const { return mem + lead + (e - lo) * static_cast<int>(sizeof(E)); }
   __device__ __forceinline__ bool has(int e) const { return e >= lo && e < hi; }
   __device__ __forceinline__ uint16_t* word(int e) const { return reinterpret_cast<uint16_t*>(at(e)); }
-  // One warp: whole 16-byte words by a bulk copy, the ends element by element.
+  // One warp: whole 16-byte words by a bulk copy, the ends element by element.  The row that lay here
+  // was read and in places written by plain accesses; the fence orders the copy behind them.
   __device__ __forceinline__ void fetch(const E* z, uint64_t* bar) const {
     const int lane = threadIdx.x & 31;
+    fence_proxy_async_smem();
+    __syncwarp();
     const int bytes = (hi - lo) * static_cast<int>(sizeof(E));
     const int head = min(bytes, static_cast<int>((16u - lead) & 15u)), body = (bytes - head) & ~15;
     if (lane == 0) {
