@@ -498,6 +498,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_ker
     const auto open_row = [&](int i) {
       if (kStage) {
         mbar_wait(bar_of(i), (plan.stages == 2 ? i >> 1 : i) & 1, a.status, &sm.abort);
+        __syncwarp();   // the row's ends came by plain stores of single lanes; take_out's lanes write over them
         const bool twice = list.take_out(stage_of(i));
         if (lane == 0) sm.list[i & 1].twice = twice;
         __syncwarp();

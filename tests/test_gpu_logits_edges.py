@@ -1,0 +1,44 @@
+"""Operators on rows of logits at the places where a row is cut: ends of slices, parts of a row in
+several CTAs, rows that follow one another in a cluster.  Bounds as in test_gpu_logits."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_logits import DT, check_distill, logits, store, teacher
+
+pytestmark = pytest.mark.gpu
+
+
+def slice_ends(V, width=4):
+    """The first and last `width` tokens of every slice of a row."""
+    slices = 8 if V >= 65536 else 4 if V >= 32768 else 2 if V >= 16384 else 1
+    chunks = -(-V // 8)
+    per = -(-chunks // slices)
+    out = []
+    for s in range(slices):
+        lo, hi = min(V, 8 * s * per), min(V, 8 * (s + 1) * per)
+        out += [*range(lo, lo + width), *range(hi - width, hi)]
+    return np.unique(out)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [9003, 40005, 70001])
+def test_listed_tokens_at_the_ends_of_a_slice(cuda_lib, tail, dtype, V):
+    """A row's ends, which do not arrive in whole 16-byte words, hold listed tokens: at every
+    alignment the row gives what it gives aligned."""
+    T = 6
+    z, rng = logits(T, V, V)
+    ends = slice_ends(V)
+    z[:, ends] = rng.normal(4.0, 2.0, (T, ends.size))   # mass that would be missed in the tail's sum
+    ids = np.stack([rng.permutation(ends) for _ in range(T)]).astype(np.int32)
+    _, val = teacher(T, V, ends.size, rng)
+    w = rng.normal(size=T)
+    want_loss, want = check_distill(cuda_lib, store(z, dtype), ids, val, tail, w=w)
+    it, vt = torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda()
+    wt = torch.from_numpy(w.astype(np.float32)).cuda()
+    for lead in range(1, 8):
+        for pad in (0, 8):
+            loss, d = cuda_lib.distill_topk_backward(store(z, dtype, pad, lead), it, vt, wt, tail)
+            assert torch.equal(loss, want_loss) and torch.equal(d, want)
+    assert cuda_lib.nvfp4_status_check() == 0
