@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_ker
         list.gather(a, z_of(i + 1));
         list.template reduce<!kStage>(c1, marks_of(i + 1), sm.list[(i + 1) & 1]);
       }
-      mbar_wait(&sm.joined[i & 1], (i >> 1) & 1, a.status, &sm.abort);
+      mbar_wait_cluster(&sm.joined[i & 1], (i >> 1) & 1, a.status, &sm.abort);   // messages of other CTAs are read next
       const Message* flat = &sm.part[i & 1][0][0];
       const int n = slices * kVocabWarps;
       Stats x = empty_stats(), y = empty_stats();

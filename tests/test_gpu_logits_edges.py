@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_logits import DT, check_distill, logits, store, teacher
+from test_gpu_logits import check_distill, logits, store, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -41,4 +41,25 @@ def test_listed_tokens_at_the_ends_of_a_slice(cuda_lib, tail, dtype, V):
         for pad in (0, 8):
             loss, d = cuda_lib.distill_topk_backward(store(z, dtype, pad, lead), it, vt, wt, tail)
             assert torch.equal(loss, want_loss) and torch.equal(d, want)
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype,V,T", [("bf16", 131072, 1300), ("f32", 70001, 640), ("f16", 33001, 200)])
+def test_rows_of_a_cluster_exchange_their_own_sums(cuda_lib, tail, dtype, V, T):
+    """Neighbouring rows whose slices' maxima differ by tens, over several CTAs: every row of a long
+    batch gives what it gives alone, so no CTA took another row's message for its own."""
+    n, K = 8, 24
+    z, rng = logits(n, V, V)
+    z += 15.0 * (-1.0) ** np.arange(n)[:, None]                        # neighbours differ by 30,
+    z += np.repeat(rng.normal(0, 10.0, (n, 64)), -(-V // 64), 1)[:, :V]   # and a row's slices by tens
+    ids, val = teacher(n, V, K, rng)
+    it, vt, zt = torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), store(z, dtype)
+    one = [cuda_lib.distill_topk_backward(zt[r:r + 1], it[r:r + 1], vt[r:r + 1], None, tail) for r in range(n)]
+    few_loss, few = torch.cat([o[0] for o in one]), torch.cat([o[1] for o in one])
+    check_distill(cuda_lib, zt, ids, val, tail)
+    pick = torch.arange(T, device="cuda") % n
+    for _ in range(3):
+        loss, d = cuda_lib.distill_topk_backward(zt[pick], it[pick], vt[pick], None, tail)
+        assert torch.equal(loss, few_loss[pick]) and torch.equal(d, few[pick])
     assert cuda_lib.nvfp4_status_check() == 0
