@@ -597,8 +597,10 @@ nvfp4_status distill_topk(const void* logits, nvfp4_act_dtype dtype, int64_t T, 
 
 /* The same loss and its gradient in one call (nothing of the forward is needed):
  *   dlogits[t, j] = dloss[t] dloss_t/dlogits_tj, rounded once to `dtype`:
- *     scale dloss (p_j - q_j) at listed tokens; elsewhere scale dloss p_j, and with the tail
- *     scale dloss p_j (1 - q_r / p_r); 0 at excluded tokens.
+ *     scale dloss (M p_j - q_j) at listed tokens; elsewhere scale dloss M p_j, and with the tail
+ *     scale dloss p_j (M - q_r / p_r); 0 at excluded tokens.  M is the teacher's mass that the
+ *     loss counts: 1, but with the tail sum q where that is above 1 or where no unlisted token
+ *     is allowed.
  *   dloss: device float [T] or NULL (ones).  dlogits as in token_logprobs_backward. */
 nvfp4_status distill_topk_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,
                                    const int32_t* teacher_ids, const float* teacher_values, int32_t K, int tail,

@@ -4,7 +4,9 @@
 //   c = scale z, lse = ln sum exp(c), p = exp(c - lse);  S = the teacher's list, values t
 //   tail off: q = softmax(t over S);   tail on: q = exp(t), q_r = max(0, 1 - sum q)
 //   L = sum_S q (ln q - (c - lse))  [+ q_r (ln q_r - ln p_r), p_r = the student's mass outside S]
-//   dL/dc = p - q on S;  outside p, or with the tail p - q_r p / p_r = exp(c - lse_r) (p_r - q_r)
+//   dL/dc = M p - q on S;  outside M p, or with the tail M p - q_r p / p_r = exp(c - lse_r) (M p_r - q_r)
+//   M = the mass that L counts: 1, but with the tail sum q where that is above 1 or where no token outside
+//   S is allowed (p_r = 0: nothing stands for the rest, and its term is left out of L)
 //
 // With the tail, the sum over the tokens outside S is taken on its own, with its own running
 // maximum: 1 - sum_S p would cancel when the student's mass lies on S.  lse then is that of the
@@ -58,7 +60,7 @@ struct ListSmem {
   int twice;   // one of the ids in this CTA's slices stands there twice
 };
 // What the row's sums give: outside the list the gradient is coef 2^((z - mb) c1); at a listed token
-// p = inv 2^((z - m) c1).  With the tail, st covers the tokens outside the list.
+// M p = inv 2^((z - m) c1).  With the tail, st covers the tokens outside the list.
 struct RowResult {
   float mb, coef, m, inv;
   float rest, total;   // 2^((mb - m) c1) and the sum over all tokens, both relative to m
@@ -240,20 +242,21 @@ struct ListRegs {
 template <bool kTail>
 __device__ __forceinline__ RowResult finish_row(const Stats& st, const ListSmem& l, float c1) {
   RowResult r;
+  const float mass = !kTail ? 1.f : st.s == 0.f ? l.Q : fmaxf(1.f, l.Q);   // M
   r.mb = st.m;
   if (kTail) {
     r.m = fmaxf(l.mz, st.m);
     r.rest = ex2((st.m - r.m) * c1);
     r.total = fmaf(r.rest, st.s, l.s == 0.f ? 0.f : ex2((l.mz - r.m) * c1) * l.s);
-    // (p_r - q_r) / sum outside the list
-    r.coef = st.s == 0.f ? 0.f : r.rest * rcp(r.total) - fmaxf(0.f, 1.f - l.Q) * rcp(st.s);
+    // (M p_r - q_r) / sum outside the list
+    r.coef = st.s == 0.f ? 0.f : mass * r.rest * rcp(r.total) - fmaxf(0.f, 1.f - l.Q) * rcp(st.s);
   } else {
     r.m = st.m;
     r.rest = 1.f;
     r.total = st.s;
     r.coef = st.s == 0.f ? 0.f : rcp(st.s);
   }
-  r.inv = r.total == 0.f ? 0.f : rcp(r.total);
+  r.inv = r.total == 0.f ? 0.f : mass * rcp(r.total);
   return r;
 }
 struct RowLoss {
@@ -278,7 +281,7 @@ __device__ __forceinline__ RowLoss row_loss(const Stats& st, const RowResult& r,
   return o;
 }
 
-// The gradient at entry j of the list: w (p - q), 0 at an excluded token.
+// The gradient at entry j of the list: w (M p - q), 0 at an excluded token.
 __device__ __forceinline__ float listed_gradient(const ListSmem& l, int j, const RowResult& r, float c1, float w) {
   const float z = l.z[j];
   return z == -INFINITY ? 0.f : w * (ex2((z - r.m) * c1) * r.inv - l.q[j]);

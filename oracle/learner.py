@@ -77,7 +77,7 @@ def distill(z, ids, values, tail=True, scale=1.0):
         q = np.exp(v) if tail else np.exp(v - v.max()) / np.exp(v - v.max()).sum()
         on = q > 0
         loss[t] = np.sum(q[on] * (np.log(q[on]) - lp[t, j[on]]))
-        grad[t] = p[t]
+        mass = q.sum()      # the teacher's mass that the loss counts
         if tail:
             listed = np.zeros(V, bool)
             listed[j] = True
@@ -86,6 +86,8 @@ def distill(z, ids, values, tail=True, scale=1.0):
             if pr > 0 and qr > 0:
                 loss[t] += qr * (np.log(qr) - np.log(pr))
                 grad[t][~listed] -= qr * p[t][~listed] / pr
+                mass += qr
+        grad[t] += mass * p[t]
         grad[t][j] -= q
     grad[np.isneginf(z)] = 0.0
     return loss, grad * scale, lse

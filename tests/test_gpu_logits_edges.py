@@ -63,3 +63,46 @@ def test_rows_of_a_cluster_exchange_their_own_sums(cuda_lib, tail, dtype, V, T):
         loss, d = cuda_lib.distill_topk_backward(zt[pick], it[pick], vt[pick], None, tail)
         assert torch.equal(loss, few_loss[pick]) and torch.equal(d, few[pick])
     assert cuda_lib.nvfp4_status_check() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V,K", [(5, 3), (1003, 20), (33001, 100), (131072, 64)])
+def test_distill_masses_that_do_not_add_up_to_one(cuda_lib, dtype, V, K):
+    """With the tail: the list alone is allowed and holds 0.8 or 1.3; it holds 1.3 in an open row; it
+    holds 1.3 and one of its tokens is excluded by the student without having mass.  check_distill's
+    bound takes p twice over, which covers 1.3 p with the rounding of 1.3, (K / 8 + 16) u."""
+    z, rng = logits(4, V, V + K)
+    ids, val = teacher(4, V, K, rng)
+    for r in (0, 1):
+        keep = z[r, ids[r]].copy()
+        z[r] = -np.inf
+        z[r, ids[r]] = np.where(np.isfinite(keep), keep, 0.0)
+    val[1:] += np.float32(np.log(1.3 / 0.8))
+    val[3, 1] = -np.inf
+    z[3, ids[3, 1]] = -np.inf
+    zt = store(z, dtype)
+    w = np.array([1.0, -0.5, 2.0, 1.0])
+    _, d = check_distill(cuda_lib, zt, ids, val, True, 1.3, w)
+    if dtype == "f32":   # the loss does not change with a shift of the row
+        assert (d.double().sum(1).abs() < 1e-4).all()
+
+
+def test_distill_gradient_by_differences_where_the_masses_do_not_add_up(cuda_lib):
+    """As test_gradient_by_differences, for lists of more than one and rows of the list alone."""
+    V, K = 2003, 40
+    z, rng = logits(6, V, 8)
+    ids, val = teacher(6, V, K, rng)
+    val[3:] += np.float32(np.log(1.4 / 0.8))
+    for r in (0, 1, 5):
+        keep = z[r, ids[r]].copy()
+        z[r] = -np.inf
+        z[r, ids[r]] = keep
+    zt, it, vt = store(z, "f32"), torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda()
+    w = torch.rand(6, generator=torch.Generator().manual_seed(1)).cuda()
+    _, d = cuda_lib.distill_topk_backward(zt, it, vt, w)
+    step = 2.0 ** -5
+    for seed in range(3):
+        dirn = torch.randn(zt.shape, generator=torch.Generator().manual_seed(10 + seed)).cuda()
+        lo = lambda x: (w * cuda_lib.distill_topk(x, it, vt)[0]).double().sum().item()
+        num = (lo(zt + step * dirn) - lo(zt - step * dirn)) / (2 * step)
+        assert abs(num - (d.double() * dirn.double()).sum().item()) < 6 * 4e-6 / step + step ** 2 * 10

@@ -96,3 +96,17 @@ def test_norm_gradients_by_differences(kind):
     np.testing.assert_allclose(dnext, _differences(lambda v: f(wn=v), wn), atol=1e-7)
     if gate is not None:
         np.testing.assert_allclose(dg, _differences(lambda v: f(gate=v), gate), atol=1e-7)
+
+
+def test_distill_gradient_where_the_masses_do_not_add_up_to_one():
+    """With the tail: a mask that leaves the list alone while the list's mass is below one (nothing stands
+    for the rest), a list of more than one, and both."""
+    z, _ = _rows(5, T=4, V=9)
+    z[[0, 2], 3:] = -np.inf
+    z[0, :3] = [1.0, 2.0, 0.5]
+    ids = np.tile([0, 1, 2], (4, 1))
+    q = np.array([[0.4, 0.3, 0.1], [0.6, 0.5, 0.2], [0.6, 0.5, 0.2], [0.4, 0.3, 0.1]])
+    grad = O.distill(z, ids, np.log(q), True, 1.3)[1]
+    np.testing.assert_allclose(grad, _differences(lambda x: O.distill(x, ids, np.log(q), True, 1.3)[0].sum(), z),
+                               atol=1e-8)
+    np.testing.assert_allclose(grad.sum(1), 0.0, atol=1e-14)   # the loss does not change with a shift of the row
