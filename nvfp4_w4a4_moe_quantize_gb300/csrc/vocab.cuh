@@ -324,8 +324,9 @@ struct Running {
     }
     if constexpr (kEntropy && sizeof(E) == 2) {
       // Excluded tokens far below the maximum: as a far, finite value they add 0 to s and u, without a
-      // clamp of every t.  2^-200 is 0 and kFar c1 finite.
-      if ((Packed<E>::kFarValue - m) * c1 < -200.f && c1 < 1e6f) {
+      // clamp of every t.  2^-200 is 0; down to -1e38 every t is finite (0 * inf would be NaN).
+      const float far = (Packed<E>::kFarValue - m) * c1;
+      if (far < -200.f && far > -1e38f) {
         sum<true>(raw, left, c1);
         return cm;
       }

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_logits import check_distill, logits, store, teacher
+from test_gpu_logits import check_distill, check_forward, logits, near, store, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,15 @@ def test_distill_gradient_by_differences_where_the_masses_do_not_add_up(cuda_lib
         lo = lambda x: (w * cuda_lib.distill_topk(x, it, vt)[0]).double().sum().item()
         num = (lo(zt + step * dirn) - lo(zt - step * dirn)) / (2 * step)
         assert abs(num - (d.double() * dirn.double()).sum().item()) < 6 * 4e-6 / step + step ** 2 * 10
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [3001, 40009])
+def test_entropy_of_rows_with_a_huge_maximum(cuda_lib, dtype, V):
+    """A maximum near the type's largest value: the others' distance from it is beyond float32, their
+    probability and their part of the entropy are zero."""
+    z, rng = logits(4, V, V, masked=0.2)
+    y = rng.integers(0, V, 4).astype(np.int32)
+    z[np.arange(4), y] = [3.3e38, 2.5e38, 1e38, 1e33]
+    got, ref = check_forward(cuda_lib, store(z, dtype), y, 1.0, 0)
+    assert (got[2] == 0).all() and (got[0] == 0).all() and (ref["entropy"] == 0).all()
