@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(
     for (int i = 0; i < 4; ++i) {
       const float2 lt = unpack2(fma2(z8.pair(i), cc, ll));
       const F2 p = pack2(ex2(lt.x), ex2(lt.y));
-      const F2 f = kEntropy ? fma2(bb, pack2(fmaxf(lt.x, -1e30f), fmaxf(lt.y, -1e30f)), aa) : aa;
+      // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from B * inf
+      const F2 f = kEntropy ? fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa) : aa;
       const float2 d = unpack2(mul2(p, f));
       v[2 * i] = d.x;
       v[2 * i + 1] = d.y;

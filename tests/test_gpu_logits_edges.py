@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_logits import check_distill, check_forward, logits, near, store, teacher
+from test_gpu_logits import check_backward, check_distill, check_forward, logits, near, store, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -106,6 +106,17 @@ def test_distill_gradient_by_differences_where_the_masses_do_not_add_up(cuda_lib
         lo = lambda x: (w * cuda_lib.distill_topk(x, it, vt)[0]).double().sum().item()
         num = (lo(zt + step * dirn) - lo(zt - step * dirn)) / (2 * step)
         assert abs(num - (d.double() * dirn.double()).sum().item()) < 6 * 4e-6 / step + step ** 2 * 10
+
+
+@pytest.mark.parametrize("h,scale", [(1e10, 1.0), (1e8, 1e3)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_entropy_gradient_of_large_weight_at_excluded_tokens(cuda_lib, h, scale, dtype):
+    """Excluded tokens have no gradient however large its weight is."""
+    z, rng = logits(5, 6007, 23, masked=0.4)
+    zt = store(z, dtype)
+    y = rng.integers(0, 6007, 5).astype(np.int32)
+    d = check_backward(cuda_lib, zt, y, rng.normal(size=5), h * (1.0 + rng.random(5)), scale)
+    assert torch.isfinite(d).all() and not d[torch.isneginf(zt)].any() and d.any()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
