@@ -509,16 +509,18 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(
   // nothing to learn from the row: ignored, or nothing above the lowest values (a lse of that
   // size has lost ln s, and p with it)
   const bool skip = (a.targets != nullptr && y == a.ignore) || lse < -1e30f;
-  const float c1 = a.scale * kLog2e, l1 = -lse * kLog2e;
-  // with t = log2 p:  dz = p (A + B t), + scale g at the target
+  // with t = log2 p:  dz = p (A + B t), + scale g at the target.  ln p = scale z - lse is rounded once and
+  // brought to base 2 after that: scale log2(e) and lse log2(e), rounded first, would each add a rounding of
+  // lse's size to lse's own
   const float A = -a.scale * (g + (kEntropy ? h * a.entropy[t] : 0.f)), B = -a.scale * h * kLn2;
-  const F2 cc = pack2(c1, c1), ll = pack2(l1, l1), aa = pack2(A, A), bb = pack2(B, B);
+  const F2 cc = pack2(a.scale, a.scale), ll = pack2(-lse, -lse), to2 = pack2(kLog2e, kLog2e);
+  const F2 aa = pack2(A, A), bb = pack2(B, B);
   const float zy = a.scale * g;
   map_row<E, 4>(z, a.V, out, lo, hi, [&](int e0, const Chunk<E>& z8, float(&v)[8]) {
     const unsigned at = y - e0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 lt = unpack2(fma2(z8.pair(i), cc, ll));
+      const float2 lt = unpack2(mul2(fma2(z8.pair(i), cc, ll), to2));
       const F2 p = pack2(ex2(lt.x), ex2(lt.y));
       // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from B * inf
       const F2 f = kEntropy ? fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa) : aa;

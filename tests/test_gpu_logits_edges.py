@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_logits import check_backward, check_distill, check_forward, logits, near, store, teacher
+from oracle import learner as O
+from test_gpu_logits import U, check_backward, check_distill, check_forward, eps, f64, logits, near, store, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +130,22 @@ def test_entropy_of_rows_with_a_huge_maximum(cuda_lib, dtype, V):
     z[np.arange(4), y] = [3.3e38, 2.5e38, 1e38, 1e33]
     got, ref = check_forward(cuda_lib, store(z, dtype), y, 1.0, 0)
     assert (got[2] == 0).all() and (got[0] == 0).all() and (ref["entropy"] == 0).all()
+
+
+@pytest.mark.parametrize("scale", [0.70948, 1.0, 1.4443842, 1.4487727])
+def test_backward_of_rows_far_from_zero(cuda_lib, scale):
+    """A probability recomputed from lse carries lse's own rounding and no other of that size: u |lse|
+    relatively, beside what rows near zero have (eps, 84 u, 4 u |ln p|)."""
+    T, V = 256, 1003
+    z, rng = logits(T, V, 77)
+    z += (np.exp(rng.uniform(np.log(1e4), np.log(1e6), T)) * rng.choice([-1.0, 1.0], T))[:, None]
+    zt = store(z, "f32")
+    y = torch.from_numpy(rng.integers(0, V, T).astype(np.int32)).cuda()
+    g = np.float32(rng.normal(size=T)).astype(np.float64)
+    _, lse, _, _, _ = cuda_lib.token_logprobs(zt, y, scale=scale)
+    got = f64(cuda_lib.token_logprobs_backward(zt, lse, y, torch.from_numpy(g.astype(np.float32)).cuda(), scale=scale))
+    s = float(np.float32(scale))
+    lp, p, l = O.softmax_stats(f64(zt) * s)
+    ref = O.token_logprobs_backward(f64(zt), y.cpu().numpy(), g, None, s)
+    rel = np.expm1(eps(V) + U * np.abs(l)[:, None] + 84 * U + 4 * U * np.abs(lp))
+    near(got, ref, s * np.abs(g)[:, None] * p * rel + 4 * U * np.abs(ref) + 1e-37)
