@@ -564,9 +564,10 @@ nvfp4_status token_logprobs(const void* logits, nvfp4_act_dtype dtype, int64_t T
 
 /* The gradient of sum_t dlogprob[t] logprob[t] + dentropy[t] entropy[t]:
  *   dlogits[t, j] = scale (dlogprob (1[j = target] - p_j) - dentropy p_j (ln p_j + entropy)),
- * zero in ignored rows, in rows without an allowed token, in rows with lse < -1e30 (nothing but a
- * mask's lowest values, whose p a float32 lse no longer holds) and at excluded tokens.  p_j is
- * recomputed from lse and carries its rounding, 2^-24 |lse| relatively.
+ * zero in ignored rows, in rows without an allowed token, in rows with lse < -2^24 (nothing but a
+ * mask's values, lowest or -1e9 added to every token: a float32 lse of that size no longer holds p)
+ * and at excluded tokens.  p_j is recomputed from lse and carries its rounding, 2^-24 |lse|
+ * relatively.
  *   lse, entropy: the forward's; targets and dlogprob, entropy and dentropy: device or NULL
  *     (dlogprob needs targets, dentropy needs entropy).  A target that the forward refused
  *     adds nothing.

@@ -492,6 +492,7 @@ struct LogprobBackwardArgs {
 };
 
 constexpr int kBackwardTile = 16384;   // elements of a row a CTA
+constexpr float kLowestLse = -16777216.f;   // -2^24: below, float32 is 2 and more apart, and p = exp(c - lse) lost
 
 // One exponential an element; the tiles are independent, so the loads of 4 chunks a thread and the CTAs of
 // an SM cover the latency (8192 x 131072 BF16: 615 us, 6.98 TB/s, the rate of a copy).
@@ -506,9 +507,9 @@ __global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(
   // a target that the forward refused adds nothing
   const float g = a.dlogprob != nullptr && y >= 0 && y < a.V ? a.dlogprob[t] : 0.f;
   const float h = kEntropy ? a.dentropy[t] : 0.f;
-  // nothing to learn from the row: ignored, or nothing above the lowest values (a lse of that
-  // size has lost ln s, and p with it)
-  const bool skip = (a.targets != nullptr && y == a.ignore) || lse < -1e30f;
+  // nothing to learn from the row: ignored, or nothing above a mask's values, lowest or -1e9 added to every
+  // token (a lse of that size has lost ln s, and p with it)
+  const bool skip = (a.targets != nullptr && y == a.ignore) || lse < kLowestLse;
   // with t = log2 p:  dz = p (A + B t), + scale g at the target.  ln p = scale z - lse is rounded once and
   // brought to base 2 after that: scale log2(e) and lse log2(e), rounded first, would each add a rounding of
   // lse's size to lse's own

@@ -149,3 +149,21 @@ def test_backward_of_rows_far_from_zero(cuda_lib, scale):
     ref = O.token_logprobs_backward(f64(zt), y.cpu().numpy(), g, None, s)
     rel = np.expm1(eps(V) + U * np.abs(l)[:, None] + 84 * U + 4 * U * np.abs(lp))
     near(got, ref, s * np.abs(g)[:, None] * p * rel + 4 * U * np.abs(ref) + 1e-37)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+def test_backward_of_rows_that_an_additive_mask_leaves_empty(cuda_lib, dtype, scale):
+    """A mask that adds -1e9 to every token: lse lies where float32 is 64 apart and tells nothing of p; the
+    row has nothing to learn from."""
+    z, rng = logits(4, 4001, 3)
+    z[1] -= 1e9
+    z[2] -= 3e7
+    z[3, 100:] -= 1e9
+    zt = store(z, dtype)
+    y = torch.zeros(4, dtype=torch.int32, device="cuda")
+    one = torch.ones(4, device="cuda")
+    _, lse, ent, _, _ = cuda_lib.token_logprobs(zt, y, scale=scale)
+    d = cuda_lib.token_logprobs_backward(zt, lse, y, one, entropy=ent, dentropy=one, scale=scale)
+    assert torch.isfinite(d).all() and not d[1:3].any()
+    assert d[0].any() and d[3, :100].any() and not d[3, 100:].any()
