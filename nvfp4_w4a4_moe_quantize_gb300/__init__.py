@@ -636,12 +636,14 @@ def moe_expert_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, we
 
 def _rows(t: torch.Tensor, what: str) -> tuple:
     """(rows, cols, type code, pitch) of a [rows, cols] CUDA tensor of an activation type whose
-    columns are adjacent."""
+    columns are adjacent, on the current device (with a given stream: that stream's)."""
     code = ACT_DTYPES.get(t.dtype)
     if code is None or t.dim() != 2:
         raise ValueError(f"{what} must be a 2-D BF16, float16 or float32 tensor")
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
+    if t.get_device() != torch.cuda.current_device():   # launches, their limits and the status word are its own
+        raise ValueError(f"{what} must be on the current CUDA device, or on the given stream's")
     (rows, cols), (pitch, step) = t.shape, t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{what} must have unit column stride")
