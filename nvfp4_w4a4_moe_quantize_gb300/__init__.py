@@ -672,6 +672,13 @@ def _per_row(t, shape: tuple, dtype, dev: int, what: str):
     return t.contiguous()
 
 
+def _int32(v: int, what: str) -> int:
+    """v for a 32-bit argument, which would be cut to its low bits without a word."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{what} must fit into 32 bits")
+    return v
+
+
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
                    ignore_index: int = -100, entropy: bool = True, stream=None):
     """Log probabilities of given tokens, entropy and top alternatives of logits [T, V] (BF16,
@@ -684,6 +691,7 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, to
     T, V, code, ld = _rows(logits, "logits")
     dev, index = logits.device, logits.get_device()
     targets = _per_row(targets, (T,), torch.int32, index, "targets")
+    ignore_index, top_k = _int32(ignore_index, "ignore_index"), _int32(top_k, "top_k")
     lse = torch.empty(T, dtype=torch.float32, device=dev)
     logprob = torch.empty_like(lse) if targets is not None else None
     ent = torch.empty_like(lse) if entropy else None
@@ -707,6 +715,7 @@ def token_logprobs_backward(logits: torch.Tensor, lse: torch.Tensor, targets: to
     T, V, code, ld = _rows(logits, "logits")
     index = logits.get_device()
     targets = _per_row(targets, (T,), torch.int32, index, "targets")
+    ignore_index = _int32(ignore_index, "ignore_index")
     lse = _per_row(lse, (T,), torch.float32, index, "lse")
     entropy = _per_row(entropy, (T,), torch.float32, index, "entropy")
     dlogprob = _per_row(dlogprob, (T,), torch.float32, index, "dlogprob")

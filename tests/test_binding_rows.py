@@ -99,3 +99,19 @@ def test_a_stream_of_another_device_is_refused(current, name):
         calls(0)[name](stream=Stream(1))
     with pytest.raises(AssertionError, match="reached"):
         calls(0)[name](stream=Stream(0))
+
+
+@pytest.mark.parametrize("index", [2 ** 32, 2 ** 31, -2 ** 31 - 1])
+def test_ignore_index_beyond_32_bits_is_refused(current, index):
+    """It is compared with int32 targets: cut to 32 bits, 2^32 would ignore token 0."""
+    z, y, f = Rows(4, 64), Rows(4, dtype=torch.int32), Rows(4, dtype=torch.float32)
+    with pytest.raises(ValueError, match="ignore_index"):
+        L.token_logprobs(z, y, ignore_index=index)
+    with pytest.raises(ValueError, match="ignore_index"):
+        L.token_logprobs_backward(z, f, y, f, ignore_index=index)
+
+
+@pytest.mark.parametrize("k", [2 ** 32 + 3, -2 ** 32 + 3])
+def test_top_k_beyond_32_bits_is_refused(current, k):
+    with pytest.raises(ValueError, match="top_k"):
+        L.token_logprobs(Rows(0, 64), top_k=k)
