@@ -167,3 +167,37 @@ def test_backward_of_rows_that_an_additive_mask_leaves_empty(cuda_lib, dtype, sc
     d = cuda_lib.token_logprobs_backward(zt, lse, y, one, entropy=ent, dentropy=one, scale=scale)
     assert torch.isfinite(d).all() and not d[1:3].any()
     assert d[0].any() and d[3, :100].any() and not d[3, 100:].any()
+
+
+@pytest.mark.parametrize("T", [2, 640])
+def test_a_few_more_threads_than_alternatives(cuda_lib, T):
+    """1100 allowed neighbours are 138 threads' chunks: hardly more than the list is long, with many more
+    candidates."""
+    V = 40000
+    rng = np.random.default_rng(T)
+    z = np.full((T, V), -np.inf)
+    z[:, 8005:9105] = rng.normal(0.0, 1.0, (T, 1100))
+    check_forward(cuda_lib, store(z, "f32"), np.full(T, 8500, np.int32), 1.0, 128)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(200, 131072), (400, 131072), (200, 70001), (400, 70001), (200, 33001), (330, 20011)])
+def test_several_slices_a_cta_of_a_cluster(cuda_lib, dtype, T, V):
+    """Between a CTA a slice and a CTA a row: every row gives what it gives alone."""
+    n = 8
+    z, rng = logits(n, V, V + 1)
+    y = torch.from_numpy(rng.integers(0, V, n).astype(np.int32)).cuda()
+    ids, val = teacher(n, V, 30, rng)
+    it, vt, zt = torch.from_numpy(ids).cuda(), torch.from_numpy(val).cuda(), store(z, dtype)
+    pick = torch.from_numpy(rng.integers(0, n, T)).cuda()
+    many = zt[pick]
+    for k in (0, 20, 128):
+        alone = [cuda_lib.token_logprobs(zt[r:r + 1], y[r:r + 1], top_k=k) for r in range(n)]
+        got = cuda_lib.token_logprobs(many, y[pick], top_k=k)
+        for i, a in enumerate(got):
+            assert a is None or torch.equal(a, torch.cat([o[i] for o in alone])[pick])
+    check_forward(cuda_lib, zt, y.cpu().numpy(), 1.0, 128)
+    for tail in (False, True):
+        alone = [cuda_lib.distill_topk(zt[r:r + 1], it[r:r + 1], vt[r:r + 1], tail) for r in range(n)]
+        for i, a in enumerate(cuda_lib.distill_topk(many, it[pick], vt[pick], tail)):
+            assert torch.equal(a, torch.cat([o[i] for o in alone])[pick])
