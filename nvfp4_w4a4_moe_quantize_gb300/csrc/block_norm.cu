@@ -8,13 +8,17 @@
 // once.  A row belongs to a group of G threads, G a function of H alone, 16 elements a
 // thread; sums run in an order that H fixes, so a row's bits do not depend on the batch.
 // What bounds these kernels is HBM, if enough bytes are on their way: a group's next rows arrive in
-// shared memory by bulk copies while it works on one, and the weights stay there.  Rows
-// that are not 16-byte aligned are read from global memory element by element.
+// shared memory by bulk copies while it works on one, and the weights stay there.  If one of
+// the arrays has rows that are not 16-byte aligned, all are read and written element by
+// element, with no row ahead, and the backward spills registers; where the width is a multiple of 8 all
+// the same, a thread's elements are neighbours and a warp's reads do not coalesce.
 // Backward: a CTA takes a range of rows of one gate row and keeps the column sums of the
 // weights' and gate's gradients in registers; the ranges' sums are added by a second kernel
 // in a fixed order (no atomics).
-// Measured at 32768 x 2048 BF16 with a gate a token and the next norm: forward 88 us (6.1 TB/s, 90% of
-// a copy's rate), backward 137 us (5.9 TB/s) of which the second kernel takes 5.  Both use 50-60% of the issue
+// Measured at 32768 x 2048 BF16 with a gate a token and the next norm: forward 90 us (6.0 TB/s, 88% of
+// a copy's rate), backward 139 us (5.8 TB/s) of which the second kernel takes 5; the norm before the block 53 us
+// (5.0 TB/s), backward 103 us (5.2 TB/s).  Not aligned, forward and backward: 213 and 566 us at a width of
+// 2047, 400 and 615 us at a width of 2048 and a pitch of 2051.  Both use 50-60% of the issue
 // slots; more rows ahead, other numbers of CTAs, and 8 or 32 elements a thread were slower
 // (forward 91-123 us, backward 142-198 us).
 #include "launch.h"

@@ -16,7 +16,7 @@
 // enters them afterwards, so nothing but scalars follows the exchange between CTAs.
 //
 // The loss alone streams like the log probabilities; a bitmap of S in shared memory leaves the
-// listed tokens out.  With the gradient a row's slices lie in the shared memory of a cluster
+// listed tokens out (8192 x 131072 BF16, K = 64: 306 us with the tail, 317 without, 7.0 and 6.8 TB/s).  With the gradient a row's slices lie in the shared memory of a cluster
 // between the sum and the gradient, so HBM sees the row read once and written once
 // (8192 x 131072 BF16, K = 64 with the tail: 706 us, 6.1 TB/s, 90% of a copy's rate; 1000 x 50021
 // float16, K = 100: 53 us, 3.8 TB/s).  What bounds it is the row's chain -- arrival, sum,

@@ -13,7 +13,7 @@
 // order: a candidate's key is its value and id.
 //
 // Bound: HBM for the pass (8192 x 131072 BF16, a tenth of the rows ignored: 288 us, 6.7 TB/s of the
-// rows read; backward 615 us, 6.9 TB/s read and written); what a list adds is latency at the end of
+// rows read; backward 616 us, 7.0 TB/s read and written); what a list adds is latency at the end of
 // a row, hidden behind the other three CTAs of the SM in part (2048 x 131072: no list 93 us, 20
 // entries 120 us, 128 entries 135 us; of a row's 66000 cycles the bound takes 2400, the cells 1800, reading
 // them again 7200, the sort 2900).  One row is bound by latency: 131072 BF16 logits over the 8 CTAs
@@ -136,7 +136,8 @@ __device__ __forceinline__ int rank_keys(uint64_t* key, int n, int k, uint64_t* 
 }
 
 // A lower bound of the row's k-th best key, from the threads' best values (`mine`); the whole CTA.
-// 0 when fewer than k threads hold anything.
+// 0 when fewer than k threads hold anything, or hardly more (n <= enough): every allowed element then is a
+// candidate, where they do not fit in rounds.
 //   The values are searched bit by bit for a bound that at least k threads reach, until hardly
 //   more do: every bit costs a vote of the CTA, and a few candidates too many cost less.
 __device__ __forceinline__ uint64_t list_bound(float mine, TopSmem& t, const Cells& cells, int n_cells, int k,
@@ -495,7 +496,7 @@ constexpr int kBackwardTile = 16384;   // elements of a row a CTA
 constexpr float kLowestLse = -16777216.f;   // -2^24: below, float32 is 2 and more apart, and p = exp(c - lse) lost
 
 // One exponential an element; the tiles are independent, so the loads of 4 chunks a thread and the CTAs of
-// an SM cover the latency (8192 x 131072 BF16: 615 us, 6.98 TB/s, the rate of a copy).
+// an SM cover the latency (8192 x 131072 BF16: 614 us, with the entropy 616 us, 6.97 TB/s, the rate of a copy).
 template <typename E, bool kEntropy>
 __global__ void __launch_bounds__(kVocabThreads) token_logprobs_backward_kernel(const LogprobBackwardArgs a) {
   const int64_t t = blockIdx.x / a.tiles;
