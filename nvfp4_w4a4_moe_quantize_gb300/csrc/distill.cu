@@ -51,7 +51,7 @@ struct DistillArgs {
 };
 
 // The list of a row, and its sums.  mz is the maximum of its logits, s = sum 2^((z - mz) c1),
-// A = sum q ln q, B = sum q (z - mz), Q = sum q.
+// A = sum q ln q, B = scale sum q (z - mz), Q = sum q.
 struct ListSmem {
   int id[kMaxList];   // of the K entries; the places up to a multiple of 32 hold -1
   float q[kMaxList], z[kMaxList];
@@ -143,7 +143,8 @@ struct ListRegs {
   }
   // Marks the ids that lie in the CTA's slices in `listed` (clear there) and leaves the sums in sm.
   template <bool kMark>
-  __device__ __forceinline__ void reduce(float c1, const Marks& listed, ListSmem& sm) const {
+  __device__ __forceinline__ void reduce(float scale, const Marks& listed, ListSmem& sm) const {
+    const float c1 = scale * kLog2e;
     const int lane = threadIdx.x & 31;
     bool again = false;
     float mv = -INFINITY, mz = -FLT_MAX;
@@ -176,7 +177,8 @@ struct ListRegs {
       const float q = kTail ? e[j] : e[j] / esum;
       if (q != 0.f) {   // 0 ln 0 = 0
         A += q * (kTail ? v[j] : v[j] - mv - ln_e);
-        B += q * (zi[j] - mz);
+        // (q scale first: a difference of the lowest values' size times more than 1 is beyond float32)
+        B += zi[j] == -INFINITY ? -INFINITY : q * scale * (zi[j] - mz);
       }
       Q += q;
       const int i = lane + 32 * j;
@@ -268,15 +270,15 @@ __device__ __forceinline__ RowLoss row_loss(const Stats& st, const RowResult& r,
   float tail = 0.f;
   if (kTail && st.s != 0.f) {   // some token outside the list is allowed (NaN counts)
     const float qr = fmaxf(0.f, 1.f - l.Q);
-    const float lr = fmaf(r.mb - r.m, scale, logf(st.s) - ln_s);   // ln p_r
-    if (qr > 0.f) tail = qr * (logf(qr) - lr);
+    // ln p_r = scale (mb - m) + ln s_r - ln s, each part times q_r
+    if (qr > 0.f) tail = fmaf(-(qr * scale), r.mb - r.m, qr * (logf(qr) - (logf(st.s) - ln_s)));
   }
   // sum q (ln q - ln p) with ln p = scale (z - m) - ln s; a student without any allowed token
   // has p = 0 everywhere
   RowLoss o;
   if (l.Q == 0.f) o.loss = tail;
   else if (r.total == 0.f) o.loss = INFINITY;
-  else o.loss = l.A - scale * (l.B + l.Q * (l.mz - r.m)) + ln_s * l.Q + tail;
+  else o.loss = l.A - (l.B + l.Q * scale * (l.mz - r.m)) + ln_s * l.Q + tail;
   o.lse = r.total == 0.f ? -INFINITY : fmaf(r.m, scale, ln_s);
   return o;
 }
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kVocabThreads) distill_topk_kernel(const Disti
     mine.gather(a, row.p);
   }
   __syncthreads();
-  if (warp == 0) mine.template reduce<true>(c1, listed, sm.list);
+  if (warp == 0) mine.template reduce<true>(a.scale, listed, sm.list);
   __syncthreads();
   if (ctas > 1) cluster.barrier_wait();
   const ListSmem& l = sm.list;
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_ker
     if (lane == 0 && kStage && plan.stages == 1 && n_rows > 1) prefetch_row(z_of(1), lo, hi);
     list.read(a, t0);
     list.gather(a, z_of(0));
-    list.template reduce<!kStage>(c1, marks_of(0), sm.list[0]);
+    list.template reduce<!kStage>(a.scale, marks_of(0), sm.list[0]);
     open_row(0);
     for (int i = 0; i < n_rows; ++i) {
       const int64_t t = t0 + i;
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 4) distill_topk_backward_ker
         list.read(a, t + 1);
         if (!kStage && i > 0) list.clear(sm.list[(i + 1) & 1], marks_of(i + 1));
         list.gather(a, z_of(i + 1));
-        list.template reduce<!kStage>(c1, marks_of(i + 1), sm.list[(i + 1) & 1]);
+        list.template reduce<!kStage>(a.scale, marks_of(i + 1), sm.list[(i + 1) & 1]);
       }
       mbar_wait_cluster(&sm.joined[i & 1], (i >> 1) & 1, a.status, &sm.abort);   // messages of other CTAs are read next
       const Message* flat = &sm.part[i & 1][0][0];

@@ -201,3 +201,30 @@ def test_several_slices_a_cta_of_a_cluster(cuda_lib, dtype, T, V):
         alone = [cuda_lib.distill_topk(zt[r:r + 1], it[r:r + 1], vt[r:r + 1], tail) for r in range(n)]
         for i, a in enumerate(cuda_lib.distill_topk(many, it[pick], vt[pick], tail)):
             assert torch.equal(a, torch.cat([o[i] for o in alone])[pick])
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_loss_at_the_lowest_values_is_finite(cuda_lib, tail, dtype):
+    """The type's lowest value is a value like any other: where the loss is one that float32 holds, it is not
+    infinite.  Listed tokens at the lowest value, with masses that add up to 1.3 (and 0.9); the
+    unlisted ones there.  One product of the loss exceeds all others; it carries the roundings of q,
+    scale and the sums, 16 u and u a listed token."""
+    low = float(torch.finfo({"bf16": torch.bfloat16, "f32": torch.float32}[dtype]).min)
+    z, _ = logits(3, 3001, 6)
+    z[0, :20] = z[1, :20] = low
+    z[2, :] = low
+    z[2, :20] = 0.5
+    q = np.full((3, 20), 1.0 / 20) * np.array([[1.3], [0.9], [0.7]])
+    ids = torch.arange(20, dtype=torch.int32, device="cuda").repeat(3, 1)
+    val = torch.from_numpy(np.log(q).astype(np.float32)).cuda()
+    for scale in (0.05, 0.7):
+        s = float(np.float32(scale))
+        mass = np.array([1.3, 0.9, 0.3]) if tail else np.array([1.0, 1.0, 0.0])
+        want = -s * low * mass
+        zt = store(z, dtype)
+        loss = cuda_lib.distill_topk(zt, ids, val, tail, scale)[0]
+        both, d = cuda_lib.distill_topk_backward(zt, ids, val, None, tail, scale)
+        ok = want < 3e38
+        near(f64(loss)[ok], want[ok], 40 * U * want[ok] + 100.0)
+        assert torch.equal(loss, both) and torch.isfinite(d).all()
