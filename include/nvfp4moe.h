@@ -125,7 +125,10 @@ enum {
   NVFP4_OP_QUANTIZE_T = 4,      /* args: batches * C (rows of the transpose), R */
   NVFP4_OP_MOE_BACKWARD = 5,    /* args: T, k, E, H, I */
   NVFP4_OP_PREPARE_WEIGHTS_T = 6, /* args: E */
-  NVFP4_OP_NORM_BACKWARD = 7    /* args: T, gate_rows (0: none or one number a row), -, H */
+  NVFP4_OP_NORM_BACKWARD = 7,   /* args: T, gate_rows (0: none or one number a row), -, H */
+  NVFP4_OP_BALANCE_LOSS = 8,    /* args: T, S (sequences), E */
+  NVFP4_OP_HEAD_LOGPROBS = 9,           /* args: T, V, -, H */
+  NVFP4_OP_HEAD_LOGPROBS_BACKWARD = 10  /* args: T, V, -, H */
 };
 size_t nvfp4_workspace_size(int op, int64_t T_or_rows, int64_t k_or_cols, int64_t E,
                             int64_t H, int64_t I);
@@ -607,6 +610,83 @@ nvfp4_status distill_topk_backward(const void* logits, nvfp4_act_dtype dtype, in
                                    const int32_t* teacher_ids, const float* teacher_values, int32_t K, int tail,
                                    float scale, const float* dloss, float* loss, float* lse, void* dlogits,
                                    int64_t ldd, void* stream);
+
+/* The same log probabilities without the logits in memory: from the hidden rows and the head's
+ * weight (the softmax cross entropy over the vocabulary is -logprob).
+ *   hidden: device [T, ldh], weight: device [V, ldw] of `dtype` (NVFP4_ACT_BF16 or
+ *     NVFP4_ACT_F16; float32 is NVFP4_ERR_UNSUPPORTED), the first H of each row are used.
+ *     H, ldh and ldw multiples of 8, both 16-byte aligned.  1 <= V <= 2^20, T <= 2^20, H <= 16384.
+ *   c = scale * <hidden_t, weight_j>, products and sums of float32, never rounded to `dtype`; lse,
+ *     p, logprob, entropy, targets and ignore_index as in token_logprobs.  A row whose target is
+ *     ignore_index may hold anything.  A row's bits depend on its hidden row, the weight, scale and
+ *     whether the entropy is asked for alone.
+ *   workspace: nvfp4_workspace_size(NVFP4_OP_HEAD_LOGPROBS, T, V, 0, H, 0) bytes, 16-byte aligned. */
+nvfp4_status head_logprobs(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, nvfp4_act_dtype dtype,
+                           int64_t T, int64_t V, int64_t H, const int32_t* targets, int32_t ignore_index, float scale,
+                           float* logprob, float* lse, float* entropy, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* The gradients of sum_t dlogprob[t] logprob[t] + dentropy[t] entropy[t]:
+ *   d_tj = dlogprob (1[j = target] - p_j) - dentropy p_j (ln p_j + entropy), zero in the rows where
+ *   token_logprobs_backward has none;  dhidden = scale d weight [T, H],  dweight = scale d^T hidden
+ *   [V, H], dense, of `dtype`, 16-byte aligned, rounded once; either may be NULL.
+ * The vocabulary goes in pieces: the logits of a piece are computed again, d of a piece is held in
+ * `dtype` (half precision: as d over a power of two of the row's weight), sums are float32 in a fixed
+ * order.  Deterministic.
+ *   lse, entropy: the forward's; targets and dlogprob, entropy and dentropy: device or NULL (dlogprob
+ *     needs targets, dentropy needs entropy).  Outputs must not overlap inputs.
+ *   workspace: nvfp4_workspace_size(NVFP4_OP_HEAD_LOGPROBS_BACKWARD, T, V, 0, H, 0) bytes, 16-byte
+ *   aligned. */
+nvfp4_status head_logprobs_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                                    nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t H, const int32_t* targets,
+                                    int32_t ignore_index, float scale, const float* lse, const float* entropy,
+                                    const float* dlogprob, const float* dentropy, void* dhidden, void* dweight,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- the router's losses */
+
+/* The balance loss of the router and the tokens that each expert got, of every sequence ("Low-Bit
+ * Precision Training Is Ready for Production...", §"What W4A4 GEMM Actually Changes": the router
+ * stays in high precision; its load decides the shape of the grouped GEMMs).  The pages give no
+ * formula; this is the library's.  With p = softmax(logits[t]), n the tokens of sequence s that
+ * count, c_e the times that they chose expert e and P_e = sum_t p_te:
+ *   loss = E / (k n^2) sum_e c_e P_e   (1 where all experts get the same share; 0 for n = 0).
+ *   logits: device [T, ld] of `dtype`, the first E used, any alignment of the element; a logit of
+ *     -inf excludes its expert (p = 0), NaN or +inf makes the row's p NaN.  ids: device int32 [T, k],
+ *     as moe_route_topk gives them; one outside [0, E) sets NVFP4_ERR_DEVICE_STATUS and is counted
+ *     nowhere.
+ *   sequences: device int32 [S + 1], row numbers that do not descend, sequence s the rows
+ *     sequences[s] .. sequences[s + 1] - 1 (none: an empty one); or NULL with S = 1: all rows.  Rows
+ *     of no sequence count nowhere.  A pair that descends or leaves [0, T] sets
+ *     NVFP4_ERR_DEVICE_STATUS and gives that sequence the loss NaN.
+ *   valid: device uint8 [T] or NULL; tokens with 0 (padding) count nowhere and are not read.
+ *   loss [S], prob_sums (P) [S, E]: device float; counts (c) [S, E], tokens (n) [S]: device int32.
+ *   Float32 sums in an order that T, S and the sequences fix.  1 <= E <= 1024, 1 <= k <= 32, k <= E,
+ *   T <= 2^24, S <= 2^20.
+ *   workspace: nvfp4_workspace_size(NVFP4_OP_BALANCE_LOSS, T, S, E, 0, 0) bytes, 16-byte aligned. */
+nvfp4_status moe_balance_loss(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,
+                              const int32_t* ids, int32_t k, const int32_t* sequences, int32_t S,
+                              const uint8_t* valid, float* loss, int32_t* counts, float* prob_sums, int32_t* tokens,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient of the router's logits: of sum_t,j dweights[t, j] w[t, j], w the weights that
+ * moe_route_topk(..., renormalize) gives (dw of moe_expert_backward fits), and of
+ * sum_s dloss[s] loss[s], in one pass, rounded once:
+ *   dlogits[t] = J_w^T dweights[t] + p_te (a_e - sum_j p_tj a_j),  a_e = dloss E c_e / (k n^2);
+ *   the counts are constants.
+ *   dweights: device float [T, k] with ids, or NULL; dloss: device float [S] with counts and tokens,
+ *     or NULL; one at least.  An id twice in a row gets both places' parts; one outside [0, E) sets
+ *     NVFP4_ERR_DEVICE_STATUS and has no weight.  counts and tokens may come from more than this
+ *     batch (sums over several devices): then the loss is that of all of them.
+ *   sequences, S, valid: as in moe_balance_loss; they say which tokens the balance loss reaches, and
+ *     do not concern dweights.
+ *   dlogits: device [T, ldd] of `dtype`; it may be `logits` itself (ldd = ld), else it must not
+ *     overlap it.  Excluded experts get 0. */
+nvfp4_status moe_router_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,
+                                 const int32_t* ids, int32_t k, const float* dweights, int renormalize,
+                                 const float* dloss, const int32_t* counts, const int32_t* tokens,
+                                 const int32_t* sequences, int32_t S, const uint8_t* valid, void* dlogits,
+                                 int64_t ldd, void* stream);
 
 /* ---------------------------------------------------------------- norms around the block */
 

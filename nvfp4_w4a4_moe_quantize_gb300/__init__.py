@@ -31,6 +31,7 @@ __all__ = [
     "moe_backward_workspace_layout",
     "token_logprobs", "token_logprobs_backward", "distill_topk", "distill_topk_backward",
     "moe_norm_in", "moe_norm_in_backward", "moe_norm_out", "moe_norm_out_backward",
+    "head_logprobs", "head_logprobs_backward", "moe_balance_loss", "moe_router_backward",
 ]
 
 SCALE_PER_TENSOR, SCALE_PER_ROW, SCALE_PER_GROUP = 0, 1, 2
@@ -39,6 +40,7 @@ SF_SWIZZLED_128x4, SF_ROWMAJOR = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 OP_QUANTIZE, OP_PREPARE_WEIGHTS, OP_MOE_FORWARD, OP_MOE_PERMUTE, OP_QUANTIZE_T = 0, 1, 2, 3, 4
 OP_MOE_BACKWARD, OP_PREPARE_WEIGHTS_T, OP_NORM_BACKWARD = 5, 6, 7
+OP_BALANCE_LOSS, OP_HEAD_LOGPROBS, OP_HEAD_LOGPROBS_BACKWARD = 8, 9, 10
 ACT_DTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 _lib = None
@@ -125,6 +127,14 @@ _SIGS = {
                                     _vp, _vp, _vp, _vp, _vp]),
     "moe_norm_out_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_int, _i64,
                                              _i64, _vp, _vp, _i64, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "head_logprobs": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _i64, _vp, _i32, _f32, _vp, _vp,
+                                     _vp, _vp, _sz, _vp]),
+    "head_logprobs_backward": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _i64, _vp, _i32, _f32,
+                                              _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_balance_loss": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _sz, _vp]),
+    "moe_router_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _i64, _vp, _i32, _vp, ctypes.c_int, _vp, _vp,
+                                           _vp, _vp, _i32, _vp, _vp, _i64, _vp]),
 }
 
 
@@ -679,6 +689,16 @@ def _int32(v: int, what: str) -> int:
     return v
 
 
+def _workspace(given, device, op: int, *sizes) -> torch.Tensor:
+    """The caller's workspace, or a new one of nvfp4_workspace_size(op, *sizes)."""
+    if given is not None:
+        if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be dense uint8 on the device of the rows")
+        return given   # its size is checked with the other arguments
+    n = int(load().nvfp4_workspace_size(op, *sizes, 0))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
                    ignore_index: int = -100, entropy: bool = True, stream=None):
     """Log probabilities of given tokens, entropy and top alternatives of logits [T, V] (BF16,
@@ -774,6 +794,136 @@ def distill_topk_backward(logits: torch.Tensor, teacher_ids: torch.Tensor, teach
     return loss, out
 
 
+def _head_rows(hidden: torch.Tensor, weight: torch.Tensor) -> tuple:
+    """(T, V, H, type code, pitches) of hidden rows [T, H] and the head's weight [V, H]."""
+    T, H, code, ldh = _rows(hidden, "hidden")
+    if weight.dim() != 2 or weight.shape[1] != H or weight.dtype != hidden.dtype or weight.device != hidden.device:
+        raise ValueError(f"weight must be [V, {H}] of the type and on the device of the hidden rows")
+    V, _, _, ldw = _rows(weight, "weight")
+    # a single row's pitch is nobody's: the next multiple of 8 that holds it
+    return T, V, H, code, ldh if T > 1 else (H + 7) // 8 * 8, ldw if V > 1 else (H + 7) // 8 * 8
+
+
+def head_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor | None = None, scale: float = 1.0,
+                  ignore_index: int = -100, entropy: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """token_logprobs of the logits hidden [T, H] @ weight [V, H]^T, which are never stored (BF16 or
+    float16; H and the pitches multiples of 8, 16-byte aligned; the logits are float32).  The cross entropy
+    is -logprob.  Returns (logprob, lse, entropy), float32 [T]; None for what was not asked."""
+    if stream is not None:
+        return _on_stream(stream, head_logprobs, locals())
+    lib = load()
+    T, V, H, code, ldh, ldw = _head_rows(hidden, weight)
+    targets = _per_row(targets, (T,), torch.int32, hidden.get_device(), "targets")
+    ignore_index = _int32(ignore_index, "ignore_index")
+    lse = torch.empty(T, dtype=torch.float32, device=hidden.device)
+    logprob = torch.empty_like(lse) if targets is not None else None
+    ent = torch.empty_like(lse) if entropy else None
+    ws = _workspace(workspace, hidden.device, OP_HEAD_LOGPROBS, T, V, 0, H)
+    _check(lib.head_logprobs(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, code, T, V, H, _ptr(targets), ignore_index,
+                             scale, _ptr(logprob), lse.data_ptr(), _ptr(ent), ws.data_ptr(), ws.numel(),
+                             _stream_of(hidden)), "head_logprobs")
+    return logprob, lse, ent
+
+
+def head_logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, lse: torch.Tensor,
+                           targets: torch.Tensor | None = None, dlogprob: torch.Tensor | None = None,
+                           entropy: torch.Tensor | None = None, dentropy: torch.Tensor | None = None,
+                           scale: float = 1.0, ignore_index: int = -100, need_hidden: bool = True,
+                           need_weight: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of sum(dlogprob * logprob + dentropy * entropy) of head_logprobs, with its lse and
+    entropy: (dhidden [T, H], dweight [V, H]) of the inputs' type; None for one that is not needed."""
+    if stream is not None:
+        return _on_stream(stream, head_logprobs_backward, locals())
+    lib = load()
+    T, V, H, code, ldh, ldw = _head_rows(hidden, weight)
+    dev, index = hidden.device, hidden.get_device()
+    targets = _per_row(targets, (T,), torch.int32, index, "targets")
+    ignore_index = _int32(ignore_index, "ignore_index")
+    lse = _per_row(lse, (T,), torch.float32, index, "lse")
+    entropy = _per_row(entropy, (T,), torch.float32, index, "entropy")
+    dlogprob = _per_row(dlogprob, (T,), torch.float32, index, "dlogprob")
+    dentropy = _per_row(dentropy, (T,), torch.float32, index, "dentropy")
+    dhidden = torch.empty((T, H), dtype=hidden.dtype, device=dev) if need_hidden else None
+    dweight = torch.empty((V, H), dtype=hidden.dtype, device=dev) if need_weight else None
+    ws = _workspace(workspace, dev, OP_HEAD_LOGPROBS_BACKWARD, T, V, 0, H)
+    _check(lib.head_logprobs_backward(hidden.data_ptr(), ldh, weight.data_ptr(), ldw, code, T, V, H, _ptr(targets),
+                                      ignore_index, scale, _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy),
+                                      _ptr(dhidden), _ptr(dweight), ws.data_ptr(), ws.numel(), _stream_of(hidden)),
+           "head_logprobs_backward")
+    return dhidden, dweight
+
+
+# --------------------------------------------------------------------------- the router's losses
+
+def _router_rows(logits: torch.Tensor, ids, sequences, valid) -> tuple:
+    """(T, E, k, type code, pitch, ids, sequences, S, valid) of the router's logits and their tokens."""
+    T, E, code, ld = _rows(logits, "logits")
+    index = logits.get_device()
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be [{T}, k]")
+    k = ids.shape[1]
+    ids = _per_row(ids, (T, k), torch.int32, index, "ids")
+    S = 1
+    if sequences is not None:
+        if sequences.dim() != 1 or sequences.shape[0] < 2:
+            raise ValueError("sequences must be [S + 1] row numbers with S at least 1")
+        S = sequences.shape[0] - 1
+        sequences = _per_row(sequences, (S + 1,), torch.int32, index, "sequences")
+    if valid is not None:
+        valid = _per_row(valid, (T,), torch.uint8 if valid.dtype == torch.uint8 else torch.bool, index, "valid")
+    return T, E, k, code, ld, ids, sequences, S, valid
+
+
+def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, sequences: torch.Tensor | None = None,
+                     valid: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The router's balance loss of every sequence, E / (k n^2) * sum_e counts_e * prob_sums_e, from its
+    logits [T, E] and the chosen ids [T, k] (int32).  sequences: int32 [S + 1] row numbers (None: all rows
+    are one); valid: bool or uint8 [T], 0 = a token that does not count.  Returns (loss float32 [S], counts int32
+    [S, E], prob_sums float32 [S, E], tokens int32 [S])."""
+    if stream is not None:
+        return _on_stream(stream, moe_balance_loss, locals())
+    lib = load()
+    T, E, k, code, ld, ids, sequences, S, valid = _router_rows(logits, ids, sequences, valid)
+    dev = logits.device
+    loss = torch.empty(S, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    sums = torch.empty((S, E), dtype=torch.float32, device=dev)
+    tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    ws = _workspace(workspace, dev, OP_BALANCE_LOSS, T, S, E, 0)
+    _check(lib.moe_balance_loss(logits.data_ptr(), code, T, E, ld, ids.data_ptr(), k, _ptr(sequences), S, _ptr(valid),
+                                loss.data_ptr(), counts.data_ptr(), sums.data_ptr(), tokens.data_ptr(), ws.data_ptr(),
+                                ws.numel(), _stream_of(logits)), "moe_balance_loss")
+    return loss, counts, sums, tokens
+
+
+def moe_router_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor | None = None,
+                        renormalize: bool = True, dloss: torch.Tensor | None = None,
+                        counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                        sequences: torch.Tensor | None = None, valid: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None, stream=None):
+    """dlogits [T, E] of the router: from dweights float32 [T, k], the gradient by moe_route_topk's weights
+    (moe_expert_backward's dw), and from dloss float32 [S], that by moe_balance_loss, whose counts and tokens
+    come with it.  out may be the logits themselves."""
+    if stream is not None:
+        return _on_stream(stream, moe_router_backward, locals())
+    lib = load()
+    T, E, k, code, ld, ids, sequences, S, valid = _router_rows(logits, ids, sequences, valid)
+    index = logits.get_device()
+    dweights = _per_row(dweights, (T, k), torch.float32, index, "dweights")
+    if dloss is not None and (counts is None or tokens is None):
+        raise ValueError("dloss comes with the counts and tokens of moe_balance_loss")
+    dloss = _per_row(dloss, (S,), torch.float32, index, "dloss")
+    counts = _per_row(counts, (S, E), torch.int32, index, "counts")
+    tokens = _per_row(tokens, (S,), torch.int32, index, "tokens")
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    ldd = _rows_like(out, logits, "out")
+    _check(lib.moe_router_backward(logits.data_ptr(), code, T, E, ld, ids.data_ptr(), k, _ptr(dweights), renormalize,
+                                   _ptr(dloss), _ptr(counts), _ptr(tokens), _ptr(sequences), S, _ptr(valid),
+                                   out.data_ptr(), ldd, _stream_of(logits)), "moe_router_backward")
+    return out
+
+
 # --------------------------------------------------------------------------- norms around the block
 
 def _norm_gate(gate, T: int, H: int, index: int):
@@ -788,12 +938,7 @@ def _norm_gate(gate, T: int, H: int, index: int):
 
 
 def _norm_workspace(given, T: int, gate_rows: int, H: int, device) -> torch.Tensor:
-    if given is not None:
-        if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
-            raise ValueError("workspace must be dense uint8 on the device of the rows")
-        return given   # its size is checked with the other arguments
-    n = int(load().nvfp4_workspace_size(OP_NORM_BACKWARD, T, gate_rows, 0, H, 0))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    return _workspace(given, device, OP_NORM_BACKWARD, T, gate_rows, 0, H)
 
 
 def moe_norm_in(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, stream=None):

@@ -200,6 +200,11 @@ nvfp4_status gemm(const uint8_t* A, const uint8_t* SFA, const float* gA, const u
 
 }  // namespace
 
+bool make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch_bytes,
+                     uint32_t box_rows, CUtensorMapDataType dt, int elt) {
+  return make_map(m, base, rows, cols, pitch_bytes, box_rows, dt, elt);
+}
+
 int num_sms() {
   const int d = current_device();
   if (g_sms[d] == 0) {
@@ -268,6 +273,13 @@ size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t E, int64_t H, 
     case NVFP4_OP_NORM_BACKWARD:       // column sums of two weights over ranges of rows
       if (a <= 0 || b < 0 || H <= 0) return 0;
       return align256(8u * (size_t)(b > 0 ? b : 1) * (size_t)block_norm_parts(a, b, H) * (size_t)H);
+    case NVFP4_OP_BALANCE_LOSS:
+      if (a <= 0 || b <= 0 || E <= 0) return 0;
+      return align256(balance_workspace(a, b, E));
+    case NVFP4_OP_HEAD_LOGPROBS:
+    case NVFP4_OP_HEAD_LOGPROBS_BACKWARD:
+      if (a <= 0 || b <= 0 || H <= 0) return 0;
+      return align256(head_workspace(a, b, H, op == NVFP4_OP_HEAD_LOGPROBS_BACKWARD));
     default:
       return 0;
   }

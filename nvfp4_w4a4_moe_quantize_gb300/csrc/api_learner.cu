@@ -50,9 +50,118 @@ bool gate_ok(const float* gate, int64_t gate_rows, int64_t T) {
   return gate_rows == 0 || (gate_rows > 0 && gate_rows <= 8192 && T % gate_rows == 0);
 }
 
+nvfp4_status head_check(nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t H, int64_t ldh, int64_t ldw, float scale) {
+  if (!dtype_ok(dtype) || T < 0 || V <= 0 || H <= 0 || ldh < H || ldw < H) return NVFP4_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * 2.f)) return NVFP4_ERR_INVALID_ARG;   // the kernels use scale log2(e)
+  if (dtype == NVFP4_ACT_F32 || V > kMaxVocab || T > ((int64_t)1 << 20) || H > 16384 || H % 8 != 0 || ldh % 8 != 0 ||
+      ldw % 8 != 0 || ldh > ((int64_t)1 << 32) || ldw > ((int64_t)1 << 32))
+    return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+// [n bytes from a] and [m bytes from b] have no byte in common.
+bool disjoint(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + static_cast<uintptr_t>(n) <= y || y + static_cast<uintptr_t>(m) <= x;
+}
+
+nvfp4_status router_check(nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld, int32_t k, const int32_t* sequences,
+                          int32_t S) {
+  if (!dtype_ok(dtype) || T < 0 || E <= 0 || ld < E || k <= 0 || k > E || S <= 0) return NVFP4_ERR_INVALID_ARG;
+  if ((sequences == nullptr && S != 1) || !aligned_or_null(sequences, 4)) return NVFP4_ERR_INVALID_ARG;
+  if (E > 1024 || k > 32 || T > kMaxRows || S > (1 << 20)) return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+nvfp4_status head_logprobs(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, nvfp4_act_dtype dtype,
+                           int64_t T, int64_t V, int64_t H, const int32_t* targets, int32_t ignore_index, float scale,
+                           float* logprob, float* lse, float* entropy, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const nvfp4_status st = head_check(dtype, T, V, H, ldh, ldw, scale);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(lse, 4) || !aligned_or_null(targets, 4) ||
+      !aligned_or_null(logprob, 4) || !aligned_or_null(entropy, 4) || (targets == nullptr) != (logprob == nullptr))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16) || workspace_bytes < nvfp4_workspace_size(NVFP4_OP_HEAD_LOGPROBS, T, V, 0, H, 0))
+    return NVFP4_ERR_WORKSPACE;
+  return from_cuda(launch_head_logprobs(hidden, ldh, weight, ldw, dtype, T, V, H, targets, ignore_index, scale, logprob,
+                                        lse, entropy, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status head_logprobs_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw,
+                                    nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t H, const int32_t* targets,
+                                    int32_t ignore_index, float scale, const float* lse, const float* entropy,
+                                    const float* dlogprob, const float* dentropy, void* dhidden, void* dweight,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  const nvfp4_status st = head_check(dtype, T, V, H, ldh, ldw, scale);
+  if (st != NVFP4_OK) return st;
+  if (dhidden == nullptr && dweight == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (dlogprob != nullptr && targets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (dentropy != nullptr && entropy == nullptr) return NVFP4_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dweight != nullptr && !aligned(dweight, 16)) return NVFP4_ERR_INVALID_ARG;
+  if (T == 0) return dweight == nullptr ? NVFP4_OK : from_cuda(cudaMemsetAsync(dweight, 0, 2 * (size_t)V * (size_t)H, s));
+  if (!aligned(hidden, 16) || !aligned(weight, 16) || (dhidden != nullptr && !aligned(dhidden, 16)) ||
+      !aligned(lse, 4) || !aligned_or_null(targets, 4) || !aligned_or_null(entropy, 4) ||
+      !aligned_or_null(dlogprob, 4) || !aligned_or_null(dentropy, 4))
+    return NVFP4_ERR_INVALID_ARG;
+  const int64_t nh = 2 * ((T - 1) * ldh + H), nw = 2 * ((V - 1) * ldw + H), gh = 2 * T * H, gw = 2 * V * H;
+  if ((dhidden != nullptr && (!disjoint(dhidden, gh, hidden, nh) || !disjoint(dhidden, gh, weight, nw))) ||
+      (dweight != nullptr && (!disjoint(dweight, gw, hidden, nh) || !disjoint(dweight, gw, weight, nw))) ||
+      (dhidden != nullptr && dweight != nullptr && !disjoint(dhidden, gh, dweight, gw)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16) || workspace_bytes < nvfp4_workspace_size(NVFP4_OP_HEAD_LOGPROBS_BACKWARD, T, V, 0, H, 0))
+    return NVFP4_ERR_WORKSPACE;
+  return from_cuda(launch_head_logprobs_backward(hidden, ldh, weight, ldw, dtype, T, V, H, targets, ignore_index, scale,
+                                                 lse, entropy, dlogprob, dentropy, dhidden, dweight, workspace, s));
+}
+
+nvfp4_status moe_balance_loss(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,
+                              const int32_t* ids, int32_t k, const int32_t* sequences, int32_t S,
+                              const uint8_t* valid, float* loss, int32_t* counts, float* prob_sums, int32_t* tokens,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  const nvfp4_status st = router_check(dtype, T, E, ld, k, sequences, S);
+  if (st != NVFP4_OK) return st;
+  if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(prob_sums, 4) || !aligned(tokens, 4))
+    return NVFP4_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const size_t n = 4 * (size_t)S;
+    cudaError_t err = cudaMemsetAsync(loss, 0, n, s);
+    if (err == cudaSuccess) err = cudaMemsetAsync(tokens, 0, n, s);
+    if (err == cudaSuccess) err = cudaMemsetAsync(counts, 0, n * (size_t)E, s);
+    if (err == cudaSuccess) err = cudaMemsetAsync(prob_sums, 0, n * (size_t)E, s);
+    return from_cuda(err);
+  }
+  if (!aligned(logits, elt_bytes(dtype)) || !aligned(ids, 4)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16) || workspace_bytes < nvfp4_workspace_size(NVFP4_OP_BALANCE_LOSS, T, S, E, 0, 0))
+    return NVFP4_ERR_WORKSPACE;
+  return from_cuda(launch_balance_loss(logits, dtype, T, E, ld, ids, k, sequences, S, valid, loss, counts, prob_sums,
+                                       tokens, workspace, s));
+}
+
+nvfp4_status moe_router_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,
+                                 const int32_t* ids, int32_t k, const float* dweights, int renormalize,
+                                 const float* dloss, const int32_t* counts, const int32_t* tokens,
+                                 const int32_t* sequences, int32_t S, const uint8_t* valid, void* dlogits,
+                                 int64_t ldd, void* stream) {
+  const nvfp4_status st = router_check(dtype, T, E, ld, k, sequences, S);
+  if (st != NVFP4_OK) return st;
+  if (ldd < E || (dweights == nullptr && dloss == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (T == 0) return NVFP4_OK;
+  const int e = elt_bytes(dtype);
+  if (!aligned(logits, e) || !aligned(dlogits, e)) return NVFP4_ERR_INVALID_ARG;
+  if (dweights != nullptr && (!aligned(dweights, 4) || !aligned(ids, 4))) return NVFP4_ERR_INVALID_ARG;
+  if (dloss != nullptr && (!aligned(dloss, 4) || !aligned(counts, 4) || !aligned(tokens, 4))) return NVFP4_ERR_INVALID_ARG;
+  if (!same_or_disjoint(logits, ld, dlogits, ldd, T, E, e)) return NVFP4_ERR_INVALID_ARG;
+  return from_cuda(launch_router_backward(logits, dtype, T, E, ld, ids, k, dweights, renormalize != 0, dloss, counts,
+                                          tokens, sequences, S, valid, dlogits, ldd,
+                                          static_cast<cudaStream_t>(stream)));
+}
 
 nvfp4_status token_logprobs(const void* logits, nvfp4_act_dtype dtype, int64_t T, int64_t V, int64_t ld,
                             const int32_t* targets, int32_t ignore_index, float scale, int32_t top_k, float* logprob,

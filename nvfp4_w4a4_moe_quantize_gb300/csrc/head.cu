@@ -1,0 +1,945 @@
+// Log probabilities straight from hidden rows and the head's weight, and their gradients: the
+// softmax cross entropy over a large vocabulary without its logits in memory.
+//
+// c_tj = scale <hidden_t, weight_j>;  lse_t = ln sum_j exp(c_tj);  p_tj = exp(c_tj - lse_t);
+// logprob_t = c_ty - lse_t;  entropy_t = -sum_j p_tj ln p_tj.  The gradient by c is
+// d_tj = dlogprob_t (1[j = y] - p_tj) - dentropy_t p_tj (ln p_tj + entropy_t), and
+// dhidden = scale d weight, dweight = scale d^T hidden.
+//
+// Forward: one product whose epilogue keeps of every row and 128 columns the largest logit, the
+// sum of exponentials below it and (entropy) their weighted sum; a second kernel joins them.
+// The columns of a partial result are fixed by V, so a row's bits depend on its hidden row, the
+// weight and scale alone, not on the other rows.
+// Backward: the vocabulary in pieces.  Of a piece the logits are computed again and turned into
+// d (16 bits, [rows, piece] in the workspace); then dhidden += d weight (float32 sums over the
+// pieces) and the piece of dweight = d^T hidden in one launch.  Rows without a token to score take
+// no part: the others are gathered first.
+//
+// One kernel runs the three products.  Roles: warp 0 loads (TMA, 64 x 64 boxes of 128-byte rows,
+// 128-byte swizzle), warp 1 issues the MMAs (tcgen05, float32 accumulators of 256 columns in
+// TMEM, two of them, so the epilogue of one tile runs under the products of the next), warps 2-9
+// are the epilogue: a thread has one row and 128 of the tile's 256 columns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+#include "pdl.cuh"
+#include "ptx.cuh"
+#include "vocab.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kBM = 128;                 // rows of a CTA's tile (one a TMEM lane)
+constexpr int kBN = 256;                 // columns
+constexpr int kBK = 64;                  // contraction a stage: one 128-byte swizzle row of 16-bit values
+constexpr int kBox = 64 * 128;           // bytes of one 64 x 64 box
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kPart = 128;               // columns of a partial result
+constexpr float kLowestLse = -16777216.f;
+
+enum : int { kStats = 0, kGrad = 1, kProducts = 2 };
+
+template <bool kPair>
+struct Ring {
+  static constexpr int kABoxes = 2;                        // 128 rows of A
+  static constexpr int kBBoxes = kPair ? 2 : 4;            // 256 rows of B, or this CTA's half
+  static constexpr int kStageBytes = (kABoxes + kBBoxes) * kBox;
+  static constexpr int kStages = kPair ? 6 : 4;
+};
+
+template <bool kPair>
+struct HeadSmem {
+  uint8_t stage[Ring<kPair>::kStages][Ring<kPair>::kStageBytes];
+  uint8_t out[kEpiWarps][32 * 128];      // 32-row boxes on their way out
+  uint64_t full[Ring<kPair>::kStages];
+  uint64_t empty[Ring<kPair>::kStages];
+  uint64_t accf[2];
+  uint64_t acce[2];
+  uint64_t fin;
+  uint32_t tmem_base;
+  int abort;
+};
+template <bool kPair>
+constexpr size_t smem_bytes() { return sizeof(HeadSmem<kPair>) + 1024; }
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
+
+// What a row of the gradient needs: d = p (a + b log2 p), + zy at the target.
+struct RowGrad {
+  float a, b, lse, zy;
+};
+
+struct HeadArgs {
+  int64_t T;                 // rows of `hidden`
+  const int32_t* n_rows;     // rows that take part, nullable: T
+  bool always_gathered;      // the gathered rows are read even if all of them take part (products, half precision)
+  int V, H;
+  int f16;
+  float scale;
+  int* status;
+  // statistics
+  const int32_t* targets;    // nullable
+  const int32_t* index;      // row -> row of targets, nullable: itself
+  float* part_m;             // [parts][pitch]
+  float* part_s;
+  float* part_u;             // nullable: no entropy
+  int64_t pitch;
+  float* target_logit;       // [rows], unscaled
+  // gradient
+  int v0, width;             // the piece of the vocabulary
+  const RowGrad* rows;
+  const int32_t* row_target;
+  // products
+  int x_splits;              // parts of dhidden's contraction
+  int64_t x_pitch;           // rows between their sums
+  bool x_first;              // the first piece stores, the others add
+  bool want_x, want_w;
+  const float* w_factor;     // nullable: 1
+};
+
+__device__ __forceinline__ uint32_t idesc_16(bool f16, uint32_t M, bool a_mn, bool b_mn) {
+  const uint32_t fmt = f16 ? 0u : 1u;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(kBN >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// One tile of work.
+struct Unit {
+  bool w;                    // products: a tile of dweight (else of dhidden)
+  int m, n, split;           // tile numbers (m in CTA-pair rows where there are pairs)
+  int k0, k1;                // stages of the contraction
+};
+
+template <int kMode, bool kPair>
+struct Plan {
+  int rows, m_tiles, n_tiles, total;
+  int xm, xn, x_units, x_kb, wm, w_kb;
+  __device__ Plan(const HeadArgs& a, int n) {
+    constexpr int kTileM = kPair ? 2 * kBM : kBM;
+    rows = n;
+    if (kMode == kProducts) {
+      xm = (n + kTileM - 1) / kTileM;
+      xn = (a.H + kBN - 1) / kBN;
+      x_kb = (a.width + kBK - 1) / kBK;
+      x_units = a.want_x ? xm * xn * a.x_splits : 0;
+      wm = (a.width + kTileM - 1) / kTileM;
+      w_kb = (n + kBK - 1) / kBK;
+      total = x_units + (a.want_w ? wm * xn : 0);
+    } else {
+      m_tiles = (n + kTileM - 1) / kTileM;
+      n_tiles = (a.width + kBN - 1) / kBN;
+      total = m_tiles * n_tiles;
+    }
+  }
+  __device__ Unit unit(const HeadArgs& a, int t) const {
+    Unit u{};
+    if (kMode != kProducts) {
+      u.n = t / m_tiles;                 // the weight's rows are read once, the hidden rows stay in L2
+      u.m = t - u.n * m_tiles;
+      u.k1 = (a.H + kBK - 1) / kBK;
+    } else if (t < x_units) {
+      const int per = xm * xn;
+      u.split = t / per;
+      const int r = t - u.split * per;
+      u.m = r / xn;
+      u.n = r - u.m * xn;
+      u.k0 = (int)((int64_t)x_kb * u.split / a.x_splits);
+      u.k1 = (int)((int64_t)x_kb * (u.split + 1) / a.x_splits);
+    } else {
+      const int r = t - x_units;
+      u.w = true;
+      u.m = r / xn;
+      u.n = r - u.m * xn;
+      u.k1 = w_kb;
+    }
+    return u;
+  }
+};
+
+template <int kMode, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    head_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap gathered,
+                const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap dlogits,
+                const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1, const HeadArgs a) {
+  using R = Ring<kPair>;
+  constexpr int kStages = R::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  HeadSmem<kPair>& sm =
+      *reinterpret_cast<HeadSmem<kPair>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.accf[i], 1);
+      mbar_init(&sm.acce[i], kPair ? 2 * kEpiWarps : kEpiWarps);
+    }
+    mbar_init(&sm.fin, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if (kPair) {
+      tmem_alloc_pair(&sm.tmem_base, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&sm.tmem_base, 512);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();   // both CTAs' barriers exist before any remote arrival
+  tc_fence_after();
+  grid_dep_sync();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return kPair ? mbar_wait_cluster(bar, parity, a.status, abort) : mbar_wait(bar, parity, a.status, abort);
+  };
+  const int n_rows = a.n_rows != nullptr ? *a.n_rows : (int)a.T;
+  const Plan<kMode, kPair> plan(a, n_rows);
+  const int first = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int stride = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  constexpr int kTileM = kPair ? 2 * kBM : kBM;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const CUtensorMap* x = a.always_gathered || n_rows < a.T ? &gathered : &hidden;
+      uint32_t stage = 0, phase = 0;
+      for (int t = first; t < plan.total; t += stride) {
+        const Unit u = plan.unit(a, t);
+        const int am = u.m * kTileM + (int)rank * kBM;                     // this CTA's rows of A
+        const int bn = u.n * kBN + (kPair ? (int)rank * (kBN / 2) : 0);    // and of B
+        for (int kb = u.k0; kb < u.k1; ++kb) {
+          if (!wait(&sm.empty[stage], phase ^ 1u)) goto loads_done;
+          uint8_t* dst = sm.stage[stage];
+          // a pair's bytes all count on CTA 0's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], (kPair ? 2 : 1) * R::kStageBytes);
+          const uint32_t bar = kPair ? cluster_addr(&sm.full[stage], 0) : smem_u32(&sm.full[stage]);
+          auto load = [&](int box, const CUtensorMap* map, int cx, int cy) {
+            if (kPair) tma_load_2d_pair(dst + box * kBox, map, cx, cy, bar);
+            else tma_load_2d(dst + box * kBox, map, cx, cy, &sm.full[stage]);
+          };
+          const int k = kb * kBK;
+          if (kMode != kProducts) {
+#pragma unroll
+            for (int i = 0; i < R::kABoxes; ++i) load(i, x, k, am + 64 * i);
+#pragma unroll
+            for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, k, a.v0 + bn + 64 * i);
+          } else if (!u.w) {
+#pragma unroll
+            for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, k, am + 64 * i);
+#pragma unroll
+            for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, bn + 64 * i, a.v0 + k);
+          } else {
+#pragma unroll
+            for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, am + 64 * i, k);
+#pragma unroll
+            for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, x, bn + 64 * i, k);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    loads_done:;
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t stage = 0, phase = 0;
+      int it = 0;
+      for (int t = first; t < plan.total; t += stride, ++it) {
+        const Unit u = plan.unit(a, t);
+        const uint32_t acc = it & 1, acc_phase = (it >> 1) & 1;
+        if (!wait(&sm.acce[acc], acc_phase ^ 1u)) break;
+        tc_fence_after();
+        const bool a_mn = kMode == kProducts && u.w, b_mn = kMode == kProducts;
+        const uint32_t idesc = idesc_16(a.f16 != 0, kTileM, a_mn, b_mn);
+        // K-major: a step of 16 is 32 bytes of each row.  Other-major: a box is 64 rows of the
+        // contraction by 64 columns; a step is 16 rows (2048 bytes), the next 64 columns one box on.
+        const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+        const uint32_t a_lbo = a_mn ? kBox : 16, b_lbo = b_mn ? kBox : 16;
+        const uint32_t d = tmem + acc * kBN;
+        for (int kb = u.k0; kb < u.k1; ++kb) {
+          if (!wait(&sm.full[stage], phase)) goto mma_done;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm.stage[stage]), sb = sa + R::kABoxes * kBox;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t ad = smem_desc(sa + a_step * j, a_lbo, 1024, 2);
+            const uint64_t bd = smem_desc(sb + b_step * j, b_lbo, 1024, 2);
+            const uint32_t on = kb > u.k0 || j > 0 ? 1u : 0u;
+            if (kPair) tc_mma_f16_pair(d, ad, bd, idesc, on);
+            else tc_mma_f16(d, ad, bd, idesc, on);
+          }
+          if (kPair) {
+            tc_commit_pair(cluster_addr(&sm.empty[stage], 0));
+            tc_commit_pair(cluster_addr(&sm.empty[stage], 1));
+          } else {
+            tc_commit(&sm.empty[stage]);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (kPair) {
+          tc_commit_pair(cluster_addr(&sm.accf[acc], 0));
+          tc_commit_pair(cluster_addr(&sm.accf[acc], 1));
+        } else {
+          tc_commit(&sm.accf[acc]);
+        }
+      }
+    mma_done:
+      // whatever the exit, no MMA is still running when the TMEM is freed (a bounded wait of its
+      // own, also after an abort)
+      if (kPair) tc_commit_pair(cluster_addr(&sm.fin, 0));
+      else tc_commit(&sm.fin);
+      volatile int no_abort = 0;
+      mbar_wait(&sm.fin, 0, a.status, &no_abort, 1000000000ull);
+    }
+  } else {
+    const int q = warp & 3, ew = warp - 2, half = ew >> 2;   // TMEM lanes, columns of the tile
+    uint8_t* buf = sm.out[ew];
+    const uint32_t acce0 = kPair ? cluster_addr(&sm.acce[0], 0) : 0u;
+    const float c1 = a.scale * kLog2e;
+    int it = 0;
+    for (int t = first; t < plan.total; t += stride, ++it) {
+      const Unit u = plan.unit(a, t);
+      const uint32_t acc = it & 1, acc_phase = (it >> 1) & 1;
+      const int row0 = u.m * kTileM + (int)rank * kBM + q * 32, row = row0 + lane;
+      const int col0 = u.n * kBN + half * 128;
+      if (!__all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], acc_phase))) break;
+      tc_fence_after();
+      uint32_t v[4][32];
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) NVFP4_TMEM_LD_X32(taddr + 32 * c, v[c]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster(acce0 + acc * (uint32_t)sizeof(uint64_t));
+        else mbar_arrive(&sm.acce[acc]);
+      }
+      auto val = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
+
+      if constexpr (kMode == kStats) {
+        const int live = min(max(a.width - col0, 0), 128);
+        if (live < 128) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= live) v[i >> 5][i & 31] = 0xFF800000u;   // -inf
+        }
+        if (row0 >= n_rows) continue;
+        float m = val(0);
+#pragma unroll
+        for (int i = 1; i < 128; ++i) m = fmaxf(m, val(i));
+        const float mm = m == -INFINITY ? 0.f : m;
+        const F2 neg = pack2(-mm, -mm), cc = pack2(c1, c1);
+        F2 s2 = pack2(0.f, 0.f), u2 = s2;
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) {
+          const F2 d = mul2(add2(pack2(val(i), val(i + 1)), neg), cc);
+          const float2 f = unpack2(d);
+          const F2 e = pack2(ex2(f.x), ex2(f.y));
+          s2 = add2(s2, e);
+          // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from -inf
+          if (a.part_u != nullptr) u2 = fma2(e, pack2(fmaxf(f.x, -1000.f), fmaxf(f.y, -1000.f)), u2);
+        }
+        if (row < n_rows) {
+          const float2 s = unpack2(s2), w = unpack2(u2);
+          const int64_t at = (int64_t)(2 * u.n + half) * a.pitch + row;
+          a.part_m[at] = m;
+          a.part_s[at] = s.x + s.y;
+          if (a.part_u != nullptr) a.part_u[at] = w.x + w.y;
+          if (a.targets != nullptr) {
+            const int rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
+            if (rel >= 0 && rel < live) {
+              float y = 0.f;
+#pragma unroll
+              for (int i = 0; i < 128; ++i)
+                if (i == rel) y = val(i);
+              a.target_logit[row] = y;
+            }
+          }
+        }
+      } else if constexpr (kMode == kGrad) {
+        const int live = min(max(a.width - col0, 0), 128);
+        if (row0 >= (n_rows + 63) / 64 * 64) continue;   // nobody reads these rows
+        RowGrad g{0.f, 0.f, 0.f, 0.f};
+        int rel = -1;
+        const bool on = row < n_rows;
+        if (on) {
+          g = a.rows[row];
+          rel = a.row_target[row] - a.v0 - col0;
+        }
+        const F2 cc = pack2(a.scale, a.scale), ll = pack2(-g.lse, -g.lse), to2 = pack2(kLog2e, kLog2e);
+        const F2 aa = pack2(g.a, g.a), bb = pack2(g.b, g.b);
+#pragma unroll
+        for (int b2 = 0; b2 < 2; ++b2) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int j = 64 * b2 + 2 * i;
+            const float2 lt = unpack2(mul2(fma2(pack2(val(j), val(j + 1)), cc, ll), to2));
+            const F2 p = pack2(ex2(lt.x), ex2(lt.y));
+            float2 d = unpack2(mul2(p, fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa)));
+            if (j == rel) d.x += g.zy;
+            if (j + 1 == rel) d.y += g.zy;
+            if (!on || j >= live) d.x = 0.f;
+            if (!on || j + 1 >= live) d.y = 0.f;
+            if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(d.y), "f"(d.x));
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(d.y), "f"(d.x));
+          }
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&out0, buf, col0 + 64 * b2, row0);
+            bulk_commit();
+          }
+        }
+      } else {
+        const bool empty = u.k0 >= u.k1;
+        if (!u.w) {
+          // float32 sums of dhidden
+          if (row0 >= n_rows) continue;
+          const int y = (int)((int64_t)u.split * a.x_pitch) + row0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int x = col0 + 32 * c;
+            if (x >= a.H) break;
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  empty ? make_uint4(0, 0, 0, 0)
+                        : make_uint4(v[c][4 * j], v[c][4 * j + 1], v[c][4 * j + 2], v[c][4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (a.x_first) tma_store_2d(&out0, buf, x, y);
+              else tma_add_2d(&out0, buf, x, y);
+              bulk_commit();
+            }
+          }
+        } else {
+          // rows of dweight
+          const int y = a.v0 + row0;
+          if (y >= a.V) continue;
+          const float f = a.w_factor != nullptr ? *a.w_factor : 1.f;
+#pragma unroll
+          for (int b2 = 0; b2 < 2; ++b2) {
+            const int x = col0 + 64 * b2;
+            if (x >= a.H) break;
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int j = 64 * b2 + 2 * i;
+              const float dx = empty ? 0.f : val(j) * f, dy = empty ? 0.f : val(j + 1) * f;
+              if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dy), "f"(dx));
+              else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dy), "f"(dx));
+            }
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&out1, buf, x, y);
+              bulk_commit();
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();   // no remote arrival or peer read is left in flight
+  tc_fence_after();
+  if (warp == 1) {
+    if (kPair) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------ joining
+
+struct JoinArgs {
+  int64_t T, pitch;
+  int parts, V;
+  const float* m;
+  const float* s;
+  const float* u;
+  const float* target_logit;
+  const int32_t* targets;
+  int32_t ignore;
+  const int32_t* place;      // row -> gathered row or -1, nullable: itself
+  const int32_t* n_rows;     // nullable
+  float scale;
+  float* logprob;
+  float* lse;
+  float* entropy;
+  int* status;
+};
+
+// 32 rows a CTA, a lane each; warp w takes parts w, w + 32, ...
+__global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
+  __shared__ float sm_m[32][33], sm_s[32][33], sm_u[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_sync();
+  const float c1 = a.scale * kLog2e;
+  const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+  const int32_t y = t < a.T && a.targets != nullptr ? a.targets[t] : 0;
+  const bool skip = t >= a.T || (a.targets != nullptr && y == a.ignore);
+  const bool moved = a.n_rows != nullptr && *a.n_rows < a.T;
+  const int64_t row = skip ? -1 : moved ? a.place[t] : t;
+  float m = -INFINITY, s = 0.f, u = 0.f;
+  auto join = [&](float m2, float s2, float u2) {
+    if (s2 == 0.f) return;                       // nothing allowed there
+    const float top = fmaxf(m, m2);
+    const float d1 = s == 0.f ? 0.f : (m - top) * c1, d2 = (m2 - top) * c1;
+    const float f1 = ex2(d1), f2 = ex2(d2);
+    u = f1 * fmaf(s, d1, u) + f2 * fmaf(s2, d2, u2);
+    s = f1 * s + f2 * s2;
+    m = top;
+  };
+  if (row >= 0) {
+#pragma unroll 8
+    for (int c = warp; c < a.parts; c += 32) {
+      const int64_t at = c * a.pitch + row;
+      join(a.m[at], a.s[at], a.u != nullptr ? a.u[at] : 0.f);
+    }
+  }
+  sm_m[warp][lane] = m;
+  sm_s[warp][lane] = s;
+  sm_u[warp][lane] = u;
+  __syncthreads();
+  if (warp != 0 || t >= a.T) return;
+  for (int w = 1; w < 32; ++w) join(sm_m[w][lane], sm_s[w][lane], sm_u[w][lane]);
+  if (skip) {
+    if (a.logprob != nullptr) a.logprob[t] = 0.f;
+    a.lse[t] = 0.f;
+    if (a.entropy != nullptr) a.entropy[t] = 0.f;
+    return;
+  }
+  const bool none = s == 0.f;                    // every token at -inf
+  const float ln_s = logf(s);
+  if (a.logprob != nullptr) {
+    float lp = -INFINITY;
+    if (y < 0 || y >= a.V) {
+      set_status(a.status, kStatusBadInput);
+      lp = NAN;
+    } else if (!none) {
+      lp = fmaf(a.target_logit[row] - m, a.scale, -ln_s);
+    }
+    a.logprob[t] = lp;
+  }
+  a.lse[t] = none ? -INFINITY : fmaf(m, a.scale, ln_s);
+  if (a.entropy != nullptr) {
+    const float h = ln_s - kLn2 * (u / s);
+    a.entropy[t] = none || h < 0.f ? 0.f : h;    // round-off below 0
+  }
+}
+
+// ------------------------------------------------------------------------------ gathering
+
+struct GatherArgs {
+  const void* hidden;
+  int64_t ldh, T;
+  int H, V, f16;
+  const int32_t* targets;    // nullable
+  int32_t ignore;
+  float scale;
+  const float* lse;          // nullable: forward
+  const float* entropy;
+  const float* dlogprob;
+  const float* dentropy;
+  int32_t* place;            // [T]
+  int32_t* index;            // [T]
+  int32_t* n_rows;
+  float* factors;            // [0]: dweight's factor (half precision)
+  float* row_factor;         // [rows]: dhidden's factors
+  void* gathered;            // [rows rounded up to 64][H], where not all rows take part
+  void* weighted;            // the same times r / max r, always (backward, half precision)
+  RowGrad* rows;
+  int32_t* row_target;
+};
+
+// Half precision holds d only down to 2^-24: a row travels as d / r with r the power of two above its
+// weight, and its hidden row as hidden r / max r.
+constexpr float kUp = 16384.f;    // d / r is below 1: 2^14 leaves room below the largest value
+__device__ __forceinline__ float row_weight(const GatherArgs& a, int64_t t) {
+  const float g = a.dlogprob != nullptr ? fabsf(a.dlogprob[t]) : 0.f;
+  const float h = a.dentropy != nullptr ? fabsf(a.dentropy[t]) : 0.f;
+  const float w = a.scale * (g + 16.f * h);     // |p (ln p + entropy)| < 16
+  if (!(w < INFINITY)) return 1.f;
+  int e;
+  frexpf(w, &e);
+  return w == 0.f ? 0.f : ldexpf(1.f, min(max(e, -100), 100));
+}
+
+// The rows that take part, in their order: one CTA.
+__global__ void __launch_bounds__(1024) head_select_kernel(const GatherArgs a) {
+  __shared__ int sm_n[32];
+  __shared__ float sm_r[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_sync();
+  int base = 0;
+  float r = 0.f;
+  for (int64_t t0 = 0; t0 < a.T; t0 += 1024) {
+    const int64_t t = t0 + threadIdx.x;
+    bool on = t < a.T;
+    if (on && a.targets != nullptr) on = a.targets[t] != a.ignore;
+    if (on && a.lse != nullptr) on = !(a.lse[t] < kLowestLse);
+    const uint32_t b = __ballot_sync(0xFFFFFFFFu, on);
+    if (lane == 0) sm_n[warp] = __popc(b);
+    __syncthreads();
+    const int below = lane < 32 ? sm_n[lane] : 0;
+    int sum = below;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int at = base + __shfl_sync(0xFFFFFFFFu, sum - below, warp) + __popc(b & ((1u << lane) - 1u));
+    if (t < a.T) a.place[t] = on ? at : -1;
+    if (on) {
+      a.index[at] = (int32_t)t;
+      if (a.f16 && a.lse != nullptr) r = fmaxf(r, row_weight(a, t));
+    }
+    base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, d));
+  if (lane == 0) sm_r[warp] = r;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 32; ++w) r = fmaxf(r, sm_r[w]);
+    *a.n_rows = base;
+    if (a.factors != nullptr) {
+      a.factors[0] = a.f16 ? r / kUp : 1.f;
+      a.factors[1] = r;
+    }
+  }
+}
+
+// A warp a row: the gathered rows (zeros up to a multiple of 64), and what the gradient needs of them.
+__global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
+  grid_dep_sync();
+  const int n = *a.n_rows;
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const bool scaled = a.f16 && a.lse != nullptr;
+  if (i >= (n + 63) / 64 * 64) return;
+  const int64_t t = i < n ? a.index[i] : 0;
+  float ratio = 1.f;
+  if (i < n && a.lse != nullptr) {
+    const float r = scaled ? row_weight(a, t) : 1.f;
+    if (scaled) ratio = a.factors[1] > 0.f ? r / a.factors[1] : 1.f;
+    if (lane == 0) {
+      const float up = !scaled ? 1.f : r > 0.f ? kUp / r : 0.f;
+      const int32_t y = a.targets != nullptr ? a.targets[t] : -1;
+      const bool hit = y >= 0 && y < a.V;   // a target that the forward refused adds nothing
+      const float g = a.dlogprob != nullptr && hit ? a.dlogprob[t] * up : 0.f;
+      const float h = a.dentropy != nullptr ? a.dentropy[t] * up : 0.f;
+      RowGrad w;
+      w.a = -a.scale * (g + (a.dentropy != nullptr ? h * a.entropy[t] : 0.f));
+      w.b = -a.scale * h * kLn2;
+      w.lse = a.lse[t];
+      w.zy = a.scale * g;
+      a.rows[i] = w;
+      a.row_target[i] = hit ? y : -1;
+      a.row_factor[i] = scaled ? r / kUp : 1.f;
+    }
+  }
+  const bool gather = n < a.T;   // else the rows are read where they are
+  if (!gather && !scaled) return;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + t * a.ldh);
+  for (int c = lane; c < a.H / 8; c += 32) {
+    uint4 q = i < n ? src[c] : make_uint4(0, 0, 0, 0);
+    if (gather) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.gathered) + i * a.H)[c] = q;
+    if (scaled) {
+      __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(h[j]);
+        h[j] = __floats2half2_rn(f.x * ratio, f.y * ratio);
+      }
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.weighted) + i * a.H)[c] = q;
+    }
+  }
+}
+
+struct FinishArgs {
+  int64_t T, pitch;
+  int H, f16, splits;
+  const int32_t* place;
+  const float* row_factor;
+  const float* sums;         // [splits][pitch][H]
+  void* out;
+};
+
+__global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs a) {
+  grid_dep_sync();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = a.H / 8;
+  const int64_t t = i / per;
+  if (t >= a.T) return;
+  const int c = (int)(i - t * per) * 8;
+  const int place = a.place[t];
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (place >= 0) {
+    for (int s = 0; s < a.splits; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.pitch + place) * a.H + c);
+      const float4 x = p[0], y = p[1];
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+    const float f = a.row_factor[place];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + t * a.H + c) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------------------ host
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+bool pairs(int64_t T) { return T > kBM; }
+
+struct ForwardPlan {
+  int64_t pitch;
+  int parts;
+  bool gather;
+  size_t place, index, n, target, gathered, m, s, u, total;
+};
+ForwardPlan forward_plan(int64_t T, int64_t V, int64_t H) {
+  ForwardPlan p;
+  p.pitch = round_up(T, 32);
+  p.parts = (int)((V + kBN - 1) / kBN * 2);
+  p.gather = T > 2 * kBM;   // fewer rows are one row of tiles whatever takes part
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) & ~size_t(255);
+    return o;
+  };
+  p.n = take(4);
+  p.place = take(4 * (size_t)T);
+  p.index = take(4 * (size_t)T);
+  p.target = take(4 * (size_t)p.pitch);
+  p.gathered = take(p.gather ? 2 * (size_t)round_up(T, 64) * (size_t)H : 0);
+  p.m = take(4 * (size_t)p.parts * (size_t)p.pitch);
+  p.s = take(4 * (size_t)p.parts * (size_t)p.pitch);
+  p.u = take(4 * (size_t)p.parts * (size_t)p.pitch);
+  p.total = at;
+  return p;
+}
+
+struct BackwardPlan {
+  int64_t rows;              // T rounded up to 64
+  int64_t piece;             // columns of a piece of the vocabulary
+  int splits;
+  size_t n, factors, place, index, grad, target, row_factor, gathered, weighted, d, sums, total;
+};
+BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
+  BackwardPlan p;
+  p.rows = round_up(T, 64);
+  const int64_t vp = round_up(V, kBN);
+  int64_t piece = std::max<int64_t>(8192, round_up(((int64_t)1 << 27) / p.rows, kBN));
+  const int64_t pieces = (vp + piece - 1) / piece;
+  p.piece = round_up((vp + pieces - 1) / pieces, kBN);
+  // few rows: dhidden's contraction is cut so that every SM has a part of it
+  const int64_t tiles = (T + 2 * kBM - 1) / (2 * kBM) * ((H + kBN - 1) / kBN);
+  p.splits = pieces == 1 ? (int)std::min<int64_t>(std::max<int64_t>(1, 76 / tiles), 32) : 1;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) & ~size_t(255);
+    return o;
+  };
+  p.n = take(4);
+  p.factors = take(8);
+  p.place = take(4 * (size_t)T);
+  p.index = take(4 * (size_t)T);
+  p.grad = take(sizeof(RowGrad) * (size_t)p.rows);
+  p.target = take(4 * (size_t)p.rows);
+  p.row_factor = take(4 * (size_t)p.rows);
+  p.gathered = take(2 * (size_t)p.rows * (size_t)H);
+  p.weighted = take(2 * (size_t)p.rows * (size_t)H);   // (a call does not say whether it is half precision)
+  p.d = take(2 * (size_t)p.rows * (size_t)p.piece);
+  p.sums = take(4 * (size_t)p.splits * (size_t)p.rows * (size_t)H);
+  p.total = at;
+  return p;
+}
+
+template <int kMode, bool kPair>
+cudaError_t launch_head(const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t units, cudaStream_t s) {
+  const void* fn = (const void*)head_kernel<kMode, kPair>;
+  static std::atomic<bool> attr_set[64];
+  cudaError_t err = set_smem_attr_once(attr_set, fn, (int)smem_bytes<kPair>());
+  if (err != cudaSuccess || units == 0) return err;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPair ? 2 : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem_bytes<kPair>();
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  int64_t clusters = kPair ? num_sms() / 2 : num_sms();
+  if (units < clusters) clusters = units;
+  cfg.gridDim = dim3((unsigned)(clusters * (kPair ? 2 : 1)), 1, 1);
+  return cudaLaunchKernelEx(&cfg, head_kernel<kMode, kPair>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
+}
+template <int kMode>
+cudaError_t launch_head(bool pair, const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t units, cudaStream_t s) {
+  return pair ? launch_head<kMode, true>(maps, a, units, s) : launch_head<kMode, false>(maps, a, units, s);
+}
+
+}  // namespace
+
+size_t head_workspace(int64_t T, int64_t V, int64_t H, bool backward) {
+  return backward ? backward_plan(T, V, H).total : forward_plan(T, V, H).total;
+}
+
+cudaError_t launch_head_logprobs(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, int dtype, int64_t T,
+                                 int64_t V, int64_t H, const int32_t* targets, int32_t ignore, float scale,
+                                 float* logprob, float* lse, float* entropy, void* workspace, cudaStream_t s) {
+  const ForwardPlan p = forward_plan(T, V, H);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto f32 = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  auto i32 = [&](size_t o) { return reinterpret_cast<int32_t*>(ws + o); };
+  const bool gather = p.gather && targets != nullptr, pair = pairs(T);
+  const CUtensorMapDataType dt = dtype == kActF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap maps[6];
+  if (!make_tensor_map(&maps[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
+      !make_tensor_map(&maps[2], weight, V, H, 2 * ldw, 64, dt, 2))
+    return cudaErrorInvalidValue;
+  maps[1] = maps[0];
+  if (gather && !make_tensor_map(&maps[1], ws + p.gathered, round_up(T, 64), H, 2 * H, 64, dt, 2))
+    return cudaErrorInvalidValue;
+  maps[3] = maps[4] = maps[5] = maps[2];
+  cudaError_t err = cudaSuccess;
+  if (gather) {
+    GatherArgs g{};
+    g.hidden = hidden, g.ldh = ldh, g.T = T, g.H = (int)H, g.V = (int)V, g.f16 = dtype == kActF16;
+    g.targets = targets, g.ignore = ignore;
+    g.place = i32(p.place), g.index = i32(p.index), g.n_rows = i32(p.n), g.gathered = ws + p.gathered;
+    err = launch_pdl(false, head_select_kernel, dim3(1), dim3(1024), 0, s, g);
+    if (err == cudaSuccess)
+      err = launch_pdl(true, head_gather_kernel, dim3((unsigned)(round_up(T, 64) / 8)), dim3(256), 0, s, g);
+    if (err != cudaSuccess) return err;
+  }
+  HeadArgs a{};
+  a.T = T, a.n_rows = gather ? i32(p.n) : nullptr, a.V = (int)V, a.H = (int)H, a.f16 = dtype == kActF16;
+  a.scale = scale, a.status = device_status_ptr();
+  a.targets = targets, a.index = gather ? i32(p.index) : nullptr;
+  a.part_m = f32(p.m), a.part_s = f32(p.s), a.part_u = entropy != nullptr ? f32(p.u) : nullptr, a.pitch = p.pitch;
+  a.target_logit = f32(p.target), a.width = (int)V;
+  const int64_t tile = pair ? 2 * kBM : kBM;
+  err = launch_head<kStats>(pair, maps, a, (T + tile - 1) / tile * ((V + kBN - 1) / kBN), s);
+  if (err != cudaSuccess) return err;
+  JoinArgs j{T, p.pitch, p.parts, (int)V, a.part_m, a.part_s, a.part_u, a.target_logit, targets, ignore,
+             gather ? i32(p.place) : nullptr, a.n_rows, scale, logprob, lse, entropy, a.status};
+  return launch_pdl(true, head_join_kernel, dim3((unsigned)((T + 31) / 32)), dim3(1024), 0, s, j);
+}
+
+cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, int dtype,
+                                          int64_t T, int64_t V, int64_t H, const int32_t* targets, int32_t ignore,
+                                          float scale, const float* lse, const float* entropy, const float* dlogprob,
+                                          const float* dentropy, void* dhidden, void* dweight, void* workspace,
+                                          cudaStream_t s) {
+  const BackwardPlan p = backward_plan(T, V, H);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto f32 = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+  auto i32 = [&](size_t o) { return reinterpret_cast<int32_t*>(ws + o); };
+  const bool f16 = dtype == kActF16, pair = pairs(T);
+  const CUtensorMapDataType dt = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  GatherArgs g{};
+  g.hidden = hidden, g.ldh = ldh, g.T = T, g.H = (int)H, g.V = (int)V, g.f16 = f16;
+  g.targets = targets, g.ignore = ignore, g.scale = scale;
+  g.lse = lse, g.entropy = entropy, g.dlogprob = dlogprob, g.dentropy = dentropy;
+  g.place = i32(p.place), g.index = i32(p.index), g.n_rows = i32(p.n), g.factors = f32(p.factors);
+  g.row_factor = f32(p.row_factor), g.gathered = ws + p.gathered, g.weighted = ws + p.weighted;
+  g.rows = reinterpret_cast<RowGrad*>(ws + p.grad), g.row_target = i32(p.target);
+  cudaError_t err = launch_pdl(false, head_select_kernel, dim3(1), dim3(1024), 0, s, g);
+  if (err == cudaSuccess)
+    err = launch_pdl(true, head_gather_kernel, dim3((unsigned)(p.rows / 8)), dim3(256), 0, s, g);
+  if (err != cudaSuccess) return err;
+
+  HeadArgs a{};
+  a.T = T, a.n_rows = i32(p.n), a.V = (int)V, a.H = (int)H, a.f16 = f16;
+  a.scale = scale, a.status = device_status_ptr();
+  a.rows = g.rows, a.row_target = g.row_target;
+  a.x_splits = p.splits, a.x_pitch = p.rows;
+  a.want_x = dhidden != nullptr, a.want_w = dweight != nullptr;
+  a.w_factor = f16 ? g.factors : nullptr;
+  CUtensorMap grad[6], prod[6];
+  if (!make_tensor_map(&grad[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
+      !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * H, 64, dt, 2) ||
+      !make_tensor_map(&grad[2], weight, V, H, 2 * ldw, 64, dt, 2) ||
+      !make_tensor_map(&grad[3], ws + p.d, p.rows, p.piece, 2 * p.piece, 64, dt, 2) ||
+      !make_tensor_map(&grad[4], ws + p.d, p.rows, p.piece, 2 * p.piece, 32, dt, 2) ||
+      !make_tensor_map(&prod[4], ws + p.sums, p.splits * p.rows, H, 4 * H, 32, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4) ||
+      (dweight != nullptr && !make_tensor_map(&prod[5], dweight, V, H, 2 * H, 32, dt, 2)))
+    return cudaErrorInvalidValue;
+  grad[5] = grad[4];
+  for (int i = 0; i < 4; ++i) prod[i] = grad[i];
+  if (dweight == nullptr) prod[5] = prod[4];
+  if (f16 && !make_tensor_map(&prod[1], ws + p.weighted, p.rows, H, 2 * H, 64, dt, 2)) return cudaErrorInvalidValue;
+  const int64_t tile = pair ? 2 * kBM : kBM, xn = (H + kBN - 1) / kBN;
+  for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+    a.v0 = (int)v0, a.width = (int)std::min<int64_t>(p.piece, V - v0), a.x_first = v0 == 0;
+    a.always_gathered = false;
+    err = launch_head<kGrad>(pair, grad, a, (T + tile - 1) / tile * ((a.width + kBN - 1) / kBN), s);
+    if (err != cudaSuccess) return err;
+    const int64_t units = (a.want_x ? (T + tile - 1) / tile * xn * p.splits : 0) +
+                          (a.want_w ? (a.width + tile - 1) / tile * xn : 0);
+    a.always_gathered = f16;
+    err = launch_head<kProducts>(pair, prod, a, units, s);
+    if (err != cudaSuccess) return err;
+  }
+  if (dhidden == nullptr) return cudaSuccess;
+  FinishArgs f{T, p.rows, (int)H, f16, p.splits, g.place, g.row_factor, f32(p.sums), dhidden};
+  return launch_pdl(true, head_finish_kernel, dim3((unsigned)((T * (H / 8) + 255) / 256)), dim3(256), 0, s, f);
+}
+
+}  // namespace nvfp4

@@ -231,6 +231,36 @@ cudaError_t launch_block_norm_backward(const void* dr, int64_t lddr, const void*
                                        void* dx, void* dy, float* dweight, float* dgate, float* dnext, float* partial,
                                        cudaStream_t s);
 
+// The router's losses (router_loss.cu): 1 <= E <= 1024, 1 <= k <= 32, S sequences (offsets [S + 1], or
+// null: all rows are one).
+size_t balance_workspace(int64_t T, int64_t S, int64_t E);
+cudaError_t launch_balance_loss(const void* logits, int dtype, int64_t T, int E, int64_t ld, const int32_t* ids, int k,
+                                const int32_t* offsets, int S, const uint8_t* valid, float* loss, int32_t* counts,
+                                float* sums, int32_t* tokens, void* workspace, cudaStream_t s);
+// dweights nullable; dloss nullable, with counts and tokens.
+cudaError_t launch_router_backward(const void* logits, int dtype, int64_t T, int E, int64_t ld, const int32_t* ids,
+                                   int k, const float* dweights, bool renorm, const float* dloss,
+                                   const int32_t* counts, const int32_t* tokens, const int32_t* offsets, int S,
+                                   const uint8_t* valid, void* dlogits, int64_t ldd, cudaStream_t s);
+
+// Log probabilities from hidden rows and the head's weight (head.cu): 16-bit rows, H and the pitches
+// multiples of 8, 16-byte aligned.  targets with logprob, and entropy, nullable.
+size_t head_workspace(int64_t T, int64_t V, int64_t H, bool backward);
+cudaError_t launch_head_logprobs(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, int dtype, int64_t T,
+                                 int64_t V, int64_t H, const int32_t* targets, int32_t ignore, float scale,
+                                 float* logprob, float* lse, float* entropy, void* workspace, cudaStream_t s);
+// dhidden or dweight nullable; targets with dlogprob, and entropy with dentropy, nullable.
+cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const void* weight, int64_t ldw, int dtype,
+                                          int64_t T, int64_t V, int64_t H, const int32_t* targets, int32_t ignore,
+                                          float scale, const float* lse, const float* entropy, const float* dlogprob,
+                                          const float* dentropy, void* dhidden, void* dweight, void* workspace,
+                                          cudaStream_t s);
+
+// 2-D tensor map over a [rows, cols] matrix of `elt`-byte elements with row pitch pitch_bytes: boxes of
+// box_rows rows x 128 bytes, 128-byte swizzle.
+bool make_tensor_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t pitch_bytes,
+                     uint32_t box_rows, CUtensorMapDataType dt, int elt);
+
 constexpr int64_t kPermuteChunk = 256;    // (token, j) entries per warp in the permute
 inline int64_t permute_chunks(int64_t entries) { return (entries + kPermuteChunk - 1) / kPermuteChunk; }
 
