@@ -33,39 +33,63 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kBM = 128;                 // rows of a CTA's tile (one a TMEM lane)
-constexpr int kBN = 256;                 // columns
 constexpr int kBK = 64;                  // contraction a stage: one 128-byte swizzle row of 16-bit values
 constexpr int kBox = 64 * 128;           // bytes of one 64 x 64 box
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kPart = 128;               // columns of a partial result
+constexpr int kPart = 128;               // columns of a partial result, and of a thread of the epilogue
 constexpr float kLowestLse = -16777216.f;
 
 enum : int { kStats = 0, kGrad = 1, kProducts = 2 };
 
-template <bool kPair>
+// The statistics' logits are summed in stretches of at most 1024 products: a tensor core cuts a float32 sum
+// off where it adds to it, always towards zero, so the error of a long sum grows with its length; the
+// stretches are added to one another in registers, rounded to nearest.  Measured at H = 2048, relative errors of
+// lse / entropy and the time of 8192 x 131072 rows: one stretch 6e-7 / 1.1e-6, 2.25 ms; 1024: 3e-7 / 5e-7,
+// 2.27 ms; 512: 1.3e-7 / 2.4e-7, 2.33 ms (an accumulator takes some 4000 cycles to read under running MMAs, so
+// shorter stretches wait for it).
+constexpr int kStretch = 1024 / kBK;
+
+// Columns of a tile: 256; 128 for a row of tiles of logits by single CTAs (few rows: the weight's bytes
+// bound it, and the smaller tiles spread evenly over the SMs).
+constexpr int tile_cols(int mode, bool pair) { return pair || mode == kProducts ? 256 : 128; }
+
+template <int kMode, bool kPair>
 struct Ring {
-  static constexpr int kABoxes = 2;                        // 128 rows of A
-  static constexpr int kBBoxes = kPair ? 2 : 4;            // 256 rows of B, or this CTA's half
-  static constexpr int kStageBytes = (kABoxes + kBBoxes) * kBox;
-  static constexpr int kStages = kPair ? 6 : 4;
+  static constexpr int kBN = tile_cols(kMode, kPair);
+  static constexpr int kABoxes = 2;                                    // 128 rows of A
+  static constexpr int kBBoxes = (kPair ? kBN / 2 : kBN) / 64;         // B's rows, or this CTA's half of them
+  // A stage is two blocks of the contraction, with one barrier each way: against stages of one block it raised
+  // the tensor cores' share of the time from 84 to 98% (8192 x 131072 x 2048).
+  static constexpr int kSub = 2;
+  static constexpr int kSubBytes = (kABoxes + kBBoxes) * kBox;
+  static constexpr int kStageBytes = kSub * kSubBytes;
+  static constexpr int kStages = kBBoxes == 2 ? 3 : 2;
+  // The epilogue's warps.  256 columns: each has half of every tile, of two accumulators; 128: warps 0-3 and
+  // 4-7 take turns with the tiles, each four with two accumulators of their own.
+  static constexpr int kGroups = kBN == 256 ? 1 : 2;
+  static constexpr int kAccWarps = kEpiWarps / kGroups;
+  static constexpr int kAccs = 2 * kGroups;
 };
 
-template <bool kPair>
+template <int kMode, bool kPair>
 struct HeadSmem {
-  uint8_t stage[Ring<kPair>::kStages][Ring<kPair>::kStageBytes];
+  using R = Ring<kMode, kPair>;
+  uint8_t stage[R::kStages][R::kStageBytes];
   uint8_t out[kEpiWarps][32 * 128];      // 32-row boxes on their way out
-  uint64_t full[Ring<kPair>::kStages];
-  uint64_t empty[Ring<kPair>::kStages];
-  uint64_t accf[2];
-  uint64_t acce[2];
+  uint64_t full[R::kStages];
+  uint64_t empty[R::kStages];
+  uint64_t accf[R::kAccs];
+  uint64_t acce[R::kAccs];
   uint64_t fin;
   uint32_t tmem_base;
   int abort;
 };
-template <bool kPair>
-constexpr size_t smem_bytes() { return sizeof(HeadSmem<kPair>) + 1024; }
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
+template <int kMode, bool kPair>
+constexpr size_t smem_bytes() { return sizeof(HeadSmem<kMode, kPair>) + 1024; }
+static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kStats, true>() <= 232448 &&
+                  smem_bytes<kProducts, false>() <= 232448,
+              "shared memory budget");
 
 // What a row of the gradient needs: d = p (a + b log2 p), + zy at the target.
 struct RowGrad {
@@ -80,6 +104,7 @@ struct HeadArgs {
   int f16;
   float scale;
   int* status;
+  int x_rows;                // rows of a box of hidden rows: 64, or fewer where there are no more
   // statistics
   const int32_t* targets;    // nullable
   const int32_t* index;      // row -> row of targets, nullable: itself
@@ -92,6 +117,7 @@ struct HeadArgs {
   int v0, width;             // the piece of the vocabulary
   const RowGrad* rows;
   const int32_t* row_target;
+  bool entropy;              // some row's b is not 0
   // products
   int x_splits;              // parts of dhidden's contraction
   int64_t x_pitch;           // rows between their sums
@@ -100,62 +126,108 @@ struct HeadArgs {
   const float* w_factor;     // nullable: 1
 };
 
-__device__ __forceinline__ uint32_t idesc_16(bool f16, uint32_t M, bool a_mn, bool b_mn) {
+__device__ __forceinline__ uint32_t idesc_16(bool f16, uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
   const uint32_t fmt = f16 ? 0u : 1u;
   return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(kBN >> 3) << 17) | ((M >> 4) << 24);
+         ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // One tile of work.
 struct Unit {
   bool w;                    // products: a tile of dweight (else of dhidden)
   int m, n, split;           // tile numbers (m in CTA-pair rows where there are pairs)
+  int cols;                  // columns to compute: a multiple of 32
   int k0, k1;                // stages of the contraction
+  int turns, len;            // stretches, stages of one (the last may be shorter)
 };
 
+// The tiles of one CTA or pair, unit(0), unit(1), ... until it says false.
 template <int kMode, bool kPair>
 struct Plan {
-  int rows, m_tiles, n_tiles, total;
-  int xm, xn, x_units, x_kb, wm, w_kb;
+  static constexpr int kBN = tile_cols(kMode, kPair);
+  static constexpr int kTileM = kPair ? 2 * kBM : kBM;
+  int p, P;                  // this one, of how many
+  int m_tiles, n_tiles, total;
+  // products: the kind with the longer contraction goes first, one after the other to everyone; those
+  // who got one less take more of the other kind
+  bool x_long;
+  int xm, xn, x_kb, w_kb, longs, shorts, extra, both, more;
   __device__ Plan(const HeadArgs& a, int n) {
-    constexpr int kTileM = kPair ? 2 * kBM : kBM;
-    rows = n;
+    p = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    P = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
     if (kMode == kProducts) {
       xm = (n + kTileM - 1) / kTileM;
       xn = (a.H + kBN - 1) / kBN;
       x_kb = (a.width + kBK - 1) / kBK;
-      x_units = a.want_x ? xm * xn * a.x_splits : 0;
-      wm = (a.width + kTileM - 1) / kTileM;
       w_kb = (n + kBK - 1) / kBK;
-      total = x_units + (a.want_w ? wm * xn : 0);
+      const int xs = a.want_x ? xm * xn * a.x_splits : 0, ws = a.want_w ? (a.width + kTileM - 1) / kTileM * xn : 0;
+      // a tile's cost in stages of the contraction, its epilogue as 8
+      const int cx = x_kb / a.x_splits + 8, cw = w_kb + 8;
+      x_long = cx >= cw;
+      longs = x_long ? xs : ws;
+      shorts = x_long ? ws : xs;
+      extra = longs % P;                           // the first `extra` have one long tile more
+      const int ratio = x_long ? cx / cw : cw / cx;
+      // `both` short tiles for everyone, `more` for those without a long one more
+      more = extra > 0 ? ratio : 0;
+      if ((int64_t)more * (P - extra) >= shorts) {
+        both = 0;
+        more = extra > 0 ? (shorts + P - extra - 1) / (P - extra) : 0;
+      } else {
+        both = (shorts - more * (P - extra) + P - 1) / P;
+      }
     } else {
       m_tiles = (n + kTileM - 1) / kTileM;
       n_tiles = (a.width + kBN - 1) / kBN;
       total = m_tiles * n_tiles;
     }
   }
-  __device__ Unit unit(const HeadArgs& a, int t) const {
-    Unit u{};
+  __device__ bool unit(const HeadArgs& a, int i, Unit& u) const {
+    u = Unit{};
     if (kMode != kProducts) {
+      const int t = p + i * P;
+      if (t >= total) return false;
       u.n = t / m_tiles;                 // the weight's rows are read once, the hidden rows stay in L2
       u.m = t - u.n * m_tiles;
+      u.cols = kBN;
       u.k1 = (a.H + kBK - 1) / kBK;
-    } else if (t < x_units) {
+      u.turns = kMode == kStats ? (u.k1 + kStretch - 1) / kStretch : 1;
+      u.len = (u.k1 + u.turns - 1) / u.turns;
+      u.turns = (u.k1 + u.len - 1) / u.len;
+      return true;
+    }
+    int t;
+    const int mine = longs / P + (p < extra ? 1 : 0);
+    const bool first = i < mine;
+    if (first) {
+      t = p + i * P;
+    } else {
+      i -= mine;
+      if (i < both) {
+        t = p + i * P;
+      } else {
+        i -= both;
+        if (p < extra || i >= more) return false;
+        t = both * P + i * (P - extra) + p - extra;
+      }
+      if (t >= shorts) return false;
+    }
+    u.w = first != x_long;
+    if (!u.w) {
       const int per = xm * xn;
       u.split = t / per;
-      const int r = t - u.split * per;
-      u.m = r / xn;
-      u.n = r - u.m * xn;
+      t -= u.split * per;
       u.k0 = (int)((int64_t)x_kb * u.split / a.x_splits);
       u.k1 = (int)((int64_t)x_kb * (u.split + 1) / a.x_splits);
     } else {
-      const int r = t - x_units;
-      u.w = true;
-      u.m = r / xn;
-      u.n = r - u.m * xn;
       u.k1 = w_kb;
     }
-    return u;
+    u.m = t / xn;
+    u.n = t - u.m * xn;
+    u.cols = min(kBN, (a.H - u.n * kBN + 31) / 32 * 32);
+    u.turns = 1;
+    u.len = u.k1 - u.k0;
+    return true;
   }
 };
 
@@ -164,11 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     head_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap gathered,
                 const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap dlogits,
                 const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1, const HeadArgs a) {
-  using R = Ring<kPair>;
-  constexpr int kStages = R::kStages;
+  using R = Ring<kMode, kPair>;
+  constexpr int kStages = R::kStages, kBN = R::kBN;
   extern __shared__ uint8_t smem_raw[];
-  HeadSmem<kPair>& sm =
-      *reinterpret_cast<HeadSmem<kPair>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using Smem = HeadSmem<kMode, kPair>;
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
 
@@ -177,9 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < R::kAccs; ++i) {
       mbar_init(&sm.accf[i], 1);
-      mbar_init(&sm.acce[i], kPair ? 2 * kEpiWarps : kEpiWarps);
+      mbar_init(&sm.acce[i], kPair ? 2 * R::kAccWarps : R::kAccWarps);
     }
     mbar_init(&sm.fin, 1);
     sm.abort = 0;
@@ -201,102 +273,126 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_sync();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return kPair ? mbar_wait_cluster(bar, parity, a.status, abort) : mbar_wait(bar, parity, a.status, abort);
-  };
+  // Loads and MMAs complete these barriers (the async proxy); only `acce` hears from threads of the other CTA.
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status, abort); };
   const int n_rows = a.n_rows != nullptr ? *a.n_rows : (int)a.T;
   const Plan<kMode, kPair> plan(a, n_rows);
-  const int first = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int stride = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   constexpr int kTileM = kPair ? 2 * kBM : kBM;
 
   if (warp == 0) {
     if (lane == 0) {
       const CUtensorMap* x = a.always_gathered || n_rows < a.T ? &gathered : &hidden;
       uint32_t stage = 0, phase = 0;
-      for (int t = first; t < plan.total; t += stride) {
-        const Unit u = plan.unit(a, t);
-        const int am = u.m * kTileM + (int)rank * kBM;                     // this CTA's rows of A
-        const int bn = u.n * kBN + (kPair ? (int)rank * (kBN / 2) : 0);    // and of B
-        for (int kb = u.k0; kb < u.k1; ++kb) {
-          if (!wait(&sm.empty[stage], phase ^ 1u)) goto loads_done;
-          uint8_t* dst = sm.stage[stage];
-          // a pair's bytes all count on CTA 0's barrier
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], (kPair ? 2 : 1) * R::kStageBytes);
-          const uint32_t bar = kPair ? cluster_addr(&sm.full[stage], 0) : smem_u32(&sm.full[stage]);
-          auto load = [&](int box, const CUtensorMap* map, int cx, int cy) {
-            if (kPair) tma_load_2d_pair(dst + box * kBox, map, cx, cy, bar);
-            else tma_load_2d(dst + box * kBox, map, cx, cy, &sm.full[stage]);
-          };
-          const int k = kb * kBK;
-          if (kMode != kProducts) {
+      Unit u;
+      for (int t = 0; plan.unit(a, t, u); ++t) {
+        const int am = u.m * kTileM + (int)rank * kBM;                       // this CTA's rows of A
+        const int bn = u.n * kBN + (kPair ? (int)rank * (u.cols / 2) : 0);   // and of B
+        for (int i = 0; i < u.turns; ++i) {
+          const int kb1 = min(u.k0 + (i + 1) * u.len, u.k1);
+          for (int kb0 = u.k0 + i * u.len; kb0 < kb1; kb0 += R::kSub) {
+            if (!wait(&sm.empty[stage], phase ^ 1u)) goto loads_done;
+            const int subs = min(R::kSub, kb1 - kb0);
+            // a pair's bytes all count on CTA 0's barrier
+            const int a_boxes = !kPair && kMode != kProducts && a.T <= 64 ? 1 : R::kABoxes;   // no more rows
+            const uint32_t bytes = subs * (R::kBBoxes * kBox + a_boxes * (kMode != kProducts ? a.x_rows * 128 : kBox));
+            if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], (kPair ? 2 : 1) * bytes);
+            const uint32_t bar = kPair ? cluster_addr(&sm.full[stage], 0) : smem_u32(&sm.full[stage]);
+            for (int sub = 0; sub < subs; ++sub) {
+              uint8_t* dst = sm.stage[stage] + sub * R::kSubBytes;
+              auto load = [&](int box, const CUtensorMap* map, int cx, int cy) {
+                if (kPair) tma_load_2d_pair(dst + box * kBox, map, cx, cy, bar);
+                else tma_load_2d(dst + box * kBox, map, cx, cy, &sm.full[stage]);
+              };
+              const int k = (kb0 + sub) * kBK;
+              if (kMode != kProducts) {
 #pragma unroll
-            for (int i = 0; i < R::kABoxes; ++i) load(i, x, k, am + 64 * i);
+                for (int i = 0; i < R::kABoxes; ++i)
+                  if (i < a_boxes) load(i, x, k, am + 64 * i);
 #pragma unroll
-            for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, k, a.v0 + bn + 64 * i);
-          } else if (!u.w) {
+                for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, k, a.v0 + bn + 64 * i);
+              } else if (!u.w) {
 #pragma unroll
-            for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, k, am + 64 * i);
+                for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, k, am + 64 * i);
 #pragma unroll
-            for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, bn + 64 * i, a.v0 + k);
-          } else {
+                for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, bn + 64 * i, a.v0 + k);
+              } else {
 #pragma unroll
-            for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, am + 64 * i, k);
+                for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, am + 64 * i, k);
 #pragma unroll
-            for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, x, bn + 64 * i, k);
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+                for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, x, bn + 64 * i, k);
+              }
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
       }
     loads_done:;
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t st0 = smem_u32(sm.stage[0]);
+      constexpr uint32_t kStageDesc = R::kStageBytes >> 4;
+      const uint64_t a_k = smem_desc(st0, 16, 1024, 2), b_k = smem_desc(st0 + R::kABoxes * kBox, 16, 1024, 2);
+      const uint64_t a_m = smem_desc(st0, kBox, 1024, 2), b_m = smem_desc(st0 + R::kABoxes * kBox, kBox, 1024, 2);
+      // What the next step waits for is asked for before this step's MMAs are issued: their issue takes about
+      // as long as they run, and the answer is there when it is needed.
       uint32_t stage = 0, phase = 0;
-      int it = 0;
-      for (int t = first; t < plan.total; t += stride, ++it) {
-        const Unit u = plan.unit(a, t);
-        const uint32_t acc = it & 1, acc_phase = (it >> 1) & 1;
-        if (!wait(&sm.acce[acc], acc_phase ^ 1u)) break;
-        tc_fence_after();
+      bool full_ready = mbar_try_wait(&sm.full[0], 0);
+      Unit u;
+      uint32_t turn[R::kGroups] = {};
+      auto next_acc = [&](int group) { return 2 * group + (turn[R::kGroups == 1 ? 0 : group] & 1); };
+      auto next_par = [&](int group) { return ((turn[R::kGroups == 1 ? 0 : group] >> 1) & 1) ^ 1u; };
+      bool more = plan.unit(a, 0, u);
+      bool acc_ready = more && mbar_try_wait(&sm.acce[0], 1u);
+      for (int it = 0; more;) {
         const bool a_mn = kMode == kProducts && u.w, b_mn = kMode == kProducts;
-        const uint32_t idesc = idesc_16(a.f16 != 0, kTileM, a_mn, b_mn);
+        const uint32_t idesc = idesc_16(a.f16 != 0, kTileM, u.cols, a_mn, b_mn);
         // K-major: a step of 16 is 32 bytes of each row.  Other-major: a box is 64 rows of the
         // contraction by 64 columns; a step is 16 rows (2048 bytes), the next 64 columns one box on.
-        const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
-        const uint32_t a_lbo = a_mn ? kBox : 16, b_lbo = b_mn ? kBox : 16;
-        const uint32_t d = tmem + acc * kBN;
-        for (int kb = u.k0; kb < u.k1; ++kb) {
-          if (!wait(&sm.full[stage], phase)) goto mma_done;
+        const uint64_t a0 = a_mn ? a_m : a_k, b0 = b_mn ? b_m : b_k;
+        const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
+        const int k1 = u.k1, len = u.len, turns = u.turns, group = R::kGroups == 1 ? 0 : it & 1;
+        int kb = u.k0;
+        more = plan.unit(a, ++it, u);   // the next tile, while this one's products run
+        for (int i = 0; i < turns; ++i) {
+          const uint32_t acc = next_acc(group), d = tmem + acc * kBN;
+          if (!acc_ready && !wait(&sm.acce[acc], next_par(group))) goto mma_done;
           tc_fence_after();
-          const uint32_t sa = smem_u32(sm.stage[stage]), sb = sa + R::kABoxes * kBox;
+          ++turn[R::kGroups == 1 ? 0 : group];
+          const int group2 = R::kGroups == 2 && i + 1 == turns ? group ^ 1 : group;   // the next turn's
+          const int kb0 = kb;
+          kb = min(kb0 + len, k1);
+          acc_ready = false;
+          for (int b = kb0; b < kb; b += R::kSub) {
+            if (!full_ready && !wait(&sm.full[stage], phase)) goto mma_done;
+            const uint64_t ad = a0 + stage * kStageDesc, bd = b0 + stage * kStageDesc;
+            uint64_t* const empty = &sm.empty[stage];
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            full_ready = mbar_try_wait(&sm.full[stage], phase);
+            if (b + R::kSub >= kb) acc_ready = mbar_try_wait(&sm.acce[next_acc(group2)], next_par(group2));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint64_t ad = smem_desc(sa + a_step * j, a_lbo, 1024, 2);
-            const uint64_t bd = smem_desc(sb + b_step * j, b_lbo, 1024, 2);
-            const uint32_t on = kb > u.k0 || j > 0 ? 1u : 0u;
-            if (kPair) tc_mma_f16_pair(d, ad, bd, idesc, on);
-            else tc_mma_f16(d, ad, bd, idesc, on);
+            for (int sub = 0; sub < R::kSub; ++sub) {
+              if (b + sub >= kb) break;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                constexpr uint32_t kNext = R::kSubBytes >> 4;
+                const uint64_t as = ad + sub * kNext + a_step * j, bs = bd + sub * kNext + b_step * j;
+                const uint32_t on = b > kb0 || sub + j > 0 ? 1u : 0u;
+                if (kPair) tc_mma_f16_pair(d, as, bs, idesc, on);
+                else tc_mma_f16(d, as, bs, idesc, on);
+              }
+            }
+            if (kPair) tc_commit_pair_both(empty);
+            else tc_commit(empty);
           }
-          if (kPair) {
-            tc_commit_pair(cluster_addr(&sm.empty[stage], 0));
-            tc_commit_pair(cluster_addr(&sm.empty[stage], 1));
-          } else {
-            tc_commit(&sm.empty[stage]);
-          }
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        if (kPair) {
-          tc_commit_pair(cluster_addr(&sm.accf[acc], 0));
-          tc_commit_pair(cluster_addr(&sm.accf[acc], 1));
-        } else {
-          tc_commit(&sm.accf[acc]);
+          if (kPair) tc_commit_pair_both(&sm.accf[acc]);
+          else tc_commit(&sm.accf[acc]);
         }
       }
     mma_done:
@@ -308,29 +404,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&sm.fin, 0, a.status, &no_abort, 1000000000ull);
     }
   } else {
-    const int q = warp & 3, ew = warp - 2, half = ew >> 2;   // TMEM lanes, columns of the tile
+    const int q = warp & 3, ew = warp - 2;                   // q: the TMEM lanes that this warp may read
+    const int half = R::kGroups == 1 ? ew >> 2 : 0, group = R::kGroups == 1 ? 0 : ew >> 2;
     uint8_t* buf = sm.out[ew];
     const uint32_t acce0 = kPair ? cluster_addr(&sm.acce[0], 0) : 0u;
     const float c1 = a.scale * kLog2e;
-    int it = 0;
-    for (int t = first; t < plan.total; t += stride, ++it) {
-      const Unit u = plan.unit(a, t);
-      const uint32_t acc = it & 1, acc_phase = (it >> 1) & 1;
+    uint32_t turn = 0;
+    Unit u;
+    for (int it = 0; plan.unit(a, it, u); ++it) {
+      if (R::kGroups == 2 && (it & 1) != group) continue;
       const int row0 = u.m * kTileM + (int)rank * kBM + q * 32, row = row0 + lane;
       const int col0 = u.n * kBN + half * 128;
-      if (!__all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], acc_phase))) break;
-      tc_fence_after();
       uint32_t v[4][32];
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+      bool ready = true;
+      for (int i = 0; i < (kMode == kStats ? u.turns : 1); ++i) {
+        const uint32_t acc = 2 * group + (turn & 1);
+        ready = __all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1));
+        if (!ready) break;
+        ++turn;
+        tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+        if (i == 0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) NVFP4_TMEM_LD_X32(taddr + 32 * c, v[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (kPair) mbar_arrive_cluster(acce0 + acc * (uint32_t)sizeof(uint64_t));
-        else mbar_arrive(&sm.acce[acc]);
+          for (int c = 0; c < 4; ++c) NVFP4_TMEM_LD_X32(taddr + 32 * c, v[c]);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[16];
+            NVFP4_TMEM_LD_X16(taddr + 16 * c, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              uint32_t& x = v[c >> 1][(c & 1) * 16 + j];
+              x = __float_as_uint(__uint_as_float(x) + __uint_as_float(w[j]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kPair) mbar_arrive_cluster(acce0 + acc * (uint32_t)sizeof(uint64_t));
+          else mbar_arrive(&sm.acce[acc]);
+        }
       }
+      if (!ready) break;
       auto val = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
 
       if constexpr (kMode == kStats) {
@@ -340,25 +458,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 128; ++i)
             if (i >= live) v[i >> 5][i & 31] = 0xFF800000u;   // -inf
         }
-        if (row0 >= n_rows) continue;
+        if (row0 >= n_rows || live == 0) continue;
         float m = val(0);
 #pragma unroll
-        for (int i = 1; i < 128; ++i) m = fmaxf(m, val(i));
+        for (int i = 1; i < 127; i += 2) m = fmaxf(fmaxf(m, val(i)), val(i + 1));
+        m = fmaxf(m, val(127));
         const float mm = m == -INFINITY ? 0.f : m;
         const F2 neg = pack2(-mm, -mm), cc = pack2(c1, c1);
         F2 s2 = pack2(0.f, 0.f), u2 = s2;
+        if (a.part_u == nullptr) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) {
-          const F2 d = mul2(add2(pack2(val(i), val(i + 1)), neg), cc);
-          const float2 f = unpack2(d);
-          const F2 e = pack2(ex2(f.x), ex2(f.y));
-          s2 = add2(s2, e);
-          // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from -inf
-          if (a.part_u != nullptr) u2 = fma2(e, pack2(fmaxf(f.x, -1000.f), fmaxf(f.y, -1000.f)), u2);
+          for (int i = 0; i < 128; i += 2) {
+            const float2 f = unpack2(mul2(add2(pack2(val(i), val(i + 1)), neg), cc));
+            s2 = add2(s2, pack2(ex2(f.x), ex2(f.y)));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; i += 2) {
+            const F2 d = mul2(add2(pack2(val(i), val(i + 1)), neg), cc);
+            const float2 f = unpack2(d);
+            const F2 e = pack2(ex2(f.x), ex2(f.y));
+            s2 = add2(s2, e);
+            u2 = fma2(e, d, u2);
+          }
+          const float2 w = unpack2(u2);
+          if (!(fabsf(w.x + w.y) < INFINITY)) {
+            // a logit of -inf among them: its 0 times -inf is left out (2^-1000 is 0 too)
+            u2 = pack2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 128; ++i) {
+              const float f = (val(i) - mm) * c1;
+              u2 = fma2(pack2(ex2(f), 0.f), pack2(fmaxf(f, -1000.f), 0.f), u2);
+            }
+          }
         }
         if (row < n_rows) {
           const float2 s = unpack2(s2), w = unpack2(u2);
-          const int64_t at = (int64_t)(2 * u.n + half) * a.pitch + row;
+          const int64_t at = (int64_t)(u.n * (kBN / kPart) + half) * a.pitch + row;
           a.part_m[at] = m;
           a.part_s[at] = s.x + s.y;
           if (a.part_u != nullptr) a.part_u[at] = w.x + w.y;
@@ -386,20 +522,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const F2 cc = pack2(a.scale, a.scale), ll = pack2(-g.lse, -g.lse), to2 = pack2(kLog2e, kLog2e);
         const F2 aa = pack2(g.a, g.a), bb = pack2(g.b, g.b);
 #pragma unroll
+        for (int i = 0; i < 128; i += 2) {
+          const F2 lt = mul2(fma2(pack2(val(i), val(i + 1)), cc, ll), to2);
+          const float2 f = unpack2(lt);
+          const F2 p = pack2(ex2(f.x), ex2(f.y));
+          // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from b * inf
+          const F2 w = a.entropy ? fma2(bb, pack2(fmaxf(f.x, -1000.f), fmaxf(f.y, -1000.f)), aa) : aa;
+          const float2 d = unpack2(mul2(p, w));
+          v[i >> 5][i & 31] = __float_as_uint(d.x);
+          v[i >> 5][(i & 31) + 1] = __float_as_uint(d.y);
+        }
+        if ((unsigned)rel < 128u) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i == rel) v[i >> 5][i & 31] = __float_as_uint(val(i) + g.zy);
+        }
+        if (live < 128 || !on) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (!on || i >= live) v[i >> 5][i & 31] = 0;
+        }
+#pragma unroll
         for (int b2 = 0; b2 < 2; ++b2) {
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int j = 64 * b2 + 2 * i;
-            const float2 lt = unpack2(mul2(fma2(pack2(val(j), val(j + 1)), cc, ll), to2));
-            const F2 p = pack2(ex2(lt.x), ex2(lt.y));
-            float2 d = unpack2(mul2(p, fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa)));
-            if (j == rel) d.x += g.zy;
-            if (j + 1 == rel) d.y += g.zy;
-            if (!on || j >= live) d.x = 0.f;
-            if (!on || j + 1 >= live) d.y = 0.f;
-            if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(d.y), "f"(d.x));
-            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(d.y), "f"(d.x));
+            if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(val(j + 1)), "f"(val(j)));
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(val(j + 1)), "f"(val(j)));
           }
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
@@ -528,10 +678,30 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
     m = top;
   };
   if (row >= 0) {
-#pragma unroll 8
-    for (int c = warp; c < a.parts; c += 32) {
-      const int64_t at = c * a.pitch + row;
-      join(a.m[at], a.s[at], a.u != nullptr ? a.u[at] : 0.f);
+    for (int c0 = warp; c0 < a.parts; c0 += 32 * 8) {   // eight parts at a time
+      float mi[8], si[8], ui[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + 32 * i;
+        const int64_t at = c * a.pitch + row;
+        const bool in = c < a.parts;
+        mi[i] = in ? a.m[at] : -INFINITY;
+        si[i] = in ? a.s[at] : 0.f;
+        ui[i] = in && a.u != nullptr ? a.u[at] : 0.f;
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, mi[i]);
+      float d = s == 0.f ? 0.f : (m - top) * c1, f = ex2(d);
+      float s2 = f * s, u2 = f * fmaf(s, d, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d = si[i] == 0.f ? 0.f : (mi[i] - top) * c1;
+        f = ex2(d);
+        s2 = fmaf(f, si[i], s2);
+        u2 = fmaf(f, fmaf(si[i], d, ui[i]), u2);
+      }
+      m = top, s = s2, u = u2;
     }
   }
   sm_m[warp][lane] = m;
@@ -748,7 +918,7 @@ struct ForwardPlan {
 ForwardPlan forward_plan(int64_t T, int64_t V, int64_t H) {
   ForwardPlan p;
   p.pitch = round_up(T, 32);
-  p.parts = (int)((V + kBN - 1) / kBN * 2);
+  p.parts = (int)((V + kPart - 1) / kPart);
   p.gather = T > 2 * kBM;   // fewer rows are one row of tiles whatever takes part
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -777,13 +947,13 @@ struct BackwardPlan {
 BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   BackwardPlan p;
   p.rows = round_up(T, 64);
-  const int64_t vp = round_up(V, kBN);
-  int64_t piece = std::max<int64_t>(8192, round_up(((int64_t)1 << 27) / p.rows, kBN));
+  const int64_t vp = round_up(V, 256);
+  int64_t piece = std::max<int64_t>(8192, round_up(((int64_t)1 << 28) / p.rows, 256));
   const int64_t pieces = (vp + piece - 1) / piece;
-  p.piece = round_up((vp + pieces - 1) / pieces, kBN);
+  p.piece = round_up((vp + pieces - 1) / pieces, 256);
   // few rows: dhidden's contraction is cut so that every SM has a part of it
-  const int64_t tiles = (T + 2 * kBM - 1) / (2 * kBM) * ((H + kBN - 1) / kBN);
-  p.splits = pieces == 1 ? (int)std::min<int64_t>(std::max<int64_t>(1, 76 / tiles), 32) : 1;
+  const int64_t tile = pairs(T) ? 2 * kBM : kBM, tiles = (T + tile - 1) / tile * ((H + 255) / 256);
+  p.splits = pieces == 1 ? (int)std::min<int64_t>(std::max<int64_t>(1, (pairs(T) ? 76 : 152) / tiles), 32) : 1;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -809,7 +979,7 @@ template <int kMode, bool kPair>
 cudaError_t launch_head(const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t units, cudaStream_t s) {
   const void* fn = (const void*)head_kernel<kMode, kPair>;
   static std::atomic<bool> attr_set[64];
-  cudaError_t err = set_smem_attr_once(attr_set, fn, (int)smem_bytes<kPair>());
+  cudaError_t err = set_smem_attr_once(attr_set, fn, (int)smem_bytes<kMode, kPair>());
   if (err != cudaSuccess || units == 0) return err;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -820,7 +990,7 @@ cudaError_t launch_head(const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem_bytes<kPair>();
+  cfg.dynamicSmemBytes = smem_bytes<kMode, kPair>();
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 2 : 1;
@@ -848,9 +1018,10 @@ cudaError_t launch_head_logprobs(const void* hidden, int64_t ldh, const void* we
   auto f32 = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   auto i32 = [&](size_t o) { return reinterpret_cast<int32_t*>(ws + o); };
   const bool gather = p.gather && targets != nullptr, pair = pairs(T);
+  const int x_rows = (int)std::min<int64_t>(64, round_up(T, 8));
   const CUtensorMapDataType dt = dtype == kActF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap maps[6];
-  if (!make_tensor_map(&maps[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
+  if (!make_tensor_map(&maps[0], hidden, T, H, 2 * ldh, x_rows, dt, 2) ||
       !make_tensor_map(&maps[2], weight, V, H, 2 * ldw, 64, dt, 2))
     return cudaErrorInvalidValue;
   maps[1] = maps[0];
@@ -869,13 +1040,14 @@ cudaError_t launch_head_logprobs(const void* hidden, int64_t ldh, const void* we
     if (err != cudaSuccess) return err;
   }
   HeadArgs a{};
-  a.T = T, a.n_rows = gather ? i32(p.n) : nullptr, a.V = (int)V, a.H = (int)H, a.f16 = dtype == kActF16;
+  a.T = T, a.x_rows = x_rows, a.n_rows = gather ? i32(p.n) : nullptr, a.V = (int)V, a.H = (int)H, a.f16 = dtype == kActF16;
   a.scale = scale, a.status = device_status_ptr();
   a.targets = targets, a.index = gather ? i32(p.index) : nullptr;
   a.part_m = f32(p.m), a.part_s = f32(p.s), a.part_u = entropy != nullptr ? f32(p.u) : nullptr, a.pitch = p.pitch;
   a.target_logit = f32(p.target), a.width = (int)V;
   const int64_t tile = pair ? 2 * kBM : kBM;
-  err = launch_head<kStats>(pair, maps, a, (T + tile - 1) / tile * ((V + kBN - 1) / kBN), s);
+  const int64_t cols = tile_cols(kStats, pair);
+  err = launch_head<kStats>(pair, maps, a, (T + tile - 1) / tile * ((V + cols - 1) / cols), s);
   if (err != cudaSuccess) return err;
   JoinArgs j{T, p.pitch, p.parts, (int)V, a.part_m, a.part_s, a.part_u, a.target_logit, targets, ignore,
              gather ? i32(p.place) : nullptr, a.n_rows, scale, logprob, lse, entropy, a.status};
@@ -906,15 +1078,16 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   if (err != cudaSuccess) return err;
 
   HeadArgs a{};
-  a.T = T, a.n_rows = i32(p.n), a.V = (int)V, a.H = (int)H, a.f16 = f16;
+  const int x_rows = (int)std::min<int64_t>(64, round_up(T, 8));
+  a.T = T, a.x_rows = x_rows, a.n_rows = i32(p.n), a.V = (int)V, a.H = (int)H, a.f16 = f16;
   a.scale = scale, a.status = device_status_ptr();
-  a.rows = g.rows, a.row_target = g.row_target;
+  a.rows = g.rows, a.row_target = g.row_target, a.entropy = dentropy != nullptr;
   a.x_splits = p.splits, a.x_pitch = p.rows;
   a.want_x = dhidden != nullptr, a.want_w = dweight != nullptr;
   a.w_factor = f16 ? g.factors : nullptr;
   CUtensorMap grad[6], prod[6];
-  if (!make_tensor_map(&grad[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
-      !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * H, 64, dt, 2) ||
+  if (!make_tensor_map(&grad[0], hidden, T, H, 2 * ldh, x_rows, dt, 2) ||
+      !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * H, x_rows, dt, 2) ||
       !make_tensor_map(&grad[2], weight, V, H, 2 * ldw, 64, dt, 2) ||
       !make_tensor_map(&grad[3], ws + p.d, p.rows, p.piece, 2 * p.piece, 64, dt, 2) ||
       !make_tensor_map(&grad[4], ws + p.d, p.rows, p.piece, 2 * p.piece, 32, dt, 2) ||
@@ -922,14 +1095,16 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
       (dweight != nullptr && !make_tensor_map(&prod[5], dweight, V, H, 2 * H, 32, dt, 2)))
     return cudaErrorInvalidValue;
   grad[5] = grad[4];
-  for (int i = 0; i < 4; ++i) prod[i] = grad[i];
+  for (int i = 2; i < 4; ++i) prod[i] = grad[i];
+  if (!make_tensor_map(&prod[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
+      !make_tensor_map(&prod[1], ws + (f16 ? p.weighted : p.gathered), p.rows, H, 2 * H, 64, dt, 2))
+    return cudaErrorInvalidValue;
   if (dweight == nullptr) prod[5] = prod[4];
-  if (f16 && !make_tensor_map(&prod[1], ws + p.weighted, p.rows, H, 2 * H, 64, dt, 2)) return cudaErrorInvalidValue;
-  const int64_t tile = pair ? 2 * kBM : kBM, xn = (H + kBN - 1) / kBN;
+  const int64_t tile = pair ? 2 * kBM : kBM, xn = (H + 255) / 256, cols = tile_cols(kGrad, pair);
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
     a.v0 = (int)v0, a.width = (int)std::min<int64_t>(p.piece, V - v0), a.x_first = v0 == 0;
     a.always_gathered = false;
-    err = launch_head<kGrad>(pair, grad, a, (T + tile - 1) / tile * ((a.width + kBN - 1) / kBN), s);
+    err = launch_head<kGrad>(pair, grad, a, (T + tile - 1) / tile * ((a.width + cols - 1) / cols), s);
     if (err != cudaSuccess) return err;
     const int64_t units = (a.want_x ? (T + tile - 1) / tile * xn * p.splits : 0) +
                           (a.want_w ? (a.width + tile - 1) / tile * xn : 0);
