@@ -76,7 +76,7 @@ template <int kMode, bool kPair>
 struct HeadSmem {
   using R = Ring<kMode, kPair>;
   uint8_t stage[R::kStages][R::kStageBytes];
-  uint8_t out[kEpiWarps][32 * 128];      // 32-row boxes on their way out
+  uint8_t out[kEpiWarps][32 * 128];      // boxes of dweight on their way out
   uint64_t full[R::kStages];
   uint64_t empty[R::kStages];
   uint64_t accf[R::kAccs];
@@ -118,7 +118,10 @@ struct HeadArgs {
   const RowGrad* rows;
   const int32_t* row_target;
   bool entropy;              // some row's b is not 0
+  uint16_t* d_out;           // [rows][d_pitch]
+  int64_t d_pitch;
   // products
+  float* x_sums;             // [x_splits][x_pitch][H]
   int x_splits;              // parts of dhidden's contraction
   int64_t x_pitch;           // rows between their sums
   bool x_first;              // the first piece stores, the others add
@@ -231,11 +234,30 @@ struct Plan {
   }
 };
 
+// 32 bytes a thread: whole sectors, whatever the other rows' threads do.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, int f16) {
+  uint32_t w;
+  if (f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
 template <int kMode, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     head_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap gathered,
                 const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap dlogits,
-                const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1, const HeadArgs a) {
+                const __grid_constant__ CUtensorMap dweight, const HeadArgs a) {
   using R = Ring<kMode, kPair>;
   constexpr int kStages = R::kStages, kBN = R::kBN;
   extern __shared__ uint8_t smem_raw[];
@@ -271,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kPair) cluster_sync();   // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
   grid_dep_sync();
+  fence_proxy_async_global();   // the loads read what the last kernels' threads wrote
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   // Loads and MMAs complete these barriers (the async proxy); only `acce` hears from threads of the other CTA.
@@ -406,18 +429,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int q = warp & 3, ew = warp - 2;                   // q: the TMEM lanes that this warp may read
     const int half = R::kGroups == 1 ? ew >> 2 : 0, group = R::kGroups == 1 ? 0 : ew >> 2;
-    uint8_t* buf = sm.out[ew];
     const uint32_t acce0 = kPair ? cluster_addr(&sm.acce[0], 0) : 0u;
+    uint8_t* buf = sm.out[ew];
     const float c1 = a.scale * kLog2e;
+    auto release = [&](uint32_t acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster(acce0 + acc * (uint32_t)sizeof(uint64_t));
+        else mbar_arrive(&sm.acce[acc]);
+      }
+    };
     uint32_t turn = 0;
     Unit u;
     for (int it = 0; plan.unit(a, it, u); ++it) {
       if (R::kGroups == 2 && (it & 1) != group) continue;
       const int row0 = u.m * kTileM + (int)rank * kBM + q * 32, row = row0 + lane;
       const int col0 = u.n * kBN + half * 128;
+      if constexpr (kMode == kStats) {
+      int rel = -1;                                          // the target's place among this thread's columns
+      if (a.targets != nullptr && row < n_rows)
+        rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
       uint32_t v[4][32];
       bool ready = true;
-      for (int i = 0; i < (kMode == kStats ? u.turns : 1); ++i) {
+      for (int i = 0; i < u.turns; ++i) {
         const uint32_t acc = 2 * group + (turn & 1);
         ready = __all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1));
         if (!ready) break;
@@ -441,17 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (kPair) mbar_arrive_cluster(acce0 + acc * (uint32_t)sizeof(uint64_t));
-          else mbar_arrive(&sm.acce[acc]);
-        }
+        release(acc);
       }
       if (!ready) break;
       auto val = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
 
-      if constexpr (kMode == kStats) {
         const int live = min(max(a.width - col0, 0), 128);
         if (live < 128) {
 #pragma unroll
@@ -498,131 +527,118 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.part_m[at] = m;
           a.part_s[at] = s.x + s.y;
           if (a.part_u != nullptr) a.part_u[at] = w.x + w.y;
-          if (a.targets != nullptr) {
-            const int rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
-            if (rel >= 0 && rel < live) {
-              float y = 0.f;
+          if (rel >= 0 && rel < live) {
+            float y = 0.f;
 #pragma unroll
-              for (int i = 0; i < 128; ++i)
-                if (i == rel) y = val(i);
-              a.target_logit[row] = y;
-            }
-          }
-        }
-      } else if constexpr (kMode == kGrad) {
-        const int live = min(max(a.width - col0, 0), 128);
-        if (row0 >= (n_rows + 63) / 64 * 64) continue;   // nobody reads these rows
-        RowGrad g{0.f, 0.f, 0.f, 0.f};
-        int rel = -1;
-        const bool on = row < n_rows;
-        if (on) {
-          g = a.rows[row];
-          rel = a.row_target[row] - a.v0 - col0;
-        }
-        const F2 cc = pack2(a.scale, a.scale), ll = pack2(-g.lse, -g.lse), to2 = pack2(kLog2e, kLog2e);
-        const F2 aa = pack2(g.a, g.a), bb = pack2(g.b, g.b);
-#pragma unroll
-        for (int i = 0; i < 128; i += 2) {
-          const F2 lt = mul2(fma2(pack2(val(i), val(i + 1)), cc, ll), to2);
-          const float2 f = unpack2(lt);
-          const F2 p = pack2(ex2(f.x), ex2(f.y));
-          // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from b * inf
-          const F2 w = a.entropy ? fma2(bb, pack2(fmaxf(f.x, -1000.f), fmaxf(f.y, -1000.f)), aa) : aa;
-          const float2 d = unpack2(mul2(p, w));
-          v[i >> 5][i & 31] = __float_as_uint(d.x);
-          v[i >> 5][(i & 31) + 1] = __float_as_uint(d.y);
-        }
-        if ((unsigned)rel < 128u) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i == rel) v[i >> 5][i & 31] = __float_as_uint(val(i) + g.zy);
-        }
-        if (live < 128 || !on) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (!on || i >= live) v[i >> 5][i & 31] = 0;
-        }
-#pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2) {
-          uint32_t w[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = 64 * b2 + 2 * i;
-            if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(val(j + 1)), "f"(val(j)));
-            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(val(j + 1)), "f"(val(j)));
-          }
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&out0, buf, col0 + 64 * b2, row0);
-            bulk_commit();
+            for (int i = 0; i < 128; ++i)
+              if (i == rel) y = val(i);
+            a.target_logit[row] = y;
           }
         }
       } else {
-        const bool empty = u.k0 >= u.k1;
-        if (!u.w) {
-          // float32 sums of dhidden
-          if (row0 >= n_rows) continue;
-          const int y = (int)((int64_t)u.split * a.x_pitch) + row0;
+        // 32 columns at a time, the next ones on their way out of TMEM under the arithmetic
+        const uint32_t acc = 2 * group + (turn & 1);
+        RowGrad g{0.f, 0.f, 0.f, 0.f};
+        int rel = -1;
+        const bool on = row < n_rows;
+        if (kMode == kGrad && on) {
+          g = a.rows[row];
+          rel = a.row_target[row] - a.v0 - col0;
+        }
+        const float f = kMode == kProducts && u.w && a.w_factor != nullptr ? *a.w_factor : 1.f;
+        if (!__all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1))) break;
+        ++turn;
+        tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+        // the rows of this warp that somebody reads, the columns that there are
+        const bool wanted = kMode == kGrad ? row0 < (n_rows + 63) / 64 * 64 : u.w ? a.v0 + row0 < a.V : row0 < n_rows;
+        const int live = kMode == kGrad ? a.width - col0 : a.H - col0;
+        uint32_t v[2][32], packed[32];
+        tmem_ld_32x32b_x32(taddr, v[0]);
+        tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int x = col0 + 32 * c;
-            if (x >= a.H) break;
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
+        for (int c = 0; c < 4; ++c) {
+          uint32_t (&x)[32] = v[c & 1];
+          if (c < 3) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
+          auto val = [&](int i) { return __uint_as_float(x[i]); };
+          if constexpr (kMode == kGrad) {
+            if (wanted) {
+              const F2 cc = pack2(a.scale, a.scale), ll = pack2(-g.lse, -g.lse), to2 = pack2(kLog2e, kLog2e);
+              const F2 aa = pack2(g.a, g.a), bb = pack2(g.b, g.b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                  empty ? make_uint4(0, 0, 0, 0)
-                        : make_uint4(v[c][4 * j], v[c][4 * j + 1], v[c][4 * j + 2], v[c][4 * j + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (a.x_first) tma_store_2d(&out0, buf, x, y);
-              else tma_add_2d(&out0, buf, x, y);
-              bulk_commit();
+              for (int i = 0; i < 32; i += 2) {
+                const float2 lt = unpack2(mul2(fma2(pack2(val(i), val(i + 1)), cc, ll), to2));
+                const F2 p = pack2(ex2(lt.x), ex2(lt.y));
+                // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from b * inf
+                const F2 w = a.entropy ? fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa) : aa;
+                const float2 d = unpack2(mul2(p, w));
+                x[i] = __float_as_uint(d.x);
+                x[i + 1] = __float_as_uint(d.y);
+              }
+              if ((unsigned)(rel - 32 * c) < 32u) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i == rel - 32 * c) x[i] = __float_as_uint(val(i) + g.zy);
+              }
+              if (live < 32 * c + 32 || !on) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!on || i >= live - 32 * c) x[i] = 0;
+              }
+              uint16_t* dst = a.d_out + (int64_t)row * a.d_pitch + col0 + 32 * c;
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = pack_16bit(val(2 * i), val(2 * i + 1), a.f16);
+              store32(dst, w);
+              store32(dst + 16, w + 8);
+            }
+          } else if (!u.w) {
+            if (wanted && on) {
+              // float32 sums of dhidden, 8 columns at a time: this thread's alone
+              float* dst = a.x_sums + ((int64_t)u.split * a.x_pitch + row) * a.H + col0 + 32 * c;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                if (32 * c + i >= live) break;
+                if (u.k0 >= u.k1) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) x[i + j] = 0;
+                }
+                if (!a.x_first) {
+                  uint32_t o[8];
+                  load32(dst + i, o);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) x[i + j] = __float_as_uint(__uint_as_float(o[j]) + val(i + j));
+                }
+                store32(dst + i, x + i);
+              }
+            }
+          } else if (wanted && 64 * (c / 2) < live) {
+            // 64 columns of dweight's rows through a box: whole lines (rows behind V, columns behind H are cut)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              packed[16 * (c & 1) + i] =
+                  u.k0 >= u.k1 ? 0 : pack_16bit(val(2 * i) * f, val(2 * i + 1) * f, a.f16);
+            if (c & 1) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                    make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&dweight, buf, col0 + 32 * (c - 1), a.v0 + row0);
+                bulk_commit();
+              }
             }
           }
-        } else {
-          // rows of dweight
-          const int y = a.v0 + row0;
-          if (y >= a.V) continue;
-          const float f = a.w_factor != nullptr ? *a.w_factor : 1.f;
-#pragma unroll
-          for (int b2 = 0; b2 < 2; ++b2) {
-            const int x = col0 + 64 * b2;
-            if (x >= a.H) break;
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int j = 64 * b2 + 2 * i;
-              const float dx = empty ? 0.f : val(j) * f, dy = empty ? 0.f : val(j + 1) * f;
-              if (a.f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dy), "f"(dx));
-              else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(dy), "f"(dx));
-            }
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                  make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&out1, buf, x, y);
-              bulk_commit();
-            }
-          }
+          tmem_ld_wait();
+          if (c == 2) release(acc);   // the last columns are in registers
         }
       }
     }
-    if (lane == 0) bulk_wait_all<0>();
+    if (kMode == kProducts && lane == 0) bulk_wait_all<0>();
     __syncwarp();
   }
 
@@ -976,7 +992,7 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
 }
 
 template <int kMode, bool kPair>
-cudaError_t launch_head(const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t units, cudaStream_t s) {
+cudaError_t launch_head(const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t units, cudaStream_t s) {
   const void* fn = (const void*)head_kernel<kMode, kPair>;
   static std::atomic<bool> attr_set[64];
   cudaError_t err = set_smem_attr_once(attr_set, fn, (int)smem_bytes<kMode, kPair>());
@@ -997,10 +1013,10 @@ cudaError_t launch_head(const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t
   int64_t clusters = kPair ? num_sms() / 2 : num_sms();
   if (units < clusters) clusters = units;
   cfg.gridDim = dim3((unsigned)(clusters * (kPair ? 2 : 1)), 1, 1);
-  return cudaLaunchKernelEx(&cfg, head_kernel<kMode, kPair>, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], a);
+  return cudaLaunchKernelEx(&cfg, head_kernel<kMode, kPair>, maps[0], maps[1], maps[2], maps[3], maps[4], a);
 }
 template <int kMode>
-cudaError_t launch_head(bool pair, const CUtensorMap (&maps)[6], const HeadArgs& a, int64_t units, cudaStream_t s) {
+cudaError_t launch_head(bool pair, const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t units, cudaStream_t s) {
   return pair ? launch_head<kMode, true>(maps, a, units, s) : launch_head<kMode, false>(maps, a, units, s);
 }
 
@@ -1020,14 +1036,14 @@ cudaError_t launch_head_logprobs(const void* hidden, int64_t ldh, const void* we
   const bool gather = p.gather && targets != nullptr, pair = pairs(T);
   const int x_rows = (int)std::min<int64_t>(64, round_up(T, 8));
   const CUtensorMapDataType dt = dtype == kActF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUtensorMap maps[6];
+  CUtensorMap maps[5];
   if (!make_tensor_map(&maps[0], hidden, T, H, 2 * ldh, x_rows, dt, 2) ||
       !make_tensor_map(&maps[2], weight, V, H, 2 * ldw, 64, dt, 2))
     return cudaErrorInvalidValue;
   maps[1] = maps[0];
   if (gather && !make_tensor_map(&maps[1], ws + p.gathered, round_up(T, 64), H, 2 * H, 64, dt, 2))
     return cudaErrorInvalidValue;
-  maps[3] = maps[4] = maps[5] = maps[2];
+  maps[3] = maps[4] = maps[2];
   cudaError_t err = cudaSuccess;
   if (gather) {
     GatherArgs g{};
@@ -1081,25 +1097,22 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   const int x_rows = (int)std::min<int64_t>(64, round_up(T, 8));
   a.T = T, a.x_rows = x_rows, a.n_rows = i32(p.n), a.V = (int)V, a.H = (int)H, a.f16 = f16;
   a.scale = scale, a.status = device_status_ptr();
-  a.rows = g.rows, a.row_target = g.row_target, a.entropy = dentropy != nullptr;
+  a.rows = g.rows, a.row_target = g.row_target, a.entropy = dentropy != nullptr, 
+  a.d_out = reinterpret_cast<uint16_t*>(ws + p.d), a.d_pitch = p.piece, a.x_sums = f32(p.sums);
   a.x_splits = p.splits, a.x_pitch = p.rows;
   a.want_x = dhidden != nullptr, a.want_w = dweight != nullptr;
   a.w_factor = f16 ? g.factors : nullptr;
-  CUtensorMap grad[6], prod[6];
+  CUtensorMap grad[5], prod[5];
   if (!make_tensor_map(&grad[0], hidden, T, H, 2 * ldh, x_rows, dt, 2) ||
       !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * H, x_rows, dt, 2) ||
       !make_tensor_map(&grad[2], weight, V, H, 2 * ldw, 64, dt, 2) ||
-      !make_tensor_map(&grad[3], ws + p.d, p.rows, p.piece, 2 * p.piece, 64, dt, 2) ||
-      !make_tensor_map(&grad[4], ws + p.d, p.rows, p.piece, 2 * p.piece, 32, dt, 2) ||
-      !make_tensor_map(&prod[4], ws + p.sums, p.splits * p.rows, H, 4 * H, 32, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4) ||
-      (dweight != nullptr && !make_tensor_map(&prod[5], dweight, V, H, 2 * H, 32, dt, 2)))
+      !make_tensor_map(&grad[3], ws + p.d, p.rows, p.piece, 2 * p.piece, 64, dt, 2))
     return cudaErrorInvalidValue;
-  grad[5] = grad[4];
-  for (int i = 2; i < 4; ++i) prod[i] = grad[i];
+  prod[2] = grad[2], prod[3] = grad[3], prod[4] = grad[4] = grad[3];
+  if (dweight != nullptr && !make_tensor_map(&prod[4], dweight, V, H, 2 * H, 32, dt, 2)) return cudaErrorInvalidValue;
   if (!make_tensor_map(&prod[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
       !make_tensor_map(&prod[1], ws + (f16 ? p.weighted : p.gathered), p.rows, H, 2 * H, 64, dt, 2))
     return cudaErrorInvalidValue;
-  if (dweight == nullptr) prod[5] = prod[4];
   const int64_t tile = pair ? 2 * kBM : kBM, xn = (H + 255) / 256, cols = tile_cols(kGrad, pair);
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
     a.v0 = (int)v0, a.width = (int)std::min<int64_t>(p.piece, V - v0), a.x_first = v0 == 0;
