@@ -663,7 +663,8 @@ nvfp4_status head_logprobs_backward(const void* hidden, int64_t ldh, const void*
  *   loss [S], prob_sums (P) [S, E]: device float; counts (c) [S, E], tokens (n) [S]: device int32.
  *   Float32 sums in an order that T, S and the sequences fix.  1 <= E <= 1024, 1 <= k <= 32, k <= E,
  *   T <= 2^24, S <= 2^20.
- *   workspace: nvfp4_workspace_size(NVFP4_OP_BALANCE_LOSS, T, S, E, 0, 0) bytes, 16-byte aligned. */
+ *   workspace: nvfp4_workspace_size(NVFP4_OP_BALANCE_LOSS, T, S, E, 0, 0) bytes, 16-byte aligned; NULL
+ *   where that is 0 (one sequence of few rows). */
 nvfp4_status moe_balance_loss(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,
                               const int32_t* ids, int32_t k, const int32_t* sequences, int32_t S,
                               const uint8_t* valid, float* loss, int32_t* counts, float* prob_sums, int32_t* tokens,

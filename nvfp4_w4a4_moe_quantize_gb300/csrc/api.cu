@@ -275,7 +275,7 @@ size_t nvfp4_workspace_size(int op, int64_t a, int64_t b, int64_t E, int64_t H, 
       return align256(8u * (size_t)(b > 0 ? b : 1) * (size_t)block_norm_parts(a, b, H) * (size_t)H);
     case NVFP4_OP_BALANCE_LOSS:
       if (a <= 0 || b <= 0 || E <= 0) return 0;
-      return align256(balance_workspace(a, b, E));
+      return align256(balance_workspace(a, b, E));   // 0: none is needed
     case NVFP4_OP_HEAD_LOGPROBS:
     case NVFP4_OP_HEAD_LOGPROBS_BACKWARD:
       if (a <= 0 || b <= 0 || H <= 0) return 0;

@@ -138,8 +138,8 @@ nvfp4_status moe_balance_loss(const void* logits, nvfp4_act_dtype dtype, int64_t
     return from_cuda(err);
   }
   if (!aligned(logits, elt_bytes(dtype)) || !aligned(ids, 4)) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned(workspace, 16) || workspace_bytes < nvfp4_workspace_size(NVFP4_OP_BALANCE_LOSS, T, S, E, 0, 0))
-    return NVFP4_ERR_WORKSPACE;
+  const size_t need = nvfp4_workspace_size(NVFP4_OP_BALANCE_LOSS, T, S, E, 0, 0);
+  if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   return from_cuda(launch_balance_loss(logits, dtype, T, E, ld, ids, k, sequences, S, valid, loss, counts, prob_sums,
                                        tokens, workspace, s));
 }

@@ -7,7 +7,9 @@
 // add their own gradient: w_j = softmax over the chosen logits gives w_j (dw_j - sum_i w_i dw_i) at the
 // chosen experts; plain probabilities w_j = p_j give w_j dw_j there, less p_e sum_i w_i dw_i everywhere.
 //
-// One warp holds one row: lane l the experts l, l + 32, ...
+// A warp holds a row: lane l the experts l, l + 32, ...; it works on several rows at once, since a row's loads
+// and sums over the lanes are a long chain of little work (one row at a time measured 15 and 22 us for the losses'
+// and the gradient's kernel at 32768 x 128 float32 logits, whose traffic takes 3 and 5).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -21,7 +23,8 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kWarps = 32, kThreads = 32 * kWarps;
+constexpr int kSmallRows = 4 * kWarps;   // one CTA does it all
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
@@ -31,16 +34,29 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 
-__device__ __forceinline__ float warp_max(float v) {
+template <int kFirst = 16, int RB>
+__device__ __forceinline__ void warp_max(float (&v)[RB]) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+  for (int d = kFirst; d > 0; d >>= 1)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) v[b] = fmaxf(v[b], __shfl_xor_sync(kAll, v[b], d));
+}
+// (over groups of 2 kFirst neighbouring lanes)
+template <int kFirst = 16, int RB>
+__device__ __forceinline__ void warp_sum(float (&v)[RB]) {
+#pragma unroll
+  for (int d = kFirst; d > 0; d >>= 1)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) v[b] += __shfl_xor_sync(kAll, v[b], d);
 }
 __device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-  return v;
+  float w[1] = {v};
+  warp_sum(w);
+  return w[0];
 }
+
+// Rows that a warp works on at once.
+__host__ __device__ constexpr int rows_at_once(int nv) { return nv <= 4 ? 4 : nv <= 8 ? 2 : 1; }
 
 // First sequence that ends behind row r (S: none).  Sequences are offsets[0 .. S], not descending;
 // without them all rows are sequence 0.
@@ -55,22 +71,29 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_
   return lo;
 }
 
-// z becomes exp(z - max), its largest value the result's m, its sum the result's s.
-template <int NV>
-__device__ __forceinline__ void row_exp(float (&z)[NV], float& m, float& s) {
-  m = z[0];
+// Of every row: z becomes exp(z - max), m the max (0 where every expert is excluded), inv 1 over the sum (0 there).
+template <int RB, int NV>
+__device__ __forceinline__ void rows_exp(float (&z)[RB][NV], float (&m)[RB], float (&inv)[RB]) {
 #pragma unroll
-  for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
-  m = warp_max(m);
-  const float mm = m == -INFINITY ? 0.f : m;   // every expert excluded
-  s = 0.f;
+  for (int b = 0; b < RB; ++b) {
+    m[b] = z[b][0];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    z[i] = ex2((z[i] - mm) * kLog2e);
-    s += z[i];
+    for (int i = 1; i < NV; ++i) m[b] = fmaxf(m[b], z[b][i]);
   }
-  s = warp_sum(s);
-  m = mm;
+  warp_max(m);
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    if (m[b] == -INFINITY) m[b] = 0.f;
+    inv[b] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      z[b][i] = ex2((z[b][i] - m[b]) * kLog2e);
+      inv[b] += z[b][i];
+    }
+  }
+  warp_sum(inv);
+#pragma unroll
+  for (int b = 0; b < RB; ++b) inv[b] = inv[b] == 0.f ? 0.f : 1.f / inv[b];
 }
 
 struct BalanceArgs {
@@ -91,60 +114,97 @@ struct BalanceArgs {
   int* status;
 };
 
-template <typename T, int NV>
+// The loss of a sequence from its counts c and sums p, an expert a thread (threads beyond E give 0).
+__device__ __forceinline__ float balance_of(int E, int k, int32_t c, float p, int n, float* sm_w) {
+  float cp = warp_sum(static_cast<float>(c) * p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) sm_w[warp] = cp;
+  __syncthreads();
+  cp = warp_sum(sm_w[lane]);
+  const float f = static_cast<float>(n);
+  return n == 0 ? 0.f : static_cast<float>(E) / static_cast<float>(k) * (cp / f / f);
+}
+
+// kWhole: one CTA, one sequence: the results at once.
+template <typename T, int NV, bool kWhole>
 __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const BalanceArgs a) {
+  constexpr int RB = rows_at_once(NV);
   extern __shared__ float sm[];
   float* sm_p = sm;                                                    // [kWarps][E]
   int32_t* sm_c = reinterpret_cast<int32_t*>(sm + kWarps * a.E);       // [E]
   __shared__ int sm_n[kWarps];
+  __shared__ float sm_w[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_sync();
   const int64_t r0 = blockIdx.x * a.chunk, r1 = min(a.T, r0 + a.chunk);
-  for (int s = sequence_of(a.offsets, a.S, r0, a.T); s < a.S; ++s) {
-    const int64_t lo = max(r0, a.offsets ? (int64_t)a.offsets[s] : 0), hi = min(r1, a.offsets ? (int64_t)a.offsets[s + 1] : a.T);
-    if (lo >= r1) break;
-    if (lo >= hi) continue;
+  for (int s = kWhole ? 0 : sequence_of(a.offsets, a.S, r0, a.T); s < a.S; ++s) {
+    const int64_t lo = max(r0, a.offsets ? (int64_t)a.offsets[s] : 0);
+    const int64_t hi = min(r1, a.offsets ? (int64_t)a.offsets[s + 1] : a.T);
+    if (!kWhole) {
+      if (lo >= r1) break;
+      if (lo >= hi) continue;
+    }
     for (int e = threadIdx.x; e < a.E; e += kThreads) sm_c[e] = 0;
     __syncthreads();
     float p[NV];
     int n = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) p[i] = 0.f;
-    for (int64_t r = lo + warp; r < hi; r += kWarps) {
-      if (a.valid != nullptr && a.valid[r] == 0) continue;
-      const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-      float z[NV];
+    for (int64_t r = lo + warp; r < hi; r += kWarps * RB) {
+      float z[RB][NV], m[RB], inv[RB];
+      int id[RB];
+      bool on[RB];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) z[i] = lane + 32 * i < a.E ? as_f32(row[lane + 32 * i]) : -INFINITY;
-      const int id = lane < a.k ? a.ids[r * a.k + lane] : 0;
-      float m, sum;
-      row_exp<NV>(z, m, sum);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      for (int b = 0; b < RB; ++b) {
+        const int64_t t = r + b * kWarps;
+        on[b] = t < hi && (a.valid == nullptr || a.valid[t] != 0);
+        const T* row = static_cast<const T*>(a.logits) + t * a.ld;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) p[i] = fmaf(z[i], inv, p[i]);
-      if (lane < a.k) {
-        if (id < 0 || id >= a.E) set_status(a.status, kStatusBadInput);
-        else atomicAdd(&sm_c[id], 1);
+        for (int i = 0; i < NV; ++i) z[b][i] = on[b] && lane + 32 * i < a.E ? as_f32(row[lane + 32 * i]) : -INFINITY;
+        id[b] = on[b] && lane < a.k ? a.ids[t * a.k + lane] : 0;
       }
-      ++n;
+      rows_exp(z, m, inv);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) p[i] = fmaf(z[b][i], inv[b], p[i]);
+        if (on[b] && lane < a.k) {
+          if (id[b] < 0 || id[b] >= a.E) set_status(a.status, kStatusBadInput);
+          else atomicAdd(&sm_c[id[b]], 1);
+        }
+        n += on[b];
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (lane + 32 * i < a.E) sm_p[warp * a.E + lane + 32 * i] = p[i];
     if (lane == 0) sm_n[warp] = n;
     __syncthreads();
-    const int64_t slot = blockIdx.x + (int64_t)s;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-      float t = 0.f;
+    n = __reduce_add_sync(kAll, sm_n[lane]);
+    const int e = threadIdx.x;   // E <= kThreads
+    float t = 0.f;
+    if (e < a.E)
       for (int w = 0; w < kWarps; ++w) t += sm_p[w * a.E + e];
+    if (kWhole) {
+      const float loss = balance_of(a.E, a.k, e < a.E ? sm_c[e] : 0, t, n, sm_w);
+      const bool bad = a.offsets != nullptr && (a.offsets[0] < 0 || a.offsets[1] < a.offsets[0] || a.offsets[1] > a.T);
+      if (e < a.E) {
+        a.sums[e] = bad ? NAN : t;
+        a.counts[e] = sm_c[e];
+      }
+      if (threadIdx.x == 0) {
+        if (bad) set_status(a.status, kStatusBadInput);
+        a.loss[0] = bad ? NAN : loss;
+        a.tokens[0] = n;
+      }
+      return;
+    }
+    const int64_t slot = blockIdx.x + (int64_t)s;
+    if (e < a.E) {
       a.part_p[slot * a.E + e] = t;
       a.part_c[slot * a.E + e] = sm_c[e];
     }
-    if (threadIdx.x == 0) {
-      int t = 0;
-      for (int w = 0; w < kWarps; ++w) t += sm_n[w];
-      a.part_n[slot] = t;
-    }
+    if (threadIdx.x == 0) a.part_n[slot] = n;
     __syncthreads();
   }
 }
@@ -164,41 +224,44 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(const BalanceArgs 
   const int e = tid % lanes, g = tid / lanes;
   float p = 0.f;
   int32_t c = 0;
-  if (g < groups && e < a.E)
-    for (int64_t i = c0 + g; i < c1; i += groups) {
-      p += a.part_p[(i + s) * a.E + e];
-      c += a.part_c[(i + s) * a.E + e];
+  if (g < groups && e < a.E) {
+    for (int64_t i0 = c0 + g; i0 < c1; i0 += 8 * groups) {   // eight loads of each on their way
+      float pi[8];
+      int32_t ci[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t i = i0 + j * groups;
+        pi[j] = i < c1 ? a.part_p[(i + s) * a.E + e] : 0.f;
+        ci[j] = i < c1 ? a.part_c[(i + s) * a.E + e] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p += pi[j], c += ci[j];
     }
+  }
   sm_p[tid] = p;
   sm_c[tid] = c;
   if (tid < 32) {
     int n = 0;
+#pragma unroll 4
     for (int64_t i = c0 + tid; i < c1; i += 32) n += a.part_n[i + s];
     n = __reduce_add_sync(kAll, n);
     if (tid == 0) sm_n = n;
   }
   __syncthreads();
-  float cp = 0.f;
-  if (tid < lanes && e < a.E) {
+  const bool mine = tid < lanes && e < a.E;
+  if (mine) {
     for (int h = 1; h < groups; ++h) {
       p += sm_p[h * lanes + e];
       c += sm_c[h * lanes + e];
     }
     a.sums[(int64_t)s * a.E + e] = bad ? NAN : p;
     a.counts[(int64_t)s * a.E + e] = c;
-    cp = static_cast<float>(c) * p;
   }
-  cp = warp_sum(cp);
-  if ((tid & 31) == 0) sm_w[tid >> 5] = cp;
-  __syncthreads();
-  if (tid < 32) {
-    cp = warp_sum(sm_w[tid]);
-    if (tid == 0) {
-      const float n = static_cast<float>(sm_n);
-      if (bad) set_status(a.status, kStatusBadInput);
-      a.loss[s] = bad ? NAN : sm_n == 0 ? 0.f : static_cast<float>(a.E) / static_cast<float>(a.k) * (cp / n / n);
-      a.tokens[s] = sm_n;
-    }
+  const float loss = balance_of(a.E, a.k, mine ? c : 0, mine ? p : 0.f, sm_n, sm_w);
+  if (tid == 0) {
+    if (bad) set_status(a.status, kStatusBadInput);
+    a.loss[s] = bad ? NAN : loss;
+    a.tokens[s] = sm_n;
   }
 }
 
@@ -221,96 +284,152 @@ struct RouterBackwardArgs {
 
 constexpr int kBackWarps = 8;
 
-template <typename T, int NV, bool kRenorm>
-__global__ void __launch_bounds__(32 * kBackWarps) router_backward_kernel(const RouterBackwardArgs a) {
+// kFew: at most 8 experts are chosen, and sums over them take 8 lanes.
+template <typename T, int NV, bool kRenorm, bool kFew>
+__global__ void __launch_bounds__(32 * kBackWarps, NV <= 4 ? 4 : 1) router_backward_kernel(const RouterBackwardArgs a) {
+  constexpr int RB = rows_at_once(NV), kChosen = kFew ? 4 : 16;
   extern __shared__ float sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* add = sm + warp * a.E;                                   // the chosen experts' part of the warp's row
-  float* part = sm + kBackWarps * a.E + warp * 32;
-  for (int e = lane; e < a.E; e += 32) add[e] = 0.f;
+  float* add = sm + warp * RB * a.E;                              // the chosen experts' part of each row
+  float* part = sm + kBackWarps * RB * a.E + warp * 32;
+  if (a.dweights != nullptr)
+    for (int e = lane; e < RB * a.E; e += 32) add[e] = 0.f;
   __syncwarp();
   const int64_t r0 = ((int64_t)blockIdx.x * kBackWarps + warp) * a.rows, r1 = min(a.T, r0 + a.rows);
   if (r0 >= r1) return;
   const bool balance = a.dloss != nullptr;
-  int s = a.S, held = -1;                                          // the row's sequence; that of al
+  int s = a.S, held = -1;                                          // the next row's sequence; that of al
   if (balance) s = sequence_of(a.offsets, a.S, r0, a.T);
   float al[NV];
+  auto hold = [&](int q) {                                         // al = what sequence q's tokens gain
+    if (q == held) return;
+    const float n = static_cast<float>(max(a.tokens[q], 1));
+    const float f = a.dloss[q] * (static_cast<float>(a.E) / static_cast<float>(a.k)) / n / n;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) al[i] = 0.f;
-  for (int64_t r = r0; r < r1; ++r) {
-    const T* row = static_cast<const T*>(a.logits) + r * a.ld;
-    float z[NV];
+    for (int i = 0; i < NV; ++i)
+      al[i] = lane + 32 * i < a.E ? f * static_cast<float>(a.counts[(int64_t)q * a.E + lane + 32 * i]) : 0.f;
+    held = q;
+  };
+  for (int64_t r = r0; r < r1; r += RB) {
+    float z[RB][NV], m[RB], inv[RB], dw[RB], zj[RB], dot[RB];
+    int id[RB], seq[RB];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) z[i] = lane + 32 * i < a.E ? as_f32(row[lane + 32 * i]) : -INFINITY;
-    int id = -1;
-    float dw = 0.f, zj = -INFINITY;
-    if (a.dweights != nullptr && lane < a.k) {
-      id = a.ids[r * a.k + lane];
-      if (id < 0 || id >= a.E) {
+    for (int b = 0; b < RB; ++b) {
+      const int64_t t = r + b;
+      const bool on = t < r1;
+      const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) z[b][i] = on && lane + 32 * i < a.E ? as_f32(row[lane + 32 * i]) : -INFINITY;
+      const bool chosen = on && a.dweights != nullptr && lane < a.k;
+      id[b] = chosen ? a.ids[t * a.k + lane] : -1;
+      dw[b] = chosen ? a.dweights[t * a.k + lane] : 0.f;
+      if (chosen && (id[b] < 0 || id[b] >= a.E)) {
         set_status(a.status, kStatusBadInput);
-        id = -1;
-      } else {
-        dw = a.dweights[r * a.k + lane];
-        zj = as_f32(row[id]);
+        id[b] = -1;
+        dw[b] = 0.f;
+      }
+      seq[b] = -1;                                                 // the balance loss does not reach it
+      if (balance && on) {
+        if (a.offsets != nullptr)
+          while (s < a.S && a.offsets[s + 1] <= t) ++s;
+        if (s < a.S && (a.offsets == nullptr || a.offsets[s] <= t) && (a.valid == nullptr || a.valid[t] != 0)) seq[b] = s;
       }
     }
-    bool counted = false;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {                                 // the chosen experts' logits
+      zj[b] = -INFINITY;
+      if (a.dweights == nullptr) continue;
+      if (NV <= 8) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const float v = __shfl_sync(kAll, z[b][i], id[b] & 31);
+          if (id[b] >> 5 == i) zj[b] = v;
+        }
+      } else if (id[b] >= 0) {
+        zj[b] = as_f32(static_cast<const T*>(a.logits)[(r + b) * a.ld + id[b]]);
+      }
+    }
+    rows_exp(z, m, inv);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {   // dot: sum_e p_e of what every expert gains
+      dot[b] = 0.f;
+      if (seq[b] < 0) continue;
+      hold(seq[b]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dot[b] = fmaf(z[b][i], al[i], dot[b]);
+    }
     if (balance) {
-      if (a.offsets != nullptr)
-        while (s < a.S && a.offsets[s + 1] <= r) ++s;
-      counted = s < a.S && (a.offsets == nullptr || a.offsets[s] <= r) && (a.valid == nullptr || a.valid[r] != 0);
-      if (counted && held != s) {
-        const float n = static_cast<float>(max(a.tokens[s], 1));
-        const float f = a.dloss[s] * (static_cast<float>(a.E) / static_cast<float>(a.k)) / n / n;
+      warp_sum(dot);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          al[i] = lane + 32 * i < a.E ? f * static_cast<float>(a.counts[(int64_t)s * a.E + lane + 32 * i]) : 0.f;
-        held = s;
-      }
-    }
-    float m, sum;
-    row_exp<NV>(z, m, sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float dot = 0.f;   // sum_e p_e of what every expert loses
-    if (counted) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) dot = fmaf(z[i], al[i], dot);
-      dot = warp_sum(dot) * inv;
+      for (int b = 0; b < RB; ++b) dot[b] *= inv[b];
     }
     if (a.dweights != nullptr) {
-      float g;
+      float g[RB], w[RB];
       if (kRenorm) {
-        const float mj = warp_max(zj);
-        const float w = mj == -INFINITY ? 0.f : ex2((zj - mj) * kLog2e);
-        const float ws = warp_sum(w);
-        const float wn = ws == 0.f ? 0.f : w / ws;
-        g = wn * (dw - warp_sum(wn * dw));
+        float mj[RB], ws[RB], wd[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) mj[b] = zj[b];
+        warp_max<kChosen>(mj);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) ws[b] = w[b] = mj[b] == -INFINITY ? 0.f : ex2((zj[b] - mj[b]) * kLog2e);
+        warp_sum<kChosen>(ws);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          w[b] = ws[b] == 0.f ? 0.f : w[b] / ws[b];
+          wd[b] = w[b] * dw[b];
+        }
+        warp_sum<kChosen>(wd);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) g[b] = w[b] * (dw[b] - wd[b]);
       } else {
-        g = ex2((zj - m) * kLog2e) * inv * dw;
-        dot += warp_sum(g);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) w[b] = g[b] = ex2((zj[b] - m[b]) * kLog2e) * inv[b] * dw[b];
+        warp_sum(w);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) dot[b] += w[b];
       }
-      // a chosen expert's part, once each: repeated ids add up in the order of their places
-      part[lane] = g;
+      // a chosen expert's part, once each: an id is alone if its place still has the lane that wrote there
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        if (id[b] >= 0) add[b * a.E + id[b]] = __int_as_float(lane);
       __syncwarp();
-      const uint32_t same = __match_any_sync(kAll, id);
-      if (id >= 0 && lane == __ffs(same) - 1) {
-        float t = 0.f;
-        for (uint32_t b = same; b != 0; b &= b - 1) t += part[__ffs(b) - 1];
-        add[id] = t;
+      bool twice = false;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) twice |= id[b] >= 0 && __float_as_int(add[b * a.E + id[b]]) != lane;
+      if (__any_sync(kAll, twice)) {
+        // repeated ids add up in the order of their places
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          part[lane] = g[b];
+          __syncwarp();
+          const uint32_t same = __match_any_sync(kAll, id[b]);
+          float t = 0.f;
+          for (uint32_t q = same; q != 0; q &= q - 1) t += part[__ffs(q) - 1];
+          g[b] = t;
+          __syncwarp();
+        }
       }
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        if (id[b] >= 0) add[b * a.E + id[b]] = g[b];   // repeated ids write the same sum
       __syncwarp();
     }
-    T* out = static_cast<T*>(a.dlogits) + r * a.ldd;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      if (e >= a.E) continue;
-      float d = z[i] * inv * ((counted ? al[i] : 0.f) - dot);
-      if (a.dweights != nullptr) {
-        d += add[e];
-        add[e] = 0.f;
+    for (int b = 0; b < RB; ++b) {
+      if (r + b >= r1) break;
+      T* out = static_cast<T*>(a.dlogits) + (r + b) * a.ldd;
+      if (seq[b] >= 0) hold(seq[b]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        if (e >= a.E) continue;
+        float d = z[b][i] * inv[b] * ((seq[b] >= 0 ? al[i] : 0.f) - dot[b]);
+        if (a.dweights != nullptr) {
+          d += add[b * a.E + e];
+          add[b * a.E + e] = 0.f;
+        }
+        put(out + e, d);
       }
-      put(out + e, d);
     }
     __syncwarp();
   }
@@ -338,8 +457,11 @@ static int64_t balance_chunk(int64_t T) {
   const int64_t c = (T + 151) / 152;
   return c < kWarps ? kWarps : c;
 }
+// One CTA takes them all: no partial results and no second kernel.
+static bool balance_whole(int64_t T, int64_t S) { return S == 1 && T <= kSmallRows; }
 
 size_t balance_workspace(int64_t T, int64_t S, int64_t E) {
+  if (balance_whole(T, S)) return 0;
   const size_t chunk = (size_t)balance_chunk(T);
   const size_t slots = ((size_t)T + chunk - 1) / chunk + (size_t)S;
   return slots * ((size_t)E * 8 + 4);
@@ -355,16 +477,20 @@ cudaError_t launch_balance_loss(const void* logits, int dtype, int64_t T, int E,
   a.part_c = reinterpret_cast<int32_t*>(a.part_p + slots * E);
   a.part_n = a.part_c + slots * E;
   const size_t smem = (size_t)(kWarps + 1) * E * 4;
+  const bool whole = balance_whole(T, S);
+  if (whole) a.chunk = T;
   const cudaError_t err = by_type_and_width(dtype, E, [&](auto t, auto nv) {
-    auto* fn = balance_rows_kernel<decltype(t), decltype(nv)::value>;
+    using El = decltype(t);
+    constexpr int NV = decltype(nv)::value;
+    auto* fn = whole ? balance_rows_kernel<El, NV, true> : balance_rows_kernel<El, NV, false>;
     if (smem > 48 * 1024) {
-      static std::atomic<bool> attr_set[64];
-      const cudaError_t e = set_smem_attr_once(attr_set, (const void*)fn, (kWarps + 1) * 1024 * 4);
+      static std::atomic<bool> attr_set[2][64];
+      const cudaError_t e = set_smem_attr_once(attr_set[whole], (const void*)fn, (kWarps + 1) * 1024 * 4);
       if (e != cudaSuccess) return e;
     }
-    return launch_pdl(false, fn, dim3((unsigned)chunks), dim3(kThreads), smem, s, a);
+    return launch_pdl(false, fn, dim3(whole ? 1u : (unsigned)chunks), dim3(kThreads), smem, s, a);
   });
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || whole) return err;
   return launch_pdl(true, balance_reduce_kernel, dim3((unsigned)S), dim3(1024), 0, s, a);
 }
 
@@ -372,16 +498,19 @@ cudaError_t launch_router_backward(const void* logits, int dtype, int64_t T, int
                                    int k, const float* dweights, bool renorm, const float* dloss,
                                    const int32_t* counts, const int32_t* tokens, const int32_t* offsets, int S,
                                    const uint8_t* valid, void* dlogits, int64_t ldd, cudaStream_t s) {
-  int64_t rows = (T + 152 * 64 - 1) / (152 * 64);   // 64 warps an SM
+  // 64 warps an SM, whole groups of the rows that a warp takes at once
+  const int at_once = rows_at_once((E + 31) / 32);
+  const int64_t rows = ((T + 152 * 64 - 1) / (152 * 64) + at_once - 1) / at_once * at_once;
   RouterBackwardArgs a{logits, T, ld, E, k, S, ids, dweights, dloss, counts, tokens, offsets, valid, dlogits, ldd,
                        rows, device_status_ptr()};
   const int64_t ctas = (T + rows * kBackWarps - 1) / (rows * kBackWarps);
-  const size_t smem = (size_t)kBackWarps * (E + 32) * 4;
   return by_type_and_width(dtype, E, [&](auto t, auto nv) {
     using El = decltype(t);
     constexpr int NV = decltype(nv)::value;
-    if (renorm) router_backward_kernel<El, NV, true><<<(unsigned)ctas, 32 * kBackWarps, smem, s>>>(a);
-    else router_backward_kernel<El, NV, false><<<(unsigned)ctas, 32 * kBackWarps, smem, s>>>(a);
+    const size_t smem = (size_t)kBackWarps * (rows_at_once(NV) * E + 32) * 4;   // at most 33 KB
+    auto* fn = renorm ? (k <= 8 ? router_backward_kernel<El, NV, true, true> : router_backward_kernel<El, NV, true, false>)
+                      : router_backward_kernel<El, NV, false, false>;
+    fn<<<(unsigned)ctas, 32 * kBackWarps, smem, s>>>(a);
     return cudaGetLastError();
   });
 }
