@@ -696,12 +696,12 @@ def _workspace(given, device, op: int, *sizes) -> torch.Tensor:
         if given.dtype != torch.uint8 or given.device != device or not given.is_contiguous():
             raise ValueError("workspace must be dense uint8 on the device of the rows")
         return given   # its size is checked with the other arguments
-    return torch.empty(max(_workspace_bytes(op, *sizes), 16), dtype=torch.uint8, device=device)
+    return torch.empty(max(_workspace_bytes(load(), op, *sizes), 16), dtype=torch.uint8, device=device)
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_bytes(op: int, *sizes) -> int:
-    return int(load().nvfp4_workspace_size(op, *sizes, 0))
+def _workspace_bytes(lib, op: int, *sizes) -> int:
+    return int(lib.nvfp4_workspace_size(op, *sizes, 0))
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top_k: int = 0, scale: float = 1.0,
@@ -895,7 +895,7 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, sequences: torch.T
     sums = torch.empty((S, E), dtype=torch.float32, device=dev)
     tokens = torch.empty(S, dtype=torch.int32, device=dev)
     ws, ws_bytes = None, 0
-    if workspace is not None or _workspace_bytes(OP_BALANCE_LOSS, T, S, E, 0) > 0:   # few rows need none
+    if workspace is not None or _workspace_bytes(lib, OP_BALANCE_LOSS, T, S, E, 0) > 0:   # few rows need none
         ws = _workspace(workspace, dev, OP_BALANCE_LOSS, T, S, E, 0)
         ws_bytes = ws.numel()
     _check(lib.moe_balance_loss(logits.data_ptr(), code, T, E, ld, ids.data_ptr(), k, _ptr(sequences), S, _ptr(valid),

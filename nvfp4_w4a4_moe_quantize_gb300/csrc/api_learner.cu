@@ -99,12 +99,12 @@ nvfp4_status head_logprobs_backward(const void* hidden, int64_t ldh, const void*
                                     void* workspace, size_t workspace_bytes, void* stream) {
   const nvfp4_status st = head_check(dtype, T, V, H, ldh, ldw, scale);
   if (st != NVFP4_OK) return st;
-  if (dhidden == nullptr && dweight == nullptr) return NVFP4_ERR_INVALID_ARG;
-  if (dlogprob != nullptr && targets == nullptr) return NVFP4_ERR_INVALID_ARG;
-  if (dentropy != nullptr && entropy == nullptr) return NVFP4_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dweight != nullptr && !aligned(dweight, 16)) return NVFP4_ERR_INVALID_ARG;
   if (T == 0) return dweight == nullptr ? NVFP4_OK : from_cuda(cudaMemsetAsync(dweight, 0, 2 * (size_t)V * (size_t)H, s));
+  if (dhidden == nullptr && dweight == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (dlogprob != nullptr && targets == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (dentropy != nullptr && entropy == nullptr) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(hidden, 16) || !aligned(weight, 16) || (dhidden != nullptr && !aligned(dhidden, 16)) ||
       !aligned(lse, 4) || !aligned_or_null(targets, 4) || !aligned_or_null(entropy, 4) ||
       !aligned_or_null(dlogprob, 4) || !aligned_or_null(dentropy, 4))
@@ -151,8 +151,9 @@ nvfp4_status moe_router_backward(const void* logits, nvfp4_act_dtype dtype, int6
                                  int64_t ldd, void* stream) {
   const nvfp4_status st = router_check(dtype, T, E, ld, k, sequences, S);
   if (st != NVFP4_OK) return st;
-  if (ldd < E || (dweights == nullptr && dloss == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (ldd < E) return NVFP4_ERR_INVALID_ARG;
   if (T == 0) return NVFP4_OK;
+  if (dweights == nullptr && dloss == nullptr) return NVFP4_ERR_INVALID_ARG;
   const int e = elt_bytes(dtype);
   if (!aligned(logits, e) || !aligned(dlogits, e)) return NVFP4_ERR_INVALID_ARG;
   if (dweights != nullptr && (!aligned(dweights, 4) || !aligned(ids, 4))) return NVFP4_ERR_INVALID_ARG;
