@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.fin, 1);
     sm.abort = 0;
     fence_mbar_init();
+    prefetch_tensormap(&weight);
+    prefetch_tensormap(kMode == kProducts ? &dlogits : &hidden);
   }
   if (warp == 1) {
     if (kPair) {
@@ -684,14 +686,20 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
   const bool moved = a.n_rows != nullptr && *a.n_rows < a.T;
   const int64_t row = skip ? -1 : moved ? a.place[t] : t;
   float m = -INFINITY, s = 0.f, u = 0.f;
-  auto join = [&](float m2, float s2, float u2) {
-    if (s2 == 0.f) return;                       // nothing allowed there
-    const float top = fmaxf(m, m2);
-    const float d1 = s == 0.f ? 0.f : (m - top) * c1, d2 = (m2 - top) * c1;
-    const float f1 = ex2(d1), f2 = ex2(d2);
-    u = f1 * fmaf(s, d1, u) + f2 * fmaf(s2, d2, u2);
-    s = f1 * s + f2 * s2;
-    m = top;
+  auto join = [&](const float (&mi)[8], const float (&si)[8], const float (&ui)[8]) {   // s = 0: nothing allowed
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, mi[i]);
+    float d = s == 0.f ? 0.f : (m - top) * c1, f = ex2(d);
+    float s2 = f * s, u2 = f * fmaf(s, d, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d = si[i] == 0.f ? 0.f : (mi[i] - top) * c1;
+      f = ex2(d);
+      s2 = fmaf(f, si[i], s2);
+      u2 = fmaf(f, fmaf(si[i], d, ui[i]), u2);
+    }
+    m = top, s = s2, u = u2;
   };
   if (row >= 0) {
     for (int c0 = warp; c0 < a.parts; c0 += 32 * 8) {   // eight parts at a time
@@ -705,19 +713,7 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
         si[i] = in ? a.s[at] : 0.f;
         ui[i] = in && a.u != nullptr ? a.u[at] : 0.f;
       }
-      float top = m;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, mi[i]);
-      float d = s == 0.f ? 0.f : (m - top) * c1, f = ex2(d);
-      float s2 = f * s, u2 = f * fmaf(s, d, u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d = si[i] == 0.f ? 0.f : (mi[i] - top) * c1;
-        f = ex2(d);
-        s2 = fmaf(f, si[i], s2);
-        u2 = fmaf(f, fmaf(si[i], d, ui[i]), u2);
-      }
-      m = top, s = s2, u = u2;
+      join(mi, si, ui);
     }
   }
   sm_m[warp][lane] = m;
@@ -725,7 +721,13 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
   sm_u[warp][lane] = u;
   __syncthreads();
   if (warp != 0 || t >= a.T) return;
-  for (int w = 1; w < 32; ++w) join(sm_m[w][lane], sm_s[w][lane], sm_u[w][lane]);
+  m = -INFINITY, s = 0.f, u = 0.f;
+  for (int w = 0; w < 32; w += 8) {
+    float mi[8], si[8], ui[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mi[i] = sm_m[w + i][lane], si[i] = sm_s[w + i][lane], ui[i] = sm_u[w + i][lane];
+    join(mi, si, ui);
+  }
   if (skip) {
     if (a.logprob != nullptr) a.logprob[t] = 0.f;
     a.lse[t] = 0.f;
@@ -794,30 +796,48 @@ __global__ void __launch_bounds__(1024) head_select_kernel(const GatherArgs a) {
   __shared__ float sm_r[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_sync();
+  constexpr int kEach = 8;   // rows a thread, one behind the other
   int base = 0;
   float r = 0.f;
-  for (int64_t t0 = 0; t0 < a.T; t0 += 1024) {
-    const int64_t t = t0 + threadIdx.x;
-    bool on = t < a.T;
-    if (on && a.targets != nullptr) on = a.targets[t] != a.ignore;
-    if (on && a.lse != nullptr) on = !(a.lse[t] < kLowestLse);
-    const uint32_t b = __ballot_sync(0xFFFFFFFFu, on);
-    if (lane == 0) sm_n[warp] = __popc(b);
-    __syncthreads();
-    const int below = lane < 32 ? sm_n[lane] : 0;
-    int sum = below;
+  for (int64_t t0 = 0; t0 < a.T; t0 += 1024 * kEach) {
+    const int64_t t1 = t0 + threadIdx.x * kEach;
+    int32_t y[kEach];
+    float lse[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool in = t1 + i < a.T;
+      y[i] = in && a.targets != nullptr ? a.targets[t1 + i] : 0;
+      lse[i] = in && a.lse != nullptr ? a.lse[t1 + i] : 0.f;
+    }
+    uint32_t on = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (t1 + i < a.T && (a.targets == nullptr || y[i] != a.ignore) && !(lse[i] < kLowestLse)) on |= 1u << i;
+    int sum = __popc(on);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
       if (lane >= d) sum += o;
     }
-    const int at = base + __shfl_sync(0xFFFFFFFFu, sum - below, warp) + __popc(b & ((1u << lane) - 1u));
-    if (t < a.T) a.place[t] = on ? at : -1;
-    if (on) {
-      a.index[at] = (int32_t)t;
-      if (a.f16 && a.lse != nullptr) r = fmaxf(r, row_weight(a, t));
+    if (lane == 31) sm_n[warp] = sum;
+    __syncthreads();
+    int below = sm_n[lane], all = below;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, all, d);
+      if (lane >= d) all += o;
     }
-    base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    int at = base + __shfl_sync(0xFFFFFFFFu, all - below, warp) + sum - __popc(on);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t t = t1 + i;
+      if (t < a.T) a.place[t] = (on >> i) & 1u ? at : -1;
+      if ((on >> i) & 1u) {
+        a.index[at++] = (int32_t)t;
+        if (a.f16 && a.lse != nullptr) r = fmaxf(r, row_weight(a, t));
+      }
+    }
+    base += __shfl_sync(0xFFFFFFFFu, all, 31);
     __syncthreads();
   }
 #pragma unroll
