@@ -298,8 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_proxy_async_global();   // the loads read what the last kernels' threads wrote
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
-  // Loads and MMAs complete these barriers (the async proxy); only `acce` hears from threads of the other CTA.
+  // Loads and MMAs complete the other barriers (the async proxy); `acce` hears from a pair's other CTA's threads.
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status, abort); };
+  auto wait_acce = [&](uint64_t* bar, uint32_t parity) {
+    return kPair ? mbar_wait_cluster(bar, parity, a.status, abort) : mbar_wait(bar, parity, a.status, abort);
+  };
   const int n_rows = a.n_rows != nullptr ? *a.n_rows : (int)a.T;
   const Plan<kMode, kPair> plan(a, n_rows);
   constexpr int kTileM = kPair ? 2 * kBM : kBM;
@@ -362,16 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kStageDesc = R::kStageBytes >> 4;
       const uint64_t a_k = smem_desc(st0, 16, 1024, 2), b_k = smem_desc(st0 + R::kABoxes * kBox, 16, 1024, 2);
       const uint64_t a_m = smem_desc(st0, kBox, 1024, 2), b_m = smem_desc(st0 + R::kABoxes * kBox, kBox, 1024, 2);
-      // What the next step waits for is asked for before this step's MMAs are issued: their issue takes about
-      // as long as they run, and the answer is there when it is needed.
+      // Whether the next stage has arrived is asked before this stage's MMAs are issued: the answer is there when
+      // it is needed.
       uint32_t stage = 0, phase = 0;
-      bool full_ready = mbar_try_wait(&sm.full[0], 0);
+      bool full_ready = false;
       Unit u;
       uint32_t turn[R::kGroups] = {};
-      auto next_acc = [&](int group) { return 2 * group + (turn[R::kGroups == 1 ? 0 : group] & 1); };
-      auto next_par = [&](int group) { return ((turn[R::kGroups == 1 ? 0 : group] >> 1) & 1) ^ 1u; };
       bool more = plan.unit(a, 0, u);
-      bool acc_ready = more && mbar_try_wait(&sm.acce[0], 1u);
       for (int it = 0; more;) {
         const bool a_mn = kMode == kProducts && u.w, b_mn = kMode == kProducts;
         const uint32_t idesc = idesc_16(a.f16 != 0, kTileM, u.cols, a_mn, b_mn);
@@ -383,14 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kb = u.k0;
         more = plan.unit(a, ++it, u);   // the next tile, while this one's products run
         for (int i = 0; i < turns; ++i) {
-          const uint32_t acc = next_acc(group), d = tmem + acc * kBN;
-          if (!acc_ready && !wait(&sm.acce[acc], next_par(group))) goto mma_done;
+          const uint32_t n = turn[R::kGroups == 1 ? 0 : group]++;
+          const uint32_t acc = 2 * group + (n & 1), d = tmem + acc * kBN;
+          if (!wait_acce(&sm.acce[acc], ((n >> 1) & 1) ^ 1u)) goto mma_done;
           tc_fence_after();
-          ++turn[R::kGroups == 1 ? 0 : group];
-          const int group2 = R::kGroups == 2 && i + 1 == turns ? group ^ 1 : group;   // the next turn's
           const int kb0 = kb;
           kb = min(kb0 + len, k1);
-          acc_ready = false;
           for (int b = kb0; b < kb; b += R::kSub) {
             if (!full_ready && !wait(&sm.full[stage], phase)) goto mma_done;
             const uint64_t ad = a0 + stage * kStageDesc, bd = b0 + stage * kStageDesc;
@@ -399,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               stage = 0;
               phase ^= 1u;
             }
-            full_ready = mbar_try_wait(&sm.full[stage], phase);
-            if (b + R::kSub >= kb) acc_ready = mbar_try_wait(&sm.acce[next_acc(group2)], next_par(group2));
+            full_ready = mbar_test(&sm.full[stage], phase);
 #pragma unroll
             for (int sub = 0; sub < R::kSub; ++sub) {
               if (b + sub >= kb) break;
@@ -449,40 +446,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = u.m * kTileM + (int)rank * kBM + q * 32, row = row0 + lane;
       const int col0 = u.n * kBN + half * 128;
       if constexpr (kMode == kStats) {
-      int rel = -1;                                          // the target's place among this thread's columns
-      if (a.targets != nullptr && row < n_rows)
-        rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
-      uint32_t v[4][32];
-      bool ready = true;
-      for (int i = 0; i < u.turns; ++i) {
-        const uint32_t acc = 2 * group + (turn & 1);
-        ready = __all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1));
-        if (!ready) break;
-        ++turn;
-        tc_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
-        if (i == 0) {
+        int rel = -1;                                          // the target's place among this thread's columns
+        if (a.targets != nullptr && row < n_rows)
+          rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
+        uint32_t v[4][32];
+        bool ready = true;
+        for (int i = 0; i < u.turns; ++i) {
+          const uint32_t acc = 2 * group + (turn & 1);
+          ready = __all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1));
+          if (!ready) break;
+          ++turn;
+          tc_fence_after();
+          const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+          if (i == 0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) NVFP4_TMEM_LD_X32(taddr + 32 * c, v[c]);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t w[16];
-            NVFP4_TMEM_LD_X16(taddr + 16 * c, w);
+            for (int c = 0; c < 4; ++c) NVFP4_TMEM_LD_X32(taddr + 32 * c, v[c]);
             tmem_ld_wait();
+          } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              uint32_t& x = v[c >> 1][(c & 1) * 16 + j];
-              x = __float_as_uint(__uint_as_float(x) + __uint_as_float(w[j]));
+            for (int c = 0; c < 8; ++c) {
+              uint32_t w[16];
+              NVFP4_TMEM_LD_X16(taddr + 16 * c, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                uint32_t& x = v[c >> 1][(c & 1) * 16 + j];
+                x = __float_as_uint(__uint_as_float(x) + __uint_as_float(w[j]));
+              }
             }
           }
+          release(acc);
         }
-        release(acc);
-      }
-      if (!ready) break;
-      auto val = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
-
+        if (!ready) break;
+        auto val = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
         const int live = min(max(a.width - col0, 0), 128);
         if (live < 128) {
 #pragma unroll
