@@ -18,7 +18,13 @@
 // One kernel runs the three products.  Roles: warp 0 loads (TMA, 64 x 64 boxes of 128-byte rows,
 // 128-byte swizzle), warp 1 issues the MMAs (tcgen05, float32 accumulators of 256 columns in
 // TMEM, two of them, so the epilogue of one tile runs under the products of the next), warps 2-9
-// are the epilogue: a thread has one row and 128 of the tile's 256 columns.
+// are the epilogue: a thread has one row and 128 of the tile's 256 columns.  More than 128 rows run by
+// pairs of CTAs (M = 256, N = 256: 64 KB of operands for 2^22 products), fewer by single ones.
+//
+// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.21-2.26 ms, 1.75-1.79 PF/s,
+// bound by the tensor cores at the power limit (their share of the cycles is 96%; a library product holds 1.74
+// under the same limit); backward 7.04-7.18 ms, 1.65-1.69 PF/s (91% in d, 86% in the products, whose operands lie
+// across the contraction).  One row: 100 us, the weight at 5.8 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,7 +39,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kBM = 128;                 // rows of a CTA's tile (one a TMEM lane)
-constexpr int kBK = 64;                  // contraction a stage: one 128-byte swizzle row of 16-bit values
+constexpr int kBK = 64;                  // a block of the contraction: one 128-byte swizzle row of 16-bit values
 constexpr int kBox = 64 * 128;           // bytes of one 64 x 64 box
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
@@ -45,13 +51,13 @@ enum : int { kStats = 0, kGrad = 1, kProducts = 2 };
 // The statistics' logits are summed in stretches of at most 1024 products: a tensor core cuts a float32 sum
 // off where it adds to it, always towards zero, so the error of a long sum grows with its length; the
 // stretches are added to one another in registers, rounded to nearest.  Measured at H = 2048, relative errors of
-// lse / entropy and the time of 8192 x 131072 rows: one stretch 6e-7 / 1.1e-6, 2.25 ms; 1024: 3e-7 / 5e-7,
+// lse / entropy and the time of 8192 x 131072 logits: one stretch 6e-7 / 1.1e-6, 2.25 ms; 1024: 3e-7 / 5e-7,
 // 2.27 ms; 512: 1.3e-7 / 2.4e-7, 2.33 ms (an accumulator takes some 4000 cycles to read under running MMAs, so
 // shorter stretches wait for it).
 constexpr int kStretch = 1024 / kBK;
 
-// Columns of a tile: 256; 128 for a row of tiles of logits by single CTAs (few rows: the weight's bytes
-// bound it, and the smaller tiles spread evenly over the SMs).
+// Columns of a tile: 256; 128 for the logits of few rows by single CTAs, which the weight's bytes bound: the
+// smaller tiles spread more evenly over the SMs (96 x 50021 x 1032: 30 us against 34).
 constexpr int tile_cols(int mode, bool pair) { return pair || mode == kProducts ? 256 : 128; }
 
 template <int kMode, bool kPair>
@@ -234,7 +240,8 @@ struct Plan {
   }
 };
 
-// 32 bytes a thread: whole sectors, whatever the other rows' threads do.
+// 32 bytes a thread: whole sectors, whatever the other rows' threads do.  (d through shared memory and TMA
+// stores: 87% of the cycles with the tensor cores active against 92; dweight, whose tiles are shorter, the other way.)
 __device__ __forceinline__ void store32(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -462,12 +469,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) NVFP4_TMEM_LD_X32(taddr + 32 * c, v[c]);
             tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_loaded(v[c]);
           } else {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               uint32_t w[16];
               NVFP4_TMEM_LD_X16(taddr + 16 * c, w);
               tmem_ld_wait();
+              tmem_loaded(w);
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 uint32_t& x = v[c >> 1][(c & 1) * 16 + j];
@@ -554,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[2][32], packed[32];
         tmem_ld_32x32b_x32(taddr, v[0]);
         tmem_ld_wait();
+        tmem_loaded(v[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t (&x)[32] = v[c & 1];
@@ -632,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tmem_ld_wait();
+          tmem_loaded(v[(c + 1) & 1]);
           if (c == 2) release(acc);   // the last columns are in registers
         }
       }
