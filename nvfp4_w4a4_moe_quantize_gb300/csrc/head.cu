@@ -763,6 +763,9 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
 
 // ------------------------------------------------------------------------------ gathering
 
+// Gathered rows begin at whole lines (a 128-byte row of a box is one request of L2's then, not two).
+__host__ __device__ inline int64_t row_pitch(int64_t H) { return (H + 63) / 64 * 64; }
+
 struct GatherArgs {
   const void* hidden;
   int64_t ldh, T;
@@ -779,7 +782,7 @@ struct GatherArgs {
   int32_t* n_rows;
   float* factors;            // [0]: dweight's factor (half precision)
   float* row_factor;         // [rows]: dhidden's factors
-  void* gathered;            // [rows rounded up to 64][H], where not all rows take part
+  void* gathered;            // [rows rounded up to 64][row_pitch(H)], where not all rows take part
   void* weighted;            // the same times r / max r, always (backward, half precision)
   RowGrad* rows;
   int32_t* row_target;
@@ -891,12 +894,13 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
       a.row_factor[i] = scaled ? r / kUp : 1.f;
     }
   }
+  const int64_t pitch = row_pitch(a.H);
   const bool gather = n < a.T;   // else the rows are read where they are
   if (!gather && !scaled) return;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + t * a.ldh);
   for (int c = lane; c < a.H / 8; c += 32) {
     uint4 q = i < n ? src[c] : make_uint4(0, 0, 0, 0);
-    if (gather) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.gathered) + i * a.H)[c] = q;
+    if (gather) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.gathered) + i * pitch)[c] = q;
     if (scaled) {
       __half2* h = reinterpret_cast<__half2*>(&q);
 #pragma unroll
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
         const float2 f = __half22float2(h[j]);
         h[j] = __floats2half2_rn(f.x * ratio, f.y * ratio);
       }
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.weighted) + i * a.H)[c] = q;
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.weighted) + i * pitch)[c] = q;
     }
   }
 }
@@ -974,7 +978,7 @@ ForwardPlan forward_plan(int64_t T, int64_t V, int64_t H) {
   p.place = take(4 * (size_t)T);
   p.index = take(4 * (size_t)T);
   p.target = take(4 * (size_t)p.pitch);
-  p.gathered = take(p.gather ? 2 * (size_t)round_up(T, 64) * (size_t)H : 0);
+  p.gathered = take(p.gather ? 2 * (size_t)round_up(T, 64) * (size_t)row_pitch(H) : 0);
   p.m = take(4 * (size_t)p.parts * (size_t)p.pitch);
   p.s = take(4 * (size_t)p.parts * (size_t)p.pitch);
   p.u = take(4 * (size_t)p.parts * (size_t)p.pitch);
@@ -1011,8 +1015,8 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   p.grad = take(sizeof(RowGrad) * (size_t)p.rows);
   p.target = take(4 * (size_t)p.rows);
   p.row_factor = take(4 * (size_t)p.rows);
-  p.gathered = take(2 * (size_t)p.rows * (size_t)H);
-  p.weighted = take(2 * (size_t)p.rows * (size_t)H);   // (a call does not say whether it is half precision)
+  p.gathered = take(2 * (size_t)p.rows * (size_t)row_pitch(H));
+  p.weighted = take(2 * (size_t)p.rows * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
   p.d = take(2 * (size_t)p.rows * (size_t)p.piece);
   p.sums = take(4 * (size_t)p.splits * (size_t)p.rows * (size_t)H);
   p.total = at;
@@ -1069,7 +1073,7 @@ cudaError_t launch_head_logprobs(const void* hidden, int64_t ldh, const void* we
       !make_tensor_map(&maps[2], weight, V, H, 2 * ldw, 64, dt, 2))
     return cudaErrorInvalidValue;
   maps[1] = maps[0];
-  if (gather && !make_tensor_map(&maps[1], ws + p.gathered, round_up(T, 64), H, 2 * H, 64, dt, 2))
+  if (gather && !make_tensor_map(&maps[1], ws + p.gathered, round_up(T, 64), H, 2 * row_pitch(H), 64, dt, 2))
     return cudaErrorInvalidValue;
   maps[3] = maps[4] = maps[2];
   cudaError_t err = cudaSuccess;
@@ -1132,14 +1136,14 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   a.w_factor = f16 ? g.factors : nullptr;
   CUtensorMap grad[5], prod[5];
   if (!make_tensor_map(&grad[0], hidden, T, H, 2 * ldh, x_rows, dt, 2) ||
-      !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * H, x_rows, dt, 2) ||
+      !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * row_pitch(H), x_rows, dt, 2) ||
       !make_tensor_map(&grad[2], weight, V, H, 2 * ldw, 64, dt, 2) ||
       !make_tensor_map(&grad[3], ws + p.d, p.rows, p.piece, 2 * p.piece, 64, dt, 2))
     return cudaErrorInvalidValue;
   prod[2] = grad[2], prod[3] = grad[3], prod[4] = grad[4] = grad[3];
   if (dweight != nullptr && !make_tensor_map(&prod[4], dweight, V, H, 2 * H, 32, dt, 2)) return cudaErrorInvalidValue;
   if (!make_tensor_map(&prod[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
-      !make_tensor_map(&prod[1], ws + (f16 ? p.weighted : p.gathered), p.rows, H, 2 * H, 64, dt, 2))
+      !make_tensor_map(&prod[1], ws + (f16 ? p.weighted : p.gathered), p.rows, H, 2 * row_pitch(H), 64, dt, 2))
     return cudaErrorInvalidValue;
   const int64_t tile = pair ? 2 * kBM : kBM, xn = (H + 255) / 256, cols = tile_cols(kGrad, pair);
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
