@@ -201,7 +201,8 @@ struct Plan {
       u.cols = kBN;
       u.k1 = (a.H + kBK - 1) / kBK;
       u.turns = kMode == kStats ? (u.k1 + kStretch - 1) / kStretch : 1;
-      u.len = (u.k1 + u.turns - 1) / u.turns;
+      constexpr int kSub = Ring<kMode, kPair>::kSub;
+      u.len = ((u.k1 + u.turns - 1) / u.turns + kSub - 1) / kSub * kSub;   // whole stages
       u.turns = (u.k1 + u.len - 1) / u.len;
       return true;
     }
