@@ -93,9 +93,16 @@ struct HeadSmem {
 };
 template <int kMode, bool kPair>
 constexpr size_t smem_bytes() { return sizeof(HeadSmem<kMode, kPair>) + 1024; }
-static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kStats, true>() <= 232448 &&
-                  smem_bytes<kProducts, false>() <= 232448,
+static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kProducts, false>() <= 232448 &&
+                  smem_bytes<kProducts, true>() <= 232448,
               "shared memory budget");
+
+// d of up to 64 rows is held as two 16-bit numbers, the rounded value and what the rounding left: a gradient of few
+// rows hangs on a few of d's values, the targets', and would show their one rounding (of many rows the errors even
+// out at sqrt(2) of the result's own).  The second numbers are rows of their own behind the first ones', the hidden
+// rows are repeated for them; both products are bound by the weight's bytes there, and 48 x 131072 x 2048 takes 312 us
+// against 289 with one number (65 to 128 rows would fill two tiles).
+constexpr int kTwoParts = 64;
 
 // What a row of the gradient needs: d = p (a + b log2 p), + zy at the target.
 struct RowGrad {
@@ -124,6 +131,7 @@ struct HeadArgs {
   const RowGrad* rows;
   const int32_t* row_target;
   bool entropy;              // some row's b is not 0
+  int low;                   // rows from a number of d to its second part (a multiple of 16), or 0: there is none
   uint16_t* d_out;           // [rows][d_pitch]
   int64_t d_pitch;
   // products
@@ -168,7 +176,7 @@ struct Plan {
       xm = (n + kTileM - 1) / kTileM;
       xn = (a.H + kBN - 1) / kBN;
       x_kb = (a.width + kBK - 1) / kBK;
-      w_kb = (n + kBK - 1) / kBK;
+      w_kb = ((n > 0 ? n + a.low : 0) + kBK - 1) / kBK;
       const int xs = a.want_x ? xm * xn * a.x_splits : 0, ws = a.want_w ? (a.width + kTileM - 1) / kTileM * xn : 0;
       // a tile's cost in stages of the contraction, its epilogue as 8
       const int cx = x_kb / a.x_splits + 8, cw = w_kb + 8;
@@ -261,6 +269,11 @@ __device__ __forceinline__ uint32_t pack_16bit(float lo, float hi, int f16) {
   return w;
 }
 
+__device__ __forceinline__ float2 unpack_16bit(uint32_t w, int f16) {
+  if (f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
 template <int kMode, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     head_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap gathered,
@@ -329,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(&sm.empty[stage], phase ^ 1u)) goto loads_done;
             const int subs = min(R::kSub, kb1 - kb0);
             // a pair's bytes all count on CTA 0's barrier
-            const int a_boxes = !kPair && kMode != kProducts && a.T <= 64 ? 1 : R::kABoxes;   // no more rows
+            // one box of A where there are no more rows
+            const int a_boxes = !kPair && (kMode == kProducts ? !u.w && a.low > 0 && a.low <= 32 : a.T <= 64) ? 1 : R::kABoxes;
             const uint32_t bytes = subs * (R::kBBoxes * kBox + a_boxes * (kMode != kProducts ? a.x_rows * 128 : kBox));
             if (rank == 0) mbar_arrive_expect_tx(&sm.full[stage], (kPair ? 2 : 1) * bytes);
             const uint32_t bar = kPair ? cluster_addr(&sm.full[stage], 0) : smem_u32(&sm.full[stage]);
@@ -348,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, k, a.v0 + bn + 64 * i);
               } else if (!u.w) {
 #pragma unroll
-                for (int i = 0; i < R::kABoxes; ++i) load(i, &dlogits, k, am + 64 * i);
+                for (int i = 0; i < R::kABoxes; ++i)
+                  if (i < a_boxes) load(i, &dlogits, k, am + 64 * i);
 #pragma unroll
                 for (int i = 0; i < R::kBBoxes; ++i) load(R::kABoxes + i, &weight, bn + 64 * i, a.v0 + k);
               } else {
@@ -549,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc = 2 * group + (turn & 1);
         RowGrad g{0.f, 0.f, 0.f, 0.f};
         int rel = -1;
-        const bool on = row < n_rows;
+        // (the sums of d's second parts are rows of their own)
+        const bool on = row < n_rows || (kMode == kProducts && a.low > 0 && row >= a.low && row < a.low + n_rows);
         if (kMode == kGrad && on) {
           g = a.rows[row];
           rel = a.row_target[row] - a.v0 - col0;
@@ -560,7 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
         // the rows of this warp that somebody reads, the columns that there are
-        const bool wanted = kMode == kGrad ? row0 < (n_rows + 63) / 64 * 64 : u.w ? a.v0 + row0 < a.V : row0 < n_rows;
+        const bool wanted = kMode == kGrad ? row0 < (n_rows + 63) / 64 * 64 && (a.low == 0 || row < a.low)
+                            : u.w ? a.v0 + row0 < a.V : row0 < a.low + n_rows;
         const int live = kMode == kGrad ? a.width - col0 : a.H - col0;
         uint32_t v[2][32], packed[32];
         tmem_ld_32x32b_x32(taddr, v[0]);
@@ -601,6 +618,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 16; ++i) w[i] = pack_16bit(val(2 * i), val(2 * i + 1), a.f16);
               store32(dst, w);
               store32(dst + 16, w + 8);
+              if (a.low > 0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 high = unpack_16bit(w[i], a.f16);
+                  w[i] = pack_16bit(val(2 * i) - high.x, val(2 * i + 1) - high.y, a.f16);
+                }
+                dst += a.low * a.d_pitch;
+                store32(dst, w);
+                store32(dst + 16, w + 8);
+              }
             }
           } else if (!u.w) {
             if (wanted && on) {
@@ -784,7 +811,8 @@ struct GatherArgs {
   float* factors;            // [0]: dweight's factor (half precision)
   float* row_factor;         // [rows]: dhidden's factors
   void* gathered;            // [rows rounded up to 64][row_pitch(H)], where not all rows take part
-  void* weighted;            // the same times r / max r, always (backward, half precision)
+  int low;                   // where d has two parts: the copies' repetition
+  void* weighted;            // the same times r / max r (half precision) and repeated (two parts), where either is so
   RowGrad* rows;
   int32_t* row_target;
 };
@@ -896,8 +924,8 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
     }
   }
   const int64_t pitch = row_pitch(a.H);
-  const bool gather = n < a.T;   // else the rows are read where they are
-  if (!gather && !scaled) return;
+  const bool gather = n < a.T, copy = scaled || a.low > 0;   // else the rows are read where they are
+  if (!gather && !copy) return;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + t * a.ldh);
   for (int c = lane; c < a.H / 8; c += 32) {
     uint4 q = i < n ? src[c] : make_uint4(0, 0, 0, 0);
@@ -909,14 +937,18 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
         const float2 f = __half22float2(h[j]);
         h[j] = __floats2half2_rn(f.x * ratio, f.y * ratio);
       }
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.weighted) + i * pitch)[c] = q;
+    }
+    if (copy && (a.low == 0 || i < a.low)) {
+      uint16_t* dst = static_cast<uint16_t*>(a.weighted) + i * pitch;
+      reinterpret_cast<uint4*>(dst)[c] = q;
+      if (a.low > 0) reinterpret_cast<uint4*>(dst + a.low * pitch)[c] = q;
     }
   }
 }
 
 struct FinishArgs {
   int64_t T, pitch;
-  int H, f16, splits;
+  int H, f16, splits, low;
   const int32_t* place;
   const float* row_factor;
   const float* sums;         // [splits][pitch][H]
@@ -933,11 +965,23 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs a) {
   const int place = a.place[t];
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (place >= 0) {
-    for (int s = 0; s < a.splits; ++s) {
-      const float4* p = reinterpret_cast<const float4*>(a.sums + (s * a.pitch + place) * a.H + c);
-      const float4 x = p[0], y = p[1];
-      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    // the sums of d's second parts first, where there are some; eight loads on their way
+    const int all = a.low > 0 ? 2 * a.splits : a.splits;
+    for (int i0 = 0; i0 < all; i0 += 8) {
+      float4 x[8][2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j, split = i < a.splits ? i : i - a.splits;
+        const int64_t row = split * a.pitch + (a.low > 0 && i < a.splits ? a.low : 0) + place;
+        const float4* p = reinterpret_cast<const float4*>(a.sums + row * a.H + c);
+        x[j][0] = i < all ? p[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[j][1] = i < all ? p[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[0] += x[j][0].x, v[1] += x[j][0].y, v[2] += x[j][0].z, v[3] += x[j][0].w;
+        v[4] += x[j][1].x, v[5] += x[j][1].y, v[6] += x[j][1].z, v[7] += x[j][1].w;
+      }
     }
     const float f = a.row_factor[place];
 #pragma unroll
@@ -988,14 +1032,16 @@ ForwardPlan forward_plan(int64_t T, int64_t V, int64_t H) {
 }
 
 struct BackwardPlan {
-  int64_t rows;              // T rounded up to 64
+  int64_t rows;              // of d and of the sums: T rounded up to 64, or twice `low`
+  int low;                   // where d has two parts, T rounded up to 16; else 0
   int64_t piece;             // columns of a piece of the vocabulary
   int splits;
   size_t n, factors, place, index, grad, target, row_factor, gathered, weighted, d, sums, total;
 };
 BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   BackwardPlan p;
-  p.rows = round_up(T, 64);
+  p.low = T <= kTwoParts ? (int)round_up(T, 16) : 0;
+  p.rows = p.low > 0 ? 2 * p.low : round_up(T, 64);
   const int64_t vp = round_up(V, 256);
   int64_t piece = std::max<int64_t>(8192, round_up(((int64_t)1 << 28) / p.rows, 256));
   const int64_t pieces = (vp + piece - 1) / piece;
@@ -1013,11 +1059,12 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   p.factors = take(8);
   p.place = take(4 * (size_t)T);
   p.index = take(4 * (size_t)T);
-  p.grad = take(sizeof(RowGrad) * (size_t)p.rows);
-  p.target = take(4 * (size_t)p.rows);
-  p.row_factor = take(4 * (size_t)p.rows);
-  p.gathered = take(2 * (size_t)p.rows * (size_t)row_pitch(H));
-  p.weighted = take(2 * (size_t)p.rows * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
+  p.grad = take(sizeof(RowGrad) * (size_t)T);
+  p.target = take(4 * (size_t)T);
+  p.row_factor = take(4 * (size_t)T);
+  const size_t rows64 = (size_t)std::max(round_up(T, 64), p.rows);
+  p.gathered = take(2 * rows64 * (size_t)row_pitch(H));
+  p.weighted = take(2 * rows64 * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
   p.d = take(2 * (size_t)p.rows * (size_t)p.piece);
   p.sums = take(4 * (size_t)p.splits * (size_t)p.rows * (size_t)H);
   p.total = at;
@@ -1120,16 +1167,18 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   g.lse = lse, g.entropy = entropy, g.dlogprob = dlogprob, g.dentropy = dentropy;
   g.place = i32(p.place), g.index = i32(p.index), g.n_rows = i32(p.n), g.factors = f32(p.factors);
   g.row_factor = f32(p.row_factor), g.gathered = ws + p.gathered, g.weighted = ws + p.weighted;
-  g.rows = reinterpret_cast<RowGrad*>(ws + p.grad), g.row_target = i32(p.target);
+  g.low = p.low, g.rows = reinterpret_cast<RowGrad*>(ws + p.grad), g.row_target = i32(p.target);
   cudaError_t err = launch_pdl(false, head_select_kernel, dim3(1), dim3(1024), 0, s, g);
   if (err == cudaSuccess)
-    err = launch_pdl(true, head_gather_kernel, dim3((unsigned)(p.rows / 8)), dim3(256), 0, s, g);
+    err = launch_pdl(true, head_gather_kernel, dim3((unsigned)(round_up(T, 64) / 8)), dim3(256), 0, s, g);
   if (err != cudaSuccess) return err;
 
   HeadArgs a{};
   const int x_rows = (int)std::min<int64_t>(64, round_up(T, 8));
   a.T = T, a.x_rows = x_rows, a.n_rows = i32(p.n), a.V = (int)V, a.H = (int)H, a.f16 = f16;
   a.scale = scale, a.status = device_status_ptr();
+  a.low = p.low;
+  const bool weighted = f16 || p.low > 0;   // the rows that dweight's product reads are copies
   a.rows = g.rows, a.row_target = g.row_target, a.entropy = dentropy != nullptr, 
   a.d_out = reinterpret_cast<uint16_t*>(ws + p.d), a.d_pitch = p.piece, a.x_sums = f32(p.sums);
   a.x_splits = p.splits, a.x_pitch = p.rows;
@@ -1137,14 +1186,15 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   a.w_factor = f16 ? g.factors : nullptr;
   CUtensorMap grad[5], prod[5];
   if (!make_tensor_map(&grad[0], hidden, T, H, 2 * ldh, x_rows, dt, 2) ||
-      !make_tensor_map(&grad[1], ws + p.gathered, p.rows, H, 2 * row_pitch(H), x_rows, dt, 2) ||
+      !make_tensor_map(&grad[1], ws + p.gathered, round_up(T, 64), H, 2 * row_pitch(H), x_rows, dt, 2) ||
       !make_tensor_map(&grad[2], weight, V, H, 2 * ldw, 64, dt, 2) ||
       !make_tensor_map(&grad[3], ws + p.d, p.rows, p.piece, 2 * p.piece, 64, dt, 2))
     return cudaErrorInvalidValue;
   prod[2] = grad[2], prod[3] = grad[3], prod[4] = grad[4] = grad[3];
   if (dweight != nullptr && !make_tensor_map(&prod[4], dweight, V, H, 2 * H, 32, dt, 2)) return cudaErrorInvalidValue;
   if (!make_tensor_map(&prod[0], hidden, T, H, 2 * ldh, 64, dt, 2) ||
-      !make_tensor_map(&prod[1], ws + (f16 ? p.weighted : p.gathered), p.rows, H, 2 * row_pitch(H), 64, dt, 2))
+      !make_tensor_map(&prod[1], ws + (weighted ? p.weighted : p.gathered), p.low > 0 ? p.rows : round_up(T, 64), H,
+                       2 * row_pitch(H), 64, dt, 2))
     return cudaErrorInvalidValue;
   const int64_t tile = pair ? 2 * kBM : kBM, xn = (H + 255) / 256, cols = tile_cols(kGrad, pair);
   for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
@@ -1154,12 +1204,12 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
     if (err != cudaSuccess) return err;
     const int64_t units = (a.want_x ? (T + tile - 1) / tile * xn * p.splits : 0) +
                           (a.want_w ? (a.width + tile - 1) / tile * xn : 0);
-    a.always_gathered = f16;
+    a.always_gathered = weighted;
     err = launch_head<kProducts>(pair, prod, a, units, s);
     if (err != cudaSuccess) return err;
   }
   if (dhidden == nullptr) return cudaSuccess;
-  FinishArgs f{T, p.rows, (int)H, f16, p.splits, g.place, g.row_factor, f32(p.sums), dhidden};
+  FinishArgs f{T, p.rows, (int)H, f16, p.splits, a.low, g.place, g.row_factor, f32(p.sums), dhidden};
   return launch_pdl(true, head_finish_kernel, dim3((unsigned)((T * (H / 8) + 255) / 256)), dim3(256), 0, s, f);
 }
 

@@ -3,8 +3,9 @@
 Bounds, u = 2^-24.  A logit is a sum of H exact products that a tensor core adds 16 at a time, cut off (not
 rounded) at every step: within delta = 2 (H / 16 + 4) 2 u S of its value, S = scale sum_h |x_h w_h| (the largest of
 the row).  The softmax adds, for exponents of at most D in base 2, 1.4 D u for the exponent's two roundings, 4 u for
-ex2 and a rounding for each addition on the way.  d is rounded to 16 bits (half a step h of the type) and carries p's
-error; the products of d are cut off like the logits, over K / 16 steps, relative to the sum of magnitudes."""
+ex2 and a rounding for each addition on the way.  d is rounded to 16 bits (half a step h of the type; of up to
+64 rows to two such numbers, h^2) and carries p's error; the products of d are cut off like the logits, over K / 16
+steps, relative to the sum of magnitudes."""
 import numpy as np
 import pytest
 import torch
@@ -101,7 +102,9 @@ def check_backward(lib, xt, wt, y, yt, lse, ent, g=None, h=None, scale=1.0, dtyp
     mag *= scale * live[:, None]
     # of p: the logits here and in lse, the exponent, ex2; of d: its factors and its rounding
     perr = 2 * logit_bound(x, w, scale) + softmax_bound(c) + 8 * U * (1 + np.abs(wlse)) + 3 * U * np.abs(c).max(1)
-    each = mag * (HALF_STEP[dtype] * (1 + 2.0 ** -7) + 2 * perr[:, None] + 8 * U)
+    # (up to 64 rows d is two numbers: the second one's half step of the first one's)
+    rounding = HALF_STEP[dtype] ** 2 * 2 if T <= 64 else HALF_STEP[dtype] * (1 + 2.0 ** -7)
+    each = mag * (rounding + 2 * perr[:, None] + 8 * U)
     aw, ax = np.abs(w), np.abs(x) * live[:, None]
     tol_x = each @ aw + 4 * U * (V / 16 + 40) * (mag @ aw) + HALF_STEP[dtype] * np.abs(want_x)
     tol_w = each.T @ ax + 4 * U * (T / 16 + 8) * (mag.T @ ax) + HALF_STEP[dtype] * np.abs(want_w)
@@ -128,6 +131,22 @@ def test_against_the_oracle(cuda_lib, T, V, H, dtype):
     g, h = rng.normal(size=T), 0.1 * rng.normal(size=T)
     check_backward(cuda_lib, xt, wt, y, yt, lse, ent, g, None, scale, dtype)
     check_backward(cuda_lib, xt, wt, y, yt, lse, ent, g, h, scale, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 32, 33, 48, 63, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_few_rows_gradients_show_their_own_rounding_alone(cuda_lib, T, dtype):
+    """Confident rows, whose gradient hangs on the target's d: its 16-bit rounding does not show."""
+    V, H = 900, 328
+    xt, wt, y, yt, rng = head(T, V, H, dtype, 100 + T, ignored=0.0)
+    xt.copy_(f64_to(xt, f64(xt) + 1.5 * f64(wt)[y]))
+    lp, lse, ent = check_forward(cuda_lib, xt, wt, y, yt)
+    for h in (None, 0.1 * rng.normal(size=T)):
+        check_backward(cuda_lib, xt, wt, y, yt, lse, ent, rng.normal(size=T), h, 1.0, dtype)
+
+
+def f64_to(like, a):
+    return torch.from_numpy(a.astype(np.float32)).to(like.dtype).cuda()
 
 
 @pytest.mark.parametrize("T", [5, 200, 300])
