@@ -21,9 +21,9 @@
 // are the epilogue: a thread has one row and 128 of the tile's 256 columns.  More than 128 rows run by
 // pairs of CTAs (M = 256, N = 256: 64 KB of operands for 2^22 products), fewer by single ones.
 //
-// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.21-2.26 ms, 1.75-1.79 PF/s,
+// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.21-2.29 ms, 1.73-1.79 PF/s,
 // bound by the tensor cores at the power limit (their share of the cycles is 96%; a library product holds 1.74
-// under the same limit); backward 7.04-7.18 ms, 1.65-1.69 PF/s (91% in d, 86% in the products, whose operands lie
+// under the same limit); backward 7.04-7.23 ms, 1.64-1.69 PF/s (92% in d, 85% in the products, whose operands lie
 // across the contraction).  One row: 100 us, the weight at 5.8 TB/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -100,8 +100,8 @@ static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kProducts, fal
 // d of up to 64 rows is held as two 16-bit numbers, the rounded value and what the rounding left: a gradient of few
 // rows hangs on a few of d's values, the targets', and would show their one rounding (of many rows the errors even
 // out at sqrt(2) of the result's own).  The second numbers are rows of their own behind the first ones', the hidden
-// rows are repeated for them; both products are bound by the weight's bytes there, and 48 x 131072 x 2048 takes 312 us
-// against 289 with one number (65 to 128 rows would fill two tiles).
+// rows are repeated for them; both products are bound by the weight's bytes there, and 48 x 131072 x 2048 takes 310 us
+// against 287 with one number (65 to 128 rows would fill two tiles).
 constexpr int kTwoParts = 64;
 
 // What a row of the gradient needs: d = p (a + b log2 p), + zy at the target.
@@ -927,21 +927,28 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
   const bool gather = n < a.T, copy = scaled || a.low > 0;   // else the rows are read where they are
   if (!gather && !copy) return;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.hidden) + t * a.ldh);
-  for (int c = lane; c < a.H / 8; c += 32) {
-    uint4 q = i < n ? src[c] : make_uint4(0, 0, 0, 0);
-    if (gather) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.gathered) + i * pitch)[c] = q;
-    if (scaled) {
-      __half2* h = reinterpret_cast<__half2*>(&q);
+  for (int c0 = lane; c0 < a.H / 8; c0 += 32 * 8) {   // eight loads on their way
+    uint4 q[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(h[j]);
-        h[j] = __floats2half2_rn(f.x * ratio, f.y * ratio);
+    for (int k = 0; k < 8; ++k) q[k] = i < n && c0 + 32 * k < a.H / 8 ? src[c0 + 32 * k] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = c0 + 32 * k;
+      if (c >= a.H / 8) break;
+      if (gather) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.gathered) + i * pitch)[c] = q[k];
+      if (scaled) {
+        __half2* h = reinterpret_cast<__half2*>(&q[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(h[j]);
+          h[j] = __floats2half2_rn(f.x * ratio, f.y * ratio);
+        }
       }
-    }
-    if (copy && (a.low == 0 || i < a.low)) {
-      uint16_t* dst = static_cast<uint16_t*>(a.weighted) + i * pitch;
-      reinterpret_cast<uint4*>(dst)[c] = q;
-      if (a.low > 0) reinterpret_cast<uint4*>(dst + a.low * pitch)[c] = q;
+      if (copy && (a.low == 0 || i < a.low)) {
+        uint16_t* dst = static_cast<uint16_t*>(a.weighted) + i * pitch;
+        reinterpret_cast<uint4*>(dst)[c] = q[k];
+        if (a.low > 0) reinterpret_cast<uint4*>(dst + a.low * pitch)[c] = q[k];
+      }
     }
   }
 }
