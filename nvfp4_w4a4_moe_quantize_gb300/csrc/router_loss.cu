@@ -24,7 +24,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 32, kThreads = 32 * kWarps;
-constexpr int kSmallRows = 4 * kWarps;   // one CTA does it all
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
@@ -457,11 +456,15 @@ static int64_t balance_chunk(int64_t T) {
   const int64_t c = (T + 151) / 152;
   return c < kWarps ? kWarps : c;
 }
-// One CTA takes them all: no partial results and no second kernel.
-static bool balance_whole(int64_t T, int64_t S) { return S == 1 && T <= kSmallRows; }
+// One CTA takes them all, a group of rows or two a warp: no partial results and no second kernel.  On the device,
+// one kernel / two: 256 x 8 6.3 / 7.3 us, 256 x 128 7.3 / 8.1, 32 x 1024 9.0 / 10.4; 512 x 128 11.0 / 8.5, 64 x 1024
+// 12.6 / 10.3.
+static bool balance_whole(int64_t T, int64_t S, int64_t E) {
+  return S == 1 && T <= kWarps * rows_at_once((int)((E + 31) / 32)) * (E <= 256 ? 2 : 1);
+}
 
 size_t balance_workspace(int64_t T, int64_t S, int64_t E) {
-  if (balance_whole(T, S)) return 0;
+  if (balance_whole(T, S, E)) return 0;
   const size_t chunk = (size_t)balance_chunk(T);
   const size_t slots = ((size_t)T + chunk - 1) / chunk + (size_t)S;
   return slots * ((size_t)E * 8 + 4);
@@ -477,7 +480,7 @@ cudaError_t launch_balance_loss(const void* logits, int dtype, int64_t T, int E,
   a.part_c = reinterpret_cast<int32_t*>(a.part_p + slots * E);
   a.part_n = a.part_c + slots * E;
   const size_t smem = (size_t)(kWarps + 1) * E * 4;
-  const bool whole = balance_whole(T, S);
+  const bool whole = balance_whole(T, S, E);
   if (whole) a.chunk = T;
   const cudaError_t err = by_type_and_width(dtype, E, [&](auto t, auto nv) {
     using El = decltype(t);

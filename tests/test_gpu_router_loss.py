@@ -78,7 +78,8 @@ def check_gradient(lib, z, ids, zt, it, dtype, dw=None, renormalize=True, dloss=
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (64, 8, 2), (128, 128, 8), (129, 33, 5), (1000, 60, 4),
-                                   (777, 257, 6), (300, 513, 32), (2001, 1024, 16), (9000, 128, 8)])
+                                   (777, 257, 6), (300, 513, 32), (2001, 1024, 16), (9000, 128, 8), (256, 128, 8),
+                                   (257, 128, 8), (128, 256, 4), (129, 256, 4), (32, 1024, 2), (33, 1024, 2)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_one_batch(cuda_lib, T, E, k, dtype):
     zt, ids, it, rng = router(T, E, k, T + E, dtype, pad=3 if E % 2 else 0, lead=1)
