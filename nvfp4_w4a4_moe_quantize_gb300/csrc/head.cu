@@ -729,11 +729,12 @@ __global__ void __launch_bounds__(1024) head_join_kernel(const JoinArgs a) {
     float top = m;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, mi[i]);
-    float d = s == 0.f ? 0.f : (m - top) * c1, f = ex2(d);
+    // 2^-1000 is 0: the clamp changes no sum, and keeps 0 away from s * inf
+    float d = s == 0.f ? 0.f : fmaxf((m - top) * c1, -1000.f), f = ex2(d);
     float s2 = f * s, u2 = f * fmaf(s, d, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      d = si[i] == 0.f ? 0.f : (mi[i] - top) * c1;
+      d = si[i] == 0.f ? 0.f : fmaxf((mi[i] - top) * c1, -1000.f);
       f = ex2(d);
       s2 = fmaf(f, si[i], s2);
       u2 = fmaf(f, fmaf(si[i], d, ui[i]), u2);
