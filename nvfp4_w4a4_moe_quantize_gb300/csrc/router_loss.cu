@@ -486,7 +486,7 @@ cudaError_t launch_balance_loss(const void* logits, int dtype, int64_t T, int E,
     using El = decltype(t);
     constexpr int NV = decltype(nv)::value;
     auto* fn = whole ? balance_rows_kernel<El, NV, true> : balance_rows_kernel<El, NV, false>;
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {   // (48 KB are free to every launch; the kernel's static 256 bytes count as well)
       static std::atomic<bool> attr_set[2][64];
       const cudaError_t e = set_smem_attr_once(attr_set[whole], (const void*)fn, (kWarps + 1) * 1024 * 4);
       if (e != cudaSuccess) return e;
