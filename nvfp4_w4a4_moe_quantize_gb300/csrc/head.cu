@@ -1082,7 +1082,7 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   p.weighted = take(2 * rows64 * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
   p.d = take(2 * (size_t)p.rows * (size_t)p.piece);
   p.sums = take(4 * (size_t)p.splits * (size_t)p.rows * (size_t)H);
-  p.total = at;
+  p.total = at + 240;        // the areas begin at the first whole 256 bytes of a 16-byte aligned workspace
   return p;
 }
 
@@ -1171,7 +1171,8 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
                                           const float* dentropy, void* dhidden, void* dweight, void* workspace,
                                           cudaStream_t s) {
   const BackwardPlan p = backward_plan(T, V, H);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  // d and the float32 sums are accessed 32 bytes at a time
+  uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
   auto f32 = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   auto i32 = [&](size_t o) { return reinterpret_cast<int32_t*>(ws + o); };
   const bool f16 = dtype == kActF16, pair = pairs(T);

@@ -61,3 +61,26 @@ def test_one_token_far_above_the_rest(cuda_lib, T):
         dx, dw = cuda_lib.head_logprobs_backward(xt, wt, lse, yt, None, ent, one)
         assert (dx == 0).all() and (dw == 0).all()
     assert cuda_lib.nvfp4_status_check() == 0
+
+
+def test_a_workspace_may_begin_at_any_16_bytes(cuda_lib):
+    """Workspaces of just the asked size that begin 16 bytes behind a whole line: the same bits, nothing written
+    around them."""
+    for T, V, H, dtype in ((5, 300, 72, "bf16"), (100, 700, 136, "f16"), (300, 1000, 264, "bf16")):
+        xt, wt, y, yt, rng = head(T, V, H, dtype, T)
+        g = torch.from_numpy(rng.normal(size=T)).float().cuda()
+        h = torch.from_numpy(0.1 * rng.normal(size=T)).float().cuda()
+        lp, lse, ent = want = cuda_lib.head_logprobs(xt, wt, yt)
+        want_d = cuda_lib.head_logprobs_backward(xt, wt, lse, yt, g, ent, h)
+        for lead in (16, 48, 240):
+            for op, call, wanted in (
+                    (cuda_lib.OP_HEAD_LOGPROBS, lambda ws: cuda_lib.head_logprobs(xt, wt, yt, workspace=ws), want),
+                    (cuda_lib.OP_HEAD_LOGPROBS_BACKWARD,
+                     lambda ws: cuda_lib.head_logprobs_backward(xt, wt, lse, yt, g, ent, h, workspace=ws), want_d)):
+                n = cuda_lib.load().nvfp4_workspace_size(op, T, V, 0, H, 0)
+                buf = torch.full((lead + n + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+                assert buf.data_ptr() % 256 == 0
+                got = call(buf[lead:lead + n])
+                assert all(torch.equal(a, b) for a, b in zip(got, wanted))
+                assert (buf[:lead] == 0x5A).all() and (buf[lead + n:] == 0x5A).all()
+    assert cuda_lib.nvfp4_status_check() == 0
