@@ -680,7 +680,8 @@ nvfp4_status moe_balance_loss(const void* logits, nvfp4_act_dtype dtype, int64_t
  *     NVFP4_ERR_DEVICE_STATUS and has no weight.  counts and tokens may come from more than this
  *     batch (sums over several devices): then the loss is that of all of them.
  *   sequences, S, valid: as in moe_balance_loss; they say which tokens the balance loss reaches, and
- *     do not concern dweights.
+ *     do not concern dweights: with dweights every row has its weights' gradient.  Without,
+ *     the rows that the balance loss does not reach have the gradient 0, whatever they hold.
  *   dlogits: device [T, ldd] of `dtype`; it may be `logits` itself (ldd = ld), else it must not
  *     overlap it.  Excluded experts get 0. */
 nvfp4_status moe_router_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,

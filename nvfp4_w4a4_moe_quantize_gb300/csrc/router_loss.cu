@@ -333,6 +333,10 @@ __global__ void __launch_bounds__(32 * kBackWarps, NV <= 4 ? 4 : 1) router_backw
           while (s < a.S && a.offsets[s + 1] <= t) ++s;
         if (s < a.S && (a.offsets == nullptr || a.offsets[s] <= t) && (a.valid == nullptr || a.valid[t] != 0)) seq[b] = s;
       }
+      if (a.dweights == nullptr && seq[b] < 0) {                   // its gradient is 0, whatever it holds
+#pragma unroll
+        for (int i = 0; i < NV; ++i) z[b][i] = -INFINITY;
+      }
     }
 #pragma unroll
     for (int b = 0; b < RB; ++b) {                                 // the chosen experts' logits

@@ -1,9 +1,14 @@
-"""The router's losses where calls are easily refused or answered wrongly."""
+"""The router's losses where calls are easily answered wrongly: numbers of experts next to the limits of a launch,
+padding that holds anything, lists of sequences that descend."""
 import os
 import subprocess
 import sys
 
+import numpy as np
 import pytest
+import torch
+
+from test_gpu_router_loss import check_gradient, check_loss, f64, router
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -28,3 +33,21 @@ print("fine")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("E,k", [(20, 3), (128, 8), (300, 6), (1024, 4)])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_padding_may_hold_anything_in_the_balance_loss_s_gradient(cuda_lib, E, k, dtype):
+    """Tokens of no sequence and padding tokens hold NaN and infinity: their gradient is 0, the others' as ever."""
+    T = 203
+    zt, ids, it, rng = router(T, E, k, E, dtype)
+    cuts, valid = np.array([5, 60, 60, 61, 190], np.int32), rng.random(T) < 0.7
+    out = np.ones(T, bool)
+    out[5:190] = ~valid[5:190]
+    zz = np.where(out[:, None], 0.0, f64(zt))
+    bad = torch.from_numpy(out).cuda()
+    zt[bad] = torch.where(torch.arange(E, device="cuda") % 2 == 0, float("nan"), float("inf")).to(zt.dtype)
+    _, counts, _, tokens, st, vt = check_loss(cuda_lib, zz, ids, zt, it, cuts, valid)
+    got = check_gradient(cuda_lib, zz, ids, zt, it, dtype, dloss=rng.normal(size=4), parts=(counts, tokens, st, vt),
+                         sequences=cuts, valid=valid)
+    assert (got[bad] == 0).all()
