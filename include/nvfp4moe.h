@@ -658,7 +658,8 @@ nvfp4_status head_logprobs_backward(const void* hidden, int64_t ldh, const void*
  *   sequences: device int32 [S + 1], row numbers that do not descend, sequence s the rows
  *     sequences[s] .. sequences[s + 1] - 1 (none: an empty one); or NULL with S = 1: all rows.  Rows
  *     of no sequence count nowhere.  A pair that descends or leaves [0, T] sets
- *     NVFP4_ERR_DEVICE_STATUS and gives that sequence the loss NaN.
+ *     NVFP4_ERR_DEVICE_STATUS and gives that sequence the loss and sums NaN, counts and tokens 0.
+ *     Where a pair descends the other sequences may get the same, and never numbers that are not theirs.
  *   valid: device uint8 [T] or NULL; tokens with 0 (padding) count nowhere and are not read.
  *   loss [S], prob_sums (P) [S, E]: device float; counts (c) [S, E], tokens (n) [S]: device int32.
  *   Float32 sums in an order that T, S and the sequences fix.  1 <= E <= 1024, 1 <= k <= 32, k <= E,
@@ -681,7 +682,8 @@ nvfp4_status moe_balance_loss(const void* logits, nvfp4_act_dtype dtype, int64_t
  *     batch (sums over several devices): then the loss is that of all of them.
  *   sequences, S, valid: as in moe_balance_loss; they say which tokens the balance loss reaches, and
  *     do not concern dweights: with dweights every row has its weights' gradient.  Without,
- *     the rows that the balance loss does not reach have the gradient 0, whatever they hold.
+ *     the rows that the balance loss does not reach have the gradient 0, whatever they hold.  The list
+ *     is not checked here: one that moe_balance_loss refuses gives gradients of no use.
  *   dlogits: device [T, ldd] of `dtype`; it may be `logits` itself (ldd = ld), else it must not
  *     overlap it.  Excluded experts get 0. */
 nvfp4_status moe_router_backward(const void* logits, nvfp4_act_dtype dtype, int64_t T, int32_t E, int64_t ld,

@@ -106,6 +106,7 @@ struct BalanceArgs {
   float* part_p;           // [slots][E]: slot chunk + sequence (one a pair that meets: either grows along the rows)
   int32_t* part_c;         // [slots][E]
   int32_t* part_n;         // [slots]
+  int32_t* part_bad;       // [chunks]: whether the list of sequences descends in a CTA's part of it
   float* loss;
   int32_t* counts;
   float* sums;
@@ -136,12 +137,21 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const BalanceArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_sync();
   const int64_t r0 = blockIdx.x * a.chunk, r1 = min(a.T, r0 + a.chunk);
-  for (int s = kWhole ? 0 : sequence_of(a.offsets, a.S, r0, a.T); s < a.S; ++s) {
-    const int64_t lo = max(r0, a.offsets ? (int64_t)a.offsets[s] : 0);
+  bool descends = false;
+  if (!kWhole && a.offsets != nullptr)
+    for (int s = blockIdx.x * kThreads + threadIdx.x; s < a.S; s += gridDim.x * kThreads)
+      descends |= a.offsets[s + 1] < a.offsets[s];
+  // A list that descends: a single CTA takes every sequence for itself.  Several need the order for their search and
+  // their slots; they give no results, and no row is read twice on the way to that.
+  const bool each = !kWhole && gridDim.x == 1 && __syncthreads_or(descends);
+  int64_t done = r0;
+  for (int s = kWhole || each ? 0 : sequence_of(a.offsets, a.S, r0, a.T); s < a.S; ++s) {
+    const int64_t lo = max(each ? r0 : done, a.offsets ? (int64_t)a.offsets[s] : 0);
     const int64_t hi = min(r1, a.offsets ? (int64_t)a.offsets[s + 1] : a.T);
     if (!kWhole) {
-      if (lo >= r1) break;
+      if (lo >= r1 && !each) break;
       if (lo >= hi) continue;
+      done = hi;
     }
     for (int e = threadIdx.x; e < a.E; e += kThreads) sm_c[e] = 0;
     __syncthreads();
@@ -189,12 +199,12 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const BalanceArg
       const bool bad = a.offsets != nullptr && (a.offsets[0] < 0 || a.offsets[1] < a.offsets[0] || a.offsets[1] > a.T);
       if (e < a.E) {
         a.sums[e] = bad ? NAN : t;
-        a.counts[e] = sm_c[e];
+        a.counts[e] = bad ? 0 : sm_c[e];
       }
       if (threadIdx.x == 0) {
         if (bad) set_status(a.status, kStatusBadInput);
         a.loss[0] = bad ? NAN : loss;
-        a.tokens[0] = n;
+        a.tokens[0] = bad ? 0 : n;
       }
       return;
     }
@@ -205,6 +215,10 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const BalanceArg
     }
     if (threadIdx.x == 0) a.part_n[slot] = n;
     __syncthreads();
+  }
+  if (!kWhole) {
+    descends = __syncthreads_or(descends) && !each;
+    if (threadIdx.x == 0) a.part_bad[blockIdx.x] = descends;
   }
 }
 
@@ -217,7 +231,9 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(const BalanceArgs 
   grid_dep_sync();
   const int s = blockIdx.x, tid = threadIdx.x;
   const int64_t lo = a.offsets ? (int64_t)a.offsets[s] : 0, hi = a.offsets ? (int64_t)a.offsets[s + 1] : a.T;
-  const bool bad = lo < 0 || hi < lo || hi > a.T;
+  bool bad = lo < 0 || hi < lo || hi > a.T;
+  const int chunks = static_cast<int>((a.T + a.chunk - 1) / a.chunk);   // at most 152
+  const bool descends = tid < chunks && a.part_bad[tid] != 0;
   const int64_t c0 = bad || lo == hi ? 0 : lo / a.chunk, c1 = bad || lo == hi ? 0 : (hi - 1) / a.chunk + 1;
   const int lanes = (a.E + 31) / 32 * 32, groups = 1024 / lanes;   // experts side by side, groups of slots
   const int e = tid % lanes, g = tid / lanes;
@@ -246,7 +262,7 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(const BalanceArgs 
     n = __reduce_add_sync(kAll, n);
     if (tid == 0) sm_n = n;
   }
-  __syncthreads();
+  bad |= __syncthreads_or(descends) != 0;
   const bool mine = tid < lanes && e < a.E;
   if (mine) {
     for (int h = 1; h < groups; ++h) {
@@ -254,13 +270,13 @@ __global__ void __launch_bounds__(1024) balance_reduce_kernel(const BalanceArgs 
       c += sm_c[h * lanes + e];
     }
     a.sums[(int64_t)s * a.E + e] = bad ? NAN : p;
-    a.counts[(int64_t)s * a.E + e] = c;
+    a.counts[(int64_t)s * a.E + e] = bad ? 0 : c;
   }
   const float loss = balance_of(a.E, a.k, mine ? c : 0, mine ? p : 0.f, sm_n, sm_w);
   if (tid == 0) {
     if (bad) set_status(a.status, kStatusBadInput);
     a.loss[s] = bad ? NAN : loss;
-    a.tokens[s] = sm_n;
+    a.tokens[s] = bad ? 0 : sm_n;
   }
 }
 
@@ -470,19 +486,20 @@ static bool balance_whole(int64_t T, int64_t S, int64_t E) {
 size_t balance_workspace(int64_t T, int64_t S, int64_t E) {
   if (balance_whole(T, S, E)) return 0;
   const size_t chunk = (size_t)balance_chunk(T);
-  const size_t slots = ((size_t)T + chunk - 1) / chunk + (size_t)S;
-  return slots * ((size_t)E * 8 + 4);
+  const size_t chunks = ((size_t)T + chunk - 1) / chunk, slots = chunks + (size_t)S;
+  return slots * ((size_t)E * 8 + 4) + chunks * 4;
 }
 
 cudaError_t launch_balance_loss(const void* logits, int dtype, int64_t T, int E, int64_t ld, const int32_t* ids, int k,
                                 const int32_t* offsets, int S, const uint8_t* valid, float* loss, int32_t* counts,
                                 float* sums, int32_t* tokens, void* workspace, cudaStream_t s) {
-  BalanceArgs a{logits, T, ld, E, k, S, ids, offsets, valid, balance_chunk(T), nullptr, nullptr, nullptr,
+  BalanceArgs a{logits, T, ld, E, k, S, ids, offsets, valid, balance_chunk(T), nullptr, nullptr, nullptr, nullptr,
                 loss, counts, sums, tokens, device_status_ptr()};
   const int64_t chunks = (T + a.chunk - 1) / a.chunk, slots = chunks + S;
   a.part_p = static_cast<float*>(workspace);
   a.part_c = reinterpret_cast<int32_t*>(a.part_p + slots * E);
   a.part_n = a.part_c + slots * E;
+  a.part_bad = a.part_n + slots;
   const size_t smem = (size_t)(kWarps + 1) * E * 4;
   const bool whole = balance_whole(T, S, E);
   if (whole) a.chunk = T;
