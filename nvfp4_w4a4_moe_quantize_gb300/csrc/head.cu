@@ -211,7 +211,7 @@ struct Plan {
       u.m = t - u.n * m_tiles;
       u.cols = kBN;
       u.k1 = (a.H + kBK - 1) / kBK;
-      u.turns = kMode == kStats ? (u.k1 + kStretch - 1) / kStretch : 1;
+      u.turns = (u.k1 + kStretch - 1) / kStretch;
       constexpr int kSub = Ring<kMode, kPair>::kSub;
       u.len = ((u.k1 + u.turns - 1) / u.turns + kSub - 1) / kSub * kSub;   // whole stages
       u.turns = (u.k1 + u.len - 1) / u.len;
@@ -471,11 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (R::kGroups == 2 && (it & 1) != group) continue;
       const int row0 = u.m * kTileM + (int)rank * kBM + q * 32, row = row0 + lane;
       const int col0 = u.n * kBN + half * 128;
-      if constexpr (kMode == kStats) {
-        int rel = -1;                                          // the target's place among this thread's columns
-        if (a.targets != nullptr && row < n_rows)
-          rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
-        uint32_t v[4][32];
+      uint32_t v[kMode == kProducts ? 2 : 4][32];
+      if constexpr (kMode != kProducts) {
+        // the logits of this thread's 128 columns, the same bits in both kernels
         bool ready = true;
         for (int i = 0; i < u.turns; ++i) {
           const uint32_t acc = 2 * group + (turn & 1);
@@ -507,6 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(acc);
         }
         if (!ready) break;
+      }
+      if constexpr (kMode == kStats) {
+        int rel = -1;                                          // the target's place among this thread's columns
+        if (a.targets != nullptr && row < n_rows)
+          rel = a.targets[a.index != nullptr && n_rows < a.T ? a.index[row] : row] - col0;
         auto val = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
         const int live = min(max(a.width - col0, 0), 128);
         if (live < 128) {
@@ -562,27 +565,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.target_logit[row] = y;
           }
         }
-      } else {
-        // 32 columns at a time, the next ones on their way out of TMEM under the arithmetic
-        const uint32_t acc = 2 * group + (turn & 1);
+      } else if constexpr (kMode == kGrad) {
+        const bool on = row < n_rows;
         RowGrad g{0.f, 0.f, 0.f, 0.f};
         int rel = -1;
-        // (the sums of d's second parts are rows of their own)
-        const bool on = row < n_rows || (kMode == kProducts && a.low > 0 && row >= a.low && row < a.low + n_rows);
-        if (kMode == kGrad && on) {
+        if (on) {
           g = a.rows[row];
           rel = a.row_target[row] - a.v0 - col0;
         }
-        const float f = kMode == kProducts && u.w && a.w_factor != nullptr ? *a.w_factor : 1.f;
+        const int live = a.width - col0;
+        if (row0 < (n_rows + 63) / 64 * 64 && (a.low == 0 || row < a.low)) {   // the rows that the products read
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t (&x)[32] = v[c];
+            auto val = [&](int i) { return __uint_as_float(x[i]); };
+            const F2 cc = pack2(a.scale, a.scale), ll = pack2(-g.lse, -g.lse), to2 = pack2(kLog2e, kLog2e);
+            const F2 aa = pack2(g.a, g.a), bb = pack2(g.b, g.b);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 lt = unpack2(mul2(fma2(pack2(val(i), val(i + 1)), cc, ll), to2));
+              const F2 p = pack2(ex2(lt.x), ex2(lt.y));
+              // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from b * inf
+              const F2 w = a.entropy ? fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa) : aa;
+              const float2 d = unpack2(mul2(p, w));
+              x[i] = __float_as_uint(d.x);
+              x[i + 1] = __float_as_uint(d.y);
+            }
+            if ((unsigned)(rel - 32 * c) < 32u) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i == rel - 32 * c) x[i] = __float_as_uint(val(i) + g.zy);
+            }
+            if (live < 32 * c + 32 || !on) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!on || i >= live - 32 * c) x[i] = 0;
+            }
+            uint16_t* dst = a.d_out + (int64_t)row * a.d_pitch + col0 + 32 * c;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_16bit(val(2 * i), val(2 * i + 1), a.f16);
+            store32(dst, w);
+            store32(dst + 16, w + 8);
+            if (a.low > 0) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 high = unpack_16bit(w[i], a.f16);
+                w[i] = pack_16bit(val(2 * i) - high.x, val(2 * i + 1) - high.y, a.f16);
+              }
+              dst += a.low * a.d_pitch;
+              store32(dst, w);
+              store32(dst + 16, w + 8);
+            }
+          }
+        }
+        __syncwarp();
+      } else {
+        // 32 columns at a time, the next ones on their way out of TMEM under the arithmetic
+        const uint32_t acc = 2 * group + (turn & 1);
+        // (the sums of d's second parts are rows of their own)
+        const bool on = row < n_rows || (a.low > 0 && row >= a.low && row < a.low + n_rows);
+        const float f = u.w && a.w_factor != nullptr ? *a.w_factor : 1.f;
         if (!__all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1))) break;
         ++turn;
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
         // the rows of this warp that somebody reads, the columns that there are
-        const bool wanted = kMode == kGrad ? row0 < (n_rows + 63) / 64 * 64 && (a.low == 0 || row < a.low)
-                            : u.w ? a.v0 + row0 < a.V : row0 < a.low + n_rows;
-        const int live = kMode == kGrad ? a.width - col0 : a.H - col0;
-        uint32_t v[2][32], packed[32];
+        const bool wanted = u.w ? a.v0 + row0 < a.V : row0 < a.low + n_rows;
+        const int live = a.H - col0;
+        uint32_t packed[32];
         tmem_ld_32x32b_x32(taddr, v[0]);
         tmem_ld_wait();
         tmem_loaded(v[0]);
@@ -591,48 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t (&x)[32] = v[c & 1];
           if (c < 3) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
           auto val = [&](int i) { return __uint_as_float(x[i]); };
-          if constexpr (kMode == kGrad) {
-            if (wanted) {
-              const F2 cc = pack2(a.scale, a.scale), ll = pack2(-g.lse, -g.lse), to2 = pack2(kLog2e, kLog2e);
-              const F2 aa = pack2(g.a, g.a), bb = pack2(g.b, g.b);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 lt = unpack2(mul2(fma2(pack2(val(i), val(i + 1)), cc, ll), to2));
-                const F2 p = pack2(ex2(lt.x), ex2(lt.y));
-                // 2^-1000 is 0: the clamp changes no product, and keeps 0 away from b * inf
-                const F2 w = a.entropy ? fma2(bb, pack2(fmaxf(lt.x, -1000.f), fmaxf(lt.y, -1000.f)), aa) : aa;
-                const float2 d = unpack2(mul2(p, w));
-                x[i] = __float_as_uint(d.x);
-                x[i + 1] = __float_as_uint(d.y);
-              }
-              if ((unsigned)(rel - 32 * c) < 32u) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i == rel - 32 * c) x[i] = __float_as_uint(val(i) + g.zy);
-              }
-              if (live < 32 * c + 32 || !on) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!on || i >= live - 32 * c) x[i] = 0;
-              }
-              uint16_t* dst = a.d_out + (int64_t)row * a.d_pitch + col0 + 32 * c;
-              uint32_t w[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = pack_16bit(val(2 * i), val(2 * i + 1), a.f16);
-              store32(dst, w);
-              store32(dst + 16, w + 8);
-              if (a.low > 0) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float2 high = unpack_16bit(w[i], a.f16);
-                  w[i] = pack_16bit(val(2 * i) - high.x, val(2 * i + 1) - high.y, a.f16);
-                }
-                dst += a.low * a.d_pitch;
-                store32(dst, w);
-                store32(dst + 16, w + 8);
-              }
-            }
-          } else if (!u.w) {
+          if (!u.w) {
             if (wanted && on) {
               // float32 sums of dhidden, 8 columns at a time: this thread's alone
               float* dst = a.x_sums + ((int64_t)u.split * a.x_pitch + row) * a.H + col0 + 32 * c;

@@ -84,3 +84,28 @@ def test_a_workspace_may_begin_at_any_16_bytes(cuda_lib):
                 assert all(torch.equal(a, b) for a, b in zip(got, wanted))
                 assert (buf[:lead] == 0x5A).all() and (buf[lead + n:] == 0x5A).all()
     assert cuda_lib.nvfp4_status_check() == 0
+
+
+@pytest.mark.parametrize("T", [40, 100, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradients_of_almost_certain_rows(cuda_lib, T, dtype):
+    """1 - p of a target that has nearly all the probability comes out right only from the very logits that made
+    lse.  Seen in the sum of d over the tokens, which is 0: a column of ones in the weight."""
+    V, H = 1000, 2048
+    rng = np.random.default_rng(T)
+    w = rng.normal(0, 0.1, (V, H))
+    w[:, 0] = 1.0
+    y = rng.integers(0, V, T).astype(np.int32)
+    x = 0.7 * w[y]                                       # the target's logit is 14, a sum of squares
+    x[:, 0] = 0.0
+    xt, wt, yt = store(x, dtype), store(w, dtype), torch.from_numpy(y).cuda()
+    _, lse, _ = cuda_lib.head_logprobs(xt, wt, yt, entropy=False)
+    dx, _ = cuda_lib.head_logprobs_backward(xt, wt, lse, yt, torch.ones(T, device="cuda"))
+    c = f64(xt) @ f64(wt).T
+    p = np.exp(c - f64(lse)[:, None])
+    rest = 1 - p[np.arange(T), y]
+    assert rest.max() < 0.01
+    # each d's rounding, of |d| adding up to 2 (1 - p); p by the softmax's error on both ways, lse's rounding
+    tol = 2 * HALF_STEP[dtype] * (rest + 1e-4) + 2 * softmax_bound(c) + 8 * U * (1 + np.abs(f64(lse)))
+    assert np.all(np.abs(f64(dx)[:, 0]) <= tol)
+    assert cuda_lib.nvfp4_status_check() == 0
