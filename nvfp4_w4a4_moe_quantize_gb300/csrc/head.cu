@@ -51,13 +51,15 @@ constexpr float kLowestLse = -16777216.f;
 
 enum : int { kStats = 0, kGrad = 1, kProducts = 2 };
 
-// The statistics' logits are summed in stretches of at most 1024 products: a tensor core cuts a float32 sum
-// off where it adds to it, always towards zero, so the error of a long sum grows with its length; the
-// stretches are added to one another in registers, rounded to nearest.  Measured at H = 2048, relative errors of
-// lse / entropy and the time of 8192 x 131072 logits: one stretch 6e-7 / 1.1e-6, 2.25 ms; 1024: 3e-7 / 5e-7,
-// 2.27 ms; 512: 1.3e-7 / 2.4e-7, 2.33 ms (an accumulator takes some 4000 cycles to read under running MMAs, so
-// shorter stretches wait for it).
-constexpr int kStretch = 1024 / kBK;
+// Logits are summed in stretches of at most 512 products.  A tensor core adds 16 products at a time and cuts off
+// what lies below the largest of them and of the sum, always towards zero, so the error of a long sum grows with its
+// length (measured: sums of one sign lose 2.4 units in the last place a step, sums of random signs a quarter); the
+// stretches are added to one another in registers, rounded to nearest.  H = 2048, relative errors of lse / entropy and the
+// time of 8192 x 131072 logits: one stretch 6e-7 / 1.1e-6, 2.25 ms; 1024: 3e-7 / 5e-7, 2.24 ms; 512: 1.5e-7 / 2.4e-7,
+// 2.34 ms; a float32 product 0.9e-7 / 5e-7.  (An accumulator takes some 4000 cycles to read under running MMAs, so
+// shorter stretches wait for it: 256 at H = 1024 takes 770 us of 8192 x 65536 logits, 512 609, 1024 571.)  A single
+// row's log probability, 12 inputs of H = 2048: up to 1.7e-6 off with 1024, 7e-7 with 512.
+constexpr int kStretch = 512 / kBK;
 
 // Columns of a tile: 256; 128 for the logits of few rows by single CTAs, which the weight's bytes bound: the
 // smaller tiles spread more evenly over the SMs (96 x 50021 x 1032: 30 us against 34).

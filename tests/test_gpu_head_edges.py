@@ -86,6 +86,42 @@ def test_a_workspace_may_begin_at_any_16_bytes(cuda_lib):
     assert cuda_lib.nvfp4_status_check() == 0
 
 
+def slope(got, want):
+    """The mean relative error, weighted by want^2: what roundings of either sign leave out, and a cut does not."""
+    return ((got.double() - want) * want).sum().item() / (want * want).sum().item()
+
+
+def cut_steps(x, w, stretch):
+    """What sums of x_h w_h >= 0 lose at most, added 16 products at a time, in stretches.  A step aligns its addends
+    to the largest's exponent, the sum's, and keeps two bits below the last place: each product loses less than a
+    quarter of a unit in the sum's last place, the new sum less than a unit."""
+    p = (x * w).reshape(-1, 16).sum(1)
+    lost = 0.0
+    for a in range(0, len(p), stretch // 16):
+        s = np.cumsum(p[a:a + stretch // 16])
+        lost += (5 * 2.0 ** (np.floor(np.log2(np.maximum(s, 1e-300))) - 23)).sum()
+    return lost
+
+
+def test_long_logits_of_the_gradients(cuda_lib):
+    """Logits that are long sums of one sign: p is exp of them, and d of 64 equally likely tokens shows their
+    error whole.  In a single sum of 1024 steps the logits, about 56, lose 6e-3."""
+    T, V, H = 1000, 192, 16384
+    rng = np.random.default_rng(3)
+    x = store(rng.uniform(0.9, 1.1, (T, H)) * 0.0625, "f16")
+    w = store(np.where(np.arange(V)[:, None] < 64, 0.055, 0.0) + np.zeros((V, H)), "f16")
+    y = torch.full((T,), V - 1, dtype=torch.int32, device="cuda")
+    lse = torch.logsumexp(x.double() @ w.double().t(), 1).float()
+    _, dw = cuda_lib.head_logprobs_backward(x, w, lse, y, torch.ones(T, device="cuda"), need_hidden=False)
+    want = -(torch.full((T, 64), 1 / 64, dtype=torch.float64, device="cuda")).t() @ x.double()
+    # the logits' cuts in stretches of 512 products (row by row the same to 1%); lse's rounding, the exponent's
+    # and ex2's; eight deviations of the roundings of d, one a row (all 64 tokens share it), and of the result
+    c = 1.01 * cut_steps(f64(x)[0], f64(w)[0], 512)
+    tol = c + 64 * U + 20 * U + 8 * HALF_STEP["f16"] / 3 ** 0.5 * (T ** -0.5 + H ** -0.5)
+    assert c < 5e-4 and abs(slope(dw[:64], want)) <= tol
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
 @pytest.mark.parametrize("T", [40, 100, 300])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_gradients_of_almost_certain_rows(cuda_lib, T, dtype):
@@ -109,3 +145,17 @@ def test_gradients_of_almost_certain_rows(cuda_lib, T, dtype):
     tol = 2 * HALF_STEP[dtype] * (rest + 1e-4) + 2 * softmax_bound(c) + 8 * U * (1 + np.abs(f64(lse)))
     assert np.all(np.abs(f64(dx)[:, 0]) <= tol)
     assert cuda_lib.nvfp4_status_check() == 0
+
+
+@pytest.mark.parametrize("T", [1, 200])
+def test_a_logit_is_summed_in_short_stretches(cuda_lib, T):
+    """One token, whose lse is its logit: 1, and a little less than a last place of it at every further step of 16
+    products, which a sum without an end loses every time."""
+    H = 2048
+    x, w = np.ones((T, H)), np.full((1, H), 0.984375 * 2.0 ** -27)
+    w[0, 0], w[0, 1:16] = 1.0, 0.0
+    _, lse, ent = cuda_lib.head_logprobs(store(x, "bf16"), store(w, "bf16"))
+    want = (x @ w.T)[:, 0]
+    # 31 further steps of the first 512 products lose it; the other stretches do not; four sums' roundings
+    assert np.all(np.abs(f64(lse) - want) <= 31 * 0.984375 * 2.0 ** -23 + 4 * U)
+    assert (ent == 0).all() and cuda_lib.nvfp4_status_check() == 0
