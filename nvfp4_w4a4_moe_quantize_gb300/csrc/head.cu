@@ -61,6 +61,14 @@ enum : int { kStats = 0, kGrad = 1, kProducts = 2 };
 // row's log probability, 12 inputs of H = 2048: up to 1.7e-6 off with 1024, 7e-7 with 512.
 constexpr int kStretch = 512 / kBK;
 
+// The gradients' products, as long as the vocabulary or the batch, go in stretches of at most 8192, added in float32
+// through a part of the workspace that stays in L2 (a thread reads its own numbers again).  A single sum of 131072
+// lost 2.6e-4 of a target's w_y, where half precision's own rounding is 2.4e-4; in stretches 2e-5.  8192 x 131072 x 2048,
+// four of them a tile of dhidden: 7.28 -> 7.42 ms; stretches of 16384 7.40, of 4096 7.74.
+constexpr int kLong = 8192 / kBK;
+constexpr int kMaxCtas = 152;            // a GB300's SMs; the grid is no larger
+constexpr size_t kLongBytes = (size_t)kEpiWarps * 32 * 128 * 4;   // of a CTA
+
 // Columns of a tile: 256; 128 for the logits of few rows by single CTAs, which the weight's bytes bound: the
 // smaller tiles spread more evenly over the SMs (96 x 50021 x 1032: 30 us against 34).
 constexpr int tile_cols(int mode, bool pair) { return pair || mode == kProducts ? 256 : 128; }
@@ -140,6 +148,7 @@ struct HeadArgs {
   uint16_t* d_out;           // [rows][d_pitch]
   int64_t d_pitch;
   // products
+  float* long_sums;          // [CTAs][kLongBytes]: of a tile's earlier stretches; null: one stretch each
   float* x_sums;             // [x_splits][x_pitch][H]
   int x_splits;              // parts of dhidden's contraction
   int64_t x_pitch;           // rows between their sums
@@ -248,8 +257,10 @@ struct Plan {
     u.m = t / xn;
     u.n = t - u.m * xn;
     u.cols = min(kBN, (a.H - u.n * kBN + 31) / 32 * 32);
-    u.turns = 1;
-    u.len = u.k1 - u.k0;
+    const int span = u.k1 - u.k0;
+    u.turns = a.long_sums != nullptr ? max((span + kLong - 1) / kLong, 1) : 1;
+    constexpr int kSub = Ring<kMode, kPair>::kSub;
+    u.len = ((span + u.turns - 1) / u.turns + kSub - 1) / kSub * kSub;   // whole stages
     return true;
   }
 };
@@ -279,7 +290,9 @@ __device__ __forceinline__ float2 unpack_16bit(uint32_t w, int f16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-template <int kMode, bool kPair>
+// kMany: products whose contractions have several stretches.  (Asked of every tile, it slowed the tiles of one: 335 us
+// against 311 at 48 x 131072 x 2048.)
+template <int kMode, bool kPair, bool kMany>
 __global__ void __launch_bounds__(kThreads, 1)
     head_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap gathered,
                 const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap dlogits,
@@ -624,71 +637,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       } else {
         // 32 columns at a time, the next ones on their way out of TMEM under the arithmetic
-        const uint32_t acc = 2 * group + (turn & 1);
         // (the sums of d's second parts are rows of their own)
         const bool on = row < n_rows || (a.low > 0 && row >= a.low && row < a.low + n_rows);
         const float f = u.w && a.w_factor != nullptr ? *a.w_factor : 1.f;
-        if (!__all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1))) break;
-        ++turn;
-        tc_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
         // the rows of this warp that somebody reads, the columns that there are
         const bool wanted = u.w ? a.v0 + row0 < a.V : row0 < a.low + n_rows;
         const int live = a.H - col0;
-        uint32_t packed[32];
-        tmem_ld_32x32b_x32(taddr, v[0]);
-        tmem_ld_wait();
-        tmem_loaded(v[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t (&x)[32] = v[c & 1];
-          if (c < 3) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
-          auto val = [&](int i) { return __uint_as_float(x[i]); };
-          if (!u.w) {
-            if (wanted && on) {
-              // float32 sums of dhidden, 8 columns at a time: this thread's alone
-              float* dst = a.x_sums + ((int64_t)u.split * a.x_pitch + row) * a.H + col0 + 32 * c;
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                if (32 * c + i >= live) break;
-                if (u.k0 >= u.k1) {
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) x[i + j] = 0;
-                }
-                if (!a.x_first) {
-                  uint32_t o[8];
-                  load32(dst + i, o);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) x[i + j] = __float_as_uint(__uint_as_float(o[j]) + val(i + j));
-                }
-                store32(dst + i, x + i);
-              }
-            }
-          } else if (wanted && 64 * (c / 2) < live) {
-            // 64 columns of dweight's rows through a box: whole lines (rows behind V, columns behind H are cut)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              packed[16 * (c & 1) + i] =
-                  u.k0 >= u.k1 ? 0 : pack_16bit(val(2 * i) * f, val(2 * i + 1) * f, a.f16);
-            if (c & 1) {
-              if (lane == 0) bulk_wait_read<0>();
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                    make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_2d(&dweight, buf, col0 + 32 * (c - 1), a.v0 + row0);
-                bulk_commit();
-              }
-            }
-          }
+        bool ready = true;
+        for (int i = 0; i < (kMany ? u.turns : 1); ++i) {
+          const bool last = !kMany || i + 1 == u.turns;
+          const uint32_t acc = 2 * group + (turn & 1);
+          ready = __all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1));
+          if (!ready) break;
+          ++turn;
+          tc_fence_after();
+          const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+          uint32_t packed[32];
+          tmem_ld_32x32b_x32(taddr, v[0]);
           tmem_ld_wait();
-          tmem_loaded(v[(c + 1) & 1]);
-          if (c == 2) release(acc);   // the last columns are in registers
+          tmem_loaded(v[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t (&x)[32] = v[c & 1];
+            if (c < 3) tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v[(c + 1) & 1]);
+            auto val = [&](int i) { return __uint_as_float(x[i]); };
+            if (kMany && wanted && u.turns > 1) {
+              float* part = a.long_sums + ((int64_t)blockIdx.x * kEpiWarps + ew) * (128 * 32) + (c * 128 + lane) * 8;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {   // 8 columns, a warp's 32 rows side by side
+                if (i > 0) {
+                  uint32_t o[8];
+                  load32(part + j * 256, o);
+#pragma unroll
+                  for (int h = 0; h < 8; ++h) x[8 * j + h] = __float_as_uint(__uint_as_float(o[h]) + val(8 * j + h));
+                }
+                if (!last) store32(part + j * 256, x + 8 * j);
+              }
+            }
+            if (!last) {
+            } else if (!u.w) {
+              if (wanted && on) {
+                // float32 sums of dhidden, 8 columns at a time: this thread's alone
+                float* dst = a.x_sums + ((int64_t)u.split * a.x_pitch + row) * a.H + col0 + 32 * c;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  if (32 * c + i >= live) break;
+                  if (u.k0 >= u.k1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i + j] = 0;
+                  }
+                  if (!a.x_first) {
+                    uint32_t o[8];
+                    load32(dst + i, o);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i + j] = __float_as_uint(__uint_as_float(o[j]) + val(i + j));
+                  }
+                  store32(dst + i, x + i);
+                }
+              }
+            } else if (wanted && 64 * (c / 2) < live) {
+              // 64 columns of dweight's rows through a box: whole lines (rows behind V, columns behind H are cut)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                packed[16 * (c & 1) + i] =
+                    u.k0 >= u.k1 ? 0 : pack_16bit(val(2 * i) * f, val(2 * i + 1) * f, a.f16);
+              if (c & 1) {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                      make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_2d(&dweight, buf, col0 + 32 * (c - 1), a.v0 + row0);
+                  bulk_commit();
+                }
+              }
+            }
+            tmem_ld_wait();
+            tmem_loaded(v[(c + 1) & 1]);
+            if (c == 2) release(acc);   // the last columns are in registers
+          }
         }
+        if (!ready) break;
       }
     }
     if (kMode == kProducts && lane == 0) bulk_wait_all<0>();
@@ -1063,7 +1096,8 @@ struct BackwardPlan {
   int low;                   // where d has two parts, T rounded up to 16; else 0
   int64_t piece;             // columns of a piece of the vocabulary
   int splits;
-  size_t n, factors, place, index, grad, target, row_factor, gathered, weighted, d, sums, total;
+  bool many;
+  size_t n, factors, place, index, grad, target, row_factor, gathered, weighted, d, sums, long_sums, total;
 };
 BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   BackwardPlan p;
@@ -1094,15 +1128,19 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   p.weighted = take(2 * rows64 * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
   p.d = take(2 * (size_t)p.rows * (size_t)p.piece);
   p.sums = take(4 * (size_t)p.splits * (size_t)p.rows * (size_t)H);
+  // a contraction of dhidden is at most V long, of dweight T; `many`: one of them is longer than a stretch
+  p.long_sums = take(std::max(T, V) > kLong * kBK ? kMaxCtas * kLongBytes : 0);
+  const int64_t x_blocks = (std::min(p.piece, V) + kBK - 1) / kBK;
+  p.many = (x_blocks + p.splits - 1) / p.splits > kLong || T > kLong * kBK;
   p.total = at + 240;        // the areas begin at the first whole 256 bytes of a 16-byte aligned workspace
   return p;
 }
 
-template <int kMode, bool kPair>
+template <int kMode, bool kPair, bool kMany>
 cudaError_t launch_head(const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t units, cudaStream_t s) {
-  const void* fn = (const void*)head_kernel<kMode, kPair>;
+  const auto fn = head_kernel<kMode, kPair, kMany>;
   static std::atomic<bool> attr_set[64];
-  cudaError_t err = set_smem_attr_once(attr_set, fn, (int)smem_bytes<kMode, kPair>());
+  cudaError_t err = set_smem_attr_once(attr_set, (const void*)fn, (int)smem_bytes<kMode, kPair>());
   if (err != cudaSuccess || units == 0) return err;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -1118,13 +1156,16 @@ cudaError_t launch_head(const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 2 : 1;
   int64_t clusters = kPair ? num_sms() / 2 : num_sms();
-  if (units < clusters) clusters = units;
+  clusters = std::min<int64_t>({clusters, units, kMaxCtas / (kPair ? 2 : 1)});
   cfg.gridDim = dim3((unsigned)(clusters * (kPair ? 2 : 1)), 1, 1);
-  return cudaLaunchKernelEx(&cfg, head_kernel<kMode, kPair>, maps[0], maps[1], maps[2], maps[3], maps[4], a);
+  return cudaLaunchKernelEx(&cfg, fn, maps[0], maps[1], maps[2], maps[3], maps[4], a);
 }
 template <int kMode>
 cudaError_t launch_head(bool pair, const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t units, cudaStream_t s) {
-  return pair ? launch_head<kMode, true>(maps, a, units, s) : launch_head<kMode, false>(maps, a, units, s);
+  if constexpr (kMode == kProducts)
+    if (a.long_sums != nullptr)
+      return pair ? launch_head<kMode, true, true>(maps, a, units, s) : launch_head<kMode, false, true>(maps, a, units, s);
+  return pair ? launch_head<kMode, true, false>(maps, a, units, s) : launch_head<kMode, false, false>(maps, a, units, s);
 }
 
 }  // namespace
@@ -1209,6 +1250,7 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   const bool weighted = f16 || p.low > 0;   // the rows that dweight's product reads are copies
   a.rows = g.rows, a.row_target = g.row_target, a.entropy = dentropy != nullptr, 
   a.d_out = reinterpret_cast<uint16_t*>(ws + p.d), a.d_pitch = p.piece, a.x_sums = f32(p.sums);
+  a.long_sums = p.many ? f32(p.long_sums) : nullptr;
   a.x_splits = p.splits, a.x_pitch = p.rows;
   a.want_x = dhidden != nullptr, a.want_w = dweight != nullptr;
   a.w_factor = f16 ? g.factors : nullptr;

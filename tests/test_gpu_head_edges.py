@@ -91,6 +91,53 @@ def slope(got, want):
     return ((got.double() - want) * want).sum().item() / (want * want).sum().item()
 
 
+def test_long_sums_of_the_hidden_rows_gradient(cuda_lib):
+    """dhidden of rows whose target comes first among 131072 tokens: w_y is added at the start, and every later
+    step cuts the sum off.  In a single sum of 8192 steps that takes 3e-4 of the result."""
+    T, V, H = 2048, 131072, 1280
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randn(V, H, generator=gen, device="cuda").half()
+    x = (torch.randn(T, H, generator=gen, device="cuda") * 0.01).half()
+    y = torch.randint(0, 64, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    g = torch.ones(T, device="cuda")
+    _, lse, _ = cuda_lib.head_logprobs(x, w, y, entropy=False)
+    dx, _ = cuda_lib.head_logprobs_backward(x, w, lse, y, g, need_weight=False)
+    want, wd = torch.empty(T, H, dtype=torch.float64, device="cuda"), w.double()
+    for a in range(0, T, 256):
+        d = -torch.softmax(x[a:a + 256].double() @ wd.t(), 1)
+        d.scatter_add_(1, y[a:a + 256].long()[:, None], torch.ones(256, 1, dtype=torch.float64, device="cuda"))
+        want[a:a + 256] = d @ wd
+    # 512 steps a stretch of at most 2^-23 of a sum that is w_y up to some percent (half of it on average: the small
+    # addends' own cuts are of either sign); d_y = 1 - p_y, p_y about 2^-17, is rounded to 1; 2^-16 for the other
+    # roundings, of either sign and of 2.6 million elements (2^-11 / 1000 for each kind)
+    assert abs(slope(dx, want)) <= 512 * 2.0 ** -23 * 1.1 + 2.0 ** -16 + 2.0 ** -16
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
+def test_long_sums_of_the_weights_gradient(cuda_lib):
+    """dweight of 262144 rows, of which the first 64 weigh 4096 times as much as the others."""
+    T, V, H = 262144, 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w = (torch.randn(V, H, generator=gen, device="cuda") * 0.05).half()
+    x = torch.randn(T, H, generator=gen, device="cuda").half()
+    y = torch.randint(0, V, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    g = torch.full((T,), 2.0 ** -12, device="cuda")
+    g[:64] = 1.0
+    _, lse, _ = cuda_lib.head_logprobs(x, w, y, entropy=False)
+    _, dw = cuda_lib.head_logprobs_backward(x, w, lse, y, g, need_hidden=False)
+    xd = x.double()
+    d = torch.softmax(xd @ w.double().t(), 1).neg_()
+    d.scatter_add_(1, y.long()[:, None], torch.ones(T, 1, dtype=torch.float64, device="cuda"))
+    want = (d * g.double()[:, None]).t() @ xd
+    # 512 steps a stretch of at most 2^-23 of a sum that is the first rows' up to a few percent; and eight deviations of the
+    # roundings, uniform within 2^-11 of the value: the result's, and those of the heavy rows' d
+    norm = (want * want).sum()
+    own = (want ** 4).sum().sqrt() / norm
+    heavy = (d[:64] * (xd[:64] @ want.t())).norm() / norm
+    assert abs(slope(dw, want)) <= 512 * 2.0 ** -23 * 1.1 + 8 * 2.0 ** -11 / 3 ** 0.5 * (own + heavy).item()
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
 def cut_steps(x, w, stretch):
     """What sums of x_h w_h >= 0 lose at most, added 16 products at a time, in stretches.  A step aligns its addends
     to the largest's exponent, the sum's, and keeps two bits below the last place: each product loses less than a
