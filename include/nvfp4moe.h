@@ -632,7 +632,8 @@ nvfp4_status head_logprobs(const void* hidden, int64_t ldh, const void* weight, 
  *   [V, H], dense, of `dtype`, 16-byte aligned, rounded once; either may be NULL.
  * The vocabulary goes in pieces: the logits of a piece are computed again, d of a piece is held in
  * `dtype` (half precision: as d over a power of two of the row's weight; T <= 64: as two numbers, the
- * rounded one and what the rounding left), sums are float32 in a fixed order.  Deterministic.
+ * rounded one and what the rounding left), sums are float32 in a fixed order.  Deterministic.  Half
+ * precision: rows whose weight is less than 2^-22 of the heaviest's lose bits in dweight.
  *   lse, entropy: the forward's; targets and dlogprob, entropy and dentropy: device or NULL (dlogprob
  *     needs targets, dentropy needs entropy).  Outputs must not overlap inputs.
  *   workspace: nvfp4_workspace_size(NVFP4_OP_HEAD_LOGPROBS_BACKWARD, T, V, 0, H, 0) bytes, 16-byte

@@ -866,9 +866,13 @@ struct GatherArgs {
   int32_t* row_target;
 };
 
-// Half precision holds d only down to 2^-24: a row travels as d / r with r the power of two above its
-// weight, and its hidden row as hidden r / max r.
+// Half precision holds d only down to 2^-24: a row travels as d / r with r a power of two above its
+// weight, and its hidden row as hidden r / max r.  A row lighter than the heaviest has r up to 2^8 times its weight, so
+// that its hidden row keeps its bits: d reaches 2^-30 of the weight there (an even share of 2^20 tokens is still a
+// normal number), and the hidden row is as it is down to weights of 2^-8 of the heaviest, its numbers of 1 and more normal
+// ones down to 2^-22.  Below that it loses a bit for each power of two; the result reaches 2^-30 of its own largest.
 constexpr float kUp = 16384.f;    // d / r is below 1: 2^14 leaves room below the largest value
+constexpr float kDown = 256.f;
 __device__ __forceinline__ float row_weight(const GatherArgs& a, int64_t t) {
   const float g = a.dlogprob != nullptr ? fabsf(a.dlogprob[t]) : 0.f;
   const float h = a.dentropy != nullptr ? fabsf(a.dentropy[t]) : 0.f;
@@ -954,7 +958,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
   const int64_t t = i < n ? a.index[i] : 0;
   float ratio = 1.f;
   if (i < n && a.lse != nullptr) {
-    const float r = scaled ? row_weight(a, t) : 1.f;
+    const float r = scaled ? fminf(kDown * row_weight(a, t), a.factors[1]) : 1.f;
     if (scaled) ratio = a.factors[1] > 0.f ? r / a.factors[1] : 1.f;
     if (lane == 0) {
       const float up = !scaled ? 1.f : r > 0.f ? kUp / r : 0.f;

@@ -206,3 +206,31 @@ def test_a_logit_is_summed_in_short_stretches(cuda_lib, T):
     # 31 further steps of the first 512 products lose it; the other stretches do not; four sums' roundings
     assert np.all(np.abs(f64(lse) - want) <= 31 * 0.984375 * 2.0 ** -23 + 4 * U)
     assert (ent == 0).all() and cuda_lib.nvfp4_status_check() == 0
+
+
+@pytest.mark.parametrize("T", [40, 140, 300])
+@pytest.mark.parametrize("light", [2.0 ** -6, 2.0 ** -14, 2.0 ** -18, 2.0 ** -22])
+def test_half_precision_rows_far_lighter_than_the_heaviest(cuda_lib, T, light):
+    """A row's own token, which the heavier rows have no share in: its weight's gradient is the light row's alone, a
+    normal number, and as exact as any."""
+    V, H = 400, 48
+    rng = np.random.default_rng(T)
+    x = rng.choice([-1, 1], (T, H)) * rng.uniform(1.0, 3.9, (T, H))
+    x[:, 0], x[0, 0] = 3.0, -3.0
+    w = rng.normal(0, 0.05, (V, H))
+    w[:, 0] = 0.0
+    w[7, 0] = -20.0                                      # 60 for row 0, -60 for the others
+    xt, wt = store(x, "f16"), store(w, "f16")
+    y = rng.integers(8, V, T).astype(np.int32)
+    y[0] = 300                                           # row 0: token 7 is almost certain, and not its target
+    g = np.full(T, 1024.0)
+    g[0] *= light
+    yt, gt = torch.from_numpy(y).cuda(), torch.from_numpy(g).float().cuda()
+    _, lse, _ = cuda_lib.head_logprobs(xt, wt, yt, entropy=False)
+    dx, dw = cuda_lib.head_logprobs_backward(xt, wt, lse, yt, gt)
+    want = -g[0] * f64(xt)[0]                            # dweight of token 7: p = 1
+    # d's rounding (p within 2^-16 of 1), the hidden row's, which is exact where its numbers stay normal, the result's
+    assert np.all(np.abs(f64(dw)[7] - want) <= np.abs(want) * (2 * HALF_STEP["f16"] * (1 + 2.0 ** -10) + 2.0 ** -15))
+    want = g[0] * (f64(wt)[300] - f64(wt)[7])            # and the light row's own gradient
+    assert np.all(np.abs(f64(dx)[0] - want) <= np.abs(want) * (2 * HALF_STEP["f16"]) + g[0] * 20 * 2.0 ** -15)
+    assert cuda_lib.nvfp4_status_check() == 0
