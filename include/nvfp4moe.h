@@ -130,6 +130,8 @@ enum {
   NVFP4_OP_HEAD_LOGPROBS = 9,           /* args: T, V, -, H */
   NVFP4_OP_HEAD_LOGPROBS_BACKWARD = 10  /* args: T, V, -, H */
 };
+/* Of the operators 8 to 10 the size does not fall as T grows: a workspace for the largest batch serves the
+ * smaller ones as well. */
 size_t nvfp4_workspace_size(int op, int64_t T_or_rows, int64_t k_or_cols, int64_t E,
                             int64_t H, int64_t I);
 

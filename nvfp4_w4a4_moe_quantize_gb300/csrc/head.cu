@@ -1127,11 +1127,16 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   p.grad = take(sizeof(RowGrad) * (size_t)T);
   p.target = take(4 * (size_t)T);
   p.row_factor = take(4 * (size_t)T);
-  const size_t rows64 = (size_t)std::max(round_up(T, 64), p.rows);
-  p.gathered = take(2 * rows64 * (size_t)row_pitch(H));
-  p.weighted = take(2 * rows64 * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
-  p.d = take(2 * (size_t)p.rows * (size_t)p.piece);
-  p.sums = take(4 * (size_t)p.splits * (size_t)p.rows * (size_t)H);
+  // The areas are as large as any smaller T needs them, so that a workspace for the largest batch serves the others:
+  // rows <= `most`; a piece is at most 2^28 / rows + 256 or 8192 columns; splits are at most 32, and their tiles at most
+  // one for each CTA (of 128 rows, or 256 a pair), or there is one split.
+  const int64_t most = p.low > 0 && T <= 32 ? p.rows : std::max<int64_t>(round_up(T, 64), 128);
+  const int64_t cells = std::min(most * vp, std::max(((int64_t)1 << 28) + 256 * most, 8192 * most));
+  const int64_t sums = std::max(most, std::min(32 * most, kMaxCtas * kBM / ((H + 255) / 256)));
+  p.gathered = take(2 * (size_t)most * (size_t)row_pitch(H));
+  p.weighted = take(2 * (size_t)most * (size_t)row_pitch(H));   // (a call does not say whether it is half precision)
+  p.d = take(2 * (size_t)cells);
+  p.sums = take(4 * (size_t)sums * (size_t)H);
   // a contraction of dhidden is at most V long, of dweight T; `many`: one of them is longer than a stretch
   p.long_sums = take(std::max(T, V) > kLong * kBK ? kMaxCtas * kLongBytes : 0);
   const int64_t x_blocks = (std::min(p.piece, V) + kBK - 1) / kBK;

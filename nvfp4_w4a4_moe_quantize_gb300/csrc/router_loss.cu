@@ -10,6 +10,7 @@
 // A warp holds a row: lane l the experts l, l + 32, ...; it works on several rows at once, since a row's loads
 // and sums over the lanes are a long chain of little work (one row at a time measured 15 and 22 us for the losses'
 // and the gradient's kernel at 32768 x 128 float32 logits, whose traffic takes 3 and 5).
+#include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -485,8 +486,8 @@ static bool balance_whole(int64_t T, int64_t S, int64_t E) {
 
 size_t balance_workspace(int64_t T, int64_t S, int64_t E) {
   if (balance_whole(T, S, E)) return 0;
-  const size_t chunk = (size_t)balance_chunk(T);
-  const size_t chunks = ((size_t)T + chunk - 1) / chunk, slots = chunks + (size_t)S;
+  // (the most that this T or a smaller one has: a workspace for the largest batch serves the others)
+  const size_t chunks = std::min<size_t>(((size_t)T + kWarps - 1) / kWarps, 152), slots = chunks + (size_t)S;
   return slots * ((size_t)E * 8 + 4) + chunks * 4;
 }
 

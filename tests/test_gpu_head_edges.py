@@ -86,6 +86,28 @@ def test_a_workspace_may_begin_at_any_16_bytes(cuda_lib):
     assert cuda_lib.nvfp4_status_check() == 0
 
 
+def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(cuda_lib):
+    V, H = 9000, 72
+    ws = [torch.empty(cuda_lib.load().nvfp4_workspace_size(op, 700, V, 0, H, 0), dtype=torch.uint8, device="cuda")
+          for op in (cuda_lib.OP_HEAD_LOGPROBS, cuda_lib.OP_HEAD_LOGPROBS_BACKWARD)]
+    for T in (700, 1, 32, 33, 64, 65, 128, 129, 257, 600):
+        xt, wt, y, yt, rng = head(T, V, H, "f16", T)
+        g = torch.from_numpy(rng.normal(size=T)).float().cuda()
+        want = cuda_lib.head_logprobs(xt, wt, yt)
+        want_d = cuda_lib.head_logprobs_backward(xt, wt, want[1], yt, g)
+        got = cuda_lib.head_logprobs(xt, wt, yt, workspace=ws[0])
+        got_d = cuda_lib.head_logprobs_backward(xt, wt, want[1], yt, g, workspace=ws[1])
+        assert all(torch.equal(a, b) for a, b in zip((*got, *got_d), (*want, *want_d))), T
+    z = torch.randn(5000, 16, device="cuda")
+    ids = torch.zeros(5000, 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(cuda_lib.load().nvfp4_workspace_size(cuda_lib.OP_BALANCE_LOSS, 5000, 1, 16, 0, 0), dtype=torch.uint8,
+                     device="cuda")
+    for T in (5000, 4864, 4865, 300, 7):
+        want, got = cuda_lib.moe_balance_loss(z[:T], ids[:T]), cuda_lib.moe_balance_loss(z[:T], ids[:T], workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), T
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
 def slope(got, want):
     """The mean relative error, weighted by want^2: what roundings of either sign leave out, and a cut does not."""
     return ((got.double() - want) * want).sum().item() / (want * want).sum().item()
