@@ -21,10 +21,11 @@
 // are the epilogue: a thread has one row and 128 of the tile's 256 columns.  More than 128 rows run by
 // pairs of CTAs (M = 256, N = 256: 64 KB of operands for 2^22 products), fewer by single ones.
 //
-// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.21-2.29 ms, 1.73-1.79 PF/s,
-// bound by the tensor cores at the power limit (their share of the cycles is 96%; a library product holds 1.74
-// under the same limit); backward 7.04-7.23 ms, 1.64-1.69 PF/s (92% in d, 85% in the products, whose operands lie
-// across the contraction).  One row: 100 us, the weight at 5.8 TB/s.
+// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.34 ms, 1.69 PF/s, backward 7.4-7.5 ms,
+// 1.58-1.60 PF/s; a library product holds 1.74 under the same power limit.  Bound by the tensor cores and, a little
+// behind them, by what precision asks of the epilogue: the logits' stretches (2.25 ms in one) and the long products'
+// (7.28).  One row: 102 us, the weight at 5.8 TB/s.  The statistics and d hold 128 logits a thread at 168 registers, the
+// most that ten warps allow, and spill some 10 of their other values (24-40 bytes).
 #include <algorithm>
 #include <atomic>
 
@@ -111,10 +112,12 @@ static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kProducts, fal
               "shared memory budget");
 
 // d of up to 64 rows is held as two 16-bit numbers, the rounded value and what the rounding left: a gradient of few
-// rows hangs on a few of d's values, the targets', and would show their one rounding (of many rows the errors even
-// out at sqrt(2) of the result's own).  The second numbers are rows of their own behind the first ones', the hidden
-// rows are repeated for them; both products are bound by the weight's bytes there, and 48 x 131072 x 2048 takes 310 us
-// against 287 with one number (65 to 128 rows would fill two tiles).
+// rows hangs on a few of d's values, the targets', and would show their one rounding: errors of 1.4 times, on single
+// inputs 1.6 times the result's own rounding, from 65 rows on slowly evening out at sqrt(2).  The second numbers are
+// rows of their own behind the first ones', the hidden rows are repeated for them; up to 64 rows both products are bound
+// by the weight's bytes, and 48 x 131072 x 2048 takes 310 us against 287 with one number.  From 65 rows on two
+// numbers fill two tiles: 96 and 128 rows take 400 and 418 us against 308 and 310, 256 rows 375 by pairs against 310, and
+// the learner's products would take twice their time; there one number is the choice.
 constexpr int kTwoParts = 64;
 
 // What a row of the gradient needs: d = p (a + b log2 p), + zy at the target.
@@ -1107,13 +1110,15 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   BackwardPlan p;
   p.low = T <= kTwoParts ? (int)round_up(T, 16) : 0;
   p.rows = p.low > 0 ? 2 * p.low : round_up(T, 64);
+  // Pieces of 2^28 elements: 8192 x 131072 x 2048 8.06 ms with all rows, of 2^27 8.34, of 2^29 (1 GB) 7.98.
   const int64_t vp = round_up(V, 256);
   int64_t piece = std::max<int64_t>(8192, round_up(((int64_t)1 << 28) / p.rows, 256));
   const int64_t pieces = (vp + piece - 1) / piece;
   p.piece = round_up((vp + pieces - 1) / pieces, 256);
-  // few rows: dhidden's contraction is cut so that every SM has a part of it
+  // Few rows: dhidden's contraction is cut so that every SM has a part of it, into 32 at most (48 x 131072 x 512:
+  // 148 us; 16 163, 64 190).
   const int64_t tile = pairs(T) ? 2 * kBM : kBM, tiles = (T + tile - 1) / tile * ((H + 255) / 256);
-  p.splits = pieces == 1 ? (int)std::min<int64_t>(std::max<int64_t>(1, (pairs(T) ? 76 : 152) / tiles), 32) : 1;
+  p.splits = pieces == 1 ? (int)std::min<int64_t>(std::max<int64_t>(1, (pairs(T) ? kMaxCtas / 2 : kMaxCtas) / tiles), 32) : 1;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
