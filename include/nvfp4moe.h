@@ -633,8 +633,8 @@ nvfp4_status head_logprobs(const void* hidden, int64_t ldh, const void* weight, 
  *   token_logprobs_backward has none;  dhidden = scale d weight [T, H],  dweight = scale d^T hidden
  *   [V, H], dense, of `dtype`, 16-byte aligned, rounded once; either may be NULL.
  * The vocabulary goes in pieces: the logits of a piece are computed again, d of a piece is held in
- * `dtype` (half precision: as d over a power of two of the row's weight; T <= 64: as two numbers, the
- * rounded one and what the rounding left), sums are float32 in a fixed order.  Deterministic.  Half
+ * `dtype` (half precision: as d over a power of two of the row's weight), with what the rounding left
+ * of the target's d in every row and, for T <= 64, of all of d; sums are float32 in a fixed order.  Deterministic.  Half
  * precision: rows whose weight is less than 2^-22 of the heaviest's lose bits in dweight.
  *   lse, entropy: the forward's; targets and dlogprob, entropy and dentropy: device or NULL (dlogprob
  *     needs targets, dentropy needs entropy).  Outputs must not overlap inputs.

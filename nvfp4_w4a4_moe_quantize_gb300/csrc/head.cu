@@ -28,6 +28,7 @@
 // most that ten warps allow, and spill some 10 of their other values (24-40 bytes).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -111,13 +112,16 @@ static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kProducts, fal
                   smem_bytes<kProducts, true>() <= 232448,
               "shared memory budget");
 
-// d of up to 64 rows is held as two 16-bit numbers, the rounded value and what the rounding left: a gradient of few
-// rows hangs on a few of d's values, the targets', and would show their one rounding: errors of 1.4 times, on single
-// inputs 1.6 times the result's own rounding, from 65 rows on slowly evening out at sqrt(2).  The second numbers are
-// rows of their own behind the first ones', the hidden rows are repeated for them; up to 64 rows both products are bound
-// by the weight's bytes, and 48 x 131072 x 2048 takes 310 us against 287 with one number.  From 65 rows on two
-// numbers fill two tiles: 96 and 128 rows take 400 and 418 us against 308 and 310, 256 rows 375 by pairs against 310, and
-// the learner's products would take twice their time; there one number is the choice.
+// d travels in 16 bits.  A gradient hangs on the targets' d above all, so what their rounding leaves is kept in
+// float32, one number a row: dhidden gains it times the target's weight where its sums are rounded, dweight times the
+// hidden row in the epilogue of the target's tile (a list of blocks of 32 rows for every 32 tokens says where).  Errors
+// of both gradients against the result's own rounding, logits of deviation 2, 65 to 600 rows: 1.4 times, on single
+// inputs 1.6, without it; 1.00-1.01 with it.  8192 x 131072 x 2048 7.49 -> 7.55 ms, 1001 x 50021 x 1032 231 -> 246 us,
+// 96 x 131072 x 2048 308 -> 333 us (the epilogue's instructions bound few rows).
+// Of up to 64 rows all of d is held as two 16-bit numbers, the rounded value and what the rounding left: single
+// values other than the targets' show there as well.  The second numbers are rows of their own behind the first ones',
+// the hidden rows are repeated for them; both products are bound by the weight's bytes, and 48 x 131072 x 2048 takes 310 us
+// against 287 with one number (96 and 128 rows, which fill two tiles, 400 and 418 us; 256 rows by pairs 375).
 constexpr int kTwoParts = 64;
 
 // What a row of the gradient needs: d = p (a + b log2 p), + zy at the target.
@@ -148,6 +152,7 @@ struct HeadArgs {
   const int32_t* row_target;
   bool entropy;              // some row's b is not 0
   int low;                   // rows from a number of d to its second part (a multiple of 16), or 0: there is none
+  float* left;               // [rows]: what the rounding of the target's d left, nullable (d has two parts)
   uint16_t* d_out;           // [rows][d_pitch]
   int64_t d_pitch;
   // products
@@ -158,6 +163,13 @@ struct HeadArgs {
   bool x_first;              // the first piece stores, the others add
   bool want_x, want_w;
   const float* w_factor;     // nullable: 1
+  const uint32_t* marks;     // [V / 32][mark_words]: blocks of 32 rows with a target among 32 tokens; with `left`
+  int mark_words;
+  const void* x_all;         // hidden rows as they are, and gathered (or weighted)
+  int64_t x_all_ld;
+  const void* x_gathered;
+  int64_t x_gathered_ld;
+  float* fixes;              // [CTAs][kLongBytes]: what targets add to a tile
 };
 
 __device__ __forceinline__ uint32_t idesc_16(bool f16, uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
@@ -293,9 +305,9 @@ __device__ __forceinline__ float2 unpack_16bit(uint32_t w, int f16) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// kMany: products whose contractions have several stretches.  (Asked of every tile, it slowed the tiles of one: 335 us
-// against 311 at 48 x 131072 x 2048.)
-template <int kMode, bool kPair, bool kMany>
+// kMany: products whose contractions have several stretches; kLeft: dweight with what the rounding of the targets' d
+// left.  (Asked of every tile they slowed those that have neither: 335 and 341 us against 311 at 48 x 131072 x 2048.)
+template <int kMode, bool kPair, bool kMany, bool kLeft>
 __global__ void __launch_bounds__(kThreads, 1)
     head_kernel(const __grid_constant__ CUtensorMap hidden, const __grid_constant__ CUtensorMap gathered,
                 const __grid_constant__ CUtensorMap weight, const __grid_constant__ CUtensorMap dlogits,
@@ -610,9 +622,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[i + 1] = __float_as_uint(d.y);
             }
             if ((unsigned)(rel - 32 * c) < 32u) {
+              float y = 0.f;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (i == rel - 32 * c) x[i] = __float_as_uint(val(i) + g.zy);
+                if (i == rel - 32 * c) x[i] = __float_as_uint(y = val(i) + g.zy);
+              if (a.left != nullptr) {
+                const float high = unpack_16bit(pack_16bit(y, 0.f, a.f16), a.f16).x;
+                a.left[row] = fabsf(high) < INFINITY ? y - high : 0.f;
+              }
             }
             if (live < 32 * c + 32 || !on) {
 #pragma unroll
@@ -646,19 +663,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the rows of this warp that somebody reads, the columns that there are
         const bool wanted = u.w ? a.v0 + row0 < a.V : row0 < a.low + n_rows;
         const int live = a.H - col0;
-        bool ready = true;
-        for (int i = 0; i < (kMany ? u.turns : 1); ++i) {
-          const bool last = !kMany || i + 1 == u.turns;
-          const uint32_t acc = 2 * group + (turn & 1);
-          ready = __all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1));
-          if (!ready) break;
-          ++turn;
-          tc_fence_after();
-          const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
-          uint32_t packed[32];
-          tmem_ld_32x32b_x32(taddr, v[0]);
-          tmem_ld_wait();
-          tmem_loaded(v[0]);
+        // What the rounding of d left at these 32 tokens' own rows, times the rows: to the lanes that have them, in the
+        // order of the rows (lanes are columns here).
+        uint32_t fixed = 0;
+        float* fix = a.fixes + ((int64_t)blockIdx.x * kEpiWarps + ew) * (32 * 128);
+        // (the word is looked at when the first columns are out of TMEM)
+        const bool marked = u.w && wanted && live > 0 && lane < a.mark_words;
+        const uint32_t mark_at = (uint32_t)(a.v0 + row0) / 32 * a.mark_words + lane;
+        uint32_t mark_word = 0;
+        if (kLeft) asm volatile("ld.global.b32 %0, [%1];" : "=r"(mark_word) : "l"(a.marks + (marked ? mark_at : 0)) : "memory");
+        auto fix_up = [&] {
+          const bool moved = a.always_gathered || n_rows < a.T;
+          const uint16_t* x = static_cast<const uint16_t*>(moved ? a.x_gathered : a.x_all) + col0 + 4 * lane;
+          const int64_t ldx = moved ? a.x_gathered_ld : a.x_all_ld;
+          const int first = a.v0 + row0;
+          int at = -1;                                         // the token whose sum is in registers
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto store = [&] {
+            if (at >= 0 && 4 * lane < live) *reinterpret_cast<float4*>(fix + at * 128 + 4 * lane) = sum;
+          };
+          for (int w0 = 0; w0 < a.mark_words; w0 += 32) {
+            const uint32_t mine = w0 == 0 ? mark_word : w0 + lane < a.mark_words ? a.marks[mark_at + w0] : 0u;
+            for (uint32_t words = __ballot_sync(0xFFFFFFFFu, mine != 0); words != 0; words &= words - 1) {
+              const int word = __ffs(words) - 1;
+              for (uint32_t bits = __shfl_sync(0xFFFFFFFFu, mine, word); bits != 0; bits &= bits - 1) {
+                const int t0 = ((w0 + word) * 32 + __ffs(bits) - 1) * 32;
+                const int mark = t0 + lane < n_rows ? a.row_target[t0 + lane] - first : -1;
+                const float e = t0 + lane < n_rows ? a.left[t0 + lane] : 0.f;
+                uint32_t hits = __ballot_sync(0xFFFFFFFFu, (unsigned)mark < 32u);
+                while (hits != 0) {                            // four rows' loads on their way
+                  int h[4];
+                  uint2 q[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    h[k] = __ffs(hits) - 1;
+                    hits &= hits - 1;
+                    q[k] = h[k] >= 0 && 4 * lane < live ? *reinterpret_cast<const uint2*>(x + (t0 + h[k]) * ldx)
+                                                        : make_uint2(0u, 0u);
+                  }
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if (h[k] < 0) break;
+                    const int to = __shfl_sync(0xFFFFFFFFu, mark, h[k]);
+                    const float f = __shfl_sync(0xFFFFFFFFu, e, h[k]);
+                    if (to != at) {
+                      store();
+                      at = to;
+                      sum = fixed >> to & 1u && 4 * lane < live ? *reinterpret_cast<const float4*>(fix + to * 128 + 4 * lane)
+                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                      fixed |= 1u << to;
+                    }
+                    const float2 lo = unpack_16bit(q[k].x, a.f16), hi = unpack_16bit(q[k].y, a.f16);
+                    sum = make_float4(fmaf(f, lo.x, sum.x), fmaf(f, lo.y, sum.y), fmaf(f, hi.x, sum.z), fmaf(f, hi.y, sum.w));
+                  }
+                }
+              }
+            }
+          }
+          store();
+          __syncwarp();
+        };
+        // A stretch's columns, the next ones on their way.  (Two copies: where there are few rows few warps have a target
+        // among their tokens.)
+        uint32_t packed[32];
+        auto columns = [&](auto fix_here, uint32_t taddr, uint32_t acc, int i, bool last) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t (&x)[32] = v[c & 1];
@@ -699,6 +767,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             } else if (wanted && 64 * (c / 2) < live) {
+              if (decltype(fix_here)::value && (fixed >> lane & 1u)) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  if (32 * c + i >= live) break;
+                  const float4 o = *reinterpret_cast<const float4*>(fix + lane * 128 + 32 * c + i);
+                  x[i] = __float_as_uint(val(i) + o.x), x[i + 1] = __float_as_uint(val(i + 1) + o.y);
+                  x[i + 2] = __float_as_uint(val(i + 2) + o.z), x[i + 3] = __float_as_uint(val(i + 3) + o.w);
+                }
+              }
               // 64 columns of dweight's rows through a box: whole lines (rows behind V, columns behind H are cut)
 #pragma unroll
               for (int i = 0; i < 16; ++i)
@@ -723,6 +800,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_loaded(v[(c + 1) & 1]);
             if (c == 2) release(acc);   // the last columns are in registers
           }
+        };
+        bool ready = true;
+        for (int i = 0; i < (kMany ? u.turns : 1); ++i) {
+          const bool last = !kMany || i + 1 == u.turns;
+          const uint32_t acc = 2 * group + (turn & 1);
+          if (!__all_sync(0xFFFFFFFFu, wait(&sm.accf[acc], (turn >> 1) & 1))) {
+            ready = false;
+            break;
+          }
+          ++turn;
+          tc_fence_after();
+          const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kBN + half * 128;
+          tmem_ld_32x32b_x32(taddr, v[0]);
+          tmem_ld_wait();
+          tmem_loaded(v[0]);
+          if (kLeft && i == 0) {
+            if (!marked) mark_word = 0;
+            if (__any_sync(0xFFFFFFFFu, mark_word != 0) || (a.mark_words > 32 && u.w && wanted && live > 0)) fix_up();
+          }
+          if (kLeft && last && fixed != 0) columns(std::true_type(), taddr, acc, i, last);
+          else columns(std::false_type(), taddr, acc, i, last);
         }
         if (!ready) break;
       }
@@ -867,6 +965,9 @@ struct GatherArgs {
   void* weighted;            // the same times r / max r (half precision) and repeated (two parts), where either is so
   RowGrad* rows;
   int32_t* row_target;
+  float* left;               // nullable, with marks: both cleared here, the marks set
+  uint32_t* marks;
+  int mark_words;
 };
 
 // Half precision holds d only down to 2^-24: a row travels as d / r with r a power of two above its
@@ -892,6 +993,10 @@ __global__ void __launch_bounds__(1024) head_select_kernel(const GatherArgs a) {
   __shared__ float sm_r[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_sync();
+  if (a.marks != nullptr) {
+    const int64_t words = ((int64_t)a.V + 31) / 32 * a.mark_words;
+    for (int64_t i = threadIdx.x; i < words; i += 1024) a.marks[i] = 0u;
+  }
   constexpr int kEach = 8;   // rows a thread, one behind the other
   int base = 0;
   float r = 0.f;
@@ -976,6 +1081,10 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const GatherArgs a) {
       w.zy = a.scale * g;
       a.rows[i] = w;
       a.row_target[i] = hit ? y : -1;
+      if (a.left != nullptr) {
+        a.left[i] = 0.f;
+        if (hit) atomicOr(&a.marks[(int64_t)(y / 32) * a.mark_words + i / 1024], 1u << (i / 32 % 32));
+      }
       a.row_factor[i] = scaled ? r / kUp : 1.f;
     }
   }
@@ -1015,6 +1124,10 @@ struct FinishArgs {
   const int32_t* place;
   const float* row_factor;
   const float* sums;         // [splits][pitch][H]
+  const float* left;         // nullable: d has two parts
+  const int32_t* row_target;
+  const void* weight;
+  int64_t ldw;
   void* out;
 };
 
@@ -1046,7 +1159,17 @@ __global__ void __launch_bounds__(256) head_finish_kernel(const FinishArgs a) {
         v[4] += x[j][1].x, v[5] += x[j][1].y, v[6] += x[j][1].z, v[7] += x[j][1].w;
       }
     }
-    const float f = a.row_factor[place];
+    const float f = a.row_factor[place], e = a.left != nullptr ? a.left[place] : 0.f;
+    if (e != 0.f) {   // what the rounding of the target's d left
+      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) +
+                                                      a.row_target[place] * a.ldw + c);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = unpack_16bit(w[j], a.f16);
+        v[2 * j] = fmaf(e, x.x, v[2 * j]), v[2 * j + 1] = fmaf(e, x.y, v[2 * j + 1]);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= f;
   }
@@ -1104,7 +1227,9 @@ struct BackwardPlan {
   int64_t piece;             // columns of a piece of the vocabulary
   int splits;
   bool many;
-  size_t n, factors, place, index, grad, target, row_factor, gathered, weighted, d, sums, long_sums, total;
+  int mark_words;
+  size_t n, factors, place, index, grad, target, row_factor, gathered, weighted, d, sums, long_sums, left, marks, fixes,
+      total;
 };
 BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   BackwardPlan p;
@@ -1146,13 +1271,17 @@ BackwardPlan backward_plan(int64_t T, int64_t V, int64_t H) {
   p.long_sums = take(std::max(T, V) > kLong * kBK ? kMaxCtas * kLongBytes : 0);
   const int64_t x_blocks = (std::min(p.piece, V) + kBK - 1) / kBK;
   p.many = (x_blocks + p.splits - 1) / p.splits > kLong || T > kLong * kBK;
+  p.mark_words = (int)((T + 1023) / 1024);
+  p.left = take(4 * (size_t)T);
+  p.marks = take(4 * (size_t)((V + 31) / 32) * (size_t)p.mark_words);
+  p.fixes = take(p.low > 0 ? 0 : kMaxCtas * kLongBytes);
   p.total = at + 240;        // the areas begin at the first whole 256 bytes of a 16-byte aligned workspace
   return p;
 }
 
-template <int kMode, bool kPair, bool kMany>
+template <int kMode, bool kPair, bool kMany, bool kLeft>
 cudaError_t launch_head(const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t units, cudaStream_t s) {
-  const auto fn = head_kernel<kMode, kPair, kMany>;
+  const auto fn = head_kernel<kMode, kPair, kMany, kLeft>;
   static std::atomic<bool> attr_set[64];
   cudaError_t err = set_smem_attr_once(attr_set, (const void*)fn, (int)smem_bytes<kMode, kPair>());
   if (err != cudaSuccess || units == 0) return err;
@@ -1176,10 +1305,15 @@ cudaError_t launch_head(const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t
 }
 template <int kMode>
 cudaError_t launch_head(bool pair, const CUtensorMap (&maps)[5], const HeadArgs& a, int64_t units, cudaStream_t s) {
-  if constexpr (kMode == kProducts)
-    if (a.long_sums != nullptr)
-      return pair ? launch_head<kMode, true, true>(maps, a, units, s) : launch_head<kMode, false, true>(maps, a, units, s);
-  return pair ? launch_head<kMode, true, false>(maps, a, units, s) : launch_head<kMode, false, false>(maps, a, units, s);
+  if constexpr (kMode == kProducts) {   // (pairs have more than 64 rows, and one number a d)
+    const bool many = a.long_sums != nullptr;
+    if (pair) return many ? launch_head<kMode, true, true, true>(maps, a, units, s) : launch_head<kMode, true, false, true>(maps, a, units, s);
+    if (a.left != nullptr)
+      return many ? launch_head<kMode, false, true, true>(maps, a, units, s) : launch_head<kMode, false, false, true>(maps, a, units, s);
+    return many ? launch_head<kMode, false, true, false>(maps, a, units, s) : launch_head<kMode, false, false, false>(maps, a, units, s);
+  } else {
+    return pair ? launch_head<kMode, true, false, false>(maps, a, units, s) : launch_head<kMode, false, false, false>(maps, a, units, s);
+  }
 }
 
 }  // namespace
@@ -1250,6 +1384,8 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   g.lse = lse, g.entropy = entropy, g.dlogprob = dlogprob, g.dentropy = dentropy;
   g.place = i32(p.place), g.index = i32(p.index), g.n_rows = i32(p.n), g.factors = f32(p.factors);
   g.row_factor = f32(p.row_factor), g.gathered = ws + p.gathered, g.weighted = ws + p.weighted;
+  if (p.low == 0)
+    g.left = f32(p.left), g.marks = reinterpret_cast<uint32_t*>(ws + p.marks), g.mark_words = p.mark_words;
   g.low = p.low, g.rows = reinterpret_cast<RowGrad*>(ws + p.grad), g.row_target = i32(p.target);
   cudaError_t err = launch_pdl(false, head_select_kernel, dim3(1), dim3(1024), 0, s, g);
   if (err == cudaSuccess)
@@ -1266,6 +1402,8 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
   a.d_out = reinterpret_cast<uint16_t*>(ws + p.d), a.d_pitch = p.piece, a.x_sums = f32(p.sums);
   a.long_sums = p.many ? f32(p.long_sums) : nullptr;
   a.x_splits = p.splits, a.x_pitch = p.rows;
+  a.left = g.left, a.marks = g.marks, a.mark_words = g.mark_words, a.fixes = f32(p.fixes);
+  a.x_all = hidden, a.x_all_ld = ldh, a.x_gathered = weighted ? g.weighted : g.gathered, a.x_gathered_ld = row_pitch(H);
   a.want_x = dhidden != nullptr, a.want_w = dweight != nullptr;
   a.w_factor = f16 ? g.factors : nullptr;
   CUtensorMap grad[5], prod[5];
@@ -1293,7 +1431,8 @@ cudaError_t launch_head_logprobs_backward(const void* hidden, int64_t ldh, const
     if (err != cudaSuccess) return err;
   }
   if (dhidden == nullptr) return cudaSuccess;
-  FinishArgs f{T, p.rows, (int)H, f16, p.splits, a.low, g.place, g.row_factor, f32(p.sums), dhidden};
+  FinishArgs f{T, p.rows, (int)H, f16, p.splits, a.low, g.place, g.row_factor, f32(p.sums), g.left, g.row_target,
+               weight, ldw, dhidden};
   return launch_pdl(true, head_finish_kernel, dim3((unsigned)((T * (H / 8) + 255) / 256)), dim3(256), 0, s, f);
 }
 

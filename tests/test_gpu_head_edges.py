@@ -108,6 +108,43 @@ def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(cuda_lib):
     assert cuda_lib.nvfp4_status_check() == 0
 
 
+@pytest.mark.parametrize("T,H,same", [(65, 264, False), (128, 72, False), (129, 264, False), (300, 1032, False),
+                                      (1100, 328, False), (700, 136, True), (33000, 64, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_the_targets_part_of_d_is_not_rounded_twice(cuda_lib, T, H, same, dtype):
+    """Targets that no row expects: d is -dlogprob there, any float32, and what it adds shows the result's own
+    rounding alone.  The other tokens have no weight in the columns that are looked at."""
+    V, common = 631, 400
+    rng = np.random.default_rng(T)
+    w = np.zeros((V, H))
+    w[:common, 1:8] = rng.normal(0, 0.2, (common, 7))
+    w[common:, 0], w[common:, 8:] = -40.0, rng.choice([-1, 1], (V - common, H - 8)) * rng.uniform(0.02, 0.04, (V - common, H - 8))
+    x = rng.normal(size=(T, H))
+    x[:, 0] = 1.0
+    xt, wt = store(x, dtype), store(w, dtype)
+    y = np.full(T, V - 1, np.int32) if same else rng.integers(common, V, T).astype(np.int32)
+    y[rng.random(T) < 0.1] = IGNORE
+    g = rng.uniform(0.5, 2.0, T) * np.where(same, 1.0, rng.choice([-1, 1], T))
+    yt, gt = torch.from_numpy(y).cuda(), torch.from_numpy(g).float().cuda()
+    _, lse, _ = cuda_lib.head_logprobs(xt, wt, yt, entropy=False)
+    dx, dw = cuda_lib.head_logprobs_backward(xt, wt, lse, yt, gt)
+    on = y != IGNORE
+    g, x, w = f64(gt) * on, f64(xt), f64(wt)
+    hit = np.zeros((T, V - common))
+    hit[np.arange(T)[on], y[on] - common] = g[on]
+    # (p of the targets is below e^-25; float32 sums of up to T addends, cut off towards zero 2.4 units a step of 16)
+    tiny = 2.0 ** -20 + (T / 16) * 2.0 ** -22
+    all_x, all_w = (np.abs(g)[:, None] * np.abs(x)).sum(0), np.abs(g)[:, None] * np.abs(w[common:, 8:]).sum(0)
+    for got, want, mag, most in ((f64(dx)[:, 8:], hit @ w[common:, 8:], np.abs(hit) @ np.abs(w[common:, 8:]), all_w),
+                                 (f64(dw)[common:], hit.T @ x, np.abs(hit).T @ np.abs(x), all_x)):
+        tol = HALF_STEP[dtype] * np.abs(want) + tiny * mag + 2.0 ** -36 * most + (2.0 ** -24 if dtype == "f16" else 0.0)
+        bad = np.abs(got - want) > tol
+        assert not bad.any(), (bad.mean(), got[bad][:4], want[bad][:4])
+    again = cuda_lib.head_logprobs_backward(xt, wt, lse, yt, gt)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    assert cuda_lib.nvfp4_status_check() == 0
+
+
 def slope(got, want):
     """The mean relative error, weighted by want^2: what roundings of either sign leave out, and a cut does not."""
     return ((got.double() - want) * want).sum().item() / (want * want).sum().item()
