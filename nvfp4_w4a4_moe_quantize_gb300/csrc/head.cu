@@ -21,11 +21,12 @@
 // are the epilogue: a thread has one row and 128 of the tile's 256 columns.  More than 128 rows run by
 // pairs of CTAs (M = 256, N = 256: 64 KB of operands for 2^22 products), fewer by single ones.
 //
-// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.34 ms, 1.69 PF/s, backward 7.4-7.5 ms,
-// 1.58-1.60 PF/s; a library product holds 1.74 under the same power limit.  Bound by the tensor cores and, a little
-// behind them, by what precision asks of the epilogue: the logits' stretches (2.25 ms in one) and the long products'
-// (7.28).  One row: 102 us, the weight at 5.8 TB/s.  The statistics and d hold 128 logits a thread at 168 registers, the
-// most that ten warps allow, and spill some 10 of their other values (24-40 bytes).
+// Measured, 8192 x 131072 x 2048 BF16 with a tenth of the rows ignored: forward 2.32-2.34 ms, 1.69-1.71 PF/s, backward
+// 7.49-7.59 ms, 1.56-1.58 PF/s; a library product holds 1.74 under the same power limit.  Bound by the tensor cores and, a
+// little behind them, by what precision asks of the epilogue: the logits' stretches (2.25 ms in one), the long products'
+// (7.28 ms without) and what the rounding of the targets' d left.  One row: 101-102 us, the weight at 5.8 TB/s.  The
+// statistics and d hold 128 logits a thread at 168 registers, the most that ten warps allow, and spill some 10 of their
+// other values (24-52 bytes).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -117,7 +118,10 @@ static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kProducts, fal
 // hidden row in the epilogue of the target's tile (a list of blocks of 32 rows for every 32 tokens says where).  Errors
 // of both gradients against the result's own rounding, logits of deviation 2, 65 to 600 rows: 1.4 times, on single
 // inputs 1.6, without it; 1.00-1.01 with it.  8192 x 131072 x 2048 7.49 -> 7.55 ms, 1001 x 50021 x 1032 231 -> 246 us,
-// 96 x 131072 x 2048 308 -> 333 us (the epilogue's instructions bound few rows).
+// 96 x 131072 x 2048 308 -> 333 us (the epilogue's instructions bound few rows).  One warp adds up what 32 tokens gain,
+// some 400 cycles a row: 8.7 ms against 8.0 where 32 tokens have two fifths of the 8192 rows, at 32768 x 32768 x 1024 8.6
+// against 4.5.  (A kernel of its own for it: 8.4 and 6.0 ms there, but 261 us at 1001 rows, 354 at 96, 5.0 ms with targets at
+// random.)
 // Of up to 64 rows all of d is held as two 16-bit numbers, the rounded value and what the rounding left: single
 // values other than the targets' show there as well.  The second numbers are rows of their own behind the first ones',
 // the hidden rows are repeated for them; both products are bound by the weight's bytes, and 48 x 131072 x 2048 takes 310 us
