@@ -118,10 +118,10 @@ static_assert(smem_bytes<kStats, false>() <= 232448 && smem_bytes<kProducts, fal
 // hidden row in the epilogue of the target's tile (a list of blocks of 32 rows for every 32 tokens says where).  Errors
 // of both gradients against the result's own rounding, logits of deviation 2, 65 to 600 rows: 1.4 times, on single
 // inputs 1.6, without it; 1.00-1.01 with it.  8192 x 131072 x 2048 7.49 -> 7.55 ms, 1001 x 50021 x 1032 231 -> 246 us,
-// 96 x 131072 x 2048 308 -> 333 us (the epilogue's instructions bound few rows).  One warp adds up what 32 tokens gain,
-// some 400 cycles a row: 8.7 ms against 8.0 where 32 tokens have two fifths of the 8192 rows, at 32768 x 32768 x 1024 8.6
-// against 4.5.  (A kernel of its own for it: 8.4 and 6.0 ms there, but 261 us at 1001 rows, 354 at 96, 5.0 ms with targets at
-// random.)
+// 96 x 131072 x 2048 308 -> 335 us (the epilogue's instructions bound few rows).  One warp adds up what 32 tokens gain,
+// some 200 cycles a row where many have targets there: 8.4 ms against 8.05 where 32 tokens have two fifths of the 8192 rows,
+// at 32768 x 32768 x 1024 7.2 against 4.5 (four rows' loads at a time 8.7 and 8.6).  A kernel of its own for it: 8.4 and 6.0 ms
+// there, but 261 us at 1001 rows, 354 at 96, 5.0 ms with targets at random.
 // Of up to 64 rows all of d is held as two 16-bit numbers, the rounded value and what the rounding left: single
 // values other than the targets' show there as well.  The second numbers are rows of their own behind the first ones',
 // the hidden rows are repeated for them; both products are bound by the weight's bytes, and 48 x 131072 x 2048 takes 310 us
@@ -686,6 +686,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto store = [&] {
             if (at >= 0 && 4 * lane < live) *reinterpret_cast<float4*>(fix + at * 128 + 4 * lane) = sum;
           };
+          // a block's next rows, with all of their loads on their way at once
+          auto add = [&](auto flight, int t0, int mark, float e, uint32_t& hits) {
+            constexpr int kFlight = decltype(flight)::value;
+            int h[kFlight];
+            uint2 q[kFlight];
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              h[k] = __ffs(hits) - 1;
+              hits &= hits - 1;
+              q[k] = h[k] >= 0 && 4 * lane < live ? *reinterpret_cast<const uint2*>(x + (t0 + h[k]) * ldx) : make_uint2(0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              if (h[k] < 0) break;
+              const int to = __shfl_sync(0xFFFFFFFFu, mark, h[k]);
+              const float f = __shfl_sync(0xFFFFFFFFu, e, h[k]);
+              if (to != at) {
+                store();
+                at = to;
+                sum = fixed >> to & 1u && 4 * lane < live ? *reinterpret_cast<const float4*>(fix + to * 128 + 4 * lane)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                fixed |= 1u << to;
+              }
+              const float2 lo = unpack_16bit(q[k].x, a.f16), hi = unpack_16bit(q[k].y, a.f16);
+              sum = make_float4(fmaf(f, lo.x, sum.x), fmaf(f, lo.y, sum.y), fmaf(f, hi.x, sum.z), fmaf(f, hi.y, sum.w));
+            }
+          };
           for (int w0 = 0; w0 < a.mark_words; w0 += 32) {
             const uint32_t mine = w0 == 0 ? mark_word : w0 + lane < a.mark_words ? a.marks[mark_at + w0] : 0u;
             for (uint32_t words = __ballot_sync(0xFFFFFFFFu, mine != 0); words != 0; words &= words - 1) {
@@ -695,31 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int mark = t0 + lane < n_rows ? a.row_target[t0 + lane] - first : -1;
                 const float e = t0 + lane < n_rows ? a.left[t0 + lane] : 0.f;
                 uint32_t hits = __ballot_sync(0xFFFFFFFFu, (unsigned)mark < 32u);
-                while (hits != 0) {                            // four rows' loads on their way
-                  int h[4];
-                  uint2 q[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    h[k] = __ffs(hits) - 1;
-                    hits &= hits - 1;
-                    q[k] = h[k] >= 0 && 4 * lane < live ? *reinterpret_cast<const uint2*>(x + (t0 + h[k]) * ldx)
-                                                        : make_uint2(0u, 0u);
-                  }
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if (h[k] < 0) break;
-                    const int to = __shfl_sync(0xFFFFFFFFu, mark, h[k]);
-                    const float f = __shfl_sync(0xFFFFFFFFu, e, h[k]);
-                    if (to != at) {
-                      store();
-                      at = to;
-                      sum = fixed >> to & 1u && 4 * lane < live ? *reinterpret_cast<const float4*>(fix + to * 128 + 4 * lane)
-                                                                : make_float4(0.f, 0.f, 0.f, 0.f);
-                      fixed |= 1u << to;
-                    }
-                    const float2 lo = unpack_16bit(q[k].x, a.f16), hi = unpack_16bit(q[k].y, a.f16);
-                    sum = make_float4(fmaf(f, lo.x, sum.x), fmaf(f, lo.y, sum.y), fmaf(f, hi.x, sum.z), fmaf(f, hi.y, sum.w));
-                  }
+                while (hits != 0) {
+                  if (__popc(hits) > 4) add(std::integral_constant<int, 16>(), t0, mark, e, hits);
+                  else add(std::integral_constant<int, 4>(), t0, mark, e, hits);
                 }
               }
             }
